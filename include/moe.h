@@ -80,6 +80,64 @@ moe_status moe_route_topk(const float* logits, int T, int E, int k,
                           void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Step 1 with scores: routing by softmax or sigmoid scores, a balance bias,
+ * groups of experts and optional renormalisation.  Per token t:
+ *
+ *   s_e = 1 / (1 + exp(-l_e))  or  exp(l_e - max l) / sum_i exp(l_i - max l);
+ *   rank by r_e = s_e + bias_e, or by the logit l_e when `bias` is null;
+ *   n_group > 1: the E experts form n_group groups of E / n_group consecutive
+ *     ones; a group is worth its largest r (group_top 1) or the sum of the two
+ *     largest s + bias in it (group_top 2); experts outside the topk_group
+ *     best groups are no candidates;
+ *   topk_idx[t, :] are the k best candidates in descending r; ties, of
+ *     experts and of groups, go to the lower index;
+ *   topk_w[t, j] = scale * s_j, or scale * s_j / sum_i s_i over the chosen
+ *     experts when `renormalize`.  The bias never enters a weight.
+ *
+ * The choice is made in fp32, each operation rounded to nearest (the softmax's
+ * sum rounded once); with softmax scores, no bias, one group and renormalize
+ * it is moe_route_topk.
+ *
+ *   logits [T, E] fp32, finite; bias [E] fp32 or null, finite or -inf.  -inf
+ *     switches an expert off: it is chosen only where the candidates that are
+ *     on do not fill the k slots, and then has weight 0 (a row with no expert
+ *     on has all weights 0).
+ *   topk_idx [T, k] int32, topk_w [T, k] fp32 out.  ws: 256 bytes.
+ * Limits: 1 <= n_group <= MOE_MAX_GROUPS, a divisor of E; 1 <= topk_group <=
+ * n_group; topk_group * (E / n_group) >= k; group_top 1, or 2 with at least two
+ * experts per group; scale finite.  A logit that is not finite, or a bias that
+ * is NaN or +inf, sets MOE_ERR_NONFINITE in the device status; the indices of
+ * that token are then distinct and in range, its weights unspecified.
+ *
+ * moe_route_scored_backward: dlogits [T, E] fp32 = the gradient of the
+ * weights, given dtopk_w [T, k] = dL/dtopk_w and the topk_idx, logits, bias and
+ * config of the forward.  The choice is a constant: experts that were not
+ * chosen get 0, but for softmax scores that are not renormalised, whose sum
+ * runs over all experts.  A slot whose index is outside [0, E) is skipped and
+ * sets MOE_ERR_INVALID_ARG in the device status; the indices of a token are
+ * otherwise distinct, as the forward writes them.  A non-finite logit that is
+ * read sets MOE_ERR_NONFINITE.  The bias has no gradient.
+ */
+#define MOE_MAX_GROUPS 32
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct {
+  int32_t score;        /* moe_score                                          */
+  int32_t n_group;      /* 1: no groups                                       */
+  int32_t topk_group;   /* groups whose experts are candidates                */
+  int32_t group_top;    /* 1: a group's best expert; 2: the sum of its two best */
+  int32_t renormalize;  /* weights divided by the sum of the chosen scores    */
+  float scale;          /* factor on every weight                             */
+} moe_route_config;
+moe_status moe_route_scored(const float* logits, const float* bias,
+                            const moe_route_config* config, int T, int E, int k,
+                            int32_t* topk_idx, float* topk_w,
+                            void* ws, size_t ws_bytes, void* stream);
+moe_status moe_route_scored_backward(const float* dtopk_w, const int32_t* topk_idx,
+                                     const float* logits, const float* bias,
+                                     const moe_route_config* config, int T, int E, int k,
+                                     float* dlogits, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Step 2 -- per-expert counts and the stable scatter into expert groups
  * ("MegaScale-Infer", §3.4 Fused Kernels, steps (2) and (4); order inside an
  * expert by token, then top-k position: "MegaFlux", §A.2).
@@ -201,6 +259,17 @@ moe_status moe_forward(const void* x, const float* router_logits,
                        const void* W1, const void* W3, const void* W2,
                        int T, int H, int F, int E, int k, void* out,
                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_forward, with moe_route_scored in the place of step 1: the same
+ * arguments, workspace and status, and the router's bias (or null) and
+ * configuration.
+ */
+moe_status moe_forward_scored(const void* x, const float* router_logits, const float* bias,
+                              const moe_route_config* config,
+                              const void* W1, const void* W3, const void* W2,
+                              int T, int H, int F, int E, int k, void* out,
+                              void* ws, size_t ws_bytes, void* stream);
 
 /*
  * moe_forward captured once into a CUDA graph, for small batches whose
@@ -346,6 +415,23 @@ moe_status moe_backward(const void* dout, const float* router_logits,
                         int T, int H, int F, int E, int k,
                         void* dx, float* dlogits, void* dW1, void* dW3, void* dW2,
                         void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_forward_train and moe_backward with moe_route_scored in the place of
+ * step 1: bias and config as there, the same in both calls.  dlogits is
+ * moe_route_scored_backward's.
+ */
+moe_status moe_forward_scored_train(const void* x, const float* router_logits, const float* bias,
+                                    const moe_route_config* config,
+                                    const void* W1, const void* W3, const void* W2,
+                                    int T, int H, int F, int E, int k, void* out,
+                                    void* ws, size_t ws_bytes, void* stream);
+moe_status moe_backward_scored(const void* dout, const float* router_logits, const float* bias,
+                               const moe_route_config* config,
+                               const void* W1, const void* W3, const void* W2,
+                               int T, int H, int F, int E, int k,
+                               void* dx, float* dlogits, void* dW1, void* dW3, void* dW2,
+                               void* ws, size_t ws_bytes, void* stream);
 
 /*
  * moe_forward with timing marks: records events[0] on `stream` before the

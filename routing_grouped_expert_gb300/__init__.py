@@ -32,6 +32,12 @@ from .binding import (  # noqa: F401
     moe_plan_replicas,
     moe_plan_workspace_size,
     moe_route_topk,
+    RouteConfig,
+    moe_route_scored,
+    moe_route_scored_backward,
+    moe_forward_scored,
+    moe_forward_scored_train,
+    moe_backward_scored,
     moe_status_string,
     moe_workspace_size,
     Workspace,

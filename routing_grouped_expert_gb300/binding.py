@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from dataclasses import dataclass
 
 import torch
 
@@ -23,6 +24,14 @@ _VP, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 SIGNATURES = {
     "moe_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_route_topk": (_I, [_VP, _I, _I, _I, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_route_scored": (_I, [_VP, _VP, _VP, _I, _I, _I, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_route_scored_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP, _VP, _SZ, _VP]),
+    "moe_forward_scored": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP,
+                                _SZ, _VP]),
+    "moe_forward_scored_train": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP,
+                                      _VP, _SZ, _VP]),
+    "moe_backward_scored": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP,
+                                 _VP, _VP, _VP, _VP, _SZ, _VP]),
     "moe_permute": (_I, [_VP, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "moe_permute_noalloc": (_I, [_VP, _I, _I, _I, _VP, _VP, _VP, _VP, _VP]),
     "moe_grouped_ffn": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _SZ,
@@ -184,6 +193,79 @@ def moe_route_topk(logits: torch.Tensor, k: int, topk_idx=None, topk_w=None,
     return topk_idx, topk_w
 
 
+class _RouteConfigStruct(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+@dataclass(frozen=True)
+class RouteConfig:
+    """How moe_route_scored routes (see moe_route_config in include/moe.h)."""
+    score: str = "softmax"      # or "sigmoid"
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in ROUTE_SCORES:
+            raise ValueError(f"score: expected one of {sorted(ROUTE_SCORES)}, got {self.score!r}")
+        c = _RouteConfigStruct(ROUTE_SCORES[self.score], self.n_group, self.topk_group,
+                               self.group_top, int(self.renormalize), self.scale)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ptr", ctypes.c_void_p(ctypes.addressof(c)))
+
+
+def _need_bias(bias, E: int):
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias")
+
+
+def moe_route_scored(logits: torch.Tensor, k: int, config: RouteConfig, bias=None, topk_idx=None,
+                     topk_w=None, ws: Workspace | None = None):
+    """(topk_idx [T, k], topk_w [T, k]) by scores, balance bias and groups."""
+    T, E = logits.shape
+    _need(logits, torch.float32, (T, E), "logits")
+    _need_bias(bias, E)
+    topk_idx = torch.empty(T, k, dtype=torch.int32, device=logits.device) \
+        if topk_idx is None else topk_idx
+    topk_w = torch.empty(T, k, dtype=torch.float32, device=logits.device) \
+        if topk_w is None else topk_w
+    _need(topk_idx, torch.int32, (T, k), "topk_idx")
+    _need(topk_w, torch.float32, (T, k), "topk_w")
+    ws = _ws(ws, 256)
+    _check(load_library().moe_route_scored(_p(logits), _p(bias), config._ptr, T, E, k,
+                                           _p(topk_idx), _p(topk_w), ws.ptr, ws.nbytes,
+                                           _stream()), "moe_route_scored")
+    return topk_idx, topk_w
+
+
+def moe_route_scored_backward(dtopk_w: torch.Tensor, topk_idx: torch.Tensor, logits: torch.Tensor,
+                              config: RouteConfig, bias=None, dlogits=None,
+                              ws: Workspace | None = None):
+    """dlogits [T, E] of moe_route_scored's weights, given their gradient."""
+    T, E = logits.shape
+    k = dtopk_w.shape[1]
+    _need(logits, torch.float32, (T, E), "logits")
+    _need(dtopk_w, torch.float32, (T, k), "dtopk_w")
+    _need(topk_idx, torch.int32, (T, k), "topk_idx")
+    _need_bias(bias, E)
+    dlogits = torch.empty(T, E, dtype=torch.float32, device=logits.device) \
+        if dlogits is None else dlogits
+    _need(dlogits, torch.float32, (T, E), "dlogits")
+    ws = _ws(ws, 256)
+    _check(load_library().moe_route_scored_backward(_p(dtopk_w), _p(topk_idx), _p(logits),
+                                                    _p(bias), config._ptr, T, E, k, _p(dlogits),
+                                                    ws.ptr, ws.nbytes, _stream()),
+           "moe_route_scored_backward")
+    return dlogits
+
+
 def moe_permute(topk_idx: torch.Tensor, E: int, ws: Workspace | None = None, out=None):
     T, k = topk_idx.shape
     _need(topk_idx, torch.int32, (T, k), "topk_idx")
@@ -249,6 +331,31 @@ def moe_forward(x, router_logits, W1, W3, W2, k: int, out=None, ws: Workspace | 
     _check(load_library().moe_forward(_p(x), _p(router_logits), _p(W1), _p(W3), _p(W2), T, H, F,
                                       E, k, _p(out), ws.ptr, ws.nbytes, _stream()),
            "moe_forward")
+    return out
+
+
+def _need_layer(x, router_logits, W1, W3, W2):
+    T, H = x.shape
+    E, _, F = W1.shape
+    _need(x, torch.bfloat16, (T, H), "x")
+    _need(router_logits, torch.float32, (T, E), "router_logits")
+    _need(W1, torch.bfloat16, (E, H, F), "W1")
+    _need(W3, torch.bfloat16, (E, H, F), "W3")
+    _need(W2, torch.bfloat16, (E, F, H), "W2")
+    return T, H, F, E
+
+
+def moe_forward_scored(x, router_logits, W1, W3, W2, k: int, config: RouteConfig, bias=None,
+                       out=None, ws: Workspace | None = None):
+    """moe_forward routed by moe_route_scored."""
+    T, H, F, E = _need_layer(x, router_logits, W1, W3, W2)
+    _need_bias(bias, E)
+    out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device) if out is None else out
+    _need(out, torch.bfloat16, (T, H), "out")
+    ws = _ws(ws, moe_workspace_size(T, H, F, E, k))
+    _check(load_library().moe_forward_scored(_p(x), _p(router_logits), _p(bias), config._ptr,
+                                             _p(W1), _p(W3), _p(W2), T, H, F, E, k, _p(out),
+                                             ws.ptr, ws.nbytes, _stream()), "moe_forward_scored")
     return out
 
 
@@ -478,6 +585,36 @@ def moe_backward(dout, router_logits, W1, W3, W2, k: int, ws: Workspace):
     _check(load_library().moe_backward(_p(dout), _p(router_logits), _p(W1), _p(W3), _p(W2), T, H,
                                        F, E, k, _p(dx), _p(dl), _p(dW1), _p(dW3), _p(dW2),
                                        ws.ptr, ws.nbytes, _stream()), "moe_backward")
+    return dx, dl, dW1, dW3, dW2
+
+
+def moe_forward_scored_train(x, router_logits, W1, W3, W2, k: int, config: RouteConfig,
+                             ws: Workspace, bias=None, out=None):
+    """moe_forward_scored that keeps in `ws` what moe_backward_scored needs."""
+    T, H, F, E = _need_layer(x, router_logits, W1, W3, W2)
+    _need_bias(bias, E)
+    out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device) if out is None else out
+    _need(out, torch.bfloat16, (T, H), "out")
+    ws.ensure(moe_workspace_size_train(T, H, F, E, k))
+    _check(load_library().moe_forward_scored_train(
+        _p(x), _p(router_logits), _p(bias), config._ptr, _p(W1), _p(W3), _p(W2), T, H, F, E, k,
+        _p(out), ws.ptr, ws.nbytes, _stream()), "moe_forward_scored_train")
+    return out
+
+
+def moe_backward_scored(dout, router_logits, W1, W3, W2, k: int, config: RouteConfig,
+                        ws: Workspace, bias=None):
+    """Gradients after moe_forward_scored_train on the same ws: (dx, dlogits,
+    dW1, dW3, dW2)."""
+    T, H, F, E = _need_layer(dout, router_logits, W1, W3, W2)
+    _need_bias(bias, E)
+    dx = torch.empty_like(dout)
+    dl = torch.empty_like(router_logits)
+    dW1, dW3, dW2 = torch.empty_like(W1), torch.empty_like(W3), torch.empty_like(W2)
+    _check(load_library().moe_backward_scored(
+        _p(dout), _p(router_logits), _p(bias), config._ptr, _p(W1), _p(W3), _p(W2), T, H, F, E, k,
+        _p(dx), _p(dl), _p(dW1), _p(dW3), _p(dW2), ws.ptr, ws.nbytes, _stream()),
+           "moe_backward_scored")
     return dx, dl, dW1, dW3, dW2
 
 

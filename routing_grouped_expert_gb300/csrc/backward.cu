@@ -58,19 +58,22 @@ scale_gather_kernel(const __nv_bfloat16* __restrict__ dout, const int32_t* __res
   }
 }
 
-// One CTA per token: dw over the k slots, then the token's dlogits row.
+// One CTA per token: dw over the k slots, then (kDlogits) the token's dlogits
+// row, else dw itself.
+template <bool kDlogits>
 __global__ void __launch_bounds__(kDwThreads)
 dw_dlogits_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ y,
                   const int32_t* __restrict__ dest_of, const int32_t* __restrict__ topk_idx,
                   const float* __restrict__ logits, int H, int E, int k,
-                  float* __restrict__ dlogits) {
+                  float* __restrict__ dlogits, float* __restrict__ dw_out) {
   __shared__ int s_row[MOE_MAX_TOPK];
   __shared__ float s_part[kDwThreads / 32][MOE_MAX_TOPK];
   __shared__ float s_dw[MOE_MAX_TOPK];
   const int t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x < k) s_row[threadIdx.x] = dest_of[(size_t)t * k + threadIdx.x];
-  for (int e = threadIdx.x; e < E; e += kDwThreads) dlogits[(size_t)t * E + e] = 0.f;
+  if constexpr (kDlogits)
+    for (int e = threadIdx.x; e < E; e += kDwThreads) dlogits[(size_t)t * E + e] = 0.f;
   __syncthreads();
   float acc[MOE_MAX_TOPK];
 #pragma unroll
@@ -113,7 +116,9 @@ dw_dlogits_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* _
 #pragma unroll
     for (int w = 0; w < kDwThreads / 32; ++w) v += s_part[w][threadIdx.x];
     s_dw[threadIdx.x] = v;
+    if constexpr (!kDlogits) dw_out[(size_t)t * k + threadIdx.x] = v;
   }
+  if constexpr (!kDlogits) return;
   __syncthreads();
   if (warp == 0) {
     // softmax of the selected logits (slot 0 holds the largest) and its Jacobian
@@ -151,8 +156,16 @@ cudaError_t launch_dw_dlogits(const __nv_bfloat16* dout, const __nv_bfloat16* y,
                               const float* logits, int T, int H, int E, int k, float* dlogits,
                               cudaStream_t s) {
   if (T == 0) return cudaSuccess;
-  dw_dlogits_kernel<<<T, kDwThreads, 0, s>>>(dout, y, dest_of, topk_idx, logits, H, E, k,
-                                             dlogits);
+  dw_dlogits_kernel<true><<<T, kDwThreads, 0, s>>>(dout, y, dest_of, topk_idx, logits, H, E, k,
+                                                   dlogits, nullptr);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dw(const __nv_bfloat16* dout, const __nv_bfloat16* y, const int32_t* dest_of,
+                      int T, int H, int k, float* dw, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  dw_dlogits_kernel<false><<<T, kDwThreads, 0, s>>>(dout, y, dest_of, nullptr, nullptr, H, 0, k,
+                                                    nullptr, dw);
   return cudaGetLastError();
 }
 

@@ -71,6 +71,16 @@ moe_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   return MOE_OK;
 }
 
+// The scored routing's own limits, on top of ok_route_sizes.
+bool ok_route_config(const moe_route_config* c, int E, int k) {
+  if (c == nullptr || (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID)) return false;
+  if (c->n_group < 1 || c->n_group > MOE_MAX_GROUPS || E % c->n_group != 0) return false;
+  const int gsz = E / c->n_group;
+  return c->topk_group >= 1 && c->topk_group <= c->n_group &&
+         (c->group_top == 1 || (c->group_top == 2 && gsz >= 2)) &&
+         (long long)c->topk_group * gsz >= k && (c->scale - c->scale) == 0.f;   // finite
+}
+
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 #define MOE_TRY(expr)                                    \
@@ -93,6 +103,12 @@ struct SharedExpert {
   __nv_bfloat16* y;   // [T, H]
 };
 
+// How a layer routes when not by moe_route_topk.
+struct ScoredRoute {
+  const float* bias;
+  RouteCfg cfg;
+};
+
 // The launch sequence of the whole layer on device buffers.  With `ev`
 // non-null, ev[0] is recorded first and ev[i] after stage i.  With
 // `clear` false the caller has already zeroed the status word and the chunk
@@ -102,7 +118,7 @@ moe_status forward_device(const void* x, const float* logits, const void* W1, co
                           void* ws, const WsLayout& L, cudaStream_t s,
                           const cudaEvent_t* ev = nullptr, bool clear = true,
                           const SharedExpert* sh = nullptr, const EpiAux* save = nullptr,
-                          bool out_f32 = false) {
+                          bool out_f32 = false, const ScoredRoute* scored = nullptr) {
   const int P = T * k;
   const int C = num_chunks(T, k);
   int* status = ws_ptr<int>(ws, L.status);
@@ -132,7 +148,7 @@ moe_status forward_device(const void* x, const float* logits, const void* W1, co
     MOE_TRY(cudaMemsetAsync(status, 0,
                             L.chunk_base - L.status + (size_t)C * E * sizeof(int32_t), s));
   MOE_TRY(mark(0));
-  if (route_permute_small_ok(T, E, k)) {
+  if (scored == nullptr && route_permute_small_ok(T, E, k)) {
     // small batches: routing, counts, scan, block plan and scatter in one
     // launch (the scan and scatter stages are then empty); its ticket
     // counter is the first int of the zeroed chunk table
@@ -142,7 +158,11 @@ moe_status forward_device(const void* x, const float* logits, const void* W1, co
     MOE_TRY(mark(1));
     MOE_TRY(mark(2));
   } else {
-    MOE_TRY(launch_route(logits, T, E, k, topk_idx, topk_w, chunk, status, s));
+    if (scored != nullptr)
+      MOE_TRY(launch_route_scored(logits, scored->bias, scored->cfg, T, E, k, topk_idx, topk_w,
+                                  chunk, status, s));
+    else
+      MOE_TRY(launch_route(logits, T, E, k, topk_idx, topk_w, chunk, status, s));
     MOE_TRY(mark(1));
     MOE_TRY(launch_scan(chunk, C, E, counts, offsets, block_off, num_blocks, block_expert,
                         ffn_block_rows(P, E, H, F), s, pdl));
@@ -204,6 +224,41 @@ moe_status moe_route_topk(const float* logits, int T, int E, int k, int32_t* top
   int* status = static_cast<int*>(ws);
   MOE_TRY(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
   return cuda_status(launch_route(logits, T, E, k, topk_idx, topk_w, nullptr, status, s));
+}
+
+moe_status moe_route_scored(const float* logits, const float* bias, const moe_route_config* config,
+                            int T, int E, int k, int32_t* topk_idx, float* topk_w, void* ws,
+                            size_t ws_bytes, void* stream) {
+  if (!ok_route_sizes(T, E, k) || !ok_route_config(config, E, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(logits) || !ok_ptr(topk_idx) || !ok_ptr(topk_w) || !aligned16(bias))
+    return MOE_ERR_INVALID_ARG;
+  if (check_ws(ws, ws_bytes, 256) != MOE_OK) return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = static_cast<int*>(ws);
+  MOE_TRY(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
+  return cuda_status(launch_route_scored(logits, bias, make_route_cfg(*config, E), T, E, k,
+                                         topk_idx, topk_w, nullptr, status, s));
+}
+
+moe_status moe_route_scored_backward(const float* dtopk_w, const int32_t* topk_idx,
+                                     const float* logits, const float* bias,
+                                     const moe_route_config* config, int T, int E, int k,
+                                     float* dlogits, void* ws, size_t ws_bytes, void* stream) {
+  if (!ok_route_sizes(T, E, k) || !ok_route_config(config, E, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(dtopk_w) || !ok_ptr(topk_idx) || !ok_ptr(logits) || !ok_ptr(dlogits) ||
+      !aligned16(bias))
+    return MOE_ERR_INVALID_ARG;
+  if (check_ws(ws, ws_bytes, 256) != MOE_OK) return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = static_cast<int*>(ws);
+  MOE_TRY(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
+  return cuda_status(launch_route_scored_backward(dtopk_w, topk_idx, logits, bias,
+                                                  make_route_cfg(*config, E), T, E, k, dlogits,
+                                                  status, s));
 }
 
 moe_status moe_permute(const int32_t* topk_idx, int T, int E, int k, int32_t* counts,
@@ -304,6 +359,24 @@ moe_status moe_forward(const void* x, const float* router_logits, const void* W1
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   return forward_device(x, router_logits, W1, W3, W2, T, H, F, E, k, out, ws, L,
                         static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_forward_scored(const void* x, const float* router_logits, const float* bias,
+                              const moe_route_config* config, const void* W1, const void* W3,
+                              const void* W2, int T, int H, int F, int E, int k, void* out,
+                              void* ws, size_t ws_bytes, void* stream) {
+  if (!ok_sizes(T, H, F, E, k) || !ok_route_config(config, E, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(router_logits) || !aligned16(bias) || !ok_ptr(W1) || !ok_ptr(W3) ||
+      !ok_ptr(W2) || !ok_ptr(out))
+    return MOE_ERR_INVALID_ARG;
+  const WsLayout L = ws_layout(T, H, F, E, k);
+  if (check_ws(ws, ws_bytes, L.total) != MOE_OK) return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  const ScoredRoute scored{bias, make_route_cfg(*config, E)};
+  return forward_device(x, router_logits, W1, W3, W2, T, H, F, E, k, out, ws, L,
+                        static_cast<cudaStream_t>(stream), nullptr, true, nullptr, nullptr, false,
+                        &scored);
 }
 
 // A captured moe_forward: the graph and its executable instance.
@@ -590,10 +663,31 @@ moe_status moe_forward_train(const void* x, const float* router_logits, const vo
                         static_cast<cudaStream_t>(stream), nullptr, true, nullptr, &save);
 }
 
-moe_status moe_backward(const void* dout, const float* router_logits, const void* W1,
-                        const void* W3, const void* W2, int T, int H, int F, int E, int k,
-                        void* dx, float* dlogits, void* dW1, void* dW3, void* dW2, void* ws,
-                        size_t ws_bytes, void* stream) {
+moe_status moe_forward_scored_train(const void* x, const float* router_logits, const float* bias,
+                                    const moe_route_config* config, const void* W1, const void* W3,
+                                    const void* W2, int T, int H, int F, int E, int k, void* out,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  if (!ok_sizes(T, H, F, E, k) || !ok_route_config(config, E, k)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(router_logits) || !aligned16(bias) || !ok_ptr(W1) || !ok_ptr(W3) ||
+      !ok_ptr(W2) || !ok_ptr(out))
+    return MOE_ERR_INVALID_ARG;
+  const TrainLayout R = train_layout(T, H, F, E, k);
+  if (check_ws(ws, ws_bytes, R.total) != MOE_OK) return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  const EpiAux save{ws_ptr<__nv_bfloat16>(ws, R.g), ws_ptr<__nv_bfloat16>(ws, R.u), nullptr,
+                    nullptr, F};
+  const ScoredRoute scored{bias, make_route_cfg(*config, E)};
+  return forward_device(x, router_logits, W1, W3, W2, T, H, F, E, k, out, ws, R.base,
+                        static_cast<cudaStream_t>(stream), nullptr, true, nullptr, &save, false,
+                        &scored);
+}
+
+namespace {
+moe_status backward_device(const void* dout, const float* router_logits, const void* W1,
+                           const void* W3, const void* W2, int T, int H, int F, int E, int k,
+                           void* dx, float* dlogits, void* dW1, void* dW3, void* dW2, void* ws,
+                           size_t ws_bytes, void* stream, const ScoredRoute* scored) {
   if (!ok_sizes(T, H, F, E, k)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!ok_ptr(dout) || !ok_ptr(router_logits) || !ok_ptr(W1) || !ok_ptr(W3) || !ok_ptr(W2) ||
@@ -622,7 +716,14 @@ moe_status moe_backward(const void* dout, const float* router_logits, const void
   // the status word and the split counters of DGrad dx (adjacent) start at zero
   MOE_TRY(cudaMemsetAsync(status, 0, L.sk_cnt - L.status + kSkCntInts * sizeof(int), s));
   MOE_TRY(launch_scale_gather(dout_b, dest_of, topk_w, T, H, k, dY, s));
-  MOE_TRY(launch_dw_dlogits(dout_b, y, dest_of, topk_idx, router_logits, T, H, E, k, dlogits, s));
+  if (scored != nullptr) {
+    float* dw = ws_ptr<float>(ws, R.dw);
+    MOE_TRY(launch_dw(dout_b, y, dest_of, T, H, k, dw, s));
+    MOE_TRY(launch_route_scored_backward(dw, topk_idx, router_logits, scored->bias, scored->cfg, T,
+                                         E, k, dlogits, status, s));
+  } else {
+    MOE_TRY(launch_dw_dlogits(dout_b, y, dest_of, topk_idx, router_logits, T, H, E, k, dlogits, s));
+  }
   MOE_TRY(launch_dgrad(dY, ws_ptr<__nv_bfloat16>(ws, R.g), ws_ptr<__nv_bfloat16>(ws, R.u),
                        static_cast<const __nv_bfloat16*>(W1),
                        static_cast<const __nv_bfloat16*>(W3),
@@ -635,6 +736,27 @@ moe_status moe_backward(const void* dout, const float* router_logits, const void
                        static_cast<__nv_bfloat16*>(dW1), static_cast<__nv_bfloat16*>(dW3),
                        static_cast<__nv_bfloat16*>(dW2), status, s));
   return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_backward(const void* dout, const float* router_logits, const void* W1,
+                        const void* W3, const void* W2, int T, int H, int F, int E, int k,
+                        void* dx, float* dlogits, void* dW1, void* dW3, void* dW2, void* ws,
+                        size_t ws_bytes, void* stream) {
+  return backward_device(dout, router_logits, W1, W3, W2, T, H, F, E, k, dx, dlogits, dW1, dW3,
+                         dW2, ws, ws_bytes, stream, nullptr);
+}
+
+moe_status moe_backward_scored(const void* dout, const float* router_logits, const float* bias,
+                               const moe_route_config* config, const void* W1, const void* W3,
+                               const void* W2, int T, int H, int F, int E, int k, void* dx,
+                               float* dlogits, void* dW1, void* dW3, void* dW2, void* ws,
+                               size_t ws_bytes, void* stream) {
+  if (!ok_sizes(T, H, F, E, k) || !ok_route_config(config, E, k) || !aligned16(bias))
+    return MOE_ERR_INVALID_ARG;
+  const ScoredRoute scored{bias, make_route_cfg(*config, E)};
+  return backward_device(dout, router_logits, W1, W3, W2, T, H, F, E, k, dx, dlogits, dW1, dW3,
+                         dW2, ws, ws_bytes, stream, &scored);
 }
 
 size_t moe_plan_workspace_size(int E, int G) {

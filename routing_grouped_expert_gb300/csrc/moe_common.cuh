@@ -116,6 +116,7 @@ struct TrainLayout {
   size_t dY;            // bf16[P*H]
   size_t dg, du;        // bf16[P*F]
   size_t dx_perm;       // bf16[P*H]
+  size_t dw;            // f32[P]      gradient of the routing weights (scored routing)
   size_t total;
 };
 
@@ -178,6 +179,7 @@ inline TrainLayout train_layout(int T, int H, int F, int E, int k) {
   R.dg = take(P * F * 2);
   R.du = take(P * F * 2);
   R.dx_perm = take(P * H * 2);
+  R.dw = take(P * 4);
   R.total = o;
   return R;
 }
@@ -236,6 +238,24 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
 // launches with programmatic stream serialisation (see above).
 cudaError_t launch_route(const float* logits, int T, int E, int k, int32_t* topk_idx,
                          float* topk_w, int32_t* chunk_hist, int* status, cudaStream_t s);
+// A scored routing's configuration as the kernels take it.
+struct RouteCfg {
+  bool softmax, renorm;
+  float scale;
+  int n_group, topk_group, group_top;
+  int lanes_per_group;     // lanes of a warp that scan one group (a power of two)
+  uint32_t group_magic;    // expert e is in group e * group_magic >> 20
+};
+RouteCfg make_route_cfg(const moe_route_config& a, int E);
+// bias: [E] or null.  chunk_hist as for launch_route.
+cudaError_t launch_route_scored(const float* logits, const float* bias, const RouteCfg& c, int T,
+                                int E, int k, int32_t* topk_idx, float* topk_w,
+                                int32_t* chunk_hist, int* status, cudaStream_t s);
+// dlogits [T, E] of the weights' gradient dw [T, k].
+cudaError_t launch_route_scored_backward(const float* dw, const int32_t* topk_idx,
+                                         const float* logits, const float* bias, const RouteCfg& c,
+                                         int T, int E, int k, float* dlogits, int* status,
+                                         cudaStream_t s);
 cudaError_t launch_count(const int32_t* topk_idx, int T, int E, int k, int32_t* chunk_hist,
                          int* status, cudaStream_t s);
 cudaError_t launch_scan(int32_t* chunk_hist, int C, int E, int32_t* counts, int32_t* offsets,
@@ -374,6 +394,9 @@ cudaError_t launch_dw_dlogits(const __nv_bfloat16* dout, const __nv_bfloat16* y,
                               const int32_t* dest_of, const int32_t* topk_idx,
                               const float* logits, int T, int H, int E, int k, float* dlogits,
                               cudaStream_t s);
+// dw[t, j] = <dout[t], y[dest_of[t * k + j]]>
+cudaError_t launch_dw(const __nv_bfloat16* dout, const __nv_bfloat16* y, const int32_t* dest_of,
+                      int T, int H, int k, float* dw, cudaStream_t s);
 cudaError_t launch_wgrad(const __nv_bfloat16* x_perm, const __nv_bfloat16* h,
                          const __nv_bfloat16* dY, const __nv_bfloat16* dg,
                          const __nv_bfloat16* du, const int32_t* offsets, int P, int H, int F,

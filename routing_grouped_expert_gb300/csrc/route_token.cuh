@@ -32,24 +32,15 @@ __device__ __forceinline__ float route_key_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
+// The k largest of a warp's candidates: lane i's keys are those of experts
+// lane + 32 i (0: no candidate); lane j < k returns slot j's key and expert.
+// A larger key wins, equal keys go to the lower expert.
 template <int kPerLane>
-__device__ __forceinline__ bool route_token_vals(const float (&raw)[kPerLane], int E, int k,
-                                                 int lane, int* idx, float* w) {
-  bool nonfinite = false;
-  // this lane's candidates: keys, and their slots i (expert lane + 32 i)
-  uint32_t key[kPerLane];
-  int slot[kPerLane];
+__device__ __forceinline__ void route_select(uint32_t (&key)[kPerLane], int k, int lane,
+                                             uint32_t* sel_key, int* sel_idx) {
+  int slot[kPerLane];   // expert lane + 32 slot
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int e = lane + 32 * i;
-    float x = (e < E) ? raw[i] : -INFINITY;
-    if (e < E && !isfinite(x)) {
-      nonfinite = true;
-      if (isnan(x)) x = -INFINITY;   // keep the order total; the status reports it
-    }
-    key[i] = e < E ? route_key(x) : 0u;
-    slot[i] = i;
-  }
+  for (int i = 0; i < kPerLane; ++i) slot[i] = i;
   // Sort them once, larger key first (odd-even transposition, swapping only on
   // a strictly smaller key, so equal keys keep ascending expert order); then
   // round j's pick is the best head over the warp, and only the winning lane
@@ -88,6 +79,28 @@ __device__ __forceinline__ bool route_token_vals(const float (&raw)[kPerLane], i
       key[kPerLane - 1] = 0u;
     }
   }
+  *sel_key = my_key;
+  *sel_idx = my_idx;
+}
+
+template <int kPerLane>
+__device__ __forceinline__ bool route_token_vals(const float (&raw)[kPerLane], int E, int k,
+                                                 int lane, int* idx, float* w) {
+  bool nonfinite = false;
+  uint32_t key[kPerLane];   // this lane's candidates
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int e = lane + 32 * i;
+    float x = (e < E) ? raw[i] : -INFINITY;
+    if (e < E && !isfinite(x)) {
+      nonfinite = true;
+      if (isnan(x)) x = -INFINITY;   // keep the order total; the status reports it
+    }
+    key[i] = e < E ? route_key(x) : 0u;
+  }
+  uint32_t my_key;
+  int my_idx;
+  route_select<kPerLane>(key, k, lane, &my_key, &my_idx);
   const float my_sel = route_key_value(my_key);
   // softmax over the k selected logits (slot 0 holds the largest)
   const float m = __shfl_sync(0xffffffffu, my_sel, 0);
