@@ -387,6 +387,48 @@ moe_status moe_forward_gated(const void* x, const void* Wg,
                              void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Low-rank adapters of many requests at once beside a projection that all of
+ * them share (either side of the layer: an attention or shared-expert
+ * projection served for many fine-tuned variants).  With a = adapter_idx[t]:
+ *
+ *   y[t] = x[t] W + scale[a] * (x[t] A[a]^T) B[a]      (a = -1: y[t] = x[t] W)
+ *
+ *   x [T, H], W [H, N], y [T, N] bf16;
+ *   A [n, R, H] bf16, the adapters' down projections, one row per rank;
+ *   B [n, R, N] bf16, their up projections;
+ *   scale [n] fp32; adapter_idx [T] int32, -1 or 0 .. n - 1 in any order.
+ * A smaller rank is padded with zero rows.  bf16 operands, fp32 accumulation;
+ * the scaled low-rank activation is rounded to bf16 once (it is a matrix
+ * operand), y is rounded once.  Any other index in adapter_idx counts as -1
+ * and sets MOE_ERR_INVALID_ARG in the device status.  T == 1 is the form for a
+ * single token.
+ *
+ * The backward, given dy [T, N] bf16 = dL/dy and W frozen:
+ *   dx [T, H] bf16 = dy W^T + dz A,   dz[t] = scale[a] * (dy[t] B[a]^T)
+ *   dA [n, R, H] bf16: dA[a] = sum over its tokens of dz[t]^T x[t]
+ *   dB [n, R, N] bf16: dB[a] = sum of z[t]^T dy[t], z[t] = scale[a] * (x[t] A[a]^T)
+ * with exact zeros for adapters without a token.  Sums run in a fixed order.
+ *
+ * ws: moe_adapter_workspace_size bytes (.._backward for the backward, which
+ * covers both).  Limits: H and N positive multiples of 128, T < 2^30,
+ * 1 <= n <= MOE_MAX_ADAPTERS, R a multiple of 8 up to MOE_MAX_RANK.
+ */
+#define MOE_MAX_ADAPTERS 1024
+#define MOE_MAX_RANK 128
+size_t moe_adapter_workspace_size(int T, int H, int N, int n, int R);
+size_t moe_adapter_workspace_size_backward(int T, int H, int N, int n, int R);
+moe_status moe_adapter_project(const void* x, const void* W, const void* A, const void* B,
+                               const float* scale, const int32_t* adapter_idx,
+                               int T, int H, int N, int n, int R, void* y,
+                               void* ws, size_t ws_bytes, void* stream);
+moe_status moe_adapter_project_backward(const void* dy, const void* x, const void* W,
+                                        const void* A, const void* B, const float* scale,
+                                        const int32_t* adapter_idx,
+                                        int T, int H, int N, int n, int R,
+                                        void* dx, void* dA, void* dB,
+                                        void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Training: the layer's backward ("MegaFlux" §2.1 and §3.2: the backward
  * streams token blocks through DGrad and WGrad grouped GEMMs; the final
  * top-k sum's gradient gives each routing weight's gradient).

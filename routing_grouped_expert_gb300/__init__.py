@@ -25,6 +25,10 @@ from .binding import (  # noqa: F401
     moe_workspace_size_train,
     moe_forward_gated,
     moe_router_logits,
+    moe_adapter_workspace_size,
+    moe_adapter_workspace_size_backward,
+    moe_adapter_project,
+    moe_adapter_project_backward,
     moe_workspace_size_gated,
     moe_get_device_status,
     moe_grouped_ffn,

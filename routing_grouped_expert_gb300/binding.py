@@ -63,6 +63,12 @@ SIGNATURES = {
     "moe_cast_bf16": (_I, [_VP, _VP, _SZ, _VP]),
     "moe_forward_routing": (_I, [_VP, _SZ, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP,
                                  _VP]),
+    "moe_adapter_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_adapter_workspace_size_backward": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_adapter_project": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _SZ,
+                                 _VP]),
+    "moe_adapter_project_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I,
+                                          _VP, _VP, _VP, _VP, _SZ, _VP]),
     "moe_plan_workspace_size": (_SZ, [_I, _I]),
     "moe_plan_replicas": (_I, [_VP, _I, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
 }
@@ -545,6 +551,57 @@ def moe_forward_gated(x, Wg, W1, W3, W2, k: int, shared=None, out=None,
                                             F, Fs, E, k, _p(out), ws.ptr, ws.nbytes, _stream()),
            "moe_forward_gated")
     return out
+
+
+# --------------------------------------- adapters beside a shared projection
+def moe_adapter_workspace_size(T: int, H: int, N: int, n: int, R: int) -> int:
+    return int(load_library().moe_adapter_workspace_size(T, H, N, n, R))
+
+
+def moe_adapter_workspace_size_backward(T: int, H: int, N: int, n: int, R: int) -> int:
+    return int(load_library().moe_adapter_workspace_size_backward(T, H, N, n, R))
+
+
+def _need_adapters(x, W, A, B, scale, adapter_idx):
+    T, H = x.shape
+    N = W.shape[1]
+    n, R, _ = A.shape
+    _need(x, torch.bfloat16, (T, H), "x")
+    _need(W, torch.bfloat16, (H, N), "W")
+    _need(A, torch.bfloat16, (n, R, H), "A")
+    _need(B, torch.bfloat16, (n, R, N), "B")
+    _need(scale, torch.float32, (n,), "scale")
+    _need(adapter_idx, torch.int32, (T,), "adapter_idx")
+    return T, H, N, n, R
+
+
+def moe_adapter_project(x, W, A, B, scale, adapter_idx, y=None, ws: Workspace | None = None):
+    """y [T, N] = x W + scale_a (x A_a^T) B_a, a = adapter_idx[t] (-1: none);
+    A [n, R, H], B [n, R, N]."""
+    T, H, N, n, R = _need_adapters(x, W, A, B, scale, adapter_idx)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device=x.device) if y is None else y
+    _need(y, torch.bfloat16, (T, N), "y")
+    lib = load_library()
+    ws = _ws(ws, lib.moe_adapter_workspace_size(T, H, N, n, R))
+    _check(lib.moe_adapter_project(_p(x), _p(W), _p(A), _p(B), _p(scale), _p(adapter_idx), T, H,
+                                   N, n, R, _p(y), ws.ptr, ws.nbytes, _stream()),
+           "moe_adapter_project")
+    return y
+
+
+def moe_adapter_project_backward(dy, x, W, A, B, scale, adapter_idx,
+                                 ws: Workspace | None = None):
+    """(dx, dA, dB) of moe_adapter_project, given dy [T, N]."""
+    T, H, N, n, R = _need_adapters(x, W, A, B, scale, adapter_idx)
+    _need(dy, torch.bfloat16, (T, N), "dy")
+    dx, dA, dB = torch.empty_like(x), torch.empty_like(A), torch.empty_like(B)
+    lib = load_library()
+    ws = _ws(ws, lib.moe_adapter_workspace_size_backward(T, H, N, n, R))
+    _check(lib.moe_adapter_project_backward(_p(dy), _p(x), _p(W), _p(A), _p(B), _p(scale),
+                                            _p(adapter_idx), T, H, N, n, R, _p(dx), _p(dA),
+                                            _p(dB), ws.ptr, ws.nbytes, _stream()),
+           "moe_adapter_project_backward")
+    return dx, dA, dB
 
 
 # ------------------------------------------------------------- training

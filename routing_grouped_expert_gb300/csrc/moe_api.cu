@@ -759,6 +759,71 @@ moe_status moe_backward_scored(const void* dout, const float* router_logits, con
                          dW2, ws, ws_bytes, stream, &scored);
 }
 
+namespace {
+bool ok_adapter_sizes(int T, int H, int N, int n, int R) {
+  return T >= 0 && T < (1 << 30) && H >= kTileM && N >= kTileM && H % kTileM == 0 &&
+         N % kTileM == 0 && n >= 1 && n <= MOE_MAX_ADAPTERS && R >= 8 && R <= MOE_MAX_RANK &&
+         R % 8 == 0 && (long long)H * N < (1LL << 40);
+}
+}  // namespace
+
+size_t moe_adapter_workspace_size(int T, int H, int N, int n, int R) {
+  if (!ok_adapter_sizes(T, H, N, n, R)) return 0;
+  return adapter_sizes(T, H, N, n, R).total;
+}
+
+size_t moe_adapter_workspace_size_backward(int T, int H, int N, int n, int R) {
+  if (!ok_adapter_sizes(T, H, N, n, R)) return 0;
+  return adapter_sizes(T, H, N, n, R).total_backward;
+}
+
+moe_status moe_adapter_project(const void* x, const void* W, const void* A, const void* B,
+                               const float* scale, const int32_t* adapter_idx, int T, int H,
+                               int N, int n, int R, void* y, void* ws, size_t ws_bytes,
+                               void* stream) {
+  if (!ok_adapter_sizes(T, H, N, n, R)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(W) || !ok_ptr(A) || !ok_ptr(B) || !ok_ptr(scale) ||
+      !ok_ptr(adapter_idx) || !ok_ptr(y))
+    return MOE_ERR_INVALID_ARG;
+  const AdapterSizes z = adapter_sizes(T, H, N, n, R);
+  if (check_ws(ws, ws_bytes, z.total) != MOE_OK) return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOE_TRY(cudaMemsetAsync(ws, 0, 2 * sizeof(int), s));
+  using bf16 = __nv_bfloat16;
+  return cuda_status(launch_adapter_project(
+      z, static_cast<const bf16*>(x), static_cast<const bf16*>(W), static_cast<const bf16*>(A),
+      static_cast<const bf16*>(B), scale, adapter_idx, static_cast<bf16*>(y), ws, s));
+}
+
+moe_status moe_adapter_project_backward(const void* dy, const void* x, const void* W,
+                                        const void* A, const void* B, const float* scale,
+                                        const int32_t* adapter_idx, int T, int H, int N, int n,
+                                        int R, void* dx, void* dA, void* dB, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  if (!ok_adapter_sizes(T, H, N, n, R)) return MOE_ERR_INVALID_ARG;
+  if (!ok_ptr(dA) || !ok_ptr(dB)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!ok_ptr(dy) || !ok_ptr(x) || !ok_ptr(W) || !ok_ptr(A) || !ok_ptr(B) ||
+                !ok_ptr(scale) || !ok_ptr(adapter_idx) || !ok_ptr(dx)))
+    return MOE_ERR_INVALID_ARG;
+  const AdapterSizes z = adapter_sizes(T, H, N, n, R);
+  if (check_ws(ws, ws_bytes, z.total_backward) != MOE_OK) return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MOE_TRY(cudaMemsetAsync(ws, 0, 2 * sizeof(int), s));
+  if (T == 0) {   // no token: zero gradients
+    MOE_TRY(cudaMemsetAsync(dA, 0, (size_t)n * R * H * 2, s));
+    MOE_TRY(cudaMemsetAsync(dB, 0, (size_t)n * R * N * 2, s));
+    return MOE_OK;
+  }
+  using bf16 = __nv_bfloat16;
+  return cuda_status(launch_adapter_backward(
+      z, static_cast<const bf16*>(dy), static_cast<const bf16*>(x), static_cast<const bf16*>(W),
+      static_cast<const bf16*>(A), static_cast<const bf16*>(B), scale, adapter_idx,
+      static_cast<bf16*>(dx), static_cast<bf16*>(dA), static_cast<bf16*>(dB), ws, s));
+}
+
 size_t moe_plan_workspace_size(int E, int G) {
   if (E < 1 || E > MOE_MAX_EXPERTS || G < 1 || G > MOE_PLAN_MAX_GPUS || G > E) return 0;
   return plan_ws_bytes(E, G);

@@ -411,6 +411,29 @@ cudaError_t launch_plan_replicas(const int32_t* counts, int E, int G, int beta, 
                                  int32_t* rows_out, int32_t* load_out, int32_t* info,
                                  cudaStream_t s);
 
+// The adapter projection (adapter.cu): sizes, token blocks and workspace
+// offsets.
+struct AdapterSizes {
+  int T, H, N, n, R;
+  int nb, n_tt;       // tokens per block, blocks
+  int zc;             // columns of Z: R for every adapter a block can meet, rounded up to 128
+  size_t plan;        // int32[n_tt][32]  the adapters of each block, as bits
+  size_t z, dz;       // bf16[T][zc]
+  size_t total, total_backward;
+};
+AdapterSizes adapter_sizes(int T, int H, int N, int n, int R);
+cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x,
+                                   const __nv_bfloat16* W, const __nv_bfloat16* A,
+                                   const __nv_bfloat16* B, const float* scale,
+                                   const int32_t* adapter_idx, __nv_bfloat16* y, void* ws,
+                                   cudaStream_t s);
+cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* dy,
+                                    const __nv_bfloat16* x, const __nv_bfloat16* W,
+                                    const __nv_bfloat16* A, const __nv_bfloat16* B,
+                                    const float* scale, const int32_t* adapter_idx,
+                                    __nv_bfloat16* dx, __nv_bfloat16* dA, __nv_bfloat16* dB,
+                                    void* ws, cudaStream_t s);
+
 // bf16 TMA tensor map with a 128-byte swizzle; dims/strides innermost first.
 bool make_tensor_map_bf16(void* map /* CUtensorMap* */, const void* base, int rank,
                           const unsigned long long* dims, const unsigned long long* strides,

@@ -1,0 +1,171 @@
+"""The adapter projection and its gradients on the GPU against the fp64
+oracle, elementwise.  What is rounded: the result, once to bf16 (8 significant
+bits: at most 2^-8 of it); the low-rank activation z (or dz), once to bf16
+(2^-8 of the sum of |z| |B| that it enters); and fp32 sums on the tensor core,
+taken as 2^-17 of the sum of the absolute products (2^7 roundings of 2^-24)."""
+import pytest
+import torch
+
+import routing_grouped_expert_gb300 as moe
+from oracle import adapter as P
+
+pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -8
+ACC = 2.0 ** -17
+
+CASES = [  # T, H, N, n, R, order
+    (1, 128, 128, 1, 8, "one"),
+    (1, 512, 1024, 4, 8, "shuffled"),
+    (1, 2048, 128, 3, 128, "one"),
+    (7, 256, 384, 5, 24, "shuffled"),
+    (31, 2048, 256, 40, 16, "distinct"),
+    (32, 384, 128, 32, 40, "distinct"),
+    (33, 128, 256, 2, 72, "shuffled"),
+    (64, 1024, 256, 9, 8, "segments"),
+    (65, 256, 128, 300, 16, "distinct"),
+    (128, 2048, 512, 7, 128, "shuffled"),
+    (129, 384, 256, 3, 64, "segments"),
+    (200, 512, 256, 4, 16, "none"),
+    (256, 256, 256, 1, 32, "one"),
+    (257, 256, 128, 64, 8, "distinct"),
+    (300, 128, 384, 1024, 8, "shuffled"),
+    (777, 640, 256, 6, 48, "shuffled"),
+    (1000, 256, 512, 5, 16, "segments"),
+    (1300, 7168, 128, 4, 16, "segments"),
+]
+
+
+def make(case, seed=0):
+    T, H, N, n, R, order = case
+    g = torch.Generator().manual_seed(seed + T * 101 + H + n)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    bf = torch.bfloat16
+    x, dy = r(T, H).to(bf), r(T, N).to(bf)
+    W = (r(H, N) / H ** 0.5).to(bf)
+    A, B = (r(n, R, H) / H ** 0.5).to(bf), (r(n, R, N) / R ** 0.5).to(bf)
+    scale = r(n)
+    if order == "one":
+        idx = torch.full((T,), n - 1)
+    elif order == "none":
+        idx = torch.full((T,), -1)
+    elif order == "distinct":
+        idx = (torch.arange(T) * 7 + 3) % n
+    elif order == "shuffled":
+        idx = torch.randint(-1, n, (T,), generator=g)
+    else:
+        cuts = torch.randint(0, T, (6,), generator=g)
+        idx = torch.randint(-1, n, (7,), generator=g)[(cuts[None] <= torch.arange(T)[:, None])
+                                                      .sum(1)]
+    return dict(x=x, W=W, A=A, B=B, scale=scale, adapter_idx=idx.to(torch.int32)), dy
+
+
+def dev(d):
+    return {k: v.cuda() for k, v in d.items()}
+
+
+def assert_close(got, ref, mag, what):
+    g = got.detach().cpu().double()
+    tol = EPS * ref.abs() + EPS * mag["low"] + ACC * mag["sum"] + 1e-30
+    bad = ~((g - ref).abs() <= tol)
+    assert not bad.any(), (what, int(bad.sum()), [tuple(i) for i in bad.nonzero()[:4].tolist()],
+                           float(((g - ref).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_project(case):
+    d, _ = make(case)
+    ws = moe.Workspace()
+    y = moe.moe_adapter_project(**dev(d), ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    ref, mag = P.project(*d.values(), magnitudes=True)
+    assert_close(y, ref, mag, "y")
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_backward(case):
+    d, dy = make(case)
+    ws = moe.Workspace()
+    got = moe.moe_adapter_project_backward(dy.cuda(), **dev(d), ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    ref, mag = P.backward(dy, *d.values(), magnitudes=True)
+    for key, g in zip(("dx", "dA", "dB"), got):
+        assert_close(g, ref[key], mag[key], key)
+    for a in range(case[3]):
+        if not (d["adapter_idx"] == a).any():
+            assert (got[1][a] == 0).all() and (got[2][a] == 0).all()
+            break
+
+
+def test_repeated_calls_give_the_same_bits_on_any_workspace():
+    ws = moe.Workspace()
+    first = {}
+    for rep in range(3):
+        for case in (CASES[9], CASES[16], CASES[4], CASES[15]):
+            d, dy = make(case)
+            v = dev(d)
+            ws.ensure(256)
+            ws.buf.fill_(255)                       # NaN patterns in every leftover
+            y = moe.moe_adapter_project(**v, ws=ws)
+            g = moe.moe_adapter_project_backward(dy.cuda(), **v, ws=ws)
+            now = [t.cpu() for t in (y, *g)]
+            for a, b in zip(now, first.setdefault(case, now)):
+                assert torch.equal(a, b)
+
+
+def test_bad_index_counts_as_none_and_is_reported():
+    d, dy = make((100, 256, 128, 4, 16, "shuffled"))
+    d["adapter_idx"][17], d["adapter_idx"][60] = 4, -5
+    ws = moe.Workspace()
+    y = moe.moe_adapter_project(**dev(d), ws=ws)
+    assert moe.moe_get_device_status(ws) == 1
+    g = moe.moe_adapter_project_backward(dy.cuda(), **dev(d), ws=ws)
+    assert moe.moe_get_device_status(ws) == 1
+    d["adapter_idx"][17] = d["adapter_idx"][60] = -1
+    assert torch.equal(y, moe.moe_adapter_project(**dev(d), ws=ws))
+    assert moe.moe_get_device_status(ws) == 0
+    for a, b in zip(g, moe.moe_adapter_project_backward(dy.cuda(), **dev(d))):
+        assert torch.equal(a, b)
+
+
+def test_tokens_do_not_depend_on_their_neighbours():
+    """A token of a batch of other requests and the same token alone in its
+    block: the same sums, up to the order in which K is split."""
+    d, _ = make((256, 512, 256, 5, 16, "shuffled"))
+    y = moe.moe_adapter_project(**dev(d))
+    one = {k: (v[37:38] if k in ("x", "adapter_idx") else v) for k, v in d.items()}
+    alone = moe.moe_adapter_project(**dev(one))
+    ref, mag = P.project(*one.values(), magnitudes=True)
+    assert_close(alone, ref, mag, "alone")
+    assert_close(y[37:38], ref, mag, "in a batch")
+
+
+def test_empty_batch_and_another_stream():
+    d, dy = make((50, 256, 128, 3, 16, "shuffled"))
+    v = dev(d)
+    e = {**v, "x": v["x"][:0], "adapter_idx": v["adapter_idx"][:0]}
+    assert moe.moe_adapter_project(**e).shape == (0, 128)
+    dx, dA, dB = moe.moe_adapter_project_backward(dy[:0].cuda(), **e)
+    assert dx.shape == (0, 256) and (dA == 0).all() and (dB == 0).all()
+    want = moe.moe_adapter_project(**v)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = moe.moe_adapter_project(**v, ws=moe.Workspace())
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_binding_checks_types_and_shapes():
+    good = dev(make((4, 128, 256, 2, 8, "one"))[0])
+    A = good["A"]
+    for key, bad, err in (("x", good["x"].float(), TypeError), ("x", good["x"].cpu(), ValueError),
+                          ("W", good["W"].t(), ValueError),
+                          ("A", A.transpose(1, 2), ValueError),
+                          ("A", A.repeat(1, 1, 2)[:, :, ::2], ValueError),
+                          ("B", good["B"][:1], ValueError),
+                          ("scale", good["scale"].double(), TypeError),
+                          ("adapter_idx", good["adapter_idx"].long(), TypeError),
+                          ("adapter_idx", good["adapter_idx"][:3], ValueError)):
+        with pytest.raises(err):
+            moe.moe_adapter_project(**{**good, key: bad})
