@@ -29,95 +29,30 @@ using namespace ptx;
 constexpr int kM = 128;             // output features (or rank rows) per tile
 constexpr int kK = 64;              // K per stage: one 128-byte swizzle atom
 constexpr int kABytes = kM * kK * 2;
-constexpr int kThreads = 192;       // producer, MMA and four epilogue warps
-constexpr int kEpiThreads = 128;
+constexpr int kThreads = 224;       // producer, MMA, guard and four epilogue warps
 constexpr int kMaxEntries = 256;    // adapters a token block can meet
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-constexpr int kSmemRing = 196608;
 
-template <int kNB>
-struct Cfg {
-  static constexpr int kBBytes = kNB * kK * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kSmemRing / kStageBytes < 8 ? kSmemRing / kStageBytes : 8;
-  static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kTmemCols = kNB < 32 ? 32 : kNB;
-  static constexpr int kSmemBytes = kRing + 1024 /* alignment */ + 4096 /* Shared */;
-  static_assert(kNB * kM * 4 <= kRing, "the split's fp32 tile is staged in the ring");
+// What the shrink kernel leaves about one token block for the kernels after it.
+struct BlockPlan {
+  int n_ent;                       // adapters the block meets
+  int bad;                         // an adapter index was out of range
+  uint32_t bits[32];               // the same adapters as bits
+  uint16_t list[kMaxEntries];      // ascending
+  uint8_t groups[kMaxEntries];     // per entry: its 64-token groups, as bits
 };
+static_assert(sizeof(BlockPlan) <= kAdapterPlanBytes, "plan pitch");
 
-struct Shared {
-  uint64_t full[8];
-  uint64_t empty[8];
-  uint64_t acc_full;
-  uint64_t list_ready;
-  uint64_t drain;
-  uint32_t tmem_base;
-  int abort;
-  int n_ent;
-  unsigned bits[32];
-  uint16_t list[kMaxEntries];   // the block's adapters, ascending
-  int idx[256];                 // adapter of each token of the block, -1 for none
-};
-static_assert(sizeof(Shared) <= 4096, "shared block");
-
-struct Maps {
-  CUtensorMap w;     // expand: the projection's weights; shrink: the adapters' rank rows
-  CUtensorMap x;     // token rows [T, K]
-  CUtensorMap ext;   // expand: the adapters' other matrix
-  CUtensorMap z;     // expand: Z
-};
-
-struct Args {
-  int T, K, n, R, rb;       // rb: rank rows per TMA box, a power of two that divides R
-  int n_tt, split;          // token blocks; CTAs of a cluster that share a tile's K
-  const int32_t* adapter_idx;
-  const float* scale;
-  __nv_bfloat16* out;       // expand: y [T, ld]; shrink: Z [T, ld]
-  int ld;
-  int32_t* plan;            // shrink: [n_tt][kPlanInts], the blocks' adapters as bits
-  int* status;
-};
-constexpr int kPlanInts = 32;
+__device__ __forceinline__ const BlockPlan* plan_of(const void* plan, int tt) {
+  return reinterpret_cast<const BlockPlan*>(static_cast<const char*>(plan) +
+                                            (size_t)tt * kAdapterPlanBytes);
+}
 
 __device__ __forceinline__ void fence_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// The adapters that token block tt meets (the four epilogue warps).
-__device__ __forceinline__ void build_list(Shared* sh, const Args& a, int row0, int rows,
-                                           bool report) {
-  const int tid = threadIdx.x - 64, lane = threadIdx.x & 31;
-  if (tid < 32) sh->bits[tid] = 0u;
-  epi_sync();
-  bool bad = false;
-  for (int i = tid; i < rows; i += kEpiThreads) {
-    int e = __ldg(a.adapter_idx + row0 + i);
-    if (e < 0 || e >= a.n) {
-      bad |= e != -1;
-      e = -1;
-    } else {
-      atomicOr(&sh->bits[e >> 5], 1u << (e & 31));
-    }
-    sh->idx[i] = e;
-  }
-  if (bad && report) set_status(a.status, MOE_ERR_INVALID_ARG);
-  epi_sync();
-  if (tid < 32) {
-    unsigned w = sh->bits[lane];
-    const int c = __popc(w);
-    int incl = c;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += u;
-    }
-    int at = incl - c;
-    for (; w; w &= w - 1) sh->list[at++] = (uint16_t)(lane * 32 + __ffs(w) - 1);
-    if (lane == 31) sh->n_ent = incl;
-  }
-  epi_sync();
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -128,6 +63,22 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "memory");
   return v;
 }
+// The sum over the cluster's CTAs, in rank order, of the float4 at `addr` of
+// their shared memory; all loads in flight at once.
+template <int kS>
+__device__ __forceinline__ float4 cluster_sum(uint32_t addr) {
+  float4 p[kS];
+#pragma unroll
+  for (int r = 0; r < kS; ++r) p[r] = ld_cluster_f4(mapa_shared(addr, (uint32_t)r));
+#pragma unroll
+  for (int r = 1; r < kS; ++r) {
+    p[0].x += p[r].x;
+    p[0].y += p[r].y;
+    p[0].z += p[r].z;
+    p[0].w += p[r].w;
+  }
+  return p[0];
+}
 
 __device__ __forceinline__ uint2 pack4(float4 v) {
   const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -137,35 +88,412 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
   return r;
 }
 
-// One tile (128 output features x kNB tokens) per cluster of `split` CTAs, each
-// taking a contiguous share of the K stages; the partial tiles meet in
-// shared memory and are added in rank order.
-template <int kNB, bool kShrink, bool kKMajor>
+// The operand ring: `kStages` stages, the barriers of each, and the place of
+// one role in it.
+template <int kStages>
+struct Place {
+  int stage = 0;
+  uint32_t phase = 0;
+  int count = 0;   // stages passed
+  __device__ __forceinline__ void next() {
+    ++count;
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+// No TMA write may land after the CTA exits (or before its ring is reused by
+// ordinary stores): the last loads have arrived.
+template <int kStages>
+__device__ __forceinline__ void drain_loads(uint64_t* full, int from, int issued) {
+  for (int i = issued - from > kStages ? issued - kStages : from; i < issued; ++i)
+    mbar_wait(&full[i % kStages], (uint32_t)((i / kStages) & 1), nullptr, kWaitLimitNs);
+}
+
+// ---------------------------------------------------------------- shrink
+// Z[t, e R + r] = scale_a * <x[t], A_a[r]> at the token's own entry e, 0 elsewhere.
+// A cluster of kS CTAs per (token block, every gridDim.y-th unit of 128 rank rows),
+// each taking a share of K.  Bound by reading x once and the rank rows; the
+// partial tiles meet in shared memory, where only the R values that a token
+// keeps are read.
+struct ShrinkMaps {
+  CUtensorMap p;     // the adapters' rank rows [n, R, K], boxes of 64 K x rb rows
+  CUtensorMap v;     // token rows [T, K], boxes of 64 K x kNB rows
+};
+struct ShrinkArgs {
+  int T, K, n, R, rb, zc;   // rb: rank rows per box, a power of two that divides R
+  const int32_t* adapter_idx;
+  const float* scale;
+  __nv_bfloat16* z;         // [T, zc]
+  void* plan;
+  int* status;
+  bool clear;               // the first kernel of the call: clear the status
+};
+template <int kNB>
+struct ShrinkCfg {
+  static constexpr int kStageBytes = kABytes + kNB * kK * 2;
+  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kTmemCols = kNB < 32 ? 32 : kNB;
+  static constexpr int kSmemBytes = kRing + 1024 + 4096;
+  static_assert(kNB * kM * 4 <= kRing, "the partial fp32 tile is staged in the ring");
+};
+struct ShrinkShared {
+  uint64_t full[8], empty[8];
+  uint64_t acc_full, drain;
+  uint32_t tmem_base;
+  int abort, bad, n_ent;
+  unsigned bits[32];
+  uint16_t list[kMaxEntries];
+  unsigned groups[kMaxEntries];
+  int idx[256];                 // adapter of each token of the block, -1 for none
+};
+static_assert(sizeof(ShrinkShared) <= 4096, "shared block");
+
+// The adapters that token block tt meets, by the whole CTA.
+__device__ __forceinline__ void build_list(ShrinkShared* sh, const ShrinkArgs& a, int row0,
+                                           int rows) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) sh->bits[tid] = 0u;
+  if (tid == 32) sh->bad = 0;
+  for (int i = tid; i < kMaxEntries; i += kThreads) sh->groups[i] = 0u;
+  __syncthreads();
+  for (int i = tid; i < rows; i += kThreads) {
+    int e = __ldg(a.adapter_idx + row0 + i);
+    if (e < 0 || e >= a.n) {
+      if (e != -1) sh->bad = 1;
+      e = -1;
+    } else {
+      atomicOr(&sh->bits[e >> 5], 1u << (e & 31));
+    }
+    sh->idx[i] = e;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const int c = __popc(sh->bits[lane]);
+    int incl = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += u;
+    }
+    int at = incl - c;
+    for (unsigned w = sh->bits[lane]; w; w &= w - 1) sh->list[at++] = (uint16_t)(lane * 32 + __ffs(w) - 1);
+    if (lane == 31) sh->n_ent = incl;
+  }
+  __syncthreads();
+}
+// ... and the plan of it, for the kernels that follow (one CTA of the block).
+__device__ __forceinline__ void write_plan(ShrinkShared* sh, const ShrinkArgs& a, int tt,
+                                           int rows) {
+  const int tid = threadIdx.x;
+  BlockPlan* p = const_cast<BlockPlan*>(plan_of(a.plan, tt));
+  for (int i = tid; i < rows; i += kThreads) {
+    const int e = sh->idx[i];
+    if (e < 0) continue;
+    int at = __popc(sh->bits[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int w = 0; w < (e >> 5); ++w) at += __popc(sh->bits[w]);
+    atomicOr(&sh->groups[at], 1u << (i / 64));
+  }
+  __syncthreads();
+  if (tid < 32) p->bits[tid] = sh->bits[tid];
+  if (tid == 32) {
+    p->n_ent = sh->n_ent;
+    p->bad = sh->bad;
+  }
+  for (int i = tid; i < sh->n_ent; i += kThreads) {
+    p->list[i] = sh->list[i];
+    p->groups[i] = (uint8_t)sh->groups[i];
+  }
+}
+
+template <int kNB, int kS>
 __global__ void __launch_bounds__(kThreads, 1)
-adapter_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
-  using C = Cfg<kNB>;
+adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs a) {
+  using C = ShrinkCfg<kNB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Shared* sh = reinterpret_cast<Shared*>(smem + C::kRing);
+  ShrinkShared* sh = reinterpret_cast<ShrinkShared*>(smem + C::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = a.split;
-  const int rank = S > 1 ? (int)cluster_ctarank() : 0;
-  const int tile = (int)blockIdx.x / S;
-  const int tt = tile % a.n_tt, mt = tile / a.n_tt;
-  const int row0 = tt * kNB;
-  const int rows = min(kNB, a.T - row0);
+  const int rank = kS > 1 ? (int)cluster_ctarank() : 0;
+  const int tt = (int)blockIdx.x / kS;
+  const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
   const int nk = a.K / kK;
-  const int kb0 = (int)((long long)nk * rank / S), kb1 = (int)((long long)nk * (rank + 1) / S);
+  const int kb0 = nk * rank / kS, kb1 = nk * (rank + 1) / kS;
 
-  if (kShrink) pdl_trigger();
+  pdl_trigger();
+  // the call's status starts clean: this is its first kernel, and nothing is
+  // reported before a later kernel of the call or a wait of a second
+  if (a.clear && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
+  build_list(sh, a, row0, rows);
+  if (rank == 0 && blockIdx.y == 0) write_plan(sh, a, tt, rows);
+  const int q_all = sh->n_ent * a.R;
+  if ((int)blockIdx.y * kM >= q_all) return;   // the same for the whole cluster
+
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 1);
     }
     mbar_init(&sh->acc_full, 1);
-    mbar_init(&sh->list_ready, 1);
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  volatile int* abort_flag = &sh->abort;
+  Place<C::kStages> at;
+  uint32_t parity = 0;
+  for (int u = blockIdx.y; u * kM < q_all; u += gridDim.y, parity ^= 1u) {
+    const int q_end = min(kM, q_all - u * kM);
+    if (warp == 0 && lane == 0) {
+      const uint64_t pol_p = policy_evict_normal(), pol_v = policy_evict_last();
+      const int from = at.count;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
+        uint8_t* sA = smem + at.stage * C::kStageBytes;
+        uint64_t* fb = &sh->full[at.stage];
+        // rank rows past the last entry keep what the stage held: their
+        // products are not read
+        mbar_arrive_expect_tx(fb, (uint32_t)((q_end + kNB) * kK * 2));
+        tma_load_2d(sA + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
+        for (int q = 0; q < q_end; q += a.rb) {
+          const int qq = u * kM + q, e = qq / a.R;
+          tma_load_3d(sA + q * (kK * 2), &maps.p, fb, kb * kK, qq - e * a.R, sh->list[e], pol_p);
+        }
+        at.next();
+      }
+      if (!ok) {
+        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
+        *abort_flag = 1;
+      }
+      drain_loads<C::kStages>(sh->full, from, at.count);
+    } else if (warp == 1 && lane == 0) {
+      const uint32_t sbase = smem_u32(smem);
+      constexpr uint32_t kIdesc = idesc_bf16(kM, kNB, false, false);
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(&sh->full[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
+        tc_fence_after();
+        const uint32_t a0 = sbase + (uint32_t)(at.stage * C::kStageBytes), b0 = a0 + kABytes;
+#pragma unroll
+        for (int kk = 0; kk < kK / 16; ++kk)
+          mma_bf16_ss(tmem, sdesc_sw128(a0 + kk * 32, 16, 1024), sdesc_sw128(b0 + kk * 32, 16, 1024),
+                      kIdesc, (kb > kb0 || kk) ? 1u : 0u);
+        mma_commit(&sh->empty[at.stage]);
+        at.next();
+      }
+      if (!ok) {
+        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
+        *abort_flag = 1;
+      }
+      mma_commit(&sh->acc_full);
+      mma_commit(&sh->drain);
+      if (!mbar_wait(&sh->drain, parity, nullptr, kWaitLimitNs))
+        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
+    }
+    const int q = warp & 3;   // TMEM lanes 32 q ..
+    if (warp >= 3) {
+      const bool got = mbar_wait(&sh->acc_full, parity, abort_flag, kWaitLimitNs);
+      tc_fence_after();
+      if (__all_sync(0xffffffffu, got) && q * 32 < q_end) {
+        float* st = reinterpret_cast<float*>(smem);
+        for (int c0 = 0; c0 < rows; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) st[(c0 + c) * kM + q * 32 + lane] = __uint_as_float(v[c]);
+        }
+      }
+      tc_fence_before();
+    }
+    // every partial tile of the cluster is in shared memory
+    __syncwarp();
+    if constexpr (kS > 1) cluster_sync(); else __syncthreads();
+    if (!*abort_flag) {
+      // this lane's four rank rows belong to one entry (R is a multiple of 8)
+      const int e = (u * kM + 4 * lane) / a.R;
+      const int ad = 4 * lane < q_end ? (int)sh->list[e] : -2;
+      const float f = ad >= 0 ? __ldg(a.scale + ad) : 0.f;
+      const uint32_t mine = smem_u32(smem) + (uint32_t)lane * 16;
+      constexpr int kStep = kS * (kThreads / 32);
+#pragma unroll 2
+      for (int t = rank * (kThreads / 32) + warp; t < rows; t += kStep) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (sh->idx[t] == ad) {
+          s = cluster_sum<kS>(mine + (uint32_t)t * (kM * 4));
+          s = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+        }
+        *reinterpret_cast<uint2*>(a.z + (size_t)(row0 + t) * a.zc + u * kM + 4 * lane) = pack4(s);
+      }
+    }
+    // no CTA loads the next unit (by TMA, over a tile that ordinary stores
+    // wrote), or leaves, while another reads its tile; after a wait that ran out
+    // the CTAs still go through their units together
+    fence_async_smem();
+    __syncwarp();
+    if constexpr (kS > 1) cluster_sync(); else __syncthreads();
+    tc_fence_after();
+  }
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ---------------------------------------------------------------- expand
+// out = v W + Z P, tiles of 128 output features x one token block.
+struct ExpandMaps {
+  CUtensorMap w;     // the projection's weights
+  CUtensorMap v;     // token rows [T, K], boxes of 64 K x kNB rows
+  CUtensorMap p;     // the adapters' matrices [n, R, M], boxes of rb rows x 128 features
+  CUtensorMap z;     // Z [T, zc], boxes of 64 columns x kNB rows
+};
+struct ExpandArgs {
+  int T, K, M, n, R, rb, n_tt;
+  __nv_bfloat16* out;       // [T, M]
+  const void* plan;
+  int* status;
+};
+
+// The weight operand of one stage and its token rows.
+template <int kNB, bool kKMajor>
+__device__ __forceinline__ void load_base(uint8_t* st, uint64_t* fb, const ExpandMaps& maps, int kb,
+                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v) {
+  mbar_arrive_expect_tx(fb, kABytes + kNB * kK * 2);
+  if constexpr (kKMajor)
+    tma_load_2d(st, &maps.w, fb, kb * kK, mt * kM, pol_w);
+  else
+    tma_load_3d(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
+  tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
+}
+// Stage j of the adapters' part: 64 rank rows of the block's entries, in boxes
+// of rb rows, each [2 feature atoms][rb rows][128 bytes].
+template <int kNB>
+__device__ __forceinline__ void load_ext(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
+                                         const ExpandArgs& a, const BlockPlan* plan, int q_all,
+                                         int j, int mt, int row0, uint64_t pol_w, uint64_t pol_v) {
+  mbar_arrive_expect_tx(fb, kABytes + kNB * kK * 2);
+  tma_load_2d(st + kABytes, &maps.z, fb, j * kK, row0, pol_v);
+  for (int q = 0; q < kK; q += a.rb) {
+    const int qq = j * kK + q, e = qq / a.R;
+    // past the last entry: an adapter that does not exist, read as zeros
+    const int ad = qq < q_all ? (int)plan->list[e] : a.n;
+    tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, qq - e * a.R, mt * 2, ad, pol_w);
+  }
+}
+template <int kNB, bool kKMajor>
+__device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, uint32_t& acc) {
+  constexpr uint32_t kIdesc = idesc_bf16(kM, kNB, /*a_mn=*/!kKMajor, false);
+  const uint32_t b0 = a0 + kABytes;
+#pragma unroll
+  for (int kk = 0; kk < kK / 16; ++kk) {
+    // MN-major weights: 64-feature atoms 8 KB apart, 16 K rows = 2 KB; K-major
+    // operands: 8-row groups 1 KB apart, 16 K = 32 bytes
+    const uint64_t da = kKMajor ? sdesc_sw128(a0 + kk * 32, 16, 1024)
+                                : sdesc_sw128(a0 + kk * 2048, 8192, 1024);
+    mma_bf16_ss(tmem, da, sdesc_sw128(b0 + kk * 32, 16, 1024), kIdesc, acc);
+    acc = 1u;
+  }
+}
+template <int kNB>
+__device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, int rb, uint32_t& acc) {
+  constexpr uint32_t kIdesc = idesc_bf16(kM, kNB, /*a_mn=*/true, false);
+  const uint32_t b0 = a0 + kABytes;
+  const uint32_t lbo = (uint32_t)rb * 128, sbo = rb == 8 ? 2048u : 1024u;
+#pragma unroll
+  for (int kk = 0; kk < kK / 16; ++kk) {
+    const uint32_t q = 16u * kk, box = q / rb;
+    const uint32_t at = a0 + box * (uint32_t)rb * 256 + (q - box * rb) * 128;
+    mma_bf16_ss(tmem, sdesc_sw128(at, lbo, sbo), sdesc_sw128(b0 + kk * 32, 16, 1024), kIdesc, acc);
+    acc = 1u;
+  }
+}
+// The guard warp's pass over the 64 x 128 adapter weights of a stage: every
+// token of the block is multiplied by every entry's rank rows, its own z or
+// zero, so an infinity or NaN there would reach the other requests' tokens as
+// 0 * inf.  It counts as zero instead and is reported.
+__device__ __forceinline__ bool clear_nonfinite(uint8_t* st, int lane) {
+  bool found = false;
+#pragma unroll 8
+  for (int i = lane; i < kABytes / 16; i += 32) {
+    uint4 v = reinterpret_cast<const uint4*>(st)[i];
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    uint32_t hit = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // all exponent bits set, in either half
+      if ((w[c] & 0x7f80u) == 0x7f80u) hit |= 1u << (2 * c);
+      if ((w[c] & 0x7f800000u) == 0x7f800000u) hit |= 2u << (2 * c);
+    }
+    if (hit) {
+      found = true;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (hit & (1u << (2 * c))) w[c] &= 0xffff0000u;
+        if (hit & (2u << (2 * c))) w[c] &= 0x0000ffffu;
+      }
+      reinterpret_cast<uint4*>(st)[i] = v;
+    }
+  }
+  return found;
+}
+
+// Few tiles: a cluster of kS CTAs per tile, each taking a share of the K
+// stages; the partial tiles meet in shared memory and are added in rank order.
+template <int kNB>
+struct SplitCfg {
+  static constexpr int kStageBytes = kABytes + kNB * kK * 2;
+  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kTmemCols = kNB < 32 ? 32 : kNB;
+  static constexpr int kSmemBytes = kRing + 1024 + 1024;
+  static_assert(kNB * kM * 4 <= kRing, "the partial fp32 tile is staged in the ring");
+};
+// Ring slots are handed out in the order of all stages (empty[slot]); arrivals
+// are counted apart for the projection's stages (full) and the adapters'
+// (loaded, then ready once the guard has passed them), each in its own order,
+// since the guard follows the adapters' stages only.
+struct SplitShared {
+  uint64_t full[8], empty[8], loaded[8], ready[8];
+  uint64_t acc_full, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int kNB, bool kKMajor, int kS>
+__global__ void __launch_bounds__(kThreads, 1)
+adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs a) {
+  using C = SplitCfg<kNB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  SplitShared* sh = reinterpret_cast<SplitShared*>(smem + C::kRing);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kS > 1 ? (int)cluster_ctarank() : 0;
+  const int tile = (int)blockIdx.x / kS;
+  const int tt = tile % a.n_tt, mt = tile / a.n_tt;
+  const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
+  const int nk = a.K / kK;
+  const int kb0 = nk * rank / kS, kb1 = nk * (rank + 1) / kS;
+  const BlockPlan* plan = plan_of(a.plan, tt);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->loaded[s], 1);
+      mbar_init(&sh->ready[s], 1);
+    }
+    mbar_init(&sh->acc_full, 1);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     fence_mbar_init();
@@ -182,132 +510,60 @@ adapter_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
 
   if (warp == 0) {
     if (lane == 0) {
+      // a weight tile read by one block is streamed past L2
       const uint64_t pol_w = a.n_tt == 1 ? policy_evict_first() : policy_evict_normal();
-      const uint64_t pol_x = policy_evict_last();
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
+      const uint64_t pol_v = policy_evict_last();
+      Place<C::kStages> at, base, ext;
       bool ok = true;
-      auto next = [&]() {
-        ++issued;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      };
-      if (kShrink) ok = mbar_wait(&sh->list_ready, 0, abort_flag, kWaitLimitNs);
-      for (int kb = kb0; ok && kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs))) break;
-        uint8_t* sA = smem + stage * C::kStageBytes;
-        uint64_t* fb = &sh->full[stage];
-        const int k0 = kb * kK;
-        if constexpr (kShrink) {
-          // the rank rows of this tile's entries; rows past the last entry keep
-          // what the stage held (their products are dropped by the epilogue)
-          const int q_end = min(kM, sh->n_ent * a.R - mt * kM);
-          if (q_end <= 0) break;
-          mbar_arrive_expect_tx(fb, (uint32_t)(q_end * kK * 2 + C::kBBytes));
-          for (int q = 0; q < q_end; q += a.rb) {
-            const int qq = mt * kM + q, e = qq / a.R;
-            tma_load_3d(sA + q * (kK * 2), &maps.w, fb, k0, qq - e * a.R, sh->list[e], pol_w);
-          }
-        } else {
-          mbar_arrive_expect_tx(fb, C::kStageBytes);
-          if constexpr (kKMajor)
-            tma_load_2d(sA, &maps.w, fb, k0, mt * kM, pol_w);
-          else
-            tma_load_3d(sA, &maps.w, fb, 0, k0, mt * 2, pol_w);
-        }
-        tma_load_2d(sA + kABytes, &maps.x, fb, k0, row0, pol_x);
-        next();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
+        load_base<kNB, kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, kb,
+                                mt, row0, pol_w, pol_v);
+        at.next();
+        base.next();
       }
-      if constexpr (!kShrink) {
-        // K goes on over Z and the entries' rank rows
-        if (ok) ok = mbar_wait(&sh->list_ready, 0, abort_flag, kWaitLimitNs);
-        pdl_wait();             // Z is complete
-        fence_async_global();
-        const int q_all = ok ? sh->n_ent * a.R : 0;
-        const int ne = (q_all + kK - 1) / kK;
-        const int j0 = ne * rank / S, j1 = ne * (rank + 1) / S;
-        for (int j = j0; ok && j < j1; ++j) {
-          if (!(ok = mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs))) break;
-          uint8_t* sA = smem + stage * C::kStageBytes;
-          uint64_t* fb = &sh->full[stage];
-          mbar_arrive_expect_tx(fb, C::kStageBytes);
-          for (int q = 0; q < kK; q += a.rb) {
-            const int qq = j * kK + q;
-            const int e = qq / a.R;
-            // past the last entry: an adapter that does not exist, read as zeros
-            const int ad = qq < q_all ? (int)sh->list[e] : a.n;
-            tma_load_4d(sA + q * (kM * 2), &maps.ext, fb, 0, qq - e * a.R, mt * 2, ad, pol_w);
-          }
-          tma_load_2d(sA + kABytes, &maps.z, fb, j * kK, row0, pol_x);
-          next();
-        }
+      pdl_wait();             // the plan and Z are complete
+      fence_async_global();
+      const int q_all = plan->n_ent * a.R;
+      const int ne = (q_all + kK - 1) / kK;
+      for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
+        if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
+        load_ext<kNB>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan, q_all,
+                      j, mt, row0, pol_w, pol_v);
+        at.next();
+        ext.next();
       }
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         *abort_flag = 1;
       }
-      // no TMA write may land after the CTA exits: wait for the last loads
-      for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-        mbar_wait(&sh->full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), nullptr,
-                  kWaitLimitNs);
+      if (mt == 0 && rank == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
+      drain_loads<C::kStages>(sh->full, 0, base.count);
+      drain_loads<C::kStages>(sh->loaded, 0, ext.count);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t sbase = smem_u32(smem);
-      int stage = 0;
-      uint32_t phase = 0, acc = 0;
+      Place<C::kStages> at, base, ext;
+      uint32_t acc = 0;
       bool ok = true;
-      constexpr uint32_t kIdesc = idesc_bf16(kM, kNB, /*a_mn=*/!kShrink && !kKMajor, false);
-      constexpr uint32_t kIdescExt = idesc_bf16(kM, kNB, /*a_mn=*/true, false);
-      int kend = kb1;
-      if (kShrink) {
-        ok = mbar_wait(&sh->list_ready, 0, abort_flag, kWaitLimitNs);
-        if (sh->n_ent * a.R <= mt * kM) kend = kb0;   // no such tile
-      }
-      auto advance = [&]() {
-        mma_commit(&sh->empty[stage]);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      };
-      for (int kb = kb0; ok && kb < kend; ++kb) {
-        if (!(ok = mbar_wait(&sh->full[stage], phase, abort_flag, kWaitLimitNs))) break;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
-        const uint32_t a0 = sbase + (uint32_t)(stage * C::kStageBytes), b0 = a0 + kABytes;
-#pragma unroll
-        for (int kk = 0; kk < kK / 16; ++kk) {
-          // MN-major weights: 64-feature atoms 8 KB apart, 16 K rows = 2 KB;
-          // K-major operands: 8-row groups 1 KB apart, 16 K = 32 bytes
-          const uint64_t da = (kShrink || kKMajor) ? sdesc_sw128(a0 + kk * 32, 16, 1024)
-                                                   : sdesc_sw128(a0 + kk * 2048, 8192, 1024);
-          mma_bf16_ss(tmem, da, sdesc_sw128(b0 + kk * 32, 16, 1024), kIdesc, acc);
-          acc = 1u;
-        }
-        advance();
+        mma_base<kNB, kKMajor>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), acc);
+        mma_commit(&sh->empty[at.stage]);
+        at.next();
+        base.next();
       }
-      if constexpr (!kShrink) {
-        if (ok) ok = mbar_wait(&sh->list_ready, 0, abort_flag, kWaitLimitNs);
-        const int ne = ok ? (sh->n_ent * a.R + kK - 1) / kK : 0;
-        const int j0 = ne * rank / S, j1 = ne * (rank + 1) / S;
-        // boxes of rb rank rows, each [2 feature atoms][rb rows][128 bytes]
-        const uint32_t lbo = (uint32_t)a.rb * 128, sbo = a.rb == 8 ? 2048u : 1024u;
-        for (int j = j0; ok && j < j1; ++j) {
-          if (!(ok = mbar_wait(&sh->full[stage], phase, abort_flag, kWaitLimitNs))) break;
-          tc_fence_after();
-          const uint32_t a0 = sbase + (uint32_t)(stage * C::kStageBytes), b0 = a0 + kABytes;
-#pragma unroll
-          for (int kk = 0; kk < kK / 16; ++kk) {
-            const uint32_t q = 16u * kk, box = q / a.rb;
-            const uint32_t at = a0 + box * (uint32_t)a.rb * 256 + (q - box * a.rb) * 128;
-            mma_bf16_ss(tmem, sdesc_sw128(at, lbo, sbo), sdesc_sw128(b0 + kk * 32, 16, 1024),
-                        kIdescExt, acc);
-            acc = 1u;
-          }
-          advance();
-        }
+      pdl_wait();
+      const int ne = (plan->n_ent * a.R + kK - 1) / kK;
+      for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
+        if (!(ok = mbar_wait(&sh->ready[ext.stage], ext.phase, abort_flag, kWaitLimitNs))) break;
+        tc_fence_after();
+        mma_ext<kNB>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), a.rb, acc);
+        mma_commit(&sh->empty[at.stage]);
+        at.next();
+        ext.next();
       }
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
@@ -318,126 +574,320 @@ adapter_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
       if (!mbar_wait(&sh->drain, 0, nullptr, kWaitLimitNs))
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
-  } else {
-    build_list(sh, a, row0, rows, mt == 0 && rank == 0);
-    if (threadIdx.x == 64) mbar_arrive(&sh->list_ready);
-    if (kShrink && mt == 0 && rank == 0 && warp == 2)
-      a.plan[(size_t)tt * kPlanInts + lane] = (int)sh->bits[lane];
+  } else if (warp == 2) {
+    Place<C::kStages> at, ext;
+    for (int kb = kb0; kb < kb1; ++kb) at.next();
+    pdl_wait();
+    const int ne = (plan->n_ent * a.R + kK - 1) / kK;
+    bool found = false;
+    for (int j = ne * rank / kS; j < ne * (rank + 1) / kS; ++j) {
+      const bool got = mbar_wait(&sh->loaded[ext.stage], ext.phase, abort_flag, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) break;
+      found |= clear_nonfinite(smem + at.stage * C::kStageBytes, lane);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->ready[ext.stage]);
+      at.next();
+      ext.next();
+    }
+    if (found) set_status(a.status, MOE_ERR_NONFINITE);
   }
-  bool have = true;
-  if (warp >= 2) {
-    // a shrink tile past the block's entries has nothing to store
-    if (kShrink) have = sh->n_ent * a.R > mt * kM;
+  if (warp >= 3) {
     const bool got = mbar_wait(&sh->acc_full, 0, abort_flag, kWaitLimitNs);
-    if (!__all_sync(0xffffffffu, got)) have = false;
     tc_fence_after();
-    if (have) {
+    if (__all_sync(0xffffffffu, got)) {
       // TMEM lane = feature, column = token
       const int q = warp & 3;
-      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
-      const int f = q * 32 + lane;
+      float* st = reinterpret_cast<float*>(smem);
       for (int c0 = 0; c0 < rows; c0 += 16) {
         uint32_t v[16];
-        tmem_ld_32x32b_x16(tb + c0, v);
+        tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
         tmem_ld_wait();
-        float* st = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) st[(c0 + c) * kM + f] = __uint_as_float(v[c]);
+        for (int c = 0; c < 16; ++c) st[(c0 + c) * kM + q * 32 + lane] = __uint_as_float(v[c]);
       }
     }
     tc_fence_before();
   }
-  // every partial tile of the cluster is in shared memory
   __syncwarp();
-  if (S > 1) cluster_sync(); else __syncthreads();
-  if (warp >= 2 && have && !*abort_flag) {
-    const int w = warp - 2;
-    const uint32_t mine = smem_u32(smem);
-    for (int t = rank * 4 + w; t < rows; t += 4 * S) {
-      const uint32_t at = mine + (uint32_t)(t * kM * 4 + lane * 16);
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (S == 1) {
-        s = *reinterpret_cast<const float4*>(smem + t * kM * 4 + lane * 16);
-      } else {
-        for (int r = 0; r < S; ++r) {
-          const float4 p = ld_cluster_f4(mapa_shared(at, (uint32_t)r));
-          s.x += p.x;
-          s.y += p.y;
-          s.z += p.z;
-          s.w += p.w;
-        }
-      }
-      if constexpr (kShrink) {
-        const int e = (mt * kM + 4 * lane) / a.R;   // the entry of these four rank rows
-        const int own = sh->idx[t];
-        if (own >= 0 && e < sh->n_ent && sh->list[e] == own) {
-          const float f = __ldg(a.scale + own);
-          s = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
-        } else {
-          s = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-      *reinterpret_cast<uint2*>(a.out + (size_t)(row0 + t) * a.ld + mt * kM + 4 * lane) = pack4(s);
+  if constexpr (kS > 1) cluster_sync(); else __syncthreads();
+  if (!*abort_flag) {
+    const uint32_t mine = smem_u32(smem) + (uint32_t)lane * 16;
+    constexpr int kStep = kS * (kThreads / 32);
+#pragma unroll 2
+    for (int t = rank * (kThreads / 32) + warp; t < rows; t += kStep) {
+      float4 s;
+      if constexpr (kS == 1)
+        s = *reinterpret_cast<const float4*>(smem + t * (kM * 4) + lane * 16);
+      else
+        s = cluster_sum<kS>(mine + (uint32_t)t * (kM * 4));
+      *reinterpret_cast<uint2*>(a.out + (size_t)(row0 + t) * a.M + mt * kM + 4 * lane) = pack4(s);
     }
   }
   __syncwarp();
-  tc_fence_before();
   // no CTA leaves while another reads its shared memory
-  if (S > 1) cluster_sync(); else __syncthreads();
+  if constexpr (kS > 1) cluster_sync(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-// dG[a][r][d] = sum over the tokens t of adapter a of Z[t, entry(a) R + r] V[t, d]:
-// one CTA per (adapter, 128 features of V), K = the tokens of every 64-token
-// group that holds one of adapter a, in ascending order.
-struct WgradMaps {
-  CUtensorMap v;   // [T, D] as (64 features, tokens, D / 64)
-  CUtensorMap z;   // [T, zc], boxes of 64 columns x 64 tokens
-};
-struct WgradArgs {
-  int T, D, n, R, nb, n_tt;    // nb: tokens per block of the plan
-  const int32_t* adapter_idx;
-  const int32_t* plan;
-  __nv_bfloat16* out;          // [n, R, D]
-  int* status;
-};
-struct WgradCfg {
-  static constexpr int kBBytes = 2 * 64 * kK * 2;   // up to 128 rank columns
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = 6;
+// Many tiles: persistent CTAs, two accumulators of 256 tokens in TMEM, so the
+// epilogue of one tile runs under the main loop of the next.
+struct FullCfg {
+  static constexpr int kNB = 256;
+  static constexpr int kStageBytes = kABytes + kNB * kK * 2;
+  static constexpr int kStages = 4;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kSmemBytes = kRing + 1024 + 1024;
-  static constexpr int kTmemCols = 128;
+  static constexpr int kStgBytes = 16 * 32 * 2;            // 16 tokens x 32 features per warp
+  static constexpr int kSmemBytes = kRing + 1024 + 1024 + 4 * kStgBytes;
 };
-struct WgradShared {
-  uint64_t full[WgradCfg::kStages];
-  uint64_t empty[WgradCfg::kStages];
-  uint64_t acc_full;
-  uint64_t drain;
+struct FullShared {
+  uint64_t full[FullCfg::kStages], empty[FullCfg::kStages];
+  uint64_t loaded[FullCfg::kStages], ready[FullCfg::kStages];   // as in SplitShared
+  uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort;
-  volatile int stages;   // K stages in all, written by the producer before its last arrival
 };
 
+template <bool kKMajor>
+__global__ void __launch_bounds__(kThreads, 1)
+adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs a) {
+  using C = FullCfg;
+  constexpr int kNB = C::kNB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  FullShared* sh = reinterpret_cast<FullShared*>(smem + C::kRing);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nk = a.K / kK;
+  const int total = a.n_tt * (a.M / kM);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->loaded[s], 1);
+      mbar_init(&sh->ready[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh->acc_full[b], 1);
+      mbar_init(&sh->acc_empty[b], 4);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem_base, 2 * kNB);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  volatile int* abort_flag = &sh->abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
+      Place<C::kStages> at, base, ext;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const int tt = tile % a.n_tt, mt = tile / a.n_tt, row0 = tt * kNB;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
+            break;
+          load_base<kNB, kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, kb,
+                                  mt, row0, pol_w, pol_v);
+          at.next();
+          base.next();
+        }
+        pdl_wait();             // the plan and Z are complete
+        fence_async_global();
+        const BlockPlan* plan = plan_of(a.plan, tt);
+        const int q_all = plan->n_ent * a.R;
+        for (int j = 0; ok && j * kK < q_all; ++j) {
+          if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
+            break;
+          load_ext<kNB>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan,
+                        q_all, j, mt, row0, pol_w, pol_v);
+          at.next();
+          ext.next();
+        }
+        if (mt == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
+      }
+      if (!ok) {
+        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
+        *abort_flag = 1;
+      }
+      pdl_wait();
+      drain_loads<C::kStages>(sh->full, 0, base.count);
+      drain_loads<C::kStages>(sh->loaded, 0, ext.count);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t sbase = smem_u32(smem);
+      Place<C::kStages> at, base, ext;
+      Place<2> buf;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        if (!(ok = mbar_wait(&sh->acc_empty[buf.stage], buf.phase ^ 1u, abort_flag, kWaitLimitNs)))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf.stage * kNB);
+        uint32_t acc = 0;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
+          tc_fence_after();
+          mma_base<kNB, kKMajor>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), acc);
+          mma_commit(&sh->empty[at.stage]);
+          at.next();
+          base.next();
+        }
+        pdl_wait();
+        const int q_all = plan_of(a.plan, tile % a.n_tt)->n_ent * a.R;
+        for (int j = 0; ok && j * kK < q_all; ++j) {
+          if (!(ok = mbar_wait(&sh->ready[ext.stage], ext.phase, abort_flag, kWaitLimitNs)))
+            break;
+          tc_fence_after();
+          mma_ext<kNB>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), a.rb, acc);
+          mma_commit(&sh->empty[at.stage]);
+          at.next();
+          ext.next();
+        }
+        if (!ok) break;
+        mma_commit(&sh->acc_full[buf.stage]);
+        buf.next();
+      }
+      if (!ok) {
+        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
+        *abort_flag = 1;
+      }
+      mma_commit(&sh->drain);
+      if (!mbar_wait(&sh->drain, 0, nullptr, kWaitLimitNs))
+        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
+    }
+  } else if (warp == 2) {
+    Place<C::kStages> at, ext;
+    bool ok = true, found = false;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      for (int kb = 0; kb < nk; ++kb) at.next();
+      pdl_wait();
+      const int q_all = plan_of(a.plan, tile % a.n_tt)->n_ent * a.R;
+      for (int j = 0; j * kK < q_all; ++j) {
+        const bool got = mbar_wait(&sh->loaded[ext.stage], ext.phase, abort_flag, kWaitLimitNs);
+        if (!(ok = __all_sync(0xffffffffu, got))) break;
+        found |= clear_nonfinite(smem + at.stage * C::kStageBytes, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->ready[ext.stage]);
+        at.next();
+        ext.next();
+      }
+    }
+    if (found) set_status(a.status, MOE_ERR_NONFINITE);
+  } else {
+    const int q = warp & 3;
+    __nv_bfloat16* stg =
+        reinterpret_cast<__nv_bfloat16*>(smem + C::kRing + 1024 + (warp - 3) * C::kStgBytes);
+    Place<2> buf;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const int tt = tile % a.n_tt, mt = tile / a.n_tt;
+      const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
+      const bool got = mbar_wait(&sh->acc_full[buf.stage], buf.phase, abort_flag, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf.stage * kNB);
+      __nv_bfloat16* o = a.out + (size_t)row0 * a.M + mt * kM + q * 32;
+      for (int c0 = 0; c0 < rows; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tb + c0, v);
+        tmem_ld_wait();
+        // 16 tokens x 32 features, then rows of 64 bytes by four lanes each
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          stg[c * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[c]));
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 8 * h + (lane >> 2);
+          const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 32 + (lane & 3) * 8);
+          if (c0 + r < rows)
+            *reinterpret_cast<uint4*>(o + (size_t)(c0 + r) * a.M + (lane & 3) * 8) = w;
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->acc_empty[buf.stage]);
+      buf.next();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kNB);
+  }
+}
+
+// ------------------------------------------------------- weight gradients
+// G[a][r][d] = sum over the tokens t of adapter a of Z[t, entry(a) R + r] V[t, d]:
+// one CTA per (adapter, 128 columns of V), K = the tokens of every 64-token
+// group that holds one of adapter a, ascending.  Both gradients in one launch:
+// dA from (x, dZ), then dB from (dy, Z).
+struct WgradMaps {
+  CUtensorMap v[2];   // [T, D] as (64 features, tokens, D / 64)
+  CUtensorMap z[2];   // [T, zc], boxes of 64 columns x 64 tokens
+};
+struct WgradArgs {
+  int T, n, R, nb, n_tt;       // nb: tokens per block of the plan
+  int D[2];
+  const int32_t* adapter_idx;
+  const void* plan;
+  __nv_bfloat16* out[2];       // [n, R, D]
+  int* status;
+};
+// kCols: 64-column boxes of Z per stage (ranks up to 64, or up to 128).
+template <int kCols>
+struct WgradCfg {
+  static constexpr int kStageBytes = kABytes + kCols * 64 * kK * 2;
+  static constexpr int kStages = 4;      // two CTAs per SM at kCols = 1
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kRing + 1024 + 1024;
+  static constexpr int kTmemCols = 64 * kCols;
+};
+struct WgradShared {
+  uint64_t full[4], empty[4], ready[4];
+  uint64_t acc_full, drain;
+  uint32_t tmem_base;
+  int abort;
+  volatile int stages;         // K stages in all, once the producer has issued them
+  volatile int t0[4];          // first token of the group in each stage
+};
+
+template <int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
 adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) {
-  using C = WgradCfg;
+  using C = WgradCfg<kCols>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   WgradShared* sh = reinterpret_cast<WgradShared*>(smem + C::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_dt = a.D / kM;
-  const int ad = (int)blockIdx.x / n_dt, d0 = ((int)blockIdx.x % n_dt) * kM;
-  const int n_cols = a.R > 64 ? 2 : 1;                   // 64-column boxes of Z
+  const int units0 = a.n * (a.D[0] / kM);
+  const int which = (int)blockIdx.x < units0 ? 0 : 1;
+  const int unit = (int)blockIdx.x - (which ? units0 : 0);
+  const int D = a.D[which], n_dt = D / kM;
+  const int ad = unit / n_dt, d0 = (unit - ad * n_dt) * kM;
   const int N = (a.R + 15) & ~15;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->ready[s], 1);
     }
     mbar_init(&sh->acc_full, 1);
     mbar_init(&sh->drain, 1);
@@ -456,83 +906,79 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   volatile int* abort_flag = &sh->abort;
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
+    Place<C::kStages> at;
     bool ok = true;
-    for (int tt = 0; ok && tt < a.n_tt; ++tt) {
-      // the block's entries below `ad`, and whether ad is one
-      const unsigned w = (unsigned)__ldg(a.plan + (size_t)tt * kPlanInts + lane);
-      const unsigned mine = __shfl_sync(0xffffffffu, w, ad >> 5);
-      if (!((mine >> (ad & 31)) & 1u)) continue;
-      const unsigned below = lane < (ad >> 5) ? w : lane == (ad >> 5) ? w & ((1u << (ad & 31)) - 1u)
-                                                                      : 0u;
-      const int e = (int)__reduce_add_sync(0xffffffffu, (unsigned)__popc(below));
-      const int t_end = min(a.T, (tt + 1) * a.nb);
-      for (int t0 = tt * a.nb; ok && t0 < t_end; t0 += kK) {
-        const int ta = t0 + lane, tb = ta + 32;
-        const bool any = (ta < t_end && __ldg(a.adapter_idx + ta) == ad) ||
-                         (tb < t_end && __ldg(a.adapter_idx + tb) == ad);
-        if (!__any_sync(0xffffffffu, any)) continue;
-        int got = 1;
-        if (lane == 0) {
-          got = mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
-          if (got) {
-            uint8_t* sA = smem + stage * C::kStageBytes;
-            uint64_t* fb = &sh->full[stage];
-            mbar_arrive_expect_tx(fb, (uint32_t)(kABytes + n_cols * 64 * kK * 2));
-            tma_load_3d(sA, &maps.v, fb, 0, t0, d0 >> 6, pol);
-            for (int c = 0; c < n_cols; ++c)
-              tma_load_2d(sA + kABytes + c * 64 * kK * 2, &maps.z, fb, e * a.R + 64 * c, t0, pol);
-          }
+    for (int tb = 0; ok && tb < a.n_tt; tb += 32) {
+      // lane: block tb + lane, ad's entry in it and the groups that hold it
+      int e = 0;
+      unsigned g = 0;
+      if (tb + lane < a.n_tt) {
+        const BlockPlan* p = plan_of(a.plan, tb + lane);
+        const unsigned w = p->bits[ad >> 5];
+        if ((w >> (ad & 31)) & 1u) {
+          e = __popc(w & ((1u << (ad & 31)) - 1u));
+          for (int i = 0; i < (ad >> 5); ++i) e += __popc(p->bits[i]);
+          g = p->groups[e];
         }
-        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-        if (!ok) break;
-        ++issued;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
+      }
+      for (unsigned have = __ballot_sync(0xffffffffu, g != 0u); ok && have; have &= have - 1) {
+        const int src = __ffs(have) - 1;
+        const int eb = __shfl_sync(0xffffffffu, e, src);
+        unsigned gb = __shfl_sync(0xffffffffu, g, src);
+        for (; ok && gb; gb &= gb - 1) {
+          const int t0 = (tb + src) * a.nb + (__ffs(gb) - 1) * kK;
+          int got = 1;
+          if (lane == 0) {
+            got = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
+            if (got) {
+              uint8_t* st = smem + at.stage * C::kStageBytes;
+              uint64_t* fb = &sh->full[at.stage];
+              sh->t0[at.stage] = t0;
+              mbar_arrive_expect_tx(fb, C::kStageBytes);
+              tma_load_3d(st, &maps.v[which], fb, 0, t0, d0 >> 6, pol);
+#pragma unroll
+              for (int c = 0; c < kCols; ++c)
+                tma_load_2d(st + kABytes + c * 64 * kK * 2, &maps.z[which], fb, eb * a.R + 64 * c,
+                            t0, pol);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+          if (ok) at.next();
         }
       }
     }
     if (lane == 0) {
-      int last = issued > C::kStages ? issued - C::kStages : 0;   // first load not known to be read
-      if (ok) ok = mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, kWaitLimitNs);
+      int from = 0;
+      if (ok) ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
       if (ok) {
         // the end of the list travels as one more stage without data; the
         // load that used this slot before has been read
-        sh->stages = issued;
-        mbar_arrive(&sh->full[stage]);
-        if (issued >= C::kStages) last = issued - C::kStages + 1;
+        sh->stages = at.count;
+        mbar_arrive(&sh->full[at.stage]);
+        if (at.count >= C::kStages) from = at.count - C::kStages + 1;
       } else {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         *abort_flag = 1;
       }
-      for (int i = last; i < issued; ++i)
-        mbar_wait(&sh->full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), nullptr,
-                  kWaitLimitNs);
+      drain_loads<C::kStages>(sh->full, from, at.count);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t sbase = smem_u32(smem);
       const uint32_t idesc = idesc_bf16(kM, N, true, true);
-      int stage = 0, done = 0;
-      uint32_t phase = 0;
+      Place<C::kStages> at;
       bool ok = true;
       while (true) {
-        if (!(ok = mbar_wait(&sh->full[stage], phase, abort_flag, kWaitLimitNs))) break;
-        if (sh->stages == done) break;
+        if (!(ok = mbar_wait(&sh->ready[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
+        if (sh->stages == at.count) break;
         tc_fence_after();
-        const uint32_t a0 = sbase + (uint32_t)(stage * C::kStageBytes), b0 = a0 + kABytes;
+        const uint32_t a0 = sbase + (uint32_t)(at.stage * C::kStageBytes), b0 = a0 + kABytes;
 #pragma unroll
         for (int kk = 0; kk < kK / 16; ++kk)
           mma_bf16_ss(tmem, sdesc_sw128(a0 + kk * 2048, 8192, 1024),
-                      sdesc_sw128(b0 + kk * 2048, 8192, 1024), idesc, (done || kk) ? 1u : 0u);
-        mma_commit(&sh->empty[stage]);
-        ++done;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+                      sdesc_sw128(b0 + kk * 2048, 8192, 1024), idesc, (at.count || kk) ? 1u : 0u);
+        mma_commit(&sh->empty[at.stage]);
+        at.next();
       }
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
@@ -543,23 +989,52 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
       if (!mbar_wait(&sh->drain, 0, nullptr, kWaitLimitNs))
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
+  } else if (warp == 2) {
+    // Rows of V of other requests' tokens meet a zero of Z, which does not
+    // stop an infinity or NaN in them: they are cleared.
+    Place<C::kStages> at;
+    while (true) {
+      const bool got = mbar_wait(&sh->full[at.stage], at.phase, abort_flag, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) break;
+      if (sh->stages == at.count) {
+        if (lane == 0) mbar_arrive(&sh->ready[at.stage]);
+        break;
+      }
+      const int t0 = sh->t0[at.stage];
+      uint8_t* st = smem + at.stage * C::kStageBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = t0 + 32 * h + lane;
+        const bool other = t < a.T && __ldg(a.adapter_idx + t) != ad;
+        unsigned m = __ballot_sync(0xffffffffu, other);
+        for (; m; m &= m - 1) {
+          // row r: 128 bytes in each of the two feature atoms
+          const int r = 32 * h + __ffs(m) - 1;
+          if (lane < 16)
+            *reinterpret_cast<uint4*>(st + (lane >> 3) * 8192 + r * 128 + (lane & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->ready[at.stage]);
+      at.next();
+    }
   } else {
     const bool got = mbar_wait(&sh->acc_full, 0, abort_flag, kWaitLimitNs);
     if (__all_sync(0xffffffffu, got) && !*abort_flag) {
       tc_fence_after();
       const bool none = sh->stages == 0;   // no token: a zero gradient
       const int q = warp & 3;
-      const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
-      __nv_bfloat16* o = a.out + (size_t)ad * a.R * a.D + d0 + q * 32 + lane;
+      __nv_bfloat16* o = a.out[which] + (size_t)ad * a.R * D + d0 + q * 32 + lane;
       for (int c0 = 0; c0 < a.R; c0 += 16) {
         uint32_t v[16];
-        tmem_ld_32x32b_x16(tb + c0, v);
+        tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < 16; ++c)
           if (c0 + c < a.R)
-            o[(size_t)(c0 + c) * a.D] =
-                none ? __float2bfloat16_rn(0.f) : __float2bfloat16_rn(__uint_as_float(v[c]));
+            o[(size_t)(c0 + c) * D] = __float2bfloat16_rn(none ? 0.f : __uint_as_float(v[c]));
       }
     }
     tc_fence_before();
@@ -608,13 +1083,14 @@ bool map_rank_atoms(CUtensorMap* m, const void* p, int n, int R, int cols, int r
 }
 
 // CTAs per tile: the split of K (1, 2, 4 or 8 ways) that needs the fewest
-// rounds of the SMs per share of the work, at least four stages each.
+// rounds of the SMs per share of the work, at least four stages each; joining
+// more parts costs more.
 int split_of(long long tiles, int nk) {
   int best = 1;
   double cost = 1e30;
   for (int s = 1; s <= 8 && (s == 1 || nk / s >= 4); s *= 2) {
     const long long rounds = (tiles * s + device_sm_count() - 1) / device_sm_count();
-    const double c = (double)rounds / s + 0.02 * s;   // joining more parts costs more
+    const double c = (double)rounds / s * (s > 1 ? 1.1 : 1.0) + 0.02 * s;
     if (c < cost) {
       cost = c;
       best = s;
@@ -623,24 +1099,21 @@ int split_of(long long tiles, int nk) {
   return best;
 }
 
-template <int kNB, bool kShrink, bool kKMajor>
-cudaError_t launch_gemm(const Maps& maps, const Args& args, long long tiles, bool pdl,
-                        cudaStream_t s) {
-  using C = Cfg<kNB>;
-  auto kern = adapter_gemm_kernel<kNB, kShrink, kKMajor>;
-  cudaError_t err =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, int smem, bool pdl,
+                           cudaStream_t s, Args&&... args) {
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * args.split));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
-  if (args.split > 1) {
+  if (cluster > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = args.split;
+    attr[n].val.clusterDim.x = cluster;
     attr[n].val.clusterDim.y = 1;
     attr[n].val.clusterDim.z = 1;
     ++n;
@@ -652,66 +1125,93 @@ cudaError_t launch_gemm(const Maps& maps, const Args& args, long long tiles, boo
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, maps, args);
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-template <bool kShrink, bool kKMajor>
-cudaError_t launch_gemm_nb(int nb, const Maps& maps, const Args& args, long long tiles, bool pdl,
-                           cudaStream_t s) {
-  switch (nb) {
-    case 32: return launch_gemm<32, kShrink, kKMajor>(maps, args, tiles, pdl, s);
-    case 64: return launch_gemm<64, kShrink, kKMajor>(maps, args, tiles, pdl, s);
-    case 128: return launch_gemm<128, kShrink, kKMajor>(maps, args, tiles, pdl, s);
-    default: return launch_gemm<256, kShrink, kKMajor>(maps, args, tiles, pdl, s);
+template <int kNB>
+cudaError_t launch_shrink_nb(int split, const ShrinkMaps& m, const ShrinkArgs& a, int n_tt,
+                             cudaStream_t s) {
+  // units of 128 rank rows beyond the second round of the SMs are taken by
+  // the same clusters in turn: most blocks meet far fewer adapters than they could
+  const int most = a.zc / kM;
+  int gy = 2 * device_sm_count() / (n_tt * split);
+  gy = gy < 1 ? 1 : gy > most ? most : gy;
+  const dim3 grid(n_tt * split, gy);
+  constexpr int smem = ShrinkCfg<kNB>::kSmemBytes;
+  switch (split) {
+    case 1: return launch_cluster(adapter_shrink_kernel<kNB, 1>, grid, 1, smem, false, s, m, a);
+    case 2: return launch_cluster(adapter_shrink_kernel<kNB, 2>, grid, 2, smem, false, s, m, a);
+    case 4: return launch_cluster(adapter_shrink_kernel<kNB, 4>, grid, 4, smem, false, s, m, a);
+    default: return launch_cluster(adapter_shrink_kernel<kNB, 8>, grid, 8, smem, false, s, m, a);
   }
 }
 
 // Z of the rows v [T, D] and the adapters' matrices P [n, R, D].
 cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* P,
-                          int D, const float* scale, const int32_t* adapter_idx, int32_t* plan,
-                          __nv_bfloat16* Z, int* status, cudaStream_t s) {
-  const int nb = z.nb, rb = rank_box(z.R);
-  Maps m;
-  if (!map_rank_rows(&m.w, P, z.n, z.R, D, rb) || !map_rows(&m.x, v, z.T, D, nb))
+                          int D, const float* scale, const int32_t* adapter_idx, void* plan,
+                          __nv_bfloat16* Z, int* status, bool clear, cudaStream_t s) {
+  ShrinkMaps m;
+  const int rb = rank_box(z.R);
+  if (!map_rank_rows(&m.p, P, z.n, z.R, D, rb) || !map_rows(&m.v, v, z.T, D, z.nb))
     return cudaErrorInvalidValue;
-  m.ext = m.z = m.x;
-  Args a{z.T, D, z.n, z.R, rb, z.n_tt, 1, adapter_idx, scale, Z, z.zc, plan, status};
-  const long long tiles = (long long)z.n_tt * (z.zc / kM);
-  a.split = split_of(z.n_tt, D / kK);
-  return launch_gemm_nb<true, true>(nb, m, a, tiles, false, s);
+  const ShrinkArgs a{z.T, D, z.n, z.R, rb, z.zc, adapter_idx, scale, Z, plan, status, clear};
+  const int split = split_of(z.n_tt, D / kK);
+  switch (z.nb) {
+    case 32: return launch_shrink_nb<32>(split, m, a, z.n_tt, s);
+    case 64: return launch_shrink_nb<64>(split, m, a, z.n_tt, s);
+    case 128: return launch_shrink_nb<128>(split, m, a, z.n_tt, s);
+    default: return launch_shrink_nb<256>(split, m, a, z.n_tt, s);
+  }
+}
+
+template <int kNB, bool kKMajor>
+cudaError_t launch_split_nb(int split, const ExpandMaps& m, const ExpandArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)(a.n_tt * (a.M / kM) * split));
+  constexpr int smem = SplitCfg<kNB>::kSmemBytes;
+  switch (split) {
+    case 1:
+      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 1>, grid, 1, smem, true, s, m,
+                            a);
+    case 2:
+      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 2>, grid, 2, smem, true, s, m,
+                            a);
+    case 4:
+      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 4>, grid, 4, smem, true, s, m,
+                            a);
+    default:
+      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 8>, grid, 8, smem, true, s, m,
+                            a);
+  }
+}
+
+template <bool kKMajor>
+cudaError_t launch_expand_t(int nb, const ExpandMaps& m, const ExpandArgs& a, cudaStream_t s) {
+  const long long tiles = (long long)a.n_tt * (a.M / kM);
+  const int split = split_of(tiles, a.K / kK);
+  if (nb == FullCfg::kNB && split == 1 && tiles > device_sm_count())
+    return launch_cluster(adapter_expand_kernel<kKMajor>, dim3(device_sm_count()), 1,
+                          FullCfg::kSmemBytes, true, s, m, a);
+  switch (nb) {
+    case 32: return launch_split_nb<32, kKMajor>(split, m, a, s);
+    case 64: return launch_split_nb<64, kKMajor>(split, m, a, s);
+    case 128: return launch_split_nb<128, kKMajor>(split, m, a, s);
+    default: return launch_split_nb<256, kKMajor>(split, m, a, s);
+  }
 }
 
 // out [T, M] = v [T, K] W + Z P, with P [n, R, M]; W [K, M] or (k_major) [M, K].
 cudaError_t launch_expand(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* W,
                           bool k_major, const __nv_bfloat16* Z, const __nv_bfloat16* P, int K,
-                          int M, const int32_t* adapter_idx, __nv_bfloat16* out, int* status,
+                          int M, const void* plan, __nv_bfloat16* out, int* status,
                           cudaStream_t s) {
-  const int nb = z.nb, rb = rank_box(z.R);
-  Maps m;
+  ExpandMaps m;
+  const int rb = rank_box(z.R);
   if (!(k_major ? map_rows(&m.w, W, M, K, kM) : map_atoms(&m.w, W, K, M)) ||
-      !map_rows(&m.x, v, z.T, K, nb) || !map_rank_atoms(&m.ext, P, z.n, z.R, M, rb) ||
-      !map_rows(&m.z, Z, z.T, z.zc, nb))
+      !map_rows(&m.v, v, z.T, K, z.nb) || !map_rank_atoms(&m.p, P, z.n, z.R, M, rb) ||
+      !map_rows(&m.z, Z, z.T, z.zc, z.nb))
     return cudaErrorInvalidValue;
-  Args a{z.T, K, z.n, z.R, rb, z.n_tt, 1, adapter_idx, nullptr, out, M, nullptr, status};
-  const long long tiles = (long long)z.n_tt * (M / kM);
-  a.split = split_of(tiles, K / kK);
-  return k_major ? launch_gemm_nb<false, true>(nb, m, a, tiles, true, s)
-                 : launch_gemm_nb<false, false>(nb, m, a, tiles, true, s);
-}
-
-// G [n, R, D] = the adapters' sums of Z^T v.
-cudaError_t launch_wgrad(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* Z,
-                         int D, const int32_t* adapter_idx, const int32_t* plan, __nv_bfloat16* G,
-                         int* status, cudaStream_t s) {
-  WgradMaps m;
-  if (!map_atoms(&m.v, v, z.T, D) || !map_rows(&m.z, Z, z.T, z.zc, 64))
-    return cudaErrorInvalidValue;
-  const WgradArgs a{z.T, D, z.n, z.R, z.nb, z.n_tt, adapter_idx, plan, G, status};
-  cudaError_t err = cudaFuncSetAttribute(
-      adapter_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WgradCfg::kSmemBytes);
-  if (err != cudaSuccess) return err;
-  return launch_k(adapter_wgrad_kernel, dim3((unsigned)(z.n * (D / kM))), dim3(kThreads),
-                  WgradCfg::kSmemBytes, s, false, m, a);
+  const ExpandArgs a{z.T, K, M, z.n, z.R, rb, z.n_tt, out, plan, status};
+  return k_major ? launch_expand_t<true>(z.nb, m, a, s) : launch_expand_t<false>(z.nb, m, a, s);
 }
 
 }  // namespace
@@ -727,9 +1227,9 @@ AdapterSizes adapter_sizes(int T, int H, int N, int n, int R) {
   z.n_tt = (T + z.nb - 1) / z.nb;
   const int entries = n < z.nb ? n : z.nb;
   z.zc = (int)align_up((size_t)entries * R, kM);
-  size_t o = 256;   // the status word
+  size_t o = 1024;   // the status word
   z.plan = o;
-  o = align_up(o + (size_t)z.n_tt * kPlanInts * 4, 1024);
+  o += (size_t)z.n_tt * kAdapterPlanBytes;
   z.z = o;
   o = align_up(o + (size_t)T * z.zc * 2, 1024);
   z.total = o;
@@ -744,11 +1244,11 @@ cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x
                                    const int32_t* adapter_idx, __nv_bfloat16* y, void* ws,
                                    cudaStream_t s) {
   int* status = static_cast<int*>(ws);
+  void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, ws_ptr<int32_t>(ws, z.plan), Z,
-                                  status, s);
+  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true, s);
   if (err != cudaSuccess) return err;
-  return launch_expand(z, x, W, false, Z, B, z.H, z.N, adapter_idx, y, status, s);
+  return launch_expand(z, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
 }
 
 cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* dy,
@@ -758,17 +1258,23 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
                                     __nv_bfloat16* dx, __nv_bfloat16* dA, __nv_bfloat16* dB,
                                     void* ws, cudaStream_t s) {
   int* status = static_cast<int*>(ws);
-  int32_t* plan = ws_ptr<int32_t>(ws, z.plan);
+  void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
   __nv_bfloat16* dZ = ws_ptr<__nv_bfloat16>(ws, z.dz);
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, s);
+  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true, s);
   if (err == cudaSuccess)
-    err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, dZ, status, s);
-  if (err == cudaSuccess)
-    err = launch_expand(z, dy, W, true, dZ, A, z.N, z.H, adapter_idx, dx, status, s);
-  if (err == cudaSuccess) err = launch_wgrad(z, x, dZ, z.H, adapter_idx, plan, dA, status, s);
-  if (err == cudaSuccess) err = launch_wgrad(z, dy, Z, z.N, adapter_idx, plan, dB, status, s);
-  return err;
+    err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, dZ, status, false, s);
+  if (err == cudaSuccess) err = launch_expand(z, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
+  if (err != cudaSuccess) return err;
+  WgradMaps m;
+  if (!map_atoms(&m.v[0], x, z.T, z.H) || !map_rows(&m.z[0], dZ, z.T, z.zc, 64) ||
+      !map_atoms(&m.v[1], dy, z.T, z.N) || !map_rows(&m.z[1], Z, z.T, z.zc, 64))
+    return cudaErrorInvalidValue;
+  const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, adapter_idx, plan, {dA, dB}, status};
+  const dim3 grid((unsigned)(z.n * ((z.H + z.N) / kM)));
+  if (z.R > 64)
+    return launch_cluster(adapter_wgrad_kernel<2>, grid, 1, WgradCfg<2>::kSmemBytes, false, s, m, a);
+  return launch_cluster(adapter_wgrad_kernel<1>, grid, 1, WgradCfg<1>::kSmemBytes, false, s, m, a);
 }
 
 }  // namespace moe

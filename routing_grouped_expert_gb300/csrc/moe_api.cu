@@ -790,7 +790,6 @@ moe_status moe_adapter_project(const void* x, const void* W, const void* A, cons
   if (check_ws(ws, ws_bytes, z.total) != MOE_OK) return MOE_ERR_WORKSPACE;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MOE_TRY(cudaMemsetAsync(ws, 0, 2 * sizeof(int), s));
   using bf16 = __nv_bfloat16;
   return cuda_status(launch_adapter_project(
       z, static_cast<const bf16*>(x), static_cast<const bf16*>(W), static_cast<const bf16*>(A),
@@ -811,8 +810,8 @@ moe_status moe_adapter_project_backward(const void* dy, const void* x, const voi
   if (check_ws(ws, ws_bytes, z.total_backward) != MOE_OK) return MOE_ERR_WORKSPACE;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MOE_TRY(cudaMemsetAsync(ws, 0, 2 * sizeof(int), s));
   if (T == 0) {   // no token: zero gradients
+    MOE_TRY(cudaMemsetAsync(ws, 0, 2 * sizeof(int), s));
     MOE_TRY(cudaMemsetAsync(dA, 0, (size_t)n * R * H * 2, s));
     MOE_TRY(cudaMemsetAsync(dB, 0, (size_t)n * R * N * 2, s));
     return MOE_OK;

@@ -413,11 +413,12 @@ cudaError_t launch_plan_replicas(const int32_t* counts, int E, int G, int beta, 
 
 // The adapter projection (adapter.cu): sizes, token blocks and workspace
 // offsets.
+constexpr int kAdapterPlanBytes = 1024;
 struct AdapterSizes {
   int T, H, N, n, R;
   int nb, n_tt;       // tokens per block, blocks
   int zc;             // columns of Z: R for every adapter a block can meet, rounded up to 128
-  size_t plan;        // int32[n_tt][32]  the adapters of each block, as bits
+  size_t plan;        // [n_tt][kAdapterPlanBytes]  the adapters of each block
   size_t z, dz;       // bf16[T][zc]
   size_t total, total_backward;
 };

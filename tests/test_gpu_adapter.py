@@ -33,6 +33,9 @@ CASES = [  # T, H, N, n, R, order
     (777, 640, 256, 6, 48, "shuffled"),
     (1000, 256, 512, 5, 16, "segments"),
     (1300, 7168, 128, 4, 16, "segments"),
+    (2600, 256, 2048, 5, 24, "shuffled"),      # more tiles than SMs: persistent CTAs
+    (2563, 2048, 1920, 3, 16, "segments"),
+    (700, 128, 256, 200, 128, "distinct"),     # several units of rank rows per block
 ]
 
 
@@ -126,6 +129,42 @@ def test_bad_index_counts_as_none_and_is_reported():
     assert moe.moe_get_device_status(ws) == 0
     for a, b in zip(g, moe.moe_adapter_project_backward(dy.cuda(), **dev(d))):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,N", [(100, 256), (700, 256), (2600, 2048)])   # split, split, persistent
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_other_requests_do_not_see_nonfinite_values(T, N, value):
+    """A non-finite weight of one adapter, or value of one token, stays with the
+    requests it belongs to, forward and backward."""
+    d, dy = make((T, 256, N, 4, 16, "shuffled"))
+    idx = d["adapter_idx"]
+    clean = moe.moe_adapter_project(**dev(d))
+    grads = moe.moe_adapter_project_backward(dy.cuda(), **dev(d))
+    others = idx != 2
+    for key, status in (("A", 0), ("B", 2)):
+        bad = {**d, key: d[key].clone()}
+        bad[key][2, 5, 77] = value
+        ws = moe.Workspace()
+        y = moe.moe_adapter_project(**dev(bad), ws=ws)
+        assert moe.moe_get_device_status(ws) == status
+        assert torch.equal(y.cpu()[others], clean.cpu()[others])
+        dx, dA, dB = moe.moe_adapter_project_backward(dy.cuda(), **dev(bad), ws=ws)
+        assert torch.equal(dx.cpu()[others], grads[0].cpu()[others])
+        for a in (0, 1, 3):
+            assert torch.equal(dA[a], grads[1][a]) and torch.equal(dB[a], grads[2][a])
+    t = int((idx == 2).nonzero()[3, 0])
+    bad = {**d, "x": d["x"].clone()}
+    bad["x"][t, 9] = value
+    ws = moe.Workspace()
+    y = moe.moe_adapter_project(**dev(bad), ws=ws)
+    keep = torch.arange(T) != t
+    assert torch.equal(y.cpu()[keep], clean.cpu()[keep])
+    bad_dy = dy.clone()
+    bad_dy[t, 3] = value
+    dx, dA, dB = moe.moe_adapter_project_backward(bad_dy.cuda(), **dev(bad), ws=ws)
+    assert torch.equal(dx.cpu()[keep], grads[0].cpu()[keep])
+    for a in (0, 1, 3):
+        assert torch.equal(dA[a], grads[1][a]) and torch.equal(dB[a], grads[2][a])
 
 
 def test_tokens_do_not_depend_on_their_neighbours():
