@@ -37,8 +37,9 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;
 struct BlockPlan {
   int n_ent;                       // adapters the block meets
   int bad;                         // an adapter index was out of range
+  int pad[2];
   uint32_t bits[32];               // the same adapters as bits
-  uint16_t list[kMaxEntries];      // ascending
+  uint16_t list[kMaxEntries];      // ascending; 16-byte aligned
   uint8_t groups[kMaxEntries];     // per entry: its 64-token groups, as bits
 };
 static_assert(sizeof(BlockPlan) <= kAdapterPlanBytes, "plan pitch");
@@ -379,14 +380,22 @@ __device__ __forceinline__ void load_base(uint8_t* st, uint64_t* fb, const Expan
 // of rb rows, each [2 feature atoms][rb rows][128 bytes].
 template <int kNB>
 __device__ __forceinline__ void load_ext(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
-                                         const ExpandArgs& a, const BlockPlan* plan, int q_all,
-                                         int j, int mt, int row0, uint64_t pol_w, uint64_t pol_v) {
+                                         const ExpandArgs& a, const BlockPlan* plan, uint4 list,
+                                         int q_all, int j, int mt, int row0, uint64_t pol_w,
+                                         uint64_t pol_v) {
   mbar_arrive_expect_tx(fb, kABytes + kNB * kK * 2);
   tma_load_2d(st + kABytes, &maps.z, fb, j * kK, row0, pol_v);
   for (int q = 0; q < kK; q += a.rb) {
     const int qq = j * kK + q, e = qq / a.R;
-    // past the last entry: an adapter that does not exist, read as zeros
-    const int ad = qq < q_all ? (int)plan->list[e] : a.n;
+    // the first eight entries are in registers; past the last entry: an
+    // adapter that does not exist, read as zeros
+    int ad = a.n;
+    if (qq < q_all && e < 8) {
+      const uint32_t w = e < 4 ? (e < 2 ? list.x : list.y) : (e < 6 ? list.z : list.w);
+      ad = (int)((w >> (16 * (e & 1))) & 0xffffu);
+    } else if (qq < q_all) {
+      ad = (int)plan->list[e];
+    }
     tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, qq - e * a.R, mt * 2, ad, pol_w);
   }
 }
@@ -422,29 +431,26 @@ __device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, int rb, uint
 // zero, so an infinity or NaN there would reach the other requests' tokens as
 // 0 * inf.  It counts as zero instead and is reported.
 __device__ __forceinline__ bool clear_nonfinite(uint8_t* st, int lane) {
-  bool found = false;
+  // x * 0 + acc stays 0 for finite x and turns NaN for the others: two
+  // elements per instruction (one warp checks a stage in 0.2 us; comparing the
+  // exponents of every element took 1.75 us, longer than the stage's MMAs)
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll 8
   for (int i = lane; i < kABytes / 16; i += 32) {
-    uint4 v = reinterpret_cast<const uint4*>(st)[i];
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-    uint32_t hit = 0;
+    const uint4 v = reinterpret_cast<const uint4*>(st)[i];
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      // all exponent bits set, in either half
-      if ((w[c] & 0x7f80u) == 0x7f80u) hit |= 1u << (2 * c);
-      if ((w[c] & 0x7f800000u) == 0x7f800000u) hit |= 2u << (2 * c);
-    }
-    if (hit) {
-      found = true;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (hit & (1u << (2 * c))) w[c] &= 0xffff0000u;
-        if (hit & (2u << (2 * c))) w[c] &= 0x0000ffffu;
-      }
-      reinterpret_cast<uint4*>(st)[i] = v;
-    }
+    for (int c = 0; c < 4; ++c) acc[c] = __hfma2(p[c], zero, acc[c]);
   }
-  return found;
+  const __nv_bfloat162 any = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+  const bool found = __hisnan(any.x) || __hisnan(any.y);
+  if (!__any_sync(0xffffffffu, found)) return false;
+  for (int i = lane; i < kABytes / 2; i += 32) {
+    uint16_t* e = reinterpret_cast<uint16_t*>(st) + i;
+    if ((*e & 0x7f80u) == 0x7f80u) *e = 0;
+  }
+  return true;
 }
 
 // Few tiles: a cluster of kS CTAs per tile, each taking a share of the K
@@ -525,11 +531,12 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       pdl_wait();             // the plan and Z are complete
       fence_async_global();
       const int q_all = plan->n_ent * a.R;
+      const uint4 list = *reinterpret_cast<const uint4*>(plan->list);
       const int ne = (q_all + kK - 1) / kK;
       for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
         if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
-        load_ext<kNB>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan, q_all,
-                      j, mt, row0, pol_w, pol_v);
+        load_ext<kNB>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan, list,
+                      q_all, j, mt, row0, pol_w, pol_v);
         at.next();
         ext.next();
       }
@@ -695,6 +702,12 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       bool ok = true;
       for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
         const int tt = tile % a.n_tt, mt = tile / a.n_tt, row0 = tt * kNB;
+        const BlockPlan* plan = plan_of(a.plan, tt);
+        // from the second tile on the plan is known to be complete: its first
+        // words are on their way while the projection's stages are loaded
+        const bool later = tile != (int)blockIdx.x;
+        int n_ent = later ? plan->n_ent : 0;
+        uint4 list = later ? *reinterpret_cast<const uint4*>(plan->list) : make_uint4(0, 0, 0, 0);
         for (int kb = 0; kb < nk; ++kb) {
           if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
             break;
@@ -703,15 +716,18 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
           at.next();
           base.next();
         }
-        pdl_wait();             // the plan and Z are complete
-        fence_async_global();
-        const BlockPlan* plan = plan_of(a.plan, tt);
-        const int q_all = plan->n_ent * a.R;
+        if (!later) {
+          pdl_wait();             // the plan and Z are complete
+          fence_async_global();
+          n_ent = plan->n_ent;
+          list = *reinterpret_cast<const uint4*>(plan->list);
+        }
+        const int q_all = n_ent * a.R;
         for (int j = 0; ok && j * kK < q_all; ++j) {
           if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
             break;
           load_ext<kNB>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan,
-                        q_all, j, mt, row0, pol_w, pol_v);
+                        list, q_all, j, mt, row0, pol_w, pol_v);
           at.next();
           ext.next();
         }
@@ -736,6 +752,9 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
           break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf.stage * kNB);
+        const BlockPlan* plan = plan_of(a.plan, tile % a.n_tt);
+        const bool later = tile != (int)blockIdx.x;
+        int n_ent = later ? plan->n_ent : 0;   // early, as the producer's
         uint32_t acc = 0;
         for (int kb = 0; kb < nk; ++kb) {
           if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
@@ -745,8 +764,11 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
           at.next();
           base.next();
         }
-        pdl_wait();
-        const int q_all = plan_of(a.plan, tile % a.n_tt)->n_ent * a.R;
+        if (!later) {
+          pdl_wait();
+          n_ent = plan->n_ent;
+        }
+        const int q_all = n_ent * a.R;
         for (int j = 0; ok && j * kK < q_all; ++j) {
           if (!(ok = mbar_wait(&sh->ready[ext.stage], ext.phase, abort_flag, kWaitLimitNs)))
             break;
@@ -1099,6 +1121,12 @@ int split_of(long long tiles, int nk) {
   return best;
 }
 
+// CTAs of the expand launch of these sizes.
+long long expand_ctas(const AdapterSizes& z, int K, int M) {
+  const long long tiles = (long long)z.n_tt * (M / kM);
+  return tiles * split_of(tiles, K / kK);
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, int smem, bool pdl,
                            cudaStream_t s, Args&&... args) {
@@ -1149,13 +1177,20 @@ cudaError_t launch_shrink_nb(int split, const ShrinkMaps& m, const ShrinkArgs& a
 // Z of the rows v [T, D] and the adapters' matrices P [n, R, D].
 cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* P,
                           int D, const float* scale, const int32_t* adapter_idx, void* plan,
-                          __nv_bfloat16* Z, int* status, bool clear, cudaStream_t s) {
+                          __nv_bfloat16* Z, int* status, bool clear, long long beside,
+                          cudaStream_t s) {
   ShrinkMaps m;
   const int rb = rank_box(z.R);
   if (!map_rank_rows(&m.p, P, z.n, z.R, D, rb) || !map_rows(&m.v, v, z.T, D, z.nb))
     return cudaErrorInvalidValue;
   const ShrinkArgs a{z.T, D, z.n, z.R, rb, z.zc, adapter_idx, scale, Z, plan, status, clear};
-  const int split = split_of(z.n_tt, D / kK);
+  int split = split_of(z.n_tt, D / kK);
+  // Beside an expand launch of fewer CTAs than SMs, shrink keeps to the SMs it
+  // leaves: the expand's weights stream meanwhile, and a tile that had to wait
+  // for shrink's SMs came out last (decode: 8 of 128 tiles, 18 us late).
+  const long long units = (long long)z.n_tt * (z.zc / kM), sms = device_sm_count();
+  if (beside < sms)
+    while (split > 1 && units * split + beside > sms) split /= 2;
   switch (z.nb) {
     case 32: return launch_shrink_nb<32>(split, m, a, z.n_tt, s);
     case 64: return launch_shrink_nb<64>(split, m, a, z.n_tt, s);
@@ -1246,7 +1281,8 @@ cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x
   int* status = static_cast<int*>(ws);
   void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true, s);
+  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true,
+                                  expand_ctas(z, z.H, z.N), s);
   if (err != cudaSuccess) return err;
   return launch_expand(z, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
 }
@@ -1261,9 +1297,11 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
   __nv_bfloat16* dZ = ws_ptr<__nv_bfloat16>(ws, z.dz);
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true, s);
+  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true,
+                                  expand_ctas(z, z.N, z.H), s);
   if (err == cudaSuccess)
-    err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, dZ, status, false, s);
+    err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, dZ, status, false,
+                        expand_ctas(z, z.N, z.H), s);
   if (err == cudaSuccess) err = launch_expand(z, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
   if (err != cudaSuccess) return err;
   WgradMaps m;
