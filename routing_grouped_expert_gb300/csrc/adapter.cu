@@ -40,7 +40,6 @@ struct BlockPlan {
   int pad[2];
   uint32_t bits[32];               // the same adapters as bits
   uint16_t list[kMaxEntries];      // ascending; 16-byte aligned
-  uint8_t groups[kMaxEntries];     // per entry: its 64-token groups, as bits
 };
 static_assert(sizeof(BlockPlan) <= kAdapterPlanBytes, "plan pitch");
 
@@ -64,13 +63,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "memory");
   return v;
 }
-// The sum over the cluster's CTAs, in rank order, of the float4 at `addr` of
-// their shared memory; all loads in flight at once.
+// The sum over kS CTAs of the cluster, in rank order from `first`, of the float4
+// at `addr` of their shared memory; all loads in flight at once.
 template <int kS>
-__device__ __forceinline__ float4 cluster_sum(uint32_t addr) {
+__device__ __forceinline__ float4 cluster_sum(uint32_t addr, int first = 0) {
   float4 p[kS];
 #pragma unroll
-  for (int r = 0; r < kS; ++r) p[r] = ld_cluster_f4(mapa_shared(addr, (uint32_t)r));
+  for (int r = 0; r < kS; ++r) p[r] = ld_cluster_f4(mapa_shared(addr, (uint32_t)(first + r)));
 #pragma unroll
   for (int r = 1; r < kS; ++r) {
     p[0].x += p[r].x;
@@ -89,16 +88,16 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
   return r;
 }
 
-// The operand ring: `kStages` stages, the barriers of each, and the place of
-// one role in it.
-template <int kStages>
+// One role's place in a ring of n stages and their barriers.
 struct Place {
+  int n;
   int stage = 0;
   uint32_t phase = 0;
   int count = 0;   // stages passed
+  __device__ __forceinline__ explicit Place(int n_) : n(n_) {}
   __device__ __forceinline__ void next() {
     ++count;
-    if (++stage == kStages) {
+    if (++stage == n) {
       stage = 0;
       phase ^= 1u;
     }
@@ -106,21 +105,26 @@ struct Place {
 };
 // No TMA write may land after the CTA exits (or before its ring is reused by
 // ordinary stores): the last loads have arrived.
-template <int kStages>
-__device__ __forceinline__ void drain_loads(uint64_t* full, int from, int issued) {
-  for (int i = issued - from > kStages ? issued - kStages : from; i < issued; ++i)
-    mbar_wait(&full[i % kStages], (uint32_t)((i / kStages) & 1), nullptr, kWaitLimitNs);
+__device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int from, int issued) {
+  for (int i = issued - from > stages ? issued - stages : from; i < issued; ++i)
+    mbar_wait(&full[i % stages], (uint32_t)((i / stages) & 1), nullptr, kWaitLimitNs);
 }
 
 // ---------------------------------------------------------------- shrink
-// Z[t, e R + r] = scale_a * <x[t], A_a[r]> at the token's own entry e, 0 elsewhere.
-// A cluster of kS CTAs per (token block, every gridDim.y-th unit of 128 rank rows),
-// each taking a share of K.  Bound by reading x once and the rank rows; the
-// partial tiles meet in shared memory, where only the R values that a token
-// keeps are read.
+// Z[t, e R + r] = scale_a * <x[t], A_a[r]> at the token's own entry e, 0 elsewhere,
+// in units of 128 rank rows of a token block.  Bound by reading x and the rank
+// rows once, so K is split: the kC CTAs of a cluster work on kC / s units at a
+// time, s CTAs each taking a share of a unit's K, s chosen per block by how
+// many units it turns out to have.  The partial tiles meet in shared memory,
+// where only the R values that a token keeps are read.
+//
+// A block of several units whose entries have few tokens each (at most 64 per
+// unit) gathers a unit's own tokens (TMA tile::gather4, four rows at a time)
+// instead of multiplying every token of the block by every rank row.
 struct ShrinkMaps {
   CUtensorMap p;     // the adapters' rank rows [n, R, K], boxes of 64 K x rb rows
   CUtensorMap v;     // token rows [T, K], boxes of 64 K x kNB rows
+  CUtensorMap row;   // the same, boxes of one row (gathers)
 };
 struct ShrinkArgs {
   int T, K, n, R, rb, zc;   // rb: rank rows per box, a power of two that divides R
@@ -128,37 +132,60 @@ struct ShrinkArgs {
   const float* scale;
   __nv_bfloat16* z;         // [T, zc]
   void* plan;
+  uint32_t* masks;          // [n_tt][256][8]: the tokens of every entry, as bits; or null
   int* status;
   bool clear;               // the first kernel of the call: clear the status
 };
+constexpr int kGatherRows = 64;   // most tokens of a unit that gathers
 template <int kNB>
 struct ShrinkCfg {
   static constexpr int kStageBytes = kABytes + kNB * kK * 2;
   static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
   static constexpr int kRing = kStages * kStageBytes;
+  static constexpr bool kGather = kNB > kGatherRows;
+  static constexpr int kGatherBytes = kABytes + kGatherRows * kK * 2;
+  static constexpr int kGatherStages = kRing / kGatherBytes < 8 ? kRing / kGatherBytes : 8;
   static constexpr int kTmemCols = kNB < 32 ? 32 : kNB;
-  static constexpr int kSmemBytes = kRing + 1024 + 4096;
+  static constexpr int kSmemBytes = kRing + 1024 + 5120;
   static_assert(kNB * kM * 4 <= kRing, "the partial fp32 tile is staged in the ring");
 };
 struct ShrinkShared {
   uint64_t full[8], empty[8];
   uint64_t acc_full, drain;
   uint32_t tmem_base;
-  int abort, bad, n_ent;
+  int abort, bad, n_ent, most;
   unsigned bits[32];
   uint16_t list[kMaxEntries];
-  unsigned groups[kMaxEntries];
+  int count[kMaxEntries];       // tokens of each entry
   int idx[256];                 // adapter of each token of the block, -1 for none
+  uint16_t ent[256];            // its entry
+  uint16_t tok[kGatherRows];    // the tokens of a gathering unit
+  uint16_t pos[256];            // a token's place among them
+  int n_tok;
 };
-static_assert(sizeof(ShrinkShared) <= 4096, "shared block");
+static_assert(sizeof(ShrinkShared) <= 5120, "shared block");
+
+// Four rows (y0..y3) of 64 K each, stored as consecutive 128-byte rows at dst.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y0, int y1, int y2, int y3,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y0), "r"(y1),
+      "r"(y2), "r"(y3), "l"(policy)
+      : "memory");
+}
 
 // The adapters that token block tt meets, by the whole CTA.
+template <bool kCount>
 __device__ __forceinline__ void build_list(ShrinkShared* sh, const ShrinkArgs& a, int row0,
                                            int rows) {
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid < 32) sh->bits[tid] = 0u;
-  if (tid == 32) sh->bad = 0;
-  for (int i = tid; i < kMaxEntries; i += kThreads) sh->groups[i] = 0u;
+  if (tid == 32) sh->bad = sh->most = 0;
+  if (kCount)
+    for (int i = tid; i < kMaxEntries; i += kThreads) sh->count[i] = 0;
   __syncthreads();
   for (int i = tid; i < rows; i += kThreads) {
     int e = __ldg(a.adapter_idx + row0 + i);
@@ -180,36 +207,76 @@ __device__ __forceinline__ void build_list(ShrinkShared* sh, const ShrinkArgs& a
       if (lane >= off) incl += u;
     }
     int at = incl - c;
-    for (unsigned w = sh->bits[lane]; w; w &= w - 1) sh->list[at++] = (uint16_t)(lane * 32 + __ffs(w) - 1);
+    for (unsigned w = sh->bits[lane]; w; w &= w - 1)
+      sh->list[at++] = (uint16_t)(lane * 32 + __ffs(w) - 1);
     if (lane == 31) sh->n_ent = incl;
+  }
+  if (kCount) {
+    for (int i = tid; i < rows; i += kThreads) {
+      const int e = sh->idx[i];
+      int at = kMaxEntries;
+      if (e >= 0) {
+        at = __popc(sh->bits[e >> 5] & ((1u << (e & 31)) - 1u));
+        for (int w = 0; w < (e >> 5); ++w) at += __popc(sh->bits[w]);
+        atomicAdd(&sh->count[at], 1);
+      }
+      sh->ent[i] = (uint16_t)at;
+    }
   }
   __syncthreads();
 }
-// ... and the plan of it, for the kernels that follow (one CTA of the block).
-__device__ __forceinline__ void write_plan(ShrinkShared* sh, const ShrinkArgs& a, int tt,
-                                           int rows) {
+// ... and the plan of it, for the kernels that follow (one CTA of the block;
+// `scratch`: 8 KB that nothing uses yet).
+__device__ __forceinline__ void write_plan(ShrinkShared* sh, const ShrinkArgs& a, int tt, int rows,
+                                           uint32_t* scratch) {
   const int tid = threadIdx.x;
   BlockPlan* p = const_cast<BlockPlan*>(plan_of(a.plan, tt));
-  for (int i = tid; i < rows; i += kThreads) {
-    const int e = sh->idx[i];
-    if (e < 0) continue;
-    int at = __popc(sh->bits[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int w = 0; w < (e >> 5); ++w) at += __popc(sh->bits[w]);
-    atomicOr(&sh->groups[at], 1u << (i / 64));
-  }
-  __syncthreads();
   if (tid < 32) p->bits[tid] = sh->bits[tid];
   if (tid == 32) {
     p->n_ent = sh->n_ent;
     p->bad = sh->bad;
   }
-  for (int i = tid; i < sh->n_ent; i += kThreads) {
-    p->list[i] = sh->list[i];
-    p->groups[i] = (uint8_t)sh->groups[i];
+  for (int i = tid; i < sh->n_ent; i += kThreads) p->list[i] = sh->list[i];
+  if (a.masks == nullptr) return;
+  const int n = sh->n_ent * 8;
+  for (int i = tid; i < n; i += kThreads) scratch[i] = 0u;
+  __syncthreads();
+  for (int i = tid; i < rows; i += kThreads) {
+    const int e = sh->idx[i];
+    if (e < 0) continue;
+    int at = __popc(sh->bits[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int w = 0; w < (e >> 5); ++w) at += __popc(sh->bits[w]);
+    atomicOr(&scratch[at * 8 + (i >> 5)], 1u << (i & 31));
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) a.masks[(size_t)tt * kMaxEntries * 8 + i] = scratch[i];
+  fence_async_smem();   // the scratch is ring space: TMA loads follow
+  __syncthreads();
+}
+
+// This CTA's tokens of a finished unit: Z rows of 128 columns, a warp per token.
+template <int kS>
+__device__ __forceinline__ void store_unit(const ShrinkShared* sh, const ShrinkArgs& a,
+                                           const uint8_t* smem, int row0, int rows, int u,
+                                           int q_end, bool gather, int first, int r) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // this lane's four rank rows belong to one entry (R is a multiple of 8)
+  const int ad = 4 * lane < q_end ? (int)sh->list[(u * kM + 4 * lane) / a.R] : -2;
+  const float f = ad >= 0 ? __ldg(a.scale + ad) : 0.f;
+  const uint32_t mine = smem_u32(smem) + (uint32_t)lane * 16;
+#pragma unroll 2
+  for (int t = r * (kThreads / 32) + warp; t < rows; t += kS * (kThreads / 32)) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (sh->idx[t] == ad) {
+      const int j = gather ? (int)sh->pos[t] : t;
+      s = cluster_sum<kS>(mine + (uint32_t)j * (kM * 4), first);
+      s = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+    }
+    *reinterpret_cast<uint2*>(a.z + (size_t)(row0 + t) * a.zc + u * kM + 4 * lane) = pack4(s);
   }
 }
 
-template <int kNB, int kS>
+template <int kNB, int kC>
 __global__ void __launch_bounds__(kThreads, 1)
 adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs a) {
   using C = ShrinkCfg<kNB>;
@@ -218,25 +285,44 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   ShrinkShared* sh = reinterpret_cast<ShrinkShared*>(smem + C::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kS > 1 ? (int)cluster_ctarank() : 0;
-  const int tt = (int)blockIdx.x / kS;
+  const int rank = kC > 1 ? (int)cluster_ctarank() : 0;
+  const int tt = (int)blockIdx.x / kC;
   const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
   const int nk = a.K / kK;
-  const int kb0 = nk * rank / kS, kb1 = nk * (rank + 1) / kS;
 
   pdl_trigger();
   // the call's status starts clean: this is its first kernel, and nothing is
   // reported before a later kernel of the call or a wait of a second
   if (a.clear && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
-  build_list(sh, a, row0, rows);
-  if (rank == 0 && blockIdx.y == 0) write_plan(sh, a, tt, rows);
+  build_list<C::kGather>(sh, a, row0, rows);
+  if (rank == 0 && blockIdx.y == 0) write_plan(sh, a, tt, rows, reinterpret_cast<uint32_t*>(smem));
   const int q_all = sh->n_ent * a.R;
-  if ((int)blockIdx.y * kM >= q_all) return;   // the same for the whole cluster
+  const int units = (q_all + kM - 1) / kM;
+  // s CTAs per unit: as many as leave a group of CTAs for every unit
+  int s = kC;
+  while (s > 1 && units * s > (int)gridDim.y * kC) s >>= 1;
+  const int groups = kC / s, sub = rank / s, r = rank - sub * s;
+  const int u_step = (int)gridDim.y * groups, u_first = (int)blockIdx.y * groups;
+  if (u_first >= units) return;   // the same for the whole cluster
+  const int kb0 = nk * r / s, kb1 = nk * (r + 1) / s;
+  bool gather = false;
+  if constexpr (C::kGather) {
+    if (units > 1) {
+      // the largest number of tokens that one unit's entries have
+      for (int u = threadIdx.x; u < units; u += kThreads) {
+        int c = 0;
+        for (int e = u * kM / a.R; e < sh->n_ent && e * a.R < (u + 1) * kM; ++e) c += sh->count[e];
+        atomicMax(&sh->most, c);
+      }
+      __syncthreads();
+      gather = sh->most <= kGatherRows;
+    }
+  }
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
     }
     mbar_init(&sh->acc_full, 1);
     mbar_init(&sh->drain, 1);
@@ -252,45 +338,86 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
-  Place<C::kStages> at;
+  const int stage_bytes = gather ? C::kGatherBytes : C::kStageBytes;
+  const int stages = gather ? C::kGatherStages : C::kStages;
+  Place at(stages);
   uint32_t parity = 0;
-  for (int u = blockIdx.y; u * kM < q_all; u += gridDim.y, parity ^= 1u) {
+  for (int u0 = u_first; u0 < units; u0 += u_step) {
+    const int u = u0 + sub;
+    const bool have = u < units;   // the groups of a cluster go through the loop together
     const int q_end = min(kM, q_all - u * kM);
-    if (warp == 0 && lane == 0) {
+    if (C::kGather && gather) {
+      if (have && warp == 2) {
+        const int e0 = u * kM / a.R, e1 = (u * kM + q_end - 1) / a.R;
+        int n = 0;
+        for (int t0 = 0; t0 < rows; t0 += 32) {
+          const int t = t0 + lane, e = t < rows ? (int)sh->ent[t] : kMaxEntries;
+          const bool in = e >= e0 && e <= e1;
+          const unsigned m = __ballot_sync(0xffffffffu, in);
+          if (in) {
+            const int j = n + __popc(m & ((1u << lane) - 1u));
+            sh->tok[j] = (uint16_t)t;
+            sh->pos[t] = (uint16_t)j;
+          }
+          n += __popc(m);
+        }
+        if (lane == 0) sh->n_tok = n;
+      }
+      __syncthreads();
+    }
+    const int n_tok = gather && have ? sh->n_tok : rows;   // rows of the partial tile
+    const int n_mma = gather ? (n_tok + 15) & ~15 : kNB;
+    if (have && warp == 0) {
       const uint64_t pol_p = policy_evict_normal(), pol_v = policy_evict_last();
       const int from = at.count;
+      const uint32_t bytes = (uint32_t)((q_end + n_mma) * kK * 2);
+      // this lane's box of rank rows (rows past the last entry keep what the
+      // stage held: their products are not read) and its four token rows
+      const int q = lane * a.rb, e = (u * kM + q) / a.R;
+      const bool box = q < q_end;
+      const int p_row = u * kM + q - e * a.R, p_ad = box ? (int)sh->list[e] : 0;
+      int y[4];
+      const bool rows4 = gather && 4 * lane < n_mma;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y[i] = rows4 ? row0 + (int)sh->tok[min(4 * lane + i, n_tok - 1)] : 0;
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
-        uint8_t* sA = smem + at.stage * C::kStageBytes;
         uint64_t* fb = &sh->full[at.stage];
-        // rank rows past the last entry keep what the stage held: their
-        // products are not read
-        mbar_arrive_expect_tx(fb, (uint32_t)((q_end + kNB) * kK * 2));
-        tma_load_2d(sA + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
-        for (int q = 0; q < q_end; q += a.rb) {
-          const int qq = u * kM + q, e = qq / a.R;
-          tma_load_3d(sA + q * (kK * 2), &maps.p, fb, kb * kK, qq - e * a.R, sh->list[e], pol_p);
+        if (lane == 0) {
+          ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
+          if (ok) mbar_arrive_expect_tx(fb, bytes);
         }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (!ok) break;
+        uint8_t* st = smem + at.stage * stage_bytes;
+        if (rows4)
+          tma_gather4(st + kABytes + lane * 4 * (kK * 2), &maps.row, fb, kb * kK, y[0], y[1], y[2],
+                      y[3], pol_v);
+        else if (!gather && lane == 0)
+          tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
+        if (box) tma_load_3d(st + q * (kK * 2), &maps.p, fb, kb * kK, p_row, p_ad, pol_p);
         at.next();
       }
-      if (!ok) {
-        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
-        *abort_flag = 1;
+      if (lane == 0) {
+        if (!ok) {
+          set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
+          *abort_flag = 1;
+        }
+        drain_loads(sh->full, stages, from, at.count);
       }
-      drain_loads<C::kStages>(sh->full, from, at.count);
-    } else if (warp == 1 && lane == 0) {
+    } else if (have && warp == 1 && lane == 0) {
       const uint32_t sbase = smem_u32(smem);
-      constexpr uint32_t kIdesc = idesc_bf16(kM, kNB, false, false);
+      const uint32_t idesc = idesc_bf16(kM, n_mma, false, false);
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = mbar_wait(&sh->full[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
-        const uint32_t a0 = sbase + (uint32_t)(at.stage * C::kStageBytes), b0 = a0 + kABytes;
+        const uint32_t a0 = sbase + (uint32_t)(at.stage * stage_bytes), b0 = a0 + kABytes;
 #pragma unroll
         for (int kk = 0; kk < kK / 16; ++kk)
           mma_bf16_ss(tmem, sdesc_sw128(a0 + kk * 32, 16, 1024), sdesc_sw128(b0 + kk * 32, 16, 1024),
-                      kIdesc, (kb > kb0 || kk) ? 1u : 0u);
+                      idesc, (kb > kb0 || kk) ? 1u : 0u);
         mma_commit(&sh->empty[at.stage]);
         at.next();
       }
@@ -304,12 +431,12 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
     const int q = warp & 3;   // TMEM lanes 32 q ..
-    if (warp >= 3) {
+    if (have && warp >= 3) {
       const bool got = mbar_wait(&sh->acc_full, parity, abort_flag, kWaitLimitNs);
       tc_fence_after();
       if (__all_sync(0xffffffffu, got) && q * 32 < q_end) {
         float* st = reinterpret_cast<float*>(smem);
-        for (int c0 = 0; c0 < rows; c0 += 16) {
+        for (int c0 = 0; c0 < n_tok; c0 += 16) {
           uint32_t v[16];
           tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
           tmem_ld_wait();
@@ -321,31 +448,26 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
     }
     // every partial tile of the cluster is in shared memory
     __syncwarp();
-    if constexpr (kS > 1) cluster_sync(); else __syncthreads();
-    if (!*abort_flag) {
-      // this lane's four rank rows belong to one entry (R is a multiple of 8)
-      const int e = (u * kM + 4 * lane) / a.R;
-      const int ad = 4 * lane < q_end ? (int)sh->list[e] : -2;
-      const float f = ad >= 0 ? __ldg(a.scale + ad) : 0.f;
-      const uint32_t mine = smem_u32(smem) + (uint32_t)lane * 16;
-      constexpr int kStep = kS * (kThreads / 32);
-#pragma unroll 2
-      for (int t = rank * (kThreads / 32) + warp; t < rows; t += kStep) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (sh->idx[t] == ad) {
-          s = cluster_sum<kS>(mine + (uint32_t)t * (kM * 4));
-          s = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
-        }
-        *reinterpret_cast<uint2*>(a.z + (size_t)(row0 + t) * a.zc + u * kM + 4 * lane) = pack4(s);
-      }
+    if constexpr (kC > 1) cluster_sync(); else __syncthreads();
+    if (have && !*abort_flag) {
+      const int first = sub * s;
+      if (kC == 1 || s == 1)
+        store_unit<1>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
+      else if (kC == 2 || s == 2)
+        store_unit<2>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
+      else if (kC == 4 || s == 4)
+        store_unit<4>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
+      else
+        store_unit<8>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
     }
     // no CTA loads the next unit (by TMA, over a tile that ordinary stores
     // wrote), or leaves, while another reads its tile; after a wait that ran out
     // the CTAs still go through their units together
     fence_async_smem();
     __syncwarp();
-    if constexpr (kS > 1) cluster_sync(); else __syncthreads();
+    if constexpr (kC > 1) cluster_sync(); else __syncthreads();
     tc_fence_after();
+    if (have) parity ^= 1u;
   }
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
@@ -519,7 +641,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       // a weight tile read by one block is streamed past L2
       const uint64_t pol_w = a.n_tt == 1 ? policy_evict_first() : policy_evict_normal();
       const uint64_t pol_v = policy_evict_last();
-      Place<C::kStages> at, base, ext;
+      Place at(C::kStages), base(C::kStages), ext(C::kStages);
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
@@ -545,13 +667,13 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
         *abort_flag = 1;
       }
       if (mt == 0 && rank == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
-      drain_loads<C::kStages>(sh->full, 0, base.count);
-      drain_loads<C::kStages>(sh->loaded, 0, ext.count);
+      drain_loads(sh->full, C::kStages, 0, base.count);
+      drain_loads(sh->loaded, C::kStages, 0, ext.count);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t sbase = smem_u32(smem);
-      Place<C::kStages> at, base, ext;
+      Place at(C::kStages), base(C::kStages), ext(C::kStages);
       uint32_t acc = 0;
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -582,7 +704,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
   } else if (warp == 2) {
-    Place<C::kStages> at, ext;
+    Place at(C::kStages), ext(C::kStages);
     for (int kb = kb0; kb < kb1; ++kb) at.next();
     pdl_wait();
     const int ne = (plan->n_ent * a.R + kK - 1) / kK;
@@ -698,7 +820,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
-      Place<C::kStages> at, base, ext;
+      Place at(C::kStages), base(C::kStages), ext(C::kStages);
       bool ok = true;
       for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
         const int tt = tile % a.n_tt, mt = tile / a.n_tt, row0 = tt * kNB;
@@ -738,14 +860,14 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         *abort_flag = 1;
       }
       pdl_wait();
-      drain_loads<C::kStages>(sh->full, 0, base.count);
-      drain_loads<C::kStages>(sh->loaded, 0, ext.count);
+      drain_loads(sh->full, C::kStages, 0, base.count);
+      drain_loads(sh->loaded, C::kStages, 0, ext.count);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t sbase = smem_u32(smem);
-      Place<C::kStages> at, base, ext;
-      Place<2> buf;
+      Place at(C::kStages), base(C::kStages), ext(C::kStages);
+      Place buf(2);
       bool ok = true;
       for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
         if (!(ok = mbar_wait(&sh->acc_empty[buf.stage], buf.phase ^ 1u, abort_flag, kWaitLimitNs)))
@@ -791,7 +913,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
   } else if (warp == 2) {
-    Place<C::kStages> at, ext;
+    Place at(C::kStages), ext(C::kStages);
     bool ok = true, found = false;
     for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       for (int kb = 0; kb < nk; ++kb) at.next();
@@ -813,7 +935,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
     const int q = warp & 3;
     __nv_bfloat16* stg =
         reinterpret_cast<__nv_bfloat16*>(smem + C::kRing + 1024 + (warp - 3) * C::kStgBytes);
-    Place<2> buf;
+    Place buf(2);
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const int tt = tile % a.n_tt, mt = tile / a.n_tt;
       const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
@@ -867,8 +989,8 @@ struct WgradMaps {
 struct WgradArgs {
   int T, n, R, nb, n_tt;       // nb: tokens per block of the plan
   int D[2];
-  const int32_t* adapter_idx;
   const void* plan;
+  const uint32_t* masks;       // [n_tt][256][8]: the tokens of every entry, as bits
   __nv_bfloat16* out[2];       // [n, R, D]
   int* status;
 };
@@ -887,7 +1009,7 @@ struct WgradShared {
   uint32_t tmem_base;
   int abort;
   volatile int stages;         // K stages in all, once the producer has issued them
-  volatile int t0[4];          // first token of the group in each stage
+  volatile uint32_t mask[4][2];   // the adapter's own tokens among the 64 of each stage
 };
 
 template <int kCols>
@@ -928,34 +1050,43 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   volatile int* abort_flag = &sh->abort;
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
-    Place<C::kStages> at;
+    Place at(C::kStages);
     bool ok = true;
     for (int tb = 0; ok && tb < a.n_tt; tb += 32) {
-      // lane: block tb + lane, ad's entry in it and the groups that hold it
+      // lane: block tb + lane, ad's entry in it and its tokens there
       int e = 0;
-      unsigned g = 0;
+      uint4 m0 = make_uint4(0, 0, 0, 0), m1 = m0;
       if (tb + lane < a.n_tt) {
         const BlockPlan* p = plan_of(a.plan, tb + lane);
         const unsigned w = p->bits[ad >> 5];
         if ((w >> (ad & 31)) & 1u) {
           e = __popc(w & ((1u << (ad & 31)) - 1u));
           for (int i = 0; i < (ad >> 5); ++i) e += __popc(p->bits[i]);
-          g = p->groups[e];
+          const uint4* m =
+              reinterpret_cast<const uint4*>(a.masks + ((size_t)(tb + lane) * kMaxEntries + e) * 8);
+          m0 = m[0];
+          m1 = m[1];
         }
       }
-      for (unsigned have = __ballot_sync(0xffffffffu, g != 0u); ok && have; have &= have - 1) {
+      const uint32_t lo[4] = {m0.x, m0.z, m1.x, m1.z}, hi[4] = {m0.y, m0.w, m1.y, m1.w};
+      const bool any = (m0.x | m0.y | m0.z | m0.w | m1.x | m1.y | m1.z | m1.w) != 0u;
+      for (unsigned have = __ballot_sync(0xffffffffu, any); ok && have; have &= have - 1) {
         const int src = __ffs(have) - 1;
         const int eb = __shfl_sync(0xffffffffu, e, src);
-        unsigned gb = __shfl_sync(0xffffffffu, g, src);
-        for (; ok && gb; gb &= gb - 1) {
-          const int t0 = (tb + src) * a.nb + (__ffs(gb) - 1) * kK;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t ml = __shfl_sync(0xffffffffu, lo[g], src);
+          const uint32_t mh = __shfl_sync(0xffffffffu, hi[g], src);
+          if (!ok || (ml | mh) == 0u) continue;   // no token of ad in this group
+          const int t0 = (tb + src) * a.nb + g * kK;
           int got = 1;
           if (lane == 0) {
             got = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
             if (got) {
               uint8_t* st = smem + at.stage * C::kStageBytes;
               uint64_t* fb = &sh->full[at.stage];
-              sh->t0[at.stage] = t0;
+              sh->mask[at.stage][0] = ml;
+              sh->mask[at.stage][1] = mh;
               mbar_arrive_expect_tx(fb, C::kStageBytes);
               tma_load_3d(st, &maps.v[which], fb, 0, t0, d0 >> 6, pol);
 #pragma unroll
@@ -982,13 +1113,13 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         *abort_flag = 1;
       }
-      drain_loads<C::kStages>(sh->full, from, at.count);
+      drain_loads(sh->full, C::kStages, from, at.count);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t sbase = smem_u32(smem);
       const uint32_t idesc = idesc_bf16(kM, N, true, true);
-      Place<C::kStages> at;
+      Place at(C::kStages);
       bool ok = true;
       while (true) {
         if (!(ok = mbar_wait(&sh->ready[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
@@ -1014,7 +1145,7 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   } else if (warp == 2) {
     // Rows of V of other requests' tokens meet a zero of Z, which does not
     // stop an infinity or NaN in them: they are cleared.
-    Place<C::kStages> at;
+    Place at(C::kStages);
     while (true) {
       const bool got = mbar_wait(&sh->full[at.stage], at.phase, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) break;
@@ -1022,19 +1153,19 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
         if (lane == 0) mbar_arrive(&sh->ready[at.stage]);
         break;
       }
-      const int t0 = sh->t0[at.stage];
       uint8_t* st = smem + at.stage * C::kStageBytes;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int t = t0 + 32 * h + lane;
-        const bool other = t < a.T && __ldg(a.adapter_idx + t) != ad;
-        unsigned m = __ballot_sync(0xffffffffu, other);
-        for (; m; m &= m - 1) {
-          // row r: 128 bytes in each of the two feature atoms
-          const int r = 32 * h + __ffs(m) - 1;
-          if (lane < 16)
-            *reinterpret_cast<uint4*>(st + (lane >> 3) * 8192 + r * 128 + (lane & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+        // two rows at a time: row r is 128 bytes in each of the two feature
+        // atoms, a half warp's 16 vectors
+        for (unsigned m = ~sh->mask[at.stage][h]; m;) {
+          const int r0 = __ffs(m) - 1;
+          m &= m - 1;
+          const int r1 = m ? __ffs(m) - 1 : r0;
+          m &= m - 1;
+          const int r = 32 * h + (lane < 16 ? r0 : r1), v = lane & 15;
+          *reinterpret_cast<uint4*>(st + (v >> 3) * 8192 + r * 128 + (v & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
         }
       }
       fence_async_smem();
@@ -1157,16 +1288,11 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, int s
 }
 
 template <int kNB>
-cudaError_t launch_shrink_nb(int split, const ShrinkMaps& m, const ShrinkArgs& a, int n_tt,
-                             cudaStream_t s) {
-  // units of 128 rank rows beyond the second round of the SMs are taken by
-  // the same clusters in turn: most blocks meet far fewer adapters than they could
-  const int most = a.zc / kM;
-  int gy = 2 * device_sm_count() / (n_tt * split);
-  gy = gy < 1 ? 1 : gy > most ? most : gy;
-  const dim3 grid(n_tt * split, gy);
+cudaError_t launch_shrink_nb(int cluster, int gy, const ShrinkMaps& m, const ShrinkArgs& a,
+                             int n_tt, cudaStream_t s) {
+  const dim3 grid(n_tt * cluster, gy);
   constexpr int smem = ShrinkCfg<kNB>::kSmemBytes;
-  switch (split) {
+  switch (cluster) {
     case 1: return launch_cluster(adapter_shrink_kernel<kNB, 1>, grid, 1, smem, false, s, m, a);
     case 2: return launch_cluster(adapter_shrink_kernel<kNB, 2>, grid, 2, smem, false, s, m, a);
     case 4: return launch_cluster(adapter_shrink_kernel<kNB, 4>, grid, 4, smem, false, s, m, a);
@@ -1174,28 +1300,36 @@ cudaError_t launch_shrink_nb(int split, const ShrinkMaps& m, const ShrinkArgs& a
   }
 }
 
-// Z of the rows v [T, D] and the adapters' matrices P [n, R, D].
+// Z of the rows v [T, D] and the adapters' matrices P [n, R, D].  `clear`: the
+// first launch of a call; `ctas`: the expand launch that follows has so many.
 cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* P,
                           int D, const float* scale, const int32_t* adapter_idx, void* plan,
-                          __nv_bfloat16* Z, int* status, bool clear, long long beside,
-                          cudaStream_t s) {
+                          uint32_t* masks, __nv_bfloat16* Z, int* status, bool clear,
+                          long long ctas, cudaStream_t s) {
   ShrinkMaps m;
   const int rb = rank_box(z.R);
-  if (!map_rank_rows(&m.p, P, z.n, z.R, D, rb) || !map_rows(&m.v, v, z.T, D, z.nb))
+  if (!map_rank_rows(&m.p, P, z.n, z.R, D, rb) || !map_rows(&m.v, v, z.T, D, z.nb) ||
+      !map_rows(&m.row, v, z.T, D, 1))
     return cudaErrorInvalidValue;
-  const ShrinkArgs a{z.T, D, z.n, z.R, rb, z.zc, adapter_idx, scale, Z, plan, status, clear};
-  int split = split_of(z.n_tt, D / kK);
-  // Beside an expand launch of fewer CTAs than SMs, shrink keeps to the SMs it
-  // leaves: the expand's weights stream meanwhile, and a tile that had to wait
-  // for shrink's SMs came out last (decode: 8 of 128 tiles, 18 us late).
-  const long long units = (long long)z.n_tt * (z.zc / kM), sms = device_sm_count();
-  if (beside < sms)
-    while (split > 1 && units * split + beside > sms) split /= 2;
+  const ShrinkArgs a{z.T, D, z.n, z.R, rb, z.zc, adapter_idx, scale, Z, plan, masks, status, clear};
+  // as many clusters per block as the SMs take in one round and the block can
+  // have units for; the CTAs share them out once they know its adapters
+  int sms = device_sm_count();
+  // One block beside an expand launch of fewer CTAs than SMs (a decode batch):
+  // shrink keeps to the SMs that are left, since the expand's weights stream
+  // meanwhile and a tile that waited for shrink's SMs came out last (8 of 128
+  // tiles, 18 us late).
+  if (z.n_tt == 1 && ctas < sms && sms - ctas >= 8) sms -= (int)ctas;
+  int cluster = 8;
+  while (cluster > 1 && (z.n_tt * cluster > sms || D / kK / cluster < 4)) cluster /= 2;
+  const int most = (z.zc / kM * 8 + cluster - 1) / cluster;   // up to eight CTAs per unit
+  int gy = sms / (z.n_tt * cluster);
+  gy = gy < 1 ? 1 : gy > most ? most : gy;
   switch (z.nb) {
-    case 32: return launch_shrink_nb<32>(split, m, a, z.n_tt, s);
-    case 64: return launch_shrink_nb<64>(split, m, a, z.n_tt, s);
-    case 128: return launch_shrink_nb<128>(split, m, a, z.n_tt, s);
-    default: return launch_shrink_nb<256>(split, m, a, z.n_tt, s);
+    case 32: return launch_shrink_nb<32>(cluster, gy, m, a, z.n_tt, s);
+    case 64: return launch_shrink_nb<64>(cluster, gy, m, a, z.n_tt, s);
+    case 128: return launch_shrink_nb<128>(cluster, gy, m, a, z.n_tt, s);
+    default: return launch_shrink_nb<256>(cluster, gy, m, a, z.n_tt, s);
   }
 }
 
@@ -1269,7 +1403,9 @@ AdapterSizes adapter_sizes(int T, int H, int N, int n, int R) {
   o = align_up(o + (size_t)T * z.zc * 2, 1024);
   z.total = o;
   z.dz = o;
-  z.total_backward = align_up(o + (size_t)T * z.zc * 2, 1024);
+  o = align_up(o + (size_t)T * z.zc * 2, 1024);
+  z.masks = o;
+  z.total_backward = align_up(o + (size_t)z.n_tt * kMaxEntries * 8 * 4, 1024);
   return z;
 }
 
@@ -1281,8 +1417,8 @@ cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x
   int* status = static_cast<int*>(ws);
   void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true,
-                                  expand_ctas(z, z.H, z.N), s);
+  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, nullptr, Z, status,
+                                  true, expand_ctas(z, z.H, z.N), s);
   if (err != cudaSuccess) return err;
   return launch_expand(z, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
 }
@@ -1297,10 +1433,12 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
   __nv_bfloat16* dZ = ws_ptr<__nv_bfloat16>(ws, z.dz);
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, Z, status, true,
-                                  expand_ctas(z, z.N, z.H), s);
+  uint32_t* masks = ws_ptr<uint32_t>(ws, z.masks);
+  const int sms = device_sm_count();
+  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, masks, Z, status,
+                                  true, sms, s);
   if (err == cudaSuccess)
-    err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, dZ, status, false,
+    err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, nullptr, dZ, status, false,
                         expand_ctas(z, z.N, z.H), s);
   if (err == cudaSuccess) err = launch_expand(z, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
   if (err != cudaSuccess) return err;
@@ -1308,7 +1446,7 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   if (!map_atoms(&m.v[0], x, z.T, z.H) || !map_rows(&m.z[0], dZ, z.T, z.zc, 64) ||
       !map_atoms(&m.v[1], dy, z.T, z.N) || !map_rows(&m.z[1], Z, z.T, z.zc, 64))
     return cudaErrorInvalidValue;
-  const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, adapter_idx, plan, {dA, dB}, status};
+  const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, plan, masks, {dA, dB}, status};
   const dim3 grid((unsigned)(z.n * ((z.H + z.N) / kM)));
   if (z.R > 64)
     return launch_cluster(adapter_wgrad_kernel<2>, grid, 1, WgradCfg<2>::kSmemBytes, false, s, m, a);

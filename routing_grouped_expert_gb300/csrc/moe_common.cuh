@@ -420,6 +420,7 @@ struct AdapterSizes {
   int zc;             // columns of Z: R for every adapter a block can meet, rounded up to 128
   size_t plan;        // [n_tt][kAdapterPlanBytes]  the adapters of each block
   size_t z, dz;       // bf16[T][zc]
+  size_t masks;       // uint32[n_tt][256][8]  the tokens of each block's adapters, as bits
   size_t total, total_backward;
 };
 AdapterSizes adapter_sizes(int T, int H, int N, int n, int R);
