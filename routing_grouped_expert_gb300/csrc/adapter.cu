@@ -119,24 +119,31 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int from
 // where only the R values that a token keeps are read.
 //
 // A block of several units whose entries have few tokens each (at most 64 per
-// unit) gathers a unit's own tokens (TMA tile::gather4, four rows at a time)
-// instead of multiplying every token of the block by every rank row.
+// unit) gathers a unit's own tokens instead of multiplying every token of the
+// block by every rank row: five warps copy the rows' 128 bytes of each stage
+// by 16-byte asynchronous copies into the swizzled operand.  (TMA
+// tile::gather4 took about 16 ns a row: 777 tokens of 24 adapters of rank 64
+// spent 31 us on the gathers.)
 struct ShrinkMaps {
   CUtensorMap p;     // the adapters' rank rows [n, R, K], boxes of 64 K x rb rows
   CUtensorMap v;     // token rows [T, K], boxes of 64 K x kNB rows
-  CUtensorMap row;   // the same, boxes of one row (gathers)
 };
 struct ShrinkArgs {
   int T, K, n, R, rb, zc;   // rb: rank rows per box, a power of two that divides R
+  const __nv_bfloat16* rows;   // the token rows
+  const char* next;         // the adapters' matrices [n][next_bytes] of the expand launch, or null
+  long long next_bytes;
   const int32_t* adapter_idx;
   const float* scale;
   __nv_bfloat16* z;         // [T, zc]
   void* plan;
   uint32_t* masks;          // [n_tt][256][8]: the tokens of every entry, as bits; or null
   int* status;
-  bool clear;               // the first kernel of the call: clear the status
+  bool first;               // the first kernel of the call: clears the status, writes the plan
 };
 constexpr int kGatherRows = 64;   // most tokens of a unit that gathers
+constexpr int kRowWarps = 5;      // warps 2 .. 6
+constexpr int kRowAhead = 4;      // stages of row copies in flight per thread
 template <int kNB>
 struct ShrinkCfg {
   static constexpr int kStageBytes = kABytes + kNB * kK * 2;
@@ -165,16 +172,18 @@ struct ShrinkShared {
 };
 static_assert(sizeof(ShrinkShared) <= 5120, "shared block");
 
-// Four rows (y0..y3) of 64 K each, stored as consecutive 128-byte rows at dst.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int x, int y0, int y1, int y2, int y3,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y0), "r"(y1),
-      "r"(y2), "r"(y3), "l"(policy)
-      : "memory");
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 // The adapters that token block tt meets, by the whole CTA.
@@ -293,17 +302,34 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   pdl_trigger();
   // the call's status starts clean: this is its first kernel, and nothing is
   // reported before a later kernel of the call or a wait of a second
-  if (a.clear && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
+  if (a.first && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
   build_list<C::kGather>(sh, a, row0, rows);
-  if (rank == 0 && blockIdx.y == 0) write_plan(sh, a, tt, rows, reinterpret_cast<uint32_t*>(smem));
+  if (a.first && rank == 0 && blockIdx.y == 0) write_plan(sh, a, tt, rows, reinterpret_cast<uint32_t*>(smem));
   const int q_all = sh->n_ent * a.R;
   const int units = (q_all + kM - 1) / kM;
+  if (a.next != nullptr && warp == 3) {
+    // the expand launch's adapter rows start on their way into L2
+    const int parts = (int)gridDim.y * kC;
+    const long long step = 16384, per = (a.next_bytes + step - 1) / step;
+    for (long long i = (long long)(blockIdx.y * kC + rank) * 32 + lane; i < per * sh->n_ent;
+         i += parts * 32) {
+      const int e = (int)(i / per);
+      const long long off = (i - e * per) * step;
+      const long long left = a.next_bytes - off;
+      prefetch_l2(a.next + sh->list[e] * a.next_bytes + off, (uint32_t)(left < step ? left : step));
+    }
+  }
   // s CTAs per unit: as many as leave a group of CTAs for every unit
   int s = kC;
   while (s > 1 && units * s > (int)gridDim.y * kC) s >>= 1;
   const int groups = kC / s, sub = rank / s, r = rank - sub * s;
   const int u_step = (int)gridDim.y * groups, u_first = (int)blockIdx.y * groups;
-  if (u_first >= units) return;   // the same for the whole cluster
+  // A second shrink of a call starts while the first one runs (neither reads
+  // what the other writes) but does not end before it.
+  if (u_first >= units) {   // the same for the whole cluster
+    pdl_wait();
+    return;
+  }
   const int kb0 = nk * r / s, kb1 = nk * (r + 1) / s;
   bool gather = false;
   if constexpr (C::kGather) {
@@ -321,7 +347,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->full[i], gather ? 1 + kRowWarps : 1);   // TMA, and the warps that copy rows
       mbar_init(&sh->empty[i], 1);
     }
     mbar_init(&sh->acc_full, 1);
@@ -370,17 +396,12 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
     if (have && warp == 0) {
       const uint64_t pol_p = policy_evict_normal(), pol_v = policy_evict_last();
       const int from = at.count;
-      const uint32_t bytes = (uint32_t)((q_end + n_mma) * kK * 2);
+      const uint32_t bytes = (uint32_t)((q_end + (gather ? 0 : kNB)) * kK * 2);
       // this lane's box of rank rows (rows past the last entry keep what the
-      // stage held: their products are not read) and its four token rows
+      // stage held: their products are not read)
       const int q = lane * a.rb, e = (u * kM + q) / a.R;
       const bool box = q < q_end;
       const int p_row = u * kM + q - e * a.R, p_ad = box ? (int)sh->list[e] : 0;
-      int y[4];
-      const bool rows4 = gather && 4 * lane < n_mma;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        y[i] = rows4 ? row0 + (int)sh->tok[min(4 * lane + i, n_tok - 1)] : 0;
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         uint64_t* fb = &sh->full[at.stage];
@@ -391,10 +412,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         if (!ok) break;
         uint8_t* st = smem + at.stage * stage_bytes;
-        if (rows4)
-          tma_gather4(st + kABytes + lane * 4 * (kK * 2), &maps.row, fb, kb * kK, y[0], y[1], y[2],
-                      y[3], pol_v);
-        else if (!gather && lane == 0)
+        if (!gather && lane == 0)
           tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
         if (box) tma_load_3d(st + q * (kK * 2), &maps.p, fb, kb * kK, p_row, p_ad, pol_p);
         at.next();
@@ -429,6 +447,46 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       mma_commit(&sh->drain);
       if (!mbar_wait(&sh->drain, parity, nullptr, kWaitLimitNs))
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
+    }
+    if (C::kGather && gather && have && warp >= 2) {
+      // this thread's 16-byte pieces: piece c of row j, at the swizzled place
+      const int n_piece = n_mma * 8;
+      const __nv_bfloat16* src[4];
+      uint32_t dst[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int piece = (int)threadIdx.x - 64 + i * (32 * kRowWarps), j = piece >> 3, c = piece & 7;
+        dst[i] = piece < n_piece ? (uint32_t)(kABytes + j * 128 + ((c ^ (j & 7)) << 4)) : 0u;
+        // rows up to a multiple of 16 repeat the last token
+        src[i] = a.rows + (size_t)(row0 + (int)sh->tok[min(j, n_tok - 1)]) * a.K + c * 8;
+      }
+      const uint32_t sbase = smem_u32(smem);
+      Place done = at;   // the stage whose copies are awaited next
+      bool ok = true;
+      int kb = kb0;
+      for (; kb < kb1; ++kb) {
+        ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (dst[i]) cp_async16(sbase + at.stage * stage_bytes + dst[i], src[i] + (size_t)kb * kK);
+        cp_async_commit();
+        at.next();
+        if (kb - kb0 >= kRowAhead) {
+          cp_async_wait<kRowAhead>();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->full[done.stage]);
+          done.next();
+        }
+      }
+      cp_async_wait<0>();
+      fence_async_smem();
+      __syncwarp();
+      for (; done.count < at.count; done.next())
+        if (lane == 0) mbar_arrive(&sh->full[done.stage]);
+    } else if (have && warp >= 2) {
+      for (int kb = kb0; kb < kb1; ++kb) at.next();
     }
     const int q = warp & 3;   // TMEM lanes 32 q ..
     if (have && warp >= 3) {
@@ -469,6 +527,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
     tc_fence_after();
     if (have) parity ^= 1u;
   }
+  pdl_wait();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
@@ -487,26 +546,59 @@ struct ExpandArgs {
   int* status;
 };
 
+// A TMA load of this CTA that lands, and counts, at the same place in every
+// CTA of the cluster in `mask`.
+__device__ __forceinline__ void tma_load_2d_multicast(void* dst, const CUtensorMap* map,
+                                                      uint64_t* bar, int x, int y, uint16_t mask,
+                                                      uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "h"(mask),
+      "l"(policy)
+      : "memory");
+}
+// Arrive once on `bar`'s place in every CTA of `mask` when this thread's
+// tcgen05 operations so far have completed.
+__device__ __forceinline__ void mma_commit_multicast(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
+// Columns x .. x + 64 of a block's rows; in a pair, rank r loads the r-th half
+// for both CTAs.
+template <int kNB, bool kPair>
+__device__ __forceinline__ void load_tokens(uint8_t* dst, uint64_t* fb, const CUtensorMap* map, int x,
+                                            int row0, uint64_t pol, int rank) {
+  if constexpr (kPair)
+    tma_load_2d_multicast(dst + rank * (kNB / 2 * kK * 2), map, fb, x, row0 + rank * (kNB / 2), 0x3,
+                          pol);
+  else
+    tma_load_2d(dst, map, fb, x, row0, pol);
+}
 // The weight operand of one stage and its token rows.
-template <int kNB, bool kKMajor>
+template <int kNB, bool kKMajor, bool kPair = false>
 __device__ __forceinline__ void load_base(uint8_t* st, uint64_t* fb, const ExpandMaps& maps, int kb,
-                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v) {
+                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v,
+                                          int rank = 0) {
   mbar_arrive_expect_tx(fb, kABytes + kNB * kK * 2);
   if constexpr (kKMajor)
     tma_load_2d(st, &maps.w, fb, kb * kK, mt * kM, pol_w);
   else
     tma_load_3d(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
-  tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
+  load_tokens<kNB, kPair>(st + kABytes, fb, &maps.v, kb * kK, row0, pol_v, rank);
 }
 // Stage j of the adapters' part: 64 rank rows of the block's entries, in boxes
 // of rb rows, each [2 feature atoms][rb rows][128 bytes].
-template <int kNB>
+template <int kNB, bool kPair = false>
 __device__ __forceinline__ void load_ext(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
                                          const ExpandArgs& a, const BlockPlan* plan, uint4 list,
                                          int q_all, int j, int mt, int row0, uint64_t pol_w,
-                                         uint64_t pol_v) {
+                                         uint64_t pol_v, int rank = 0) {
   mbar_arrive_expect_tx(fb, kABytes + kNB * kK * 2);
-  tma_load_2d(st + kABytes, &maps.z, fb, j * kK, row0, pol_v);
+  load_tokens<kNB, kPair>(st + kABytes, fb, &maps.z, j * kK, row0, pol_v, rank);
   for (int q = 0; q < kK; q += a.rb) {
     const int qq = j * kK + q, e = qq / a.R;
     // the first eight entries are in registers; past the last entry: an
@@ -763,7 +855,10 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
 }
 
 // Many tiles: persistent CTAs, two accumulators of 256 tokens in TMEM, so the
-// epilogue of one tile runs under the main loop of the next.
+// epilogue of one tile runs under the main loop of the next.  Two CTAs of a
+// cluster take neighbouring feature tiles of the same token block: each loads
+// half of the block's rows and multicasts it to both, so a stage reads 32 KB
+// from L2 instead of 48 KB.
 struct FullCfg {
   static constexpr int kNB = 256;
   static constexpr int kStageBytes = kABytes + kNB * kK * 2;
@@ -783,6 +878,7 @@ struct FullShared {
 template <bool kKMajor>
 __global__ void __launch_bounds__(kThreads, 1)
 adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs a) {
+  // maps.v and maps.z: boxes of half a block's rows
   using C = FullCfg;
   constexpr int kNB = C::kNB;
   extern __shared__ uint8_t smem_raw[];
@@ -791,11 +887,14 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   FullShared* sh = reinterpret_cast<FullShared*>(smem + C::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nk = a.K / kK;
-  const int total = a.n_tt * (a.M / kM);
+  const int rank = (int)cluster_ctarank();
+  const int n_mp = (a.M / kM + 1) / 2;      // pairs of feature tiles (the last may be half empty)
+  const int total = a.n_tt * n_mp;
+  const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->empty[s], 2);    // both CTAs' MMAs have read the slot
       mbar_init(&sh->loaded[s], 1);
       mbar_init(&sh->ready[s], 1);
     }
@@ -812,29 +911,34 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // both CTAs' barriers are set before either signals the other's
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
+  // a role that gives up stops the roles of both CTAs
+  auto raise_abort = [=]() {
+    *abort_flag = 1;
+    st_cluster_u32(mapa_shared(smem_u32(&sh->abort), (uint32_t)(rank ^ 1)), 1u);
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
       Place at(C::kStages), base(C::kStages), ext(C::kStages);
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const int tt = tile % a.n_tt, mt = tile / a.n_tt, row0 = tt * kNB;
+      for (int tile = first; ok && tile < total; tile += step) {
+        const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank, row0 = tt * kNB;
         const BlockPlan* plan = plan_of(a.plan, tt);
         // from the second tile on the plan is known to be complete: its first
         // words are on their way while the projection's stages are loaded
-        const bool later = tile != (int)blockIdx.x;
+        const bool later = tile != first;
         int n_ent = later ? plan->n_ent : 0;
         uint4 list = later ? *reinterpret_cast<const uint4*>(plan->list) : make_uint4(0, 0, 0, 0);
         for (int kb = 0; kb < nk; ++kb) {
           if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
             break;
-          load_base<kNB, kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, kb,
-                                  mt, row0, pol_w, pol_v);
+          load_base<kNB, kKMajor, true>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, kb,
+                                  mt, row0, pol_w, pol_v, rank);
           at.next();
           base.next();
         }
@@ -848,8 +952,8 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         for (int j = 0; ok && j * kK < q_all; ++j) {
           if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
             break;
-          load_ext<kNB>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan,
-                        list, q_all, j, mt, row0, pol_w, pol_v);
+          load_ext<kNB, true>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan,
+                        list, q_all, j, mt, row0, pol_w, pol_v, rank);
           at.next();
           ext.next();
         }
@@ -857,7 +961,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       }
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
-        *abort_flag = 1;
+        raise_abort();
       }
       pdl_wait();
       drain_loads(sh->full, C::kStages, 0, base.count);
@@ -869,20 +973,20 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       Place at(C::kStages), base(C::kStages), ext(C::kStages);
       Place buf(2);
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      for (int tile = first; ok && tile < total; tile += step) {
         if (!(ok = mbar_wait(&sh->acc_empty[buf.stage], buf.phase ^ 1u, abort_flag, kWaitLimitNs)))
           break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf.stage * kNB);
         const BlockPlan* plan = plan_of(a.plan, tile % a.n_tt);
-        const bool later = tile != (int)blockIdx.x;
+        const bool later = tile != first;
         int n_ent = later ? plan->n_ent : 0;   // early, as the producer's
         uint32_t acc = 0;
         for (int kb = 0; kb < nk; ++kb) {
           if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
           tc_fence_after();
           mma_base<kNB, kKMajor>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), acc);
-          mma_commit(&sh->empty[at.stage]);
+          mma_commit_multicast(&sh->empty[at.stage], 0x3);
           at.next();
           base.next();
         }
@@ -896,7 +1000,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
             break;
           tc_fence_after();
           mma_ext<kNB>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), a.rb, acc);
-          mma_commit(&sh->empty[at.stage]);
+          mma_commit_multicast(&sh->empty[at.stage], 0x3);
           at.next();
           ext.next();
         }
@@ -906,7 +1010,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       }
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
-        *abort_flag = 1;
+        raise_abort();
       }
       mma_commit(&sh->drain);
       if (!mbar_wait(&sh->drain, 0, nullptr, kWaitLimitNs))
@@ -915,7 +1019,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   } else if (warp == 2) {
     Place at(C::kStages), ext(C::kStages);
     bool ok = true, found = false;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+    for (int tile = first; ok && tile < total; tile += step) {
       for (int kb = 0; kb < nk; ++kb) at.next();
       pdl_wait();
       const int q_all = plan_of(a.plan, tile % a.n_tt)->n_ent * a.R;
@@ -936,15 +1040,16 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
     __nv_bfloat16* stg =
         reinterpret_cast<__nv_bfloat16*>(smem + C::kRing + 1024 + (warp - 3) * C::kStgBytes);
     Place buf(2);
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const int tt = tile % a.n_tt, mt = tile / a.n_tt;
+    for (int tile = first; tile < total; tile += step) {
+      const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank;
       const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
       const bool got = mbar_wait(&sh->acc_full[buf.stage], buf.phase, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf.stage * kNB);
+      const bool real = mt * kM < a.M;   // not the second tile of a half-empty pair
       __nv_bfloat16* o = a.out + (size_t)row0 * a.M + mt * kM + q * 32;
-      for (int c0 = 0; c0 < rows; c0 += 16) {
+      for (int c0 = 0; real && c0 < rows; c0 += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(tb + c0, v);
         tmem_ld_wait();
@@ -970,7 +1075,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // neither CTA leaves while the other may still write to it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kNB);
@@ -1252,6 +1357,11 @@ int split_of(long long tiles, int nk) {
   return best;
 }
 
+// Whether the expand launch of these sizes runs on persistent pairs: with more
+// tiles than SMs, where a split of K does not balance them better.
+bool expand_full(int nb, long long tiles, int K) {
+  return nb == FullCfg::kNB && tiles > device_sm_count() && split_of(tiles, K / kK) == 1;
+}
 // CTAs of the expand launch of these sizes.
 long long expand_ctas(const AdapterSizes& z, int K, int M) {
   const long long tiles = (long long)z.n_tt * (M / kM);
@@ -1293,25 +1403,32 @@ cudaError_t launch_shrink_nb(int cluster, int gy, const ShrinkMaps& m, const Shr
   const dim3 grid(n_tt * cluster, gy);
   constexpr int smem = ShrinkCfg<kNB>::kSmemBytes;
   switch (cluster) {
-    case 1: return launch_cluster(adapter_shrink_kernel<kNB, 1>, grid, 1, smem, false, s, m, a);
-    case 2: return launch_cluster(adapter_shrink_kernel<kNB, 2>, grid, 2, smem, false, s, m, a);
-    case 4: return launch_cluster(adapter_shrink_kernel<kNB, 4>, grid, 4, smem, false, s, m, a);
-    default: return launch_cluster(adapter_shrink_kernel<kNB, 8>, grid, 8, smem, false, s, m, a);
+    case 1: return launch_cluster(adapter_shrink_kernel<kNB, 1>, grid, 1, smem, !a.first, s, m, a);
+    case 2: return launch_cluster(adapter_shrink_kernel<kNB, 2>, grid, 2, smem, !a.first, s, m, a);
+    case 4: return launch_cluster(adapter_shrink_kernel<kNB, 4>, grid, 4, smem, !a.first, s, m, a);
+    default: return launch_cluster(adapter_shrink_kernel<kNB, 8>, grid, 8, smem, !a.first, s, m, a);
   }
 }
 
-// Z of the rows v [T, D] and the adapters' matrices P [n, R, D].  `clear`: the
-// first launch of a call; `ctas`: the expand launch that follows has so many.
+// Z of the rows v [T, D] and the adapters' matrices P [n, R, D].  `first`: the
+// first launch of a call; `ctas`: the expand launch that follows has so many;
+// `next` [n, R, next_cols]: the adapters' matrices that it reads.
 cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* P,
                           int D, const float* scale, const int32_t* adapter_idx, void* plan,
-                          uint32_t* masks, __nv_bfloat16* Z, int* status, bool clear,
-                          long long ctas, cudaStream_t s) {
+                          uint32_t* masks, __nv_bfloat16* Z, int* status, bool first,
+                          long long ctas, const __nv_bfloat16* next, int next_cols,
+                          cudaStream_t s) {
   ShrinkMaps m;
   const int rb = rank_box(z.R);
-  if (!map_rank_rows(&m.p, P, z.n, z.R, D, rb) || !map_rows(&m.v, v, z.T, D, z.nb) ||
-      !map_rows(&m.row, v, z.T, D, 1))
+  if (!map_rank_rows(&m.p, P, z.n, z.R, D, rb) || !map_rows(&m.v, v, z.T, D, z.nb))
     return cudaErrorInvalidValue;
-  const ShrinkArgs a{z.T, D, z.n, z.R, rb, z.zc, adapter_idx, scale, Z, plan, masks, status, clear};
+  // few blocks: the expand's tiles meet their adapters' rows cold, after the
+  // projection's weights; with many blocks most of those reads hit L2 anyway
+  const bool ahead = next != nullptr && z.n_tt <= 4;
+  const ShrinkArgs a{z.T, D, z.n, z.R, rb, z.zc, v,
+                     ahead ? reinterpret_cast<const char*>(next) : nullptr,
+                     (long long)z.R * next_cols * 2, adapter_idx, scale, Z, plan, masks, status,
+                     first};
   // as many clusters per block as the SMs take in one round and the block can
   // have units for; the CTAs share them out once they know its adapters
   int sms = device_sm_count();
@@ -1357,8 +1474,8 @@ template <bool kKMajor>
 cudaError_t launch_expand_t(int nb, const ExpandMaps& m, const ExpandArgs& a, cudaStream_t s) {
   const long long tiles = (long long)a.n_tt * (a.M / kM);
   const int split = split_of(tiles, a.K / kK);
-  if (nb == FullCfg::kNB && split == 1 && tiles > device_sm_count())
-    return launch_cluster(adapter_expand_kernel<kKMajor>, dim3(device_sm_count()), 1,
+  if (expand_full(nb, tiles, a.K))
+    return launch_cluster(adapter_expand_kernel<kKMajor>, dim3(device_sm_count() / 2 * 2), 2,
                           FullCfg::kSmemBytes, true, s, m, a);
   switch (nb) {
     case 32: return launch_split_nb<32, kKMajor>(split, m, a, s);
@@ -1375,9 +1492,10 @@ cudaError_t launch_expand(const AdapterSizes& z, const __nv_bfloat16* v, const _
                           cudaStream_t s) {
   ExpandMaps m;
   const int rb = rank_box(z.R);
+  const int box = expand_full(z.nb, (long long)z.n_tt * (M / kM), K) ? z.nb / 2 : z.nb;
   if (!(k_major ? map_rows(&m.w, W, M, K, kM) : map_atoms(&m.w, W, K, M)) ||
-      !map_rows(&m.v, v, z.T, K, z.nb) || !map_rank_atoms(&m.p, P, z.n, z.R, M, rb) ||
-      !map_rows(&m.z, Z, z.T, z.zc, z.nb))
+      !map_rows(&m.v, v, z.T, K, box) || !map_rank_atoms(&m.p, P, z.n, z.R, M, rb) ||
+      !map_rows(&m.z, Z, z.T, z.zc, box))
     return cudaErrorInvalidValue;
   const ExpandArgs a{z.T, K, M, z.n, z.R, rb, z.n_tt, out, plan, status};
   return k_major ? launch_expand_t<true>(z.nb, m, a, s) : launch_expand_t<false>(z.nb, m, a, s);
@@ -1418,7 +1536,7 @@ cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x
   void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
   cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, nullptr, Z, status,
-                                  true, expand_ctas(z, z.H, z.N), s);
+                                  true, expand_ctas(z, z.H, z.N), B, z.N, s);
   if (err != cudaSuccess) return err;
   return launch_expand(z, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
 }
@@ -1436,10 +1554,10 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   uint32_t* masks = ws_ptr<uint32_t>(ws, z.masks);
   const int sms = device_sm_count();
   cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, masks, Z, status,
-                                  true, sms, s);
+                                  true, sms, nullptr, 0, s);
   if (err == cudaSuccess)
     err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, nullptr, dZ, status, false,
-                        expand_ctas(z, z.N, z.H), s);
+                        expand_ctas(z, z.N, z.H), A, z.H, s);
   if (err == cudaSuccess) err = launch_expand(z, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
   if (err != cudaSuccess) return err;
   WgradMaps m;

@@ -36,6 +36,11 @@ CASES = [  # T, H, N, n, R, order
     (2600, 256, 2048, 5, 24, "shuffled"),      # more tiles than SMs: persistent CTAs
     (2563, 2048, 1920, 3, 16, "segments"),
     (700, 128, 256, 200, 128, "distinct"),     # several units of rank rows per block
+    (600, 512, 256, 24, 64, "shuffled"),       # units of few tokens each: gathered rows
+    (300, 2048, 128, 100, 24, "distinct"),
+    (128, 1024, 128, 40, 40, "shuffled"),
+    (515, 7168, 128, 24, 64, "shuffled"),
+    (2049, 512, 2432, 8, 16, "shuffled"),      # an odd number of feature tiles in pairs
 ]
 
 
