@@ -126,10 +126,11 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int from
 // spent 31 us on the gathers.)
 struct ShrinkMaps {
   CUtensorMap p;     // the adapters' rank rows [n, R, K], boxes of 64 K x rb rows
-  CUtensorMap v;     // token rows [T, K], boxes of 64 K x kNB rows
+  CUtensorMap v;     // token rows [T, K], boxes of 64 K x nb rows
 };
 struct ShrinkArgs {
-  int T, K, n, R, rb, zc;   // rb: rank rows per box, a power of two that divides R
+  int T, nb, K, n, R, rb, zc;   // nb: tokens per block; rb: rank rows per box, a power
+                                // of two that divides R
   const __nv_bfloat16* rows;   // the token rows
   const char* next;         // the adapters' matrices [n][next_bytes] of the expand launch, or null
   long long next_bytes;
@@ -143,7 +144,6 @@ struct ShrinkArgs {
 };
 constexpr int kGatherRows = 64;   // most tokens of a unit that gathers
 constexpr int kRowWarps = 5;      // warps 2 .. 6
-constexpr int kRowAhead = 4;      // stages of row copies in flight per thread
 template <int kNB>
 struct ShrinkCfg {
   static constexpr int kStageBytes = kABytes + kNB * kK * 2;
@@ -178,12 +178,9 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kPending>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+// Arrive on `bar` (a counted arrival) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // The adapters that token block tt meets, by the whole CTA.
@@ -296,7 +293,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kC > 1 ? (int)cluster_ctarank() : 0;
   const int tt = (int)blockIdx.x / kC;
-  const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
+  const int row0 = tt * a.nb, rows = min(a.nb, a.T - row0);
   const int nk = a.K / kK;
 
   pdl_trigger();
@@ -347,7 +344,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&sh->full[i], gather ? 1 + kRowWarps : 1);   // TMA, and the warps that copy rows
+      mbar_init(&sh->full[i], gather ? 1 + 32 * kRowWarps : 1);   // TMA, and the threads that copy rows
       mbar_init(&sh->empty[i], 1);
     }
     mbar_init(&sh->acc_full, 1);
@@ -392,11 +389,11 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       __syncthreads();
     }
     const int n_tok = gather && have ? sh->n_tok : rows;   // rows of the partial tile
-    const int n_mma = gather ? (n_tok + 15) & ~15 : kNB;
+    const int n_mma = gather ? (n_tok + 15) & ~15 : a.nb;
     if (have && warp == 0) {
       const uint64_t pol_p = policy_evict_normal(), pol_v = policy_evict_last();
       const int from = at.count;
-      const uint32_t bytes = (uint32_t)((q_end + (gather ? 0 : kNB)) * kK * 2);
+      const uint32_t bytes = (uint32_t)((q_end + (gather ? 0 : a.nb)) * kK * 2);
       // this lane's box of rank rows (rows past the last entry keep what the
       // stage held: their products are not read)
       const int q = lane * a.rb, e = (u * kM + q) / a.R;
@@ -430,6 +427,10 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = mbar_wait(&sh->full[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
+        // copied rows: ordinary writes that the MMA reads through the async
+        // proxy.  The fence is taken here, by a thread without copies in flight:
+        // in the copying threads it waits for all of theirs (0.3 us a stage)
+        if (gather) fence_async_smem();
         tc_fence_after();
         const uint32_t a0 = sbase + (uint32_t)(at.stage * stage_bytes), b0 = a0 + kABytes;
 #pragma unroll
@@ -461,30 +462,16 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
         src[i] = a.rows + (size_t)(row0 + (int)sh->tok[min(j, n_tok - 1)]) * a.K + c * 8;
       }
       const uint32_t sbase = smem_u32(smem);
-      Place done = at;   // the stage whose copies are awaited next
-      bool ok = true;
-      int kb = kb0;
-      for (; kb < kb1; ++kb) {
-        ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const bool ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
         if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (dst[i]) cp_async16(sbase + at.stage * stage_bytes + dst[i], src[i] + (size_t)kb * kK);
-        cp_async_commit();
+        cp_async_arrive(&sh->full[at.stage]);
         at.next();
-        if (kb - kb0 >= kRowAhead) {
-          cp_async_wait<kRowAhead>();
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->full[done.stage]);
-          done.next();
-        }
       }
-      cp_async_wait<0>();
-      fence_async_smem();
-      __syncwarp();
-      for (; done.count < at.count; done.next())
-        if (lane == 0) mbar_arrive(&sh->full[done.stage]);
+      asm volatile("cp.async.wait_all;" ::: "memory");   // none is in flight when the CTA leaves
     } else if (have && warp >= 2) {
       for (int kb = kb0; kb < kb1; ++kb) at.next();
     }
@@ -535,12 +522,12 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
 // out = v W + Z P, tiles of 128 output features x one token block.
 struct ExpandMaps {
   CUtensorMap w;     // the projection's weights
-  CUtensorMap v;     // token rows [T, K], boxes of 64 K x kNB rows
+  CUtensorMap v;     // token rows [T, K], boxes of 64 K x nb rows (pairs: nb / 2)
   CUtensorMap p;     // the adapters' matrices [n, R, M], boxes of rb rows x 128 features
-  CUtensorMap z;     // Z [T, zc], boxes of 64 columns x kNB rows
+  CUtensorMap z;     // Z [T, zc], boxes of 64 columns x nb rows (pairs: nb / 2)
 };
 struct ExpandArgs {
-  int T, K, M, n, R, rb, n_tt;
+  int T, nb, K, M, n, R, rb, n_tt;   // nb: tokens per block, a multiple of 16
   __nv_bfloat16* out;       // [T, M]
   const void* plan;
   int* status;
@@ -569,53 +556,61 @@ __device__ __forceinline__ void mma_commit_multicast(uint64_t* bar, uint16_t mas
 }
 // Columns x .. x + 64 of a block's rows; in a pair, rank r loads the r-th half
 // for both CTAs.
-template <int kNB, bool kPair>
-__device__ __forceinline__ void load_tokens(uint8_t* dst, uint64_t* fb, const CUtensorMap* map, int x,
-                                            int row0, uint64_t pol, int rank) {
+template <bool kPair>
+__device__ __forceinline__ void load_tokens(uint8_t* dst, uint64_t* fb, const CUtensorMap* map, int nb,
+                                            int x, int row0, uint64_t pol, int rank) {
   if constexpr (kPair)
-    tma_load_2d_multicast(dst + rank * (kNB / 2 * kK * 2), map, fb, x, row0 + rank * (kNB / 2), 0x3,
+    tma_load_2d_multicast(dst + rank * (nb / 2 * kK * 2), map, fb, x, row0 + rank * (nb / 2), 0x3,
                           pol);
   else
     tma_load_2d(dst, map, fb, x, row0, pol);
 }
 // The weight operand of one stage and its token rows.
-template <int kNB, bool kKMajor, bool kPair = false>
-__device__ __forceinline__ void load_base(uint8_t* st, uint64_t* fb, const ExpandMaps& maps, int kb,
-                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v,
+template <bool kKMajor, bool kPair = false>
+__device__ __forceinline__ void load_base(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
+                                          int nb, int kb, int mt, int row0, uint64_t pol_w, uint64_t pol_v,
                                           int rank = 0) {
-  mbar_arrive_expect_tx(fb, kABytes + kNB * kK * 2);
+  mbar_arrive_expect_tx(fb, (uint32_t)(kABytes + nb * kK * 2));
   if constexpr (kKMajor)
     tma_load_2d(st, &maps.w, fb, kb * kK, mt * kM, pol_w);
   else
     tma_load_3d(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
-  load_tokens<kNB, kPair>(st + kABytes, fb, &maps.v, kb * kK, row0, pol_v, rank);
+  load_tokens<kPair>(st + kABytes, fb, &maps.v, nb, kb * kK, row0, pol_v, rank);
 }
-// Stage j of the adapters' part: 64 rank rows of the block's entries, in boxes
-// of rb rows, each [2 feature atoms][rb rows][128 bytes].
-template <int kNB, bool kPair = false>
+// A block's entry list in the registers of a warp: lane l holds entries 8 l .. 8 l + 7.
+__device__ __forceinline__ uint4 load_list(const BlockPlan* plan, int lane) {
+  return reinterpret_cast<const uint4*>(plan->list)[lane];
+}
+__device__ __forceinline__ int list_entry(const uint4& list, int e) {
+  const int src = (e >> 3) & 31;
+  const uint32_t x = __shfl_sync(0xffffffffu, list.x, src), y = __shfl_sync(0xffffffffu, list.y, src);
+  const uint32_t z = __shfl_sync(0xffffffffu, list.z, src), w = __shfl_sync(0xffffffffu, list.w, src);
+  const uint32_t v = e & 4 ? (e & 2 ? w : z) : (e & 2 ? y : x);
+  return (int)((v >> (16 * (e & 1))) & 0xffffu);
+}
+// Stage j of the adapters' part, by the whole producer warp: 64 rank rows of
+// the block's entries, in boxes of rb rows, each [2 feature atoms][rb rows][128
+// bytes], one box per lane.
+template <bool kPair = false>
 __device__ __forceinline__ void load_ext(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
-                                         const ExpandArgs& a, const BlockPlan* plan, uint4 list,
-                                         int q_all, int j, int mt, int row0, uint64_t pol_w,
-                                         uint64_t pol_v, int rank = 0) {
-  mbar_arrive_expect_tx(fb, kABytes + kNB * kK * 2);
-  load_tokens<kNB, kPair>(st + kABytes, fb, &maps.z, j * kK, row0, pol_v, rank);
-  for (int q = 0; q < kK; q += a.rb) {
-    const int qq = j * kK + q, e = qq / a.R;
-    // the first eight entries are in registers; past the last entry: an
-    // adapter that does not exist, read as zeros
-    int ad = a.n;
-    if (qq < q_all && e < 8) {
-      const uint32_t w = e < 4 ? (e < 2 ? list.x : list.y) : (e < 6 ? list.z : list.w);
-      ad = (int)((w >> (16 * (e & 1))) & 0xffffu);
-    } else if (qq < q_all) {
-      ad = (int)plan->list[e];
-    }
-    tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, qq - e * a.R, mt * 2, ad, pol_w);
+                                         const ExpandArgs& a, const uint4& list, int q_all, int j,
+                                         int mt, int row0, uint64_t pol_w, uint64_t pol_v,
+                                         int lane, int rank = 0) {
+  if (lane == 0) {
+    mbar_arrive_expect_tx(fb, (uint32_t)(kABytes + a.nb * kK * 2));
+    load_tokens<kPair>(st + kABytes, fb, &maps.z, a.nb, j * kK, row0, pol_v, rank);
   }
+  __syncwarp();
+  const int q = lane * a.rb, qq = j * kK + q, e = qq / a.R;
+  const int known = list_entry(list, e);
+  // past the last entry: an adapter that does not exist, read as zeros
+  if (q < kK)
+    tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, qq - e * a.R, mt * 2, qq < q_all ? known : a.n,
+                pol_w);
 }
-template <int kNB, bool kKMajor>
-__device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, uint32_t& acc) {
-  constexpr uint32_t kIdesc = idesc_bf16(kM, kNB, /*a_mn=*/!kKMajor, false);
+template <bool kKMajor>
+__device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, int nb, uint32_t& acc) {
+  const uint32_t idesc = idesc_bf16(kM, nb, /*a_mn=*/!kKMajor, false);
   const uint32_t b0 = a0 + kABytes;
 #pragma unroll
   for (int kk = 0; kk < kK / 16; ++kk) {
@@ -623,20 +618,19 @@ __device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, uint32_t& a
     // operands: 8-row groups 1 KB apart, 16 K = 32 bytes
     const uint64_t da = kKMajor ? sdesc_sw128(a0 + kk * 32, 16, 1024)
                                 : sdesc_sw128(a0 + kk * 2048, 8192, 1024);
-    mma_bf16_ss(tmem, da, sdesc_sw128(b0 + kk * 32, 16, 1024), kIdesc, acc);
+    mma_bf16_ss(tmem, da, sdesc_sw128(b0 + kk * 32, 16, 1024), idesc, acc);
     acc = 1u;
   }
 }
-template <int kNB>
-__device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, int rb, uint32_t& acc) {
-  constexpr uint32_t kIdesc = idesc_bf16(kM, kNB, /*a_mn=*/true, false);
+__device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, int nb, int rb, uint32_t& acc) {
+  const uint32_t idesc = idesc_bf16(kM, nb, /*a_mn=*/true, false);
   const uint32_t b0 = a0 + kABytes;
   const uint32_t lbo = (uint32_t)rb * 128, sbo = rb == 8 ? 2048u : 1024u;
 #pragma unroll
   for (int kk = 0; kk < kK / 16; ++kk) {
     const uint32_t q = 16u * kk, box = q / rb;
     const uint32_t at = a0 + box * (uint32_t)rb * 256 + (q - box * rb) * 128;
-    mma_bf16_ss(tmem, sdesc_sw128(at, lbo, sbo), sdesc_sw128(b0 + kk * 32, 16, 1024), kIdesc, acc);
+    mma_bf16_ss(tmem, sdesc_sw128(at, lbo, sbo), sdesc_sw128(b0 + kk * 32, 16, 1024), idesc, acc);
     acc = 1u;
   }
 }
@@ -701,7 +695,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   const int rank = kS > 1 ? (int)cluster_ctarank() : 0;
   const int tile = (int)blockIdx.x / kS;
   const int tt = tile % a.n_tt, mt = tile / a.n_tt;
-  const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
+  const int row0 = tt * a.nb, rows = min(a.nb, a.T - row0);
   const int nk = a.K / kK;
   const int kb0 = nk * rank / kS, kb1 = nk * (rank + 1) / kS;
   const BlockPlan* plan = plan_of(a.plan, tt);
@@ -729,31 +723,36 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   volatile int* abort_flag = &sh->abort;
 
   if (warp == 0) {
+    // a weight tile read by one block is streamed past L2
+    const uint64_t pol_w = a.n_tt == 1 ? policy_evict_first() : policy_evict_normal();
+    const uint64_t pol_v = policy_evict_last();
+    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (lane == 0) {
+        ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
+        if (ok)
+          load_base<kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, a.nb, kb,
+                             mt, row0, pol_w, pol_v);
+      }
+      if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
+      at.next();
+      base.next();
+    }
+    pdl_wait();             // the plan and Z are complete
+    fence_async_global();
+    const int q_all = plan->n_ent * a.R;
+    const uint4 list = load_list(plan, lane);
+    const int ne = (q_all + kK - 1) / kK;
+    for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
+      if (lane == 0) ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
+      if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
+      load_ext<>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list, q_all, j,
+                    mt, row0, pol_w, pol_v, lane);
+      at.next();
+      ext.next();
+    }
     if (lane == 0) {
-      // a weight tile read by one block is streamed past L2
-      const uint64_t pol_w = a.n_tt == 1 ? policy_evict_first() : policy_evict_normal();
-      const uint64_t pol_v = policy_evict_last();
-      Place at(C::kStages), base(C::kStages), ext(C::kStages);
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
-        load_base<kNB, kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, kb,
-                                mt, row0, pol_w, pol_v);
-        at.next();
-        base.next();
-      }
-      pdl_wait();             // the plan and Z are complete
-      fence_async_global();
-      const int q_all = plan->n_ent * a.R;
-      const uint4 list = *reinterpret_cast<const uint4*>(plan->list);
-      const int ne = (q_all + kK - 1) / kK;
-      for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
-        if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs))) break;
-        load_ext<kNB>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan, list,
-                      q_all, j, mt, row0, pol_w, pol_v);
-        at.next();
-        ext.next();
-      }
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         *abort_flag = 1;
@@ -771,7 +770,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
-        mma_base<kNB, kKMajor>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), acc);
+        mma_base<kKMajor>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, acc);
         mma_commit(&sh->empty[at.stage]);
         at.next();
         base.next();
@@ -781,7 +780,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
         if (!(ok = mbar_wait(&sh->ready[ext.stage], ext.phase, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
-        mma_ext<kNB>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), a.rb, acc);
+        mma_ext(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, a.rb, acc);
         mma_commit(&sh->empty[at.stage]);
         at.next();
         ext.next();
@@ -835,7 +834,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   if (!*abort_flag) {
     const uint32_t mine = smem_u32(smem) + (uint32_t)lane * 16;
     constexpr int kStep = kS * (kThreads / 32);
-#pragma unroll 2
+#pragma unroll 4
     for (int t = rank * (kThreads / 32) + warp; t < rows; t += kStep) {
       float4 s;
       if constexpr (kS == 1)
@@ -922,48 +921,53 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
-      Place at(C::kStages), base(C::kStages), ext(C::kStages);
-      bool ok = true;
-      for (int tile = first; ok && tile < total; tile += step) {
-        const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank, row0 = tt * kNB;
-        const BlockPlan* plan = plan_of(a.plan, tt);
-        // from the second tile on the plan is known to be complete: its first
-        // words are on their way while the projection's stages are loaded
-        const bool later = tile != first;
-        int n_ent = later ? plan->n_ent : 0;
-        uint4 list = later ? *reinterpret_cast<const uint4*>(plan->list) : make_uint4(0, 0, 0, 0);
+    const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
+    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    bool ok = true;
+    for (int tile = first; ok && tile < total; tile += step) {
+      const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank, row0 = tt * a.nb;
+      const BlockPlan* plan = plan_of(a.plan, tt);
+      // from the second tile on the plan is known to be complete: its words
+      // are on their way while the projection's stages are loaded
+      const bool later = tile != first;
+      int n_ent = later ? plan->n_ent : 0;
+      uint4 list = later ? load_list(plan, lane) : make_uint4(0, 0, 0, 0);
+      if (lane == 0) {
         for (int kb = 0; kb < nk; ++kb) {
           if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
             break;
-          load_base<kNB, kKMajor, true>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, kb,
-                                  mt, row0, pol_w, pol_v, rank);
+          load_base<kKMajor, true>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps,
+                                   a.nb, kb, mt, row0, pol_w, pol_v, rank);
           at.next();
           base.next();
         }
-        if (!later) {
-          pdl_wait();             // the plan and Z are complete
-          fence_async_global();
-          n_ent = plan->n_ent;
-          list = *reinterpret_cast<const uint4*>(plan->list);
-        }
-        const int q_all = n_ent * a.R;
-        for (int j = 0; ok && j * kK < q_all; ++j) {
-          if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
-            break;
-          load_ext<kNB, true>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, plan,
-                        list, q_all, j, mt, row0, pol_w, pol_v, rank);
-          at.next();
-          ext.next();
-        }
-        if (mt == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
+      } else {
+        for (int kb = 0; kb < nk; ++kb) at.next();
       }
+      if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
+      if (!later) {
+        pdl_wait();             // the plan and Z are complete
+        fence_async_global();
+        n_ent = plan->n_ent;
+        list = load_list(plan, lane);
+      }
+      const int q_all = n_ent * a.R;
+      for (int j = 0; j * kK < q_all; ++j) {
+        if (lane == 0) ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
+        if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
+        load_ext<true>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list,
+                            q_all, j, mt, row0, pol_w, pol_v, lane, rank);
+        at.next();
+        ext.next();
+      }
+      if (lane == 0 && mt == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
+    }
+    pdl_wait();
+    if (lane == 0) {
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         raise_abort();
       }
-      pdl_wait();
       drain_loads(sh->full, C::kStages, 0, base.count);
       drain_loads(sh->loaded, C::kStages, 0, ext.count);
     }
@@ -985,7 +989,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         for (int kb = 0; kb < nk; ++kb) {
           if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
           tc_fence_after();
-          mma_base<kNB, kKMajor>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), acc);
+          mma_base<kKMajor>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, acc);
           mma_commit_multicast(&sh->empty[at.stage], 0x3);
           at.next();
           base.next();
@@ -999,7 +1003,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
           if (!(ok = mbar_wait(&sh->ready[ext.stage], ext.phase, abort_flag, kWaitLimitNs)))
             break;
           tc_fence_after();
-          mma_ext<kNB>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), a.rb, acc);
+          mma_ext(d, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, a.rb, acc);
           mma_commit_multicast(&sh->empty[at.stage], 0x3);
           at.next();
           ext.next();
@@ -1042,7 +1046,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
     Place buf(2);
     for (int tile = first; tile < total; tile += step) {
       const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank;
-      const int row0 = tt * kNB, rows = min(kNB, a.T - row0);
+      const int row0 = tt * a.nb, rows = min(a.nb, a.T - row0);
       const bool got = mbar_wait(&sh->acc_full[buf.stage], buf.phase, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
@@ -1115,6 +1119,7 @@ struct WgradShared {
   int abort;
   volatile int stages;         // K stages in all, once the producer has issued them
   volatile uint32_t mask[4][2];   // the adapter's own tokens among the 64 of each stage
+  volatile int rows[4];           // rows of the stage that belong to its block
 };
 
 template <int kCols>
@@ -1192,6 +1197,7 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
               uint64_t* fb = &sh->full[at.stage];
               sh->mask[at.stage][0] = ml;
               sh->mask[at.stage][1] = mh;
+              sh->rows[at.stage] = min(64, a.nb - g * kK);
               mbar_arrive_expect_tx(fb, C::kStageBytes);
               tma_load_3d(st, &maps.v[which], fb, 0, t0, d0 >> 6, pol);
 #pragma unroll
@@ -1259,6 +1265,12 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
         break;
       }
       uint8_t* st = smem + at.stage * C::kStageBytes;
+      // rows past the block are another block's: what Z holds there, in this
+      // entry's columns, is not defined
+      for (int i = sh->rows[at.stage] * 8 + lane; i < 64 * 8; i += 32)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          reinterpret_cast<uint4*>(st + kABytes + c * 64 * kK * 2)[i] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // two rows at a time: row r is 128 bytes in each of the two feature
@@ -1340,32 +1352,43 @@ bool map_rank_atoms(CUtensorMap* m, const void* p, int n, int R, int cols, int r
   return make_tensor_map_bf16(m, p, 4, dims, st, box);
 }
 
-// CTAs per tile: the split of K (1, 2, 4 or 8 ways) that needs the fewest
-// rounds of the SMs per share of the work, at least four stages each; joining
-// more parts costs more.
-int split_of(long long tiles, int nk) {
-  int best = 1;
+// How an expand launch runs: persistent pairs of CTAs over `blocks` token blocks
+// of nb tokens (split 0), or a tile per cluster of `split` CTAs.
+struct ExpandPlan {
+  int blocks, nb, split;
+};
+// Tokens per block for a number of blocks: equal blocks, whole MMA columns.
+int block_rows(int T, int blocks) { return ((T + blocks - 1) / blocks + 15) & ~15; }
+// The cheapest of both by a cost in microseconds: a K stage of 64 takes 0.3 us
+// at 256 tokens (measured alone; its MMAs 0.27), in proportion to the tokens
+// down to 0.12 us, and a CTA's set-up, first loads and epilogue 6 us, which the
+// persistent CTAs pay once.
+ExpandPlan plan_expand(int T, int K, int M) {
+  const int nk = K / kK, sms = device_sm_count();
+  auto stage = [](int nb) { return nb > 102 ? 0.3 * nb / 256 : 0.12; };
+  const int least = (T + 255) / 256;
+  ExpandPlan best{least, block_rows(T, least), 1};
   double cost = 1e30;
   for (int s = 1; s <= 8 && (s == 1 || nk / s >= 4); s *= 2) {
-    const long long rounds = (tiles * s + device_sm_count() - 1) / device_sm_count();
-    const double c = (double)rounds / s * (s > 1 ? 1.1 : 1.0) + 0.02 * s;
+    const long long ctas = (long long)least * (M / kM) * s;
+    const double c = (double)((ctas + sms - 1) / sms) * (nk * stage(best.nb) / s + 6.0);
     if (c < cost) {
       cost = c;
-      best = s;
+      best.split = s;
+    }
+  }
+  const int pairs = sms / 2;
+  for (int blocks = least; blocks < least + 8; ++blocks) {
+    const int nb = block_rows(T, blocks);
+    if (nb <= 128) break;
+    const long long tiles = (long long)blocks * ((M / kM + 1) / 2);
+    const double c = (double)((tiles + pairs - 1) / pairs) * (nk * stage(nb) + 0.5) + 6.0;
+    if (c < cost) {
+      cost = c;
+      best = ExpandPlan{blocks, nb, 0};
     }
   }
   return best;
-}
-
-// Whether the expand launch of these sizes runs on persistent pairs: with more
-// tiles than SMs, where a split of K does not balance them better.
-bool expand_full(int nb, long long tiles, int K) {
-  return nb == FullCfg::kNB && tiles > device_sm_count() && split_of(tiles, K / kK) == 1;
-}
-// CTAs of the expand launch of these sizes.
-long long expand_ctas(const AdapterSizes& z, int K, int M) {
-  const long long tiles = (long long)z.n_tt * (M / kM);
-  return tiles * split_of(tiles, K / kK);
 }
 
 template <typename... KArgs, typename... Args>
@@ -1425,7 +1448,7 @@ cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const _
   // few blocks: the expand's tiles meet their adapters' rows cold, after the
   // projection's weights; with many blocks most of those reads hit L2 anyway
   const bool ahead = next != nullptr && z.n_tt <= 4;
-  const ShrinkArgs a{z.T, D, z.n, z.R, rb, z.zc, v,
+  const ShrinkArgs a{z.T, z.nb, D, z.n, z.R, rb, z.zc, v,
                      ahead ? reinterpret_cast<const char*>(next) : nullptr,
                      (long long)z.R * next_cols * 2, adapter_idx, scale, Z, plan, masks, status,
                      first};
@@ -1437,17 +1460,20 @@ cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const _
   // meanwhile and a tile that waited for shrink's SMs came out last (8 of 128
   // tiles, 18 us late).
   if (z.n_tt == 1 && ctas < sms && sms - ctas >= 8) sms -= (int)ctas;
+  // clusters of eight do not tile the GPU's processing clusters: more than
+  // three quarters of the SMs' worth of them run in two rounds (16 blocks of
+  // 4096 tokens: 30 us against 18)
   int cluster = 8;
-  while (cluster > 1 && (z.n_tt * cluster > sms || D / kK / cluster < 4)) cluster /= 2;
+  while (cluster > 1 && (z.n_tt * cluster > (cluster == 8 ? sms * 3 / 4 : sms) ||
+                         D / kK / cluster < 4))
+    cluster /= 2;
   const int most = (z.zc / kM * 8 + cluster - 1) / cluster;   // up to eight CTAs per unit
   int gy = sms / (z.n_tt * cluster);
   gy = gy < 1 ? 1 : gy > most ? most : gy;
-  switch (z.nb) {
-    case 32: return launch_shrink_nb<32>(cluster, gy, m, a, z.n_tt, s);
-    case 64: return launch_shrink_nb<64>(cluster, gy, m, a, z.n_tt, s);
-    case 128: return launch_shrink_nb<128>(cluster, gy, m, a, z.n_tt, s);
-    default: return launch_shrink_nb<256>(cluster, gy, m, a, z.n_tt, s);
-  }
+  if (z.nb <= 32) return launch_shrink_nb<32>(cluster, gy, m, a, z.n_tt, s);
+  if (z.nb <= 64) return launch_shrink_nb<64>(cluster, gy, m, a, z.n_tt, s);
+  if (z.nb <= 128) return launch_shrink_nb<128>(cluster, gy, m, a, z.n_tt, s);
+  return launch_shrink_nb<256>(cluster, gy, m, a, z.n_tt, s);
 }
 
 template <int kNB, bool kKMajor>
@@ -1471,18 +1497,14 @@ cudaError_t launch_split_nb(int split, const ExpandMaps& m, const ExpandArgs& a,
 }
 
 template <bool kKMajor>
-cudaError_t launch_expand_t(int nb, const ExpandMaps& m, const ExpandArgs& a, cudaStream_t s) {
-  const long long tiles = (long long)a.n_tt * (a.M / kM);
-  const int split = split_of(tiles, a.K / kK);
-  if (expand_full(nb, tiles, a.K))
+cudaError_t launch_expand_t(int split, const ExpandMaps& m, const ExpandArgs& a, cudaStream_t s) {
+  if (split == 0)
     return launch_cluster(adapter_expand_kernel<kKMajor>, dim3(device_sm_count() / 2 * 2), 2,
                           FullCfg::kSmemBytes, true, s, m, a);
-  switch (nb) {
-    case 32: return launch_split_nb<32, kKMajor>(split, m, a, s);
-    case 64: return launch_split_nb<64, kKMajor>(split, m, a, s);
-    case 128: return launch_split_nb<128, kKMajor>(split, m, a, s);
-    default: return launch_split_nb<256, kKMajor>(split, m, a, s);
-  }
+  if (a.nb <= 32) return launch_split_nb<32, kKMajor>(split, m, a, s);
+  if (a.nb <= 64) return launch_split_nb<64, kKMajor>(split, m, a, s);
+  if (a.nb <= 128) return launch_split_nb<128, kKMajor>(split, m, a, s);
+  return launch_split_nb<256, kKMajor>(split, m, a, s);
 }
 
 // out [T, M] = v [T, K] W + Z P, with P [n, R, M]; W [K, M] or (k_major) [M, K].
@@ -1492,26 +1514,32 @@ cudaError_t launch_expand(const AdapterSizes& z, const __nv_bfloat16* v, const _
                           cudaStream_t s) {
   ExpandMaps m;
   const int rb = rank_box(z.R);
-  const int box = expand_full(z.nb, (long long)z.n_tt * (M / kM), K) ? z.nb / 2 : z.nb;
+  const int box = z.split == 0 ? z.nb / 2 : z.nb;
   if (!(k_major ? map_rows(&m.w, W, M, K, kM) : map_atoms(&m.w, W, K, M)) ||
       !map_rows(&m.v, v, z.T, K, box) || !map_rank_atoms(&m.p, P, z.n, z.R, M, rb) ||
       !map_rows(&m.z, Z, z.T, z.zc, box))
     return cudaErrorInvalidValue;
-  const ExpandArgs a{z.T, K, M, z.n, z.R, rb, z.n_tt, out, plan, status};
-  return k_major ? launch_expand_t<true>(z.nb, m, a, s) : launch_expand_t<false>(z.nb, m, a, s);
+  const ExpandArgs a{z.T, z.nb, K, M, z.n, z.R, rb, z.n_tt, out, plan, status};
+  return k_major ? launch_expand_t<true>(z.split, m, a, s)
+                 : launch_expand_t<false>(z.split, m, a, s);
 }
 
 }  // namespace
 
-AdapterSizes adapter_sizes(int T, int H, int N, int n, int R) {
+AdapterSizes adapter_sizes(int T, int H, int N, int n, int R, bool backward) {
   AdapterSizes z{};
   z.T = T;
   z.H = H;
   z.N = N;
   z.n = n;
   z.R = R;
-  z.nb = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  z.n_tt = (T + z.nb - 1) / z.nb;
+  const ExpandPlan e = T > 0 ? (backward ? plan_expand(T, N, H) : plan_expand(T, H, N))
+                             : ExpandPlan{0, 16, 1};
+  z.nb = e.nb;
+  z.n_tt = (T + e.nb - 1) / e.nb;
+  z.split = e.split;
+  // CTAs of the expand launch, of which one block's shrink keeps clear
+  z.ctas = e.split ? (long long)z.n_tt * ((backward ? H : N) / kM) * e.split : device_sm_count();
   const int entries = n < z.nb ? n : z.nb;
   z.zc = (int)align_up((size_t)entries * R, kM);
   size_t o = 1024;   // the status word
@@ -1519,11 +1547,13 @@ AdapterSizes adapter_sizes(int T, int H, int N, int n, int R) {
   o += (size_t)z.n_tt * kAdapterPlanBytes;
   z.z = o;
   o = align_up(o + (size_t)T * z.zc * 2, 1024);
+  if (backward) {
+    z.dz = o;
+    o = align_up(o + (size_t)T * z.zc * 2, 1024);
+    z.masks = o;
+    o = align_up(o + (size_t)z.n_tt * kMaxEntries * 8 * 4, 1024);
+  }
   z.total = o;
-  z.dz = o;
-  o = align_up(o + (size_t)T * z.zc * 2, 1024);
-  z.masks = o;
-  z.total_backward = align_up(o + (size_t)z.n_tt * kMaxEntries * 8 * 4, 1024);
   return z;
 }
 
@@ -1536,7 +1566,7 @@ cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x
   void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
   cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, nullptr, Z, status,
-                                  true, expand_ctas(z, z.H, z.N), B, z.N, s);
+                                  true, z.ctas, B, z.N, s);
   if (err != cudaSuccess) return err;
   return launch_expand(z, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
 }
@@ -1557,7 +1587,7 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
                                   true, sms, nullptr, 0, s);
   if (err == cudaSuccess)
     err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, nullptr, dZ, status, false,
-                        expand_ctas(z, z.N, z.H), A, z.H, s);
+                        z.ctas, A, z.H, s);
   if (err == cudaSuccess) err = launch_expand(z, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
   if (err != cudaSuccess) return err;
   WgradMaps m;

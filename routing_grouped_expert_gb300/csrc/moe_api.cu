@@ -769,12 +769,14 @@ bool ok_adapter_sizes(int T, int H, int N, int n, int R) {
 
 size_t moe_adapter_workspace_size(int T, int H, int N, int n, int R) {
   if (!ok_adapter_sizes(T, H, N, n, R)) return 0;
-  return adapter_sizes(T, H, N, n, R).total;
+  return adapter_sizes(T, H, N, n, R, false).total;
 }
 
 size_t moe_adapter_workspace_size_backward(int T, int H, int N, int n, int R) {
   if (!ok_adapter_sizes(T, H, N, n, R)) return 0;
-  return adapter_sizes(T, H, N, n, R).total_backward;
+  const size_t forward = adapter_sizes(T, H, N, n, R, false).total;
+  const size_t backward = adapter_sizes(T, H, N, n, R, true).total;
+  return forward > backward ? forward : backward;
 }
 
 moe_status moe_adapter_project(const void* x, const void* W, const void* A, const void* B,
@@ -786,7 +788,7 @@ moe_status moe_adapter_project(const void* x, const void* W, const void* A, cons
   if (!ok_ptr(x) || !ok_ptr(W) || !ok_ptr(A) || !ok_ptr(B) || !ok_ptr(scale) ||
       !ok_ptr(adapter_idx) || !ok_ptr(y))
     return MOE_ERR_INVALID_ARG;
-  const AdapterSizes z = adapter_sizes(T, H, N, n, R);
+  const AdapterSizes z = adapter_sizes(T, H, N, n, R, false);
   if (check_ws(ws, ws_bytes, z.total) != MOE_OK) return MOE_ERR_WORKSPACE;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -806,8 +808,8 @@ moe_status moe_adapter_project_backward(const void* dy, const void* x, const voi
   if (T > 0 && (!ok_ptr(dy) || !ok_ptr(x) || !ok_ptr(W) || !ok_ptr(A) || !ok_ptr(B) ||
                 !ok_ptr(scale) || !ok_ptr(adapter_idx) || !ok_ptr(dx)))
     return MOE_ERR_INVALID_ARG;
-  const AdapterSizes z = adapter_sizes(T, H, N, n, R);
-  if (check_ws(ws, ws_bytes, z.total_backward) != MOE_OK) return MOE_ERR_WORKSPACE;
+  const AdapterSizes z = adapter_sizes(T, H, N, n, R, true);
+  if (check_ws(ws, ws_bytes, z.total) != MOE_OK) return MOE_ERR_WORKSPACE;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0) {   // no token: zero gradients

@@ -417,13 +417,15 @@ constexpr int kAdapterPlanBytes = 1024;
 struct AdapterSizes {
   int T, H, N, n, R;
   int nb, n_tt;       // tokens per block, blocks
+  int split;          // CTAs per tile of the expand launch; 0: persistent pairs
+  long long ctas;     // CTAs of the expand launch
   int zc;             // columns of Z: R for every adapter a block can meet, rounded up to 128
   size_t plan;        // [n_tt][kAdapterPlanBytes]  the adapters of each block
   size_t z, dz;       // bf16[T][zc]
   size_t masks;       // uint32[n_tt][256][8]  the tokens of each block's adapters, as bits
-  size_t total, total_backward;
+  size_t total;
 };
-AdapterSizes adapter_sizes(int T, int H, int N, int n, int R);
+AdapterSizes adapter_sizes(int T, int H, int N, int n, int R, bool backward);
 cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x,
                                    const __nv_bfloat16* W, const __nv_bfloat16* A,
                                    const __nv_bfloat16* B, const float* scale,

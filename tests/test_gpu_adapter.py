@@ -41,6 +41,8 @@ CASES = [  # T, H, N, n, R, order
     (128, 1024, 128, 40, 40, "shuffled"),
     (515, 7168, 128, 24, 64, "shuffled"),
     (2049, 512, 2432, 8, 16, "shuffled"),      # an odd number of feature tiles in pairs
+    (1025, 256, 5120, 9, 8, "segments"),       # blocks that are no multiple of 64 tokens
+    (140, 512, 128, 20, 32, "distinct"),
 ]
 
 
