@@ -120,7 +120,7 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int from
 //
 // A block of several units whose entries have few tokens each (at most 64 per
 // unit) gathers a unit's own tokens instead of multiplying every token of the
-// block by every rank row: five warps copy the rows' 128 bytes of each stage
+// block by every rank row: two warps copy the rows' 128 bytes of each stage
 // by 16-byte asynchronous copies into the swizzled operand.  (TMA
 // tile::gather4 took about 16 ns a row: 777 tokens of 24 adapters of rank 64
 // spent 31 us on the gathers.)
@@ -143,7 +143,8 @@ struct ShrinkArgs {
   bool first;               // the first kernel of the call: clears the status, writes the plan
 };
 constexpr int kGatherRows = 64;   // most tokens of a unit that gathers
-constexpr int kRowWarps = 5;      // warps 2 .. 6
+constexpr int kRowWarps = 2;      // warps 2 and 3 copy them
+constexpr int kRowPieces = kGatherRows * 8 / (32 * kRowWarps);   // 16-byte pieces per thread
 template <int kNB>
 struct ShrinkCfg {
   static constexpr int kStageBytes = kABytes + kNB * kK * 2;
@@ -429,7 +430,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
         if (!(ok = mbar_wait(&sh->full[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
         // copied rows: ordinary writes that the MMA reads through the async
         // proxy.  The fence is taken here, by a thread without copies in flight:
-        // in the copying threads it waits for all of theirs (0.3 us a stage)
+        // in the copying threads it waits for all of theirs
         if (gather) fence_async_smem();
         tc_fence_after();
         const uint32_t a0 = sbase + (uint32_t)(at.stage * stage_bytes), b0 = a0 + kABytes;
@@ -449,24 +450,27 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       if (!mbar_wait(&sh->drain, parity, nullptr, kWaitLimitNs))
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
-    if (C::kGather && gather && have && warp >= 2) {
+    if (C::kGather && gather && have && warp >= 2 && warp < 2 + kRowWarps) {
       // this thread's 16-byte pieces: piece c of row j, at the swizzled place
       const int n_piece = n_mma * 8;
-      const __nv_bfloat16* src[4];
-      uint32_t dst[4];
+      const __nv_bfloat16* src[kRowPieces];
+      uint32_t dst[kRowPieces];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kRowPieces; ++i) {
         const int piece = (int)threadIdx.x - 64 + i * (32 * kRowWarps), j = piece >> 3, c = piece & 7;
         dst[i] = piece < n_piece ? (uint32_t)(kABytes + j * 128 + ((c ^ (j & 7)) << 4)) : 0u;
         // rows up to a multiple of 16 repeat the last token
         src[i] = a.rows + (size_t)(row0 + (int)sh->tok[min(j, n_tok - 1)]) * a.K + c * 8;
       }
       const uint32_t sbase = smem_u32(smem);
+      // every thread arrives when its copies land (64 arrivals a stage; 160, of
+      // five warps, took 0.24 us by themselves, and waiting for the copies of
+      // an earlier stage before announcing it keeps slots of the ring idle)
       for (int kb = kb0; kb < kb1; ++kb) {
         const bool ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
         if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kRowPieces; ++i)
           if (dst[i]) cp_async16(sbase + at.stage * stage_bytes + dst[i], src[i] + (size_t)kb * kK);
         cp_async_arrive(&sh->full[at.stage]);
         at.next();
