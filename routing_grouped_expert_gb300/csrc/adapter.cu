@@ -88,6 +88,54 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
   return r;
 }
 
+// The role loops run warp-uniform: every lane waits and counts, one lane issues.
+// TMA and MMA instructions take their operands from uniform registers, so in
+// code that a single lane runs alone each operand is first moved there (a
+// producer of two boxes took 500 cycles a stage that way, an MMA warp 430).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15) == 0 && (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+// Wait for the phase with `parity` of the barrier at shared address `bar`;
+// bounded as ptx::mbar_wait.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok ? true : wait_slow(bar, parity, abort_flag);
+}
+// A 128-byte-swizzled operand descriptor from its two words (see
+// ptx::sdesc_sw128): the first word moves with the address >> 4.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  return ((uint64_t)hi << 32) | lo;
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  // in a cluster the address carries the CTA's rank above its 18 offset bits
+  return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+
 // One role's place in a ring of n stages and their barriers.
 struct Place {
   int n;
@@ -291,7 +339,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   ShrinkShared* sh = reinterpret_cast<ShrinkShared*>(smem + C::kRing);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = kC > 1 ? (int)cluster_ctarank() : 0;
   const int tt = (int)blockIdx.x / kC;
   const int row0 = tt * a.nb, rows = min(a.nb, a.T - row0);
@@ -362,6 +410,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
+  const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty);
   const int stage_bytes = gather ? C::kGatherBytes : C::kStageBytes;
   const int stages = gather ? C::kGatherStages : C::kStages;
   Place at(stages);
@@ -391,64 +440,74 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
     }
     const int n_tok = gather && have ? sh->n_tok : rows;   // rows of the partial tile
     const int n_mma = gather ? (n_tok + 15) & ~15 : a.nb;
-    if (have && warp == 0) {
+    // Warps 0, 4, 5 and 6 load the boxes of rank rows (box i: the i-th of them),
+    // warp 0 the token rows too; rank rows past the last entry keep what the
+    // stage held: their products are not read.
+    const int loader = warp == 0 ? 0 : warp >= 4 ? warp - 3 : -1;
+    if (have && loader >= 0) {
       const uint64_t pol_p = policy_evict_normal(), pol_v = policy_evict_last();
+      const bool leader = elect_lane();
       const int from = at.count;
       const uint32_t bytes = (uint32_t)((q_end + (gather ? 0 : a.nb)) * kK * 2);
-      // this lane's box of rank rows (rows past the last entry keep what the
-      // stage held: their products are not read)
-      const int q = lane * a.rb, e = (u * kM + q) / a.R;
-      const bool box = q < q_end;
-      const int p_row = u * kM + q - e * a.R, p_ad = box ? (int)sh->list[e] : 0;
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
-        uint64_t* fb = &sh->full[at.stage];
-        if (lane == 0) {
-          ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
-          if (ok) mbar_arrive_expect_tx(fb, bytes);
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
         if (!ok) break;
+        uint64_t* fb = &sh->full[at.stage];
         uint8_t* st = smem + at.stage * stage_bytes;
-        if (!gather && lane == 0)
-          tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
-        if (box) tma_load_3d(st + q * (kK * 2), &maps.p, fb, kb * kK, p_row, p_ad, pol_p);
+        if (loader == 0 && leader) {
+          mbar_arrive_expect_tx(fb, bytes);
+          if (!gather) tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
+        }
+        for (int q = loader * a.rb; q < q_end; q += 4 * a.rb) {
+          const int e = (u * kM + q) / a.R;
+          const int row = u * kM + q - e * a.R, ad = (int)sh->list[e];
+          if (leader) tma_load_3d(st + q * (kK * 2), &maps.p, fb, kb * kK, row, ad, pol_p);
+        }
         at.next();
       }
-      if (lane == 0) {
-        if (!ok) {
-          set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
-          *abort_flag = 1;
-        }
-        drain_loads(sh->full, stages, from, at.count);
+      if (leader && !ok) {
+        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
+        *abort_flag = 1;
       }
-    } else if (have && warp == 1 && lane == 0) {
+      if (loader == 0 && leader) drain_loads(sh->full, stages, from, at.count);
+      __syncwarp();
+    } else if (have && warp == 1) {
       const uint32_t sbase = smem_u32(smem);
       const uint32_t idesc = idesc_bf16(kM, n_mma, false, false);
+      const bool leader = elect_lane();
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(&sh->full[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
+        ok = wait_bar(full0 + at.stage * 8, at.phase, abort_flag);
+        if (!ok) break;
         // copied rows: ordinary writes that the MMA reads through the async
         // proxy.  The fence is taken here, by a thread without copies in flight:
         // in the copying threads it waits for all of theirs
         if (gather) fence_async_smem();
         tc_fence_after();
-        const uint32_t a0 = sbase + (uint32_t)(at.stage * stage_bytes), b0 = a0 + kABytes;
+        // K-major operands: 8-row groups 1 KB apart, 16 K = 32 bytes
+        const uint32_t la = desc_lo(sbase + (uint32_t)(at.stage * stage_bytes), 16);
+        const uint32_t lb = la + (kABytes >> 4);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < kK / 16; ++kk)
-          mma_bf16_ss(tmem, sdesc_sw128(a0 + kk * 32, 16, 1024), sdesc_sw128(b0 + kk * 32, 16, 1024),
-                      idesc, (kb > kb0 || kk) ? 1u : 0u);
-        mma_commit(&sh->empty[at.stage]);
+          for (int kk = 0; kk < kK / 16; ++kk)
+            mma_bf16_ss(tmem, desc_of(la + 2 * kk, desc_hi(1024)), desc_of(lb + 2 * kk, desc_hi(1024)),
+                        idesc, (kb > kb0 || kk) ? 1u : 0u);
+          mma_commit(&sh->empty[at.stage]);
+        }
         at.next();
       }
-      if (!ok) {
-        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
-        *abort_flag = 1;
+      if (leader) {
+        if (!ok) {
+          set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
+          *abort_flag = 1;
+        }
+        mma_commit(&sh->acc_full);
+        mma_commit(&sh->drain);
+        if (!mbar_wait(&sh->drain, parity, nullptr, kWaitLimitNs))
+          set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
       }
-      mma_commit(&sh->acc_full);
-      mma_commit(&sh->drain);
-      if (!mbar_wait(&sh->drain, parity, nullptr, kWaitLimitNs))
-        set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
+      __syncwarp();
     }
     if (C::kGather && gather && have && warp >= 2 && warp < 2 + kRowWarps) {
       // this thread's 16-byte pieces: piece c of row j, at the swizzled place
@@ -467,8 +526,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       // five warps, took 0.24 us by themselves, and waiting for the copies of
       // an earlier stage before announcing it keeps slots of the ring idle)
       for (int kb = kb0; kb < kb1; ++kb) {
-        const bool ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag)) break;
 #pragma unroll
         for (int i = 0; i < kRowPieces; ++i)
           if (dst[i]) cp_async16(sbase + at.stage * stage_bytes + dst[i], src[i] + (size_t)kb * kK);
@@ -476,7 +534,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
         at.next();
       }
       asm volatile("cp.async.wait_all;" ::: "memory");   // none is in flight when the CTA leaves
-    } else if (have && warp >= 2) {
+    } else if (have && (warp == 2 || warp == 3)) {
       for (int kb = kb0; kb < kb1; ++kb) at.next();
     }
     const int q = warp & 3;   // TMEM lanes 32 q ..
@@ -594,48 +652,46 @@ __device__ __forceinline__ int list_entry(const uint4& list, int e) {
 }
 // Stage j of the adapters' part, by the whole producer warp: 64 rank rows of
 // the block's entries, in boxes of rb rows, each [2 feature atoms][rb rows][128
-// bytes], one box per lane.
+// bytes].
 template <bool kPair = false>
 __device__ __forceinline__ void load_ext(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
                                          const ExpandArgs& a, const uint4& list, int q_all, int j,
                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v,
-                                         int lane, int rank = 0) {
-  if (lane == 0) {
+                                         bool leader, int rank = 0) {
+  if (leader) {
     mbar_arrive_expect_tx(fb, (uint32_t)(kABytes + a.nb * kK * 2));
     load_tokens<kPair>(st + kABytes, fb, &maps.z, a.nb, j * kK, row0, pol_v, rank);
   }
-  __syncwarp();
-  const int q = lane * a.rb, qq = j * kK + q, e = qq / a.R;
-  const int known = list_entry(list, e);
-  // past the last entry: an adapter that does not exist, read as zeros
-  if (q < kK)
-    tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, qq - e * a.R, mt * 2, qq < q_all ? known : a.n,
-                pol_w);
-}
-template <bool kKMajor>
-__device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, int nb, uint32_t& acc) {
-  const uint32_t idesc = idesc_bf16(kM, nb, /*a_mn=*/!kKMajor, false);
-  const uint32_t b0 = a0 + kABytes;
-#pragma unroll
-  for (int kk = 0; kk < kK / 16; ++kk) {
-    // MN-major weights: 64-feature atoms 8 KB apart, 16 K rows = 2 KB; K-major
-    // operands: 8-row groups 1 KB apart, 16 K = 32 bytes
-    const uint64_t da = kKMajor ? sdesc_sw128(a0 + kk * 32, 16, 1024)
-                                : sdesc_sw128(a0 + kk * 2048, 8192, 1024);
-    mma_bf16_ss(tmem, da, sdesc_sw128(b0 + kk * 32, 16, 1024), idesc, acc);
-    acc = 1u;
+  for (int q = 0; q < kK; q += a.rb) {
+    const int qq = j * kK + q, e = qq / a.R;
+    const int known = list_entry(list, e);
+    // past the last entry: an adapter that does not exist, read as zeros
+    const int ad = qq < q_all ? known : a.n;
+    if (leader)
+      tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, qq - e * a.R, mt * 2, ad, pol_w);
   }
 }
-__device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, int nb, int rb, uint32_t& acc) {
-  const uint32_t idesc = idesc_bf16(kM, nb, /*a_mn=*/true, false);
-  const uint32_t b0 = a0 + kABytes;
-  const uint32_t lbo = (uint32_t)rb * 128, sbo = rb == 8 ? 2048u : 1024u;
+// The four MMAs of a stage at shared address a0 (one lane).
+template <bool kKMajor>
+__device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, uint32_t idesc, uint32_t first) {
+  // MN-major weights: 64-feature atoms 8 KB apart, 16 K rows = 2 KB; K-major
+  // operands: 8-row groups 1 KB apart, 16 K = 32 bytes
+  const uint32_t la = kKMajor ? desc_lo(a0, 16) : desc_lo(a0, 8192);
+  const uint32_t lb = desc_lo(a0 + kABytes, 16);
+#pragma unroll
+  for (int kk = 0; kk < kK / 16; ++kk)
+    mma_bf16_ss(tmem, desc_of(la + (kKMajor ? 2 : 128) * kk, desc_hi(1024)),
+                desc_of(lb + 2 * kk, desc_hi(1024)), idesc, kk ? 1u : first);
+}
+// The same of an adapters' stage: MN-major boxes of rb rank rows.
+__device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, uint32_t idesc, int rb) {
+  const uint32_t lb = desc_lo(a0 + kABytes, 16);
+  const uint32_t lbo = (uint32_t)rb * 128, hi = desc_hi(rb == 8 ? 2048u : 1024u);
 #pragma unroll
   for (int kk = 0; kk < kK / 16; ++kk) {
-    const uint32_t q = 16u * kk, box = q / rb;
-    const uint32_t at = a0 + box * (uint32_t)rb * 256 + (q - box * rb) * 128;
-    mma_bf16_ss(tmem, sdesc_sw128(at, lbo, sbo), sdesc_sw128(b0 + kk * 32, 16, 1024), idesc, acc);
-    acc = 1u;
+    const uint32_t q = 16u * kk, in = q & (uint32_t)(rb - 1);   // rb: a power of two
+    const uint32_t la = desc_lo(a0 + (q - in) * 256 + in * 128, lbo);
+    mma_bf16_ss(tmem, desc_of(la, hi), desc_of(lb + 2 * kk, desc_hi(1024)), idesc, 1u);
   }
 }
 // The guard warp's pass over the 64 x 128 adapter weights of a stage: every
@@ -695,7 +751,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   SplitShared* sh = reinterpret_cast<SplitShared*>(smem + C::kRing);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = kS > 1 ? (int)cluster_ctarank() : 0;
   const int tile = (int)blockIdx.x / kS;
   const int tt = tile % a.n_tt, mt = tile / a.n_tt;
@@ -725,38 +781,40 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
+  const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty);
+  const uint32_t ready0 = smem_u32(sh->ready);
 
   if (warp == 0) {
     // a weight tile read by one block is streamed past L2
     const uint64_t pol_w = a.n_tt == 1 ? policy_evict_first() : policy_evict_normal();
     const uint64_t pol_v = policy_evict_last();
+    const bool leader = elect_lane();
     Place at(C::kStages), base(C::kStages), ext(C::kStages);
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (lane == 0) {
-        ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
-        if (ok)
-          load_base<kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, a.nb, kb,
-                             mt, row0, pol_w, pol_v);
-      }
-      if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
+      if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
+      if (leader)
+        load_base<kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, a.nb, kb, mt,
+                           row0, pol_w, pol_v);
       at.next();
       base.next();
     }
+    __syncwarp();
     pdl_wait();             // the plan and Z are complete
     fence_async_global();
     const int q_all = plan->n_ent * a.R;
     const uint4 list = load_list(plan, lane);
     const int ne = (q_all + kK - 1) / kK;
+    ok = __all_sync(0xffffffffu, ok);
     for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
-      if (lane == 0) ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
-      if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
-      load_ext<>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list, q_all, j,
-                    mt, row0, pol_w, pol_v, lane);
+      ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      load_ext<>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list, q_all, j, mt,
+                 row0, pol_w, pol_v, leader);
       at.next();
       ext.next();
     }
-    if (lane == 0) {
+    if (leader) {
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         *abort_flag = 1;
@@ -766,29 +824,37 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       drain_loads(sh->loaded, C::kStages, 0, ext.count);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t sbase = smem_u32(smem);
-      Place at(C::kStages), base(C::kStages), ext(C::kStages);
-      uint32_t acc = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
-        tc_fence_after();
-        mma_base<kKMajor>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, acc);
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t id_base = idesc_bf16(kM, a.nb, /*a_mn=*/!kKMajor, false);
+    const uint32_t id_ext = idesc_bf16(kM, a.nb, /*a_mn=*/true, false);
+    const bool leader = elect_lane();
+    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!(ok = wait_bar(full0 + base.stage * 8, base.phase, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+        mma_base<kKMajor>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), id_base,
+                          kb > kb0 ? 1u : 0u);
         mma_commit(&sh->empty[at.stage]);
-        at.next();
-        base.next();
       }
-      pdl_wait();
-      const int ne = (plan->n_ent * a.R + kK - 1) / kK;
-      for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
-        if (!(ok = mbar_wait(&sh->ready[ext.stage], ext.phase, abort_flag, kWaitLimitNs))) break;
-        tc_fence_after();
-        mma_ext(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, a.rb, acc);
+      at.next();
+      base.next();
+    }
+    __syncwarp();
+    pdl_wait();
+    const int ne = (plan->n_ent * a.R + kK - 1) / kK;
+    for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
+      if (!(ok = wait_bar(ready0 + ext.stage * 8, ext.phase, abort_flag))) break;
+      tc_fence_after();
+      if (leader) {
+        mma_ext(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), id_ext, a.rb);
         mma_commit(&sh->empty[at.stage]);
-        at.next();
-        ext.next();
       }
+      at.next();
+      ext.next();
+    }
+    if (leader) {
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
         *abort_flag = 1;
@@ -888,7 +954,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   FullShared* sh = reinterpret_cast<FullShared*>(smem + C::kRing);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int nk = a.K / kK;
   const int rank = (int)cluster_ctarank();
   const int n_mp = (a.M / kM + 1) / 2;      // pairs of feature tiles (the last may be half empty)
@@ -924,8 +990,12 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
     st_cluster_u32(mapa_shared(smem_u32(&sh->abort), (uint32_t)(rank ^ 1)), 1u);
   };
 
+  const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty);
+  const uint32_t ready0 = smem_u32(sh->ready);
+
   if (warp == 0) {
     const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
+    const bool leader = elect_lane();
     Place at(C::kStages), base(C::kStages), ext(C::kStages);
     bool ok = true;
     for (int tile = first; ok && tile < total; tile += step) {
@@ -936,19 +1006,16 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       const bool later = tile != first;
       int n_ent = later ? plan->n_ent : 0;
       uint4 list = later ? load_list(plan, lane) : make_uint4(0, 0, 0, 0);
-      if (lane == 0) {
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!(ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs)))
-            break;
-          load_base<kKMajor, true>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps,
-                                   a.nb, kb, mt, row0, pol_w, pol_v, rank);
-          at.next();
-          base.next();
-        }
-      } else {
-        for (int kb = 0; kb < nk; ++kb) at.next();
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
+        if (leader)
+          load_base<kKMajor, true>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, a.nb,
+                                   kb, mt, row0, pol_w, pol_v, rank);
+        at.next();
+        base.next();
       }
-      if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
+      __syncwarp();
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (!later) {
         pdl_wait();             // the plan and Z are complete
         fence_async_global();
@@ -957,17 +1024,17 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       }
       const int q_all = n_ent * a.R;
       for (int j = 0; j * kK < q_all; ++j) {
-        if (lane == 0) ok = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
-        if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
-        load_ext<true>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list,
-                            q_all, j, mt, row0, pol_w, pol_v, lane, rank);
+        ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        load_ext<true>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list, q_all,
+                       j, mt, row0, pol_w, pol_v, leader, rank);
         at.next();
         ext.next();
       }
-      if (lane == 0 && mt == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
+      if (leader && mt == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
     }
     pdl_wait();
-    if (lane == 0) {
+    if (leader) {
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         raise_abort();
@@ -976,46 +1043,52 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       drain_loads(sh->loaded, C::kStages, 0, ext.count);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t sbase = smem_u32(smem);
-      Place at(C::kStages), base(C::kStages), ext(C::kStages);
-      Place buf(2);
-      bool ok = true;
-      for (int tile = first; ok && tile < total; tile += step) {
-        if (!(ok = mbar_wait(&sh->acc_empty[buf.stage], buf.phase ^ 1u, abort_flag, kWaitLimitNs)))
-          break;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t id_base = idesc_bf16(kM, a.nb, /*a_mn=*/!kKMajor, false);
+    const uint32_t id_ext = idesc_bf16(kM, a.nb, /*a_mn=*/true, false);
+    const bool leader = elect_lane();
+    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    Place buf(2);
+    bool ok = true;
+    for (int tile = first; ok && tile < total; tile += step) {
+      if (!(ok = mbar_wait(&sh->acc_empty[buf.stage], buf.phase ^ 1u, abort_flag, kWaitLimitNs)))
+        break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(buf.stage * kNB);
+      const BlockPlan* plan = plan_of(a.plan, tile % a.n_tt);
+      const bool later = tile != first;
+      int n_ent = later ? plan->n_ent : 0;   // early, as the producer's
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!(ok = wait_bar(full0 + base.stage * 8, base.phase, abort_flag))) break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf.stage * kNB);
-        const BlockPlan* plan = plan_of(a.plan, tile % a.n_tt);
-        const bool later = tile != first;
-        int n_ent = later ? plan->n_ent : 0;   // early, as the producer's
-        uint32_t acc = 0;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!(ok = mbar_wait(&sh->full[base.stage], base.phase, abort_flag, kWaitLimitNs))) break;
-          tc_fence_after();
-          mma_base<kKMajor>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, acc);
+        if (leader) {
+          mma_base<kKMajor>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), id_base, kb ? 1u : 0u);
           mma_commit_multicast(&sh->empty[at.stage], 0x3);
-          at.next();
-          base.next();
         }
-        if (!later) {
-          pdl_wait();
-          n_ent = plan->n_ent;
-        }
-        const int q_all = n_ent * a.R;
-        for (int j = 0; ok && j * kK < q_all; ++j) {
-          if (!(ok = mbar_wait(&sh->ready[ext.stage], ext.phase, abort_flag, kWaitLimitNs)))
-            break;
-          tc_fence_after();
-          mma_ext(d, sbase + (uint32_t)(at.stage * C::kStageBytes), a.nb, a.rb, acc);
-          mma_commit_multicast(&sh->empty[at.stage], 0x3);
-          at.next();
-          ext.next();
-        }
-        if (!ok) break;
-        mma_commit(&sh->acc_full[buf.stage]);
-        buf.next();
+        at.next();
+        base.next();
       }
+      __syncwarp();
+      if (!later) {
+        pdl_wait();
+        n_ent = plan->n_ent;
+      }
+      const int q_all = n_ent * a.R;
+      for (int j = 0; ok && j * kK < q_all; ++j) {
+        if (!(ok = wait_bar(ready0 + ext.stage * 8, ext.phase, abort_flag))) break;
+        tc_fence_after();
+        if (leader) {
+          mma_ext(d, sbase + (uint32_t)(at.stage * C::kStageBytes), id_ext, a.rb);
+          mma_commit_multicast(&sh->empty[at.stage], 0x3);
+        }
+        at.next();
+        ext.next();
+      }
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (leader) mma_commit(&sh->acc_full[buf.stage]);
+      buf.next();
+    }
+    if (leader) {
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
         raise_abort();
@@ -1134,7 +1207,7 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   WgradShared* sh = reinterpret_cast<WgradShared*>(smem + C::kRing);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int units0 = a.n * (a.D[0] / kM);
   const int which = (int)blockIdx.x < units0 ? 0 : 1;
   const int unit = (int)blockIdx.x - (which ? units0 : 0);
@@ -1164,6 +1237,8 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   volatile int* abort_flag = &sh->abort;
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
+    const bool leader = elect_lane();
+    const uint32_t empty0 = smem_u32(sh->empty);
     Place at(C::kStages);
     bool ok = true;
     for (int tb = 0; ok && tb < a.n_tt; tb += 32) {
@@ -1193,24 +1268,21 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
           const uint32_t mh = __shfl_sync(0xffffffffu, hi[g], src);
           if (!ok || (ml | mh) == 0u) continue;   // no token of ad in this group
           const int t0 = (tb + src) * a.nb + g * kK;
-          int got = 1;
-          if (lane == 0) {
-            got = mbar_wait(&sh->empty[at.stage], at.phase ^ 1u, abort_flag, kWaitLimitNs);
-            if (got) {
-              uint8_t* st = smem + at.stage * C::kStageBytes;
-              uint64_t* fb = &sh->full[at.stage];
-              sh->mask[at.stage][0] = ml;
-              sh->mask[at.stage][1] = mh;
-              sh->rows[at.stage] = min(64, a.nb - g * kK);
-              mbar_arrive_expect_tx(fb, C::kStageBytes);
-              tma_load_3d(st, &maps.v[which], fb, 0, t0, d0 >> 6, pol);
+          ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && leader) {
+            uint8_t* st = smem + at.stage * C::kStageBytes;
+            uint64_t* fb = &sh->full[at.stage];
+            sh->mask[at.stage][0] = ml;
+            sh->mask[at.stage][1] = mh;
+            sh->rows[at.stage] = min(64, a.nb - g * kK);
+            mbar_arrive_expect_tx(fb, C::kStageBytes);
+            tma_load_3d(st, &maps.v[which], fb, 0, t0, d0 >> 6, pol);
 #pragma unroll
-              for (int c = 0; c < kCols; ++c)
-                tma_load_2d(st + kABytes + c * 64 * kK * 2, &maps.z[which], fb, eb * a.R + 64 * c,
-                            t0, pol);
-            }
+            for (int c = 0; c < kCols; ++c)
+              tma_load_2d(st + kABytes + c * 64 * kK * 2, &maps.z[which], fb, eb * a.R + 64 * c, t0,
+                          pol);
           }
-          ok = __shfl_sync(0xffffffffu, got, 0) != 0;
           if (ok) at.next();
         }
       }
@@ -1231,23 +1303,27 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
       drain_loads(sh->full, C::kStages, from, at.count);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t sbase = smem_u32(smem);
-      const uint32_t idesc = idesc_bf16(kM, N, true, true);
-      Place at(C::kStages);
-      bool ok = true;
-      while (true) {
-        if (!(ok = mbar_wait(&sh->ready[at.stage], at.phase, abort_flag, kWaitLimitNs))) break;
-        if (sh->stages == at.count) break;
-        tc_fence_after();
-        const uint32_t a0 = sbase + (uint32_t)(at.stage * C::kStageBytes), b0 = a0 + kABytes;
+    const uint32_t sbase = smem_u32(smem), ready0 = smem_u32(sh->ready);
+    const uint32_t idesc = idesc_bf16(kM, N, true, true);
+    const bool leader = elect_lane();
+    Place at(C::kStages);
+    bool ok = true;
+    while (true) {
+      if (!(ok = wait_bar(ready0 + at.stage * 8, at.phase, abort_flag))) break;
+      if (sh->stages == at.count) break;
+      tc_fence_after();
+      const uint32_t a0 = sbase + (uint32_t)(at.stage * C::kStageBytes);
+      const uint32_t la = desc_lo(a0, 8192), lb = desc_lo(a0 + kABytes, 8192);
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < kK / 16; ++kk)
-          mma_bf16_ss(tmem, sdesc_sw128(a0 + kk * 2048, 8192, 1024),
-                      sdesc_sw128(b0 + kk * 2048, 8192, 1024), idesc, (at.count || kk) ? 1u : 0u);
+          mma_bf16_ss(tmem, desc_of(la + 128 * kk, desc_hi(1024)), desc_of(lb + 128 * kk, desc_hi(1024)),
+                      idesc, (at.count || kk) ? 1u : 0u);
         mma_commit(&sh->empty[at.stage]);
-        at.next();
       }
+      at.next();
+    }
+    if (leader) {
       if (!ok) {
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
         *abort_flag = 1;
