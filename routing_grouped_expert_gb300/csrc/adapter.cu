@@ -449,6 +449,16 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       const bool leader = elect_lane();
       const int from = at.count;
       const uint32_t bytes = (uint32_t)((q_end + (gather ? 0 : a.nb)) * kK * 2);
+      // this warp's boxes: at most 16 of 8 rows over four warps
+      int row[4], ad[4];
+      bool box[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = (loader + 4 * i) * a.rb, e = (u * kM + q) / a.R;
+        box[i] = q < q_end;
+        row[i] = u * kM + q - e * a.R;
+        ad[i] = box[i] ? (int)sh->list[e] : 0;
+      }
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
@@ -459,11 +469,11 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
           mbar_arrive_expect_tx(fb, bytes);
           if (!gather) tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
         }
-        for (int q = loader * a.rb; q < q_end; q += 4 * a.rb) {
-          const int e = (u * kM + q) / a.R;
-          const int row = u * kM + q - e * a.R, ad = (int)sh->list[e];
-          if (leader) tma_load_3d(st + q * (kK * 2), &maps.p, fb, kb * kK, row, ad, pol_p);
-        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (box[i] && leader)
+            tma_load_3d(st + (loader + 4 * i) * a.rb * (kK * 2), &maps.p, fb, kb * kK, row[i], ad[i],
+                        pol_p);
         at.next();
       }
       if (leader && !ok) {
