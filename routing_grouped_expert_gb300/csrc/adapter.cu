@@ -32,6 +32,15 @@ constexpr int kABytes = kM * kK * 2;
 constexpr int kThreads = 224;       // producer, MMA, guard and four epilogue warps
 constexpr int kMaxEntries = 256;    // adapters a token block can meet
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr int kSmemMax = 232448;    // dynamic shared memory per CTA (227 KB)
+constexpr int kMaxStages = 9;
+// Stages of `bytes` that fit beside `other` bytes.
+__host__ __device__ constexpr int ring_stages(int bytes, int other) {
+  return (kSmemMax - 1024 - other) / bytes < kMaxStages ? (kSmemMax - 1024 - other) / bytes
+                                                        : kMaxStages;
+}
+// A stage of 128 weight rows and nb token rows.
+__host__ __device__ constexpr int stage_bytes_of(int nb) { return kABytes + nb * kK * 2; }
 
 // What the shrink kernel leaves about one token block for the kernels after it.
 struct BlockPlan {
@@ -136,6 +145,31 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
 }
 constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 
+// 32 TMEM lanes x 32 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// This warp's 32 features of the tokens below n, from TMEM to a [token][128] tile.
+__device__ __forceinline__ void stage_tile(float* st, uint32_t tb, int n) {
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(tb + c0, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c0 + c < n) st[(c0 + c) * kM] = __uint_as_float(v[c]);
+  }
+}
+
 // One role's place in a ring of n stages and their barriers.
 struct Place {
   int n;
@@ -193,20 +227,17 @@ struct ShrinkArgs {
 constexpr int kGatherRows = 64;   // most tokens of a unit that gathers
 constexpr int kRowWarps = 2;      // warps 2 and 3 copy them
 constexpr int kRowPieces = kGatherRows * 8 / (32 * kRowWarps);   // 16-byte pieces per thread
+constexpr int kShrinkOther = 5120;   // ShrinkShared
 template <int kNB>
 struct ShrinkCfg {
-  static constexpr int kStageBytes = kABytes + kNB * kK * 2;
-  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
-  static constexpr int kRing = kStages * kStageBytes;
   static constexpr bool kGather = kNB > kGatherRows;
-  static constexpr int kGatherBytes = kABytes + kGatherRows * kK * 2;
-  static constexpr int kGatherStages = kRing / kGatherBytes < 8 ? kRing / kGatherBytes : 8;
   static constexpr int kTmemCols = kNB < 32 ? 32 : kNB;
-  static constexpr int kSmemBytes = kRing + 1024 + 5120;
+  static constexpr int kSmemBytes = kSmemMax;
+  static constexpr int kRing = kSmemBytes - 1024 - kShrinkOther;
   static_assert(kNB * kM * 4 <= kRing, "the partial fp32 tile is staged in the ring");
 };
 struct ShrinkShared {
-  uint64_t full[8], empty[8];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full, drain;
   uint32_t tmem_base;
   int abort, bad, n_ent, most;
@@ -219,7 +250,7 @@ struct ShrinkShared {
   uint16_t pos[256];            // a token's place among them
   int n_tok;
 };
-static_assert(sizeof(ShrinkShared) <= 5120, "shared block");
+static_assert(sizeof(ShrinkShared) <= kShrinkOther, "shared block");
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -319,7 +350,7 @@ __device__ __forceinline__ void store_unit(const ShrinkShared* sh, const ShrinkA
   const int ad = 4 * lane < q_end ? (int)sh->list[(u * kM + 4 * lane) / a.R] : -2;
   const float f = ad >= 0 ? __ldg(a.scale + ad) : 0.f;
   const uint32_t mine = smem_u32(smem) + (uint32_t)lane * 16;
-#pragma unroll 2
+#pragma unroll 4
   for (int t = r * (kThreads / 32) + warp; t < rows; t += kS * (kThreads / 32)) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (sh->idx[t] == ad) {
@@ -392,7 +423,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&sh->full[i], gather ? 1 + 32 * kRowWarps : 1);   // TMA, and the threads that copy rows
       mbar_init(&sh->empty[i], 1);
     }
@@ -411,8 +442,8 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
   const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty);
-  const int stage_bytes = gather ? C::kGatherBytes : C::kStageBytes;
-  const int stages = gather ? C::kGatherStages : C::kStages;
+  const int stage_bytes = stage_bytes_of(gather ? kGatherRows : a.nb);
+  const int stages = ring_stages(stage_bytes, kShrinkOther);
   Place at(stages);
   uint32_t parity = 0;
   for (int u0 = u_first; u0 < units; u0 += u_step) {
@@ -552,14 +583,8 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       const bool got = mbar_wait(&sh->acc_full, parity, abort_flag, kWaitLimitNs);
       tc_fence_after();
       if (__all_sync(0xffffffffu, got) && q * 32 < q_end) {
-        float* st = reinterpret_cast<float*>(smem);
-        for (int c0 = 0; c0 < n_tok; c0 += 16) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 16; ++c) st[(c0 + c) * kM + q * 32 + lane] = __uint_as_float(v[c]);
-        }
+        stage_tile(reinterpret_cast<float*>(smem) + q * 32 + lane, tmem + ((uint32_t)(q * 32) << 16),
+                   n_tok);
       }
       tc_fence_before();
     }
@@ -733,13 +758,12 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* st, int lane) {
 
 // Few tiles: a cluster of kS CTAs per tile, each taking a share of the K
 // stages; the partial tiles meet in shared memory and are added in rank order.
+constexpr int kSplitOther = 1024;    // SplitShared
 template <int kNB>
 struct SplitCfg {
-  static constexpr int kStageBytes = kABytes + kNB * kK * 2;
-  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
-  static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kTmemCols = kNB < 32 ? 32 : kNB;
-  static constexpr int kSmemBytes = kRing + 1024 + 1024;
+  static constexpr int kSmemBytes = kSmemMax;
+  static constexpr int kRing = kSmemBytes - 1024 - kSplitOther;
   static_assert(kNB * kM * 4 <= kRing, "the partial fp32 tile is staged in the ring");
 };
 // Ring slots are handed out in the order of all stages (empty[slot]); arrivals
@@ -747,7 +771,7 @@ struct SplitCfg {
 // (loaded, then ready once the guard has passed them), each in its own order,
 // since the guard follows the adapters' stages only.
 struct SplitShared {
-  uint64_t full[8], empty[8], loaded[8], ready[8];
+  uint64_t full[kMaxStages], empty[kMaxStages], loaded[kMaxStages], ready[kMaxStages];
   uint64_t acc_full, drain;
   uint32_t tmem_base;
   int abort;
@@ -761,6 +785,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   SplitShared* sh = reinterpret_cast<SplitShared*>(smem + C::kRing);
+  const int stage_bytes = stage_bytes_of(a.nb), stages = ring_stages(stage_bytes, kSplitOther);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = kS > 1 ? (int)cluster_ctarank() : 0;
   const int tile = (int)blockIdx.x / kS;
@@ -771,7 +796,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   const BlockPlan* plan = plan_of(a.plan, tt);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 1);
       mbar_init(&sh->loaded[s], 1);
@@ -799,18 +824,19 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     const uint64_t pol_w = a.n_tt == 1 ? policy_evict_first() : policy_evict_normal();
     const uint64_t pol_v = policy_evict_last();
     const bool leader = elect_lane();
-    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    Place at(stages), base(stages), ext(stages);
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
       if (leader)
-        load_base<kKMajor>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, a.nb, kb, mt,
+        load_base<kKMajor>(smem + at.stage * stage_bytes, &sh->full[base.stage], maps, a.nb, kb, mt,
                            row0, pol_w, pol_v);
       at.next();
       base.next();
     }
     __syncwarp();
     pdl_wait();             // the plan and Z are complete
+    pdl_trigger();          // and so they are for the kernel that follows
     fence_async_global();
     const int q_all = plan->n_ent * a.R;
     const uint4 list = load_list(plan, lane);
@@ -819,7 +845,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
       ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      load_ext<>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list, q_all, j, mt,
+      load_ext<>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, list, q_all, j, mt,
                  row0, pol_w, pol_v, leader);
       at.next();
       ext.next();
@@ -830,21 +856,21 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
         *abort_flag = 1;
       }
       if (mt == 0 && rank == 0 && plan->bad) set_status(a.status, MOE_ERR_INVALID_ARG);
-      drain_loads(sh->full, C::kStages, 0, base.count);
-      drain_loads(sh->loaded, C::kStages, 0, ext.count);
+      drain_loads(sh->full, stages, 0, base.count);
+      drain_loads(sh->loaded, stages, 0, ext.count);
     }
   } else if (warp == 1) {
     const uint32_t sbase = smem_u32(smem);
     const uint32_t id_base = idesc_bf16(kM, a.nb, /*a_mn=*/!kKMajor, false);
     const uint32_t id_ext = idesc_bf16(kM, a.nb, /*a_mn=*/true, false);
     const bool leader = elect_lane();
-    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    Place at(stages), base(stages), ext(stages);
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!(ok = wait_bar(full0 + base.stage * 8, base.phase, abort_flag))) break;
       tc_fence_after();
       if (leader) {
-        mma_base<kKMajor>(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), id_base,
+        mma_base<kKMajor>(tmem, sbase + (uint32_t)(at.stage * stage_bytes), id_base,
                           kb > kb0 ? 1u : 0u);
         mma_commit(&sh->empty[at.stage]);
       }
@@ -858,7 +884,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       if (!(ok = wait_bar(ready0 + ext.stage * 8, ext.phase, abort_flag))) break;
       tc_fence_after();
       if (leader) {
-        mma_ext(tmem, sbase + (uint32_t)(at.stage * C::kStageBytes), id_ext, a.rb);
+        mma_ext(tmem, sbase + (uint32_t)(at.stage * stage_bytes), id_ext, a.rb);
         mma_commit(&sh->empty[at.stage]);
       }
       at.next();
@@ -875,7 +901,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
   } else if (warp == 2) {
-    Place at(C::kStages), ext(C::kStages);
+    Place at(stages), ext(stages);
     for (int kb = kb0; kb < kb1; ++kb) at.next();
     pdl_wait();
     const int ne = (plan->n_ent * a.R + kK - 1) / kK;
@@ -883,7 +909,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     for (int j = ne * rank / kS; j < ne * (rank + 1) / kS; ++j) {
       const bool got = mbar_wait(&sh->loaded[ext.stage], ext.phase, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) break;
-      found |= clear_nonfinite(smem + at.stage * C::kStageBytes, lane);
+      found |= clear_nonfinite(smem + at.stage * stage_bytes, lane);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ready[ext.stage]);
@@ -898,14 +924,8 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     if (__all_sync(0xffffffffu, got)) {
       // TMEM lane = feature, column = token
       const int q = warp & 3;
-      float* st = reinterpret_cast<float*>(smem);
-      for (int c0 = 0; c0 < rows; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) st[(c0 + c) * kM + q * 32 + lane] = __uint_as_float(v[c]);
-      }
+      stage_tile(reinterpret_cast<float*>(smem) + q * 32 + lane, tmem + ((uint32_t)(q * 32) << 16),
+                 rows);
     }
     tc_fence_before();
   }
@@ -940,15 +960,13 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
 // from L2 instead of 48 KB.
 struct FullCfg {
   static constexpr int kNB = 256;
-  static constexpr int kStageBytes = kABytes + kNB * kK * 2;
-  static constexpr int kStages = 4;
-  static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kStgBytes = 16 * 32 * 2;            // 16 tokens x 32 features per warp
-  static constexpr int kSmemBytes = kRing + 1024 + 1024 + 4 * kStgBytes;
+  static constexpr int kOther = 1024 + 4 * kStgBytes;      // FullShared, staging
+  static constexpr int kSmemBytes = kSmemMax;
+  static constexpr int kRing = kSmemBytes - 1024 - kOther;
 };
 struct FullShared {
-  uint64_t full[FullCfg::kStages], empty[FullCfg::kStages];
-  uint64_t loaded[FullCfg::kStages], ready[FullCfg::kStages];   // as in SplitShared
+  uint64_t full[kMaxStages], empty[kMaxStages], loaded[kMaxStages], ready[kMaxStages];   // as in SplitShared
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort;
@@ -964,6 +982,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   FullShared* sh = reinterpret_cast<FullShared*>(smem + C::kRing);
+  const int stage_bytes = stage_bytes_of(a.nb), stages = ring_stages(stage_bytes, C::kOther);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int nk = a.K / kK;
   const int rank = (int)cluster_ctarank();
@@ -971,7 +990,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   const int total = a.n_tt * n_mp;
   const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 2);    // both CTAs' MMAs have read the slot
       mbar_init(&sh->loaded[s], 1);
@@ -1006,7 +1025,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   if (warp == 0) {
     const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
     const bool leader = elect_lane();
-    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    Place at(stages), base(stages), ext(stages);
     bool ok = true;
     for (int tile = first; ok && tile < total; tile += step) {
       const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank, row0 = tt * a.nb;
@@ -1019,7 +1038,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       for (int kb = 0; kb < nk; ++kb) {
         if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
         if (leader)
-          load_base<kKMajor, true>(smem + at.stage * C::kStageBytes, &sh->full[base.stage], maps, a.nb,
+          load_base<kKMajor, true>(smem + at.stage * stage_bytes, &sh->full[base.stage], maps, a.nb,
                                    kb, mt, row0, pol_w, pol_v, rank);
         at.next();
         base.next();
@@ -1028,6 +1047,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (!later) {
         pdl_wait();             // the plan and Z are complete
+        pdl_trigger();          // and so they are for the kernel that follows
         fence_async_global();
         n_ent = plan->n_ent;
         list = load_list(plan, lane);
@@ -1036,7 +1056,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       for (int j = 0; j * kK < q_all; ++j) {
         ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        load_ext<true>(smem + at.stage * C::kStageBytes, &sh->loaded[ext.stage], maps, a, list, q_all,
+        load_ext<true>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, list, q_all,
                        j, mt, row0, pol_w, pol_v, leader, rank);
         at.next();
         ext.next();
@@ -1049,15 +1069,15 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         raise_abort();
       }
-      drain_loads(sh->full, C::kStages, 0, base.count);
-      drain_loads(sh->loaded, C::kStages, 0, ext.count);
+      drain_loads(sh->full, stages, 0, base.count);
+      drain_loads(sh->loaded, stages, 0, ext.count);
     }
   } else if (warp == 1) {
     const uint32_t sbase = smem_u32(smem);
     const uint32_t id_base = idesc_bf16(kM, a.nb, /*a_mn=*/!kKMajor, false);
     const uint32_t id_ext = idesc_bf16(kM, a.nb, /*a_mn=*/true, false);
     const bool leader = elect_lane();
-    Place at(C::kStages), base(C::kStages), ext(C::kStages);
+    Place at(stages), base(stages), ext(stages);
     Place buf(2);
     bool ok = true;
     for (int tile = first; ok && tile < total; tile += step) {
@@ -1072,7 +1092,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         if (!(ok = wait_bar(full0 + base.stage * 8, base.phase, abort_flag))) break;
         tc_fence_after();
         if (leader) {
-          mma_base<kKMajor>(d, sbase + (uint32_t)(at.stage * C::kStageBytes), id_base, kb ? 1u : 0u);
+          mma_base<kKMajor>(d, sbase + (uint32_t)(at.stage * stage_bytes), id_base, kb ? 1u : 0u);
           mma_commit_multicast(&sh->empty[at.stage], 0x3);
         }
         at.next();
@@ -1088,7 +1108,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         if (!(ok = wait_bar(ready0 + ext.stage * 8, ext.phase, abort_flag))) break;
         tc_fence_after();
         if (leader) {
-          mma_ext(d, sbase + (uint32_t)(at.stage * C::kStageBytes), id_ext, a.rb);
+          mma_ext(d, sbase + (uint32_t)(at.stage * stage_bytes), id_ext, a.rb);
           mma_commit_multicast(&sh->empty[at.stage], 0x3);
         }
         at.next();
@@ -1108,7 +1128,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
   } else if (warp == 2) {
-    Place at(C::kStages), ext(C::kStages);
+    Place at(stages), ext(stages);
     bool ok = true, found = false;
     for (int tile = first; ok && tile < total; tile += step) {
       for (int kb = 0; kb < nk; ++kb) at.next();
@@ -1117,7 +1137,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       for (int j = 0; j * kK < q_all; ++j) {
         const bool got = mbar_wait(&sh->loaded[ext.stage], ext.phase, abort_flag, kWaitLimitNs);
         if (!(ok = __all_sync(0xffffffffu, got))) break;
-        found |= clear_nonfinite(smem + at.stage * C::kStageBytes, lane);
+        found |= clear_nonfinite(smem + at.stage * stage_bytes, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ready[ext.stage]);
@@ -1177,7 +1197,11 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
 // G[a][r][d] = sum over the tokens t of adapter a of Z[t, entry(a) R + r] V[t, d]:
 // one CTA per (adapter, 128 columns of V), K = the tokens of every 64-token
 // group that holds one of adapter a, ascending.  Both gradients in one launch:
-// dA from (x, dZ), then dB from (dy, Z).
+// dA from (x, dZ), then dB from (dy, Z).  Bound by reading x and dy once more.
+// It may start while the expand launch before it still runs: expand lets it go
+// once it has itself seen both shrinks complete, so everything read here (past
+// the L1 cache) is complete, and nothing that expand writes is read; but it does
+// not end before expand.
 struct WgradMaps {
   CUtensorMap v[2];   // [T, D] as (64 features, tokens, D / 64)
   CUtensorMap z[2];   // [T, zc], boxes of 64 columns x 64 tokens
@@ -1248,6 +1272,7 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
     const bool leader = elect_lane();
+    fence_async_global();   // Z and dZ were written by ordinary stores
     const uint32_t empty0 = smem_u32(sh->empty);
     Place at(C::kStages);
     bool ok = true;
@@ -1257,14 +1282,14 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
       uint4 m0 = make_uint4(0, 0, 0, 0), m1 = m0;
       if (tb + lane < a.n_tt) {
         const BlockPlan* p = plan_of(a.plan, tb + lane);
-        const unsigned w = p->bits[ad >> 5];
+        const unsigned w = __ldcg(&p->bits[ad >> 5]);
         if ((w >> (ad & 31)) & 1u) {
           e = __popc(w & ((1u << (ad & 31)) - 1u));
-          for (int i = 0; i < (ad >> 5); ++i) e += __popc(p->bits[i]);
+          for (int i = 0; i < (ad >> 5); ++i) e += __popc(__ldcg(&p->bits[i]));
           const uint4* m =
               reinterpret_cast<const uint4*>(a.masks + ((size_t)(tb + lane) * kMaxEntries + e) * 8);
-          m0 = m[0];
-          m1 = m[1];
+          m0 = __ldcg(m);
+          m1 = __ldcg(m + 1);
         }
       }
       const uint32_t lo[4] = {m0.x, m0.z, m1.x, m1.z}, hi[4] = {m0.y, m0.w, m1.y, m1.w};
@@ -1401,6 +1426,7 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   }
   __syncwarp();
   __syncthreads();
+  pdl_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -1687,8 +1713,8 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, plan, masks, {dA, dB}, status};
   const dim3 grid((unsigned)(z.n * ((z.H + z.N) / kM)));
   if (z.R > 64)
-    return launch_cluster(adapter_wgrad_kernel<2>, grid, 1, WgradCfg<2>::kSmemBytes, false, s, m, a);
-  return launch_cluster(adapter_wgrad_kernel<1>, grid, 1, WgradCfg<1>::kSmemBytes, false, s, m, a);
+    return launch_cluster(adapter_wgrad_kernel<2>, grid, 1, WgradCfg<2>::kSmemBytes, true, s, m, a);
+  return launch_cluster(adapter_wgrad_kernel<1>, grid, 1, WgradCfg<1>::kSmemBytes, true, s, m, a);
 }
 
 }  // namespace moe
