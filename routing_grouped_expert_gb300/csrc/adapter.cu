@@ -674,36 +674,37 @@ __device__ __forceinline__ void load_base(uint8_t* st, uint64_t* fb, const Expan
     tma_load_3d(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
   load_tokens<kPair>(st + kABytes, fb, &maps.v, nb, kb * kK, row0, pol_v, rank);
 }
-// A block's entry list in the registers of a warp: lane l holds entries 8 l .. 8 l + 7.
+// A block's entry list, copied to shared memory by the warp that uses it.
+__device__ __forceinline__ void store_list(uint16_t* list, const uint4& v, int lane) {
+  __syncwarp();
+  reinterpret_cast<uint4*>(list)[lane] = v;
+  __syncwarp();
+}
 __device__ __forceinline__ uint4 load_list(const BlockPlan* plan, int lane) {
   return reinterpret_cast<const uint4*>(plan->list)[lane];
-}
-__device__ __forceinline__ int list_entry(const uint4& list, int e) {
-  const int src = (e >> 3) & 31;
-  const uint32_t x = __shfl_sync(0xffffffffu, list.x, src), y = __shfl_sync(0xffffffffu, list.y, src);
-  const uint32_t z = __shfl_sync(0xffffffffu, list.z, src), w = __shfl_sync(0xffffffffu, list.w, src);
-  const uint32_t v = e & 4 ? (e & 2 ? w : z) : (e & 2 ? y : x);
-  return (int)((v >> (16 * (e & 1))) & 0xffffu);
 }
 // Stage j of the adapters' part, by the whole producer warp: 64 rank rows of
 // the block's entries, in boxes of rb rows, each [2 feature atoms][rb rows][128
 // bytes].
 template <bool kPair = false>
 __device__ __forceinline__ void load_ext(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
-                                         const ExpandArgs& a, const uint4& list, int q_all, int j,
+                                         const ExpandArgs& a, const uint16_t* list, int q_all, int j,
                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v,
                                          bool leader, int rank = 0) {
   if (leader) {
     mbar_arrive_expect_tx(fb, (uint32_t)(kABytes + a.nb * kK * 2));
     load_tokens<kPair>(st + kABytes, fb, &maps.z, a.nb, j * kK, row0, pol_v, rank);
   }
+  int e = j * kK / a.R, row = j * kK - e * a.R;
   for (int q = 0; q < kK; q += a.rb) {
-    const int qq = j * kK + q, e = qq / a.R;
-    const int known = list_entry(list, e);
     // past the last entry: an adapter that does not exist, read as zeros
-    const int ad = qq < q_all ? known : a.n;
-    if (leader)
-      tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, qq - e * a.R, mt * 2, ad, pol_w);
+    const int ad = j * kK + q < q_all ? (int)list[e] : a.n;
+    if (leader) tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, row, mt * 2, ad, pol_w);
+    row += a.rb;
+    if (row == a.R) {
+      row = 0;
+      ++e;
+    }
   }
 }
 // The four MMAs of a stage at shared address a0 (one lane).
@@ -729,18 +730,19 @@ __device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, uint32_t ide
     mma_bf16_ss(tmem, desc_of(la, hi), desc_of(lb + 2 * kk, desc_hi(1024)), idesc, 1u);
   }
 }
-// The guard warp's pass over the 64 x 128 adapter weights of a stage: every
+// A guard's pass over the 64 x 128 adapter weights of a stage: every
 // token of the block is multiplied by every entry's rank rows, its own z or
 // zero, so an infinity or NaN there would reach the other requests' tokens as
 // 0 * inf.  It counts as zero instead and is reported.
-__device__ __forceinline__ bool clear_nonfinite(uint8_t* st, int lane) {
+// Slice `part` of `parts` of the stage.
+__device__ __forceinline__ bool clear_nonfinite(uint8_t* st, int lane, int part, int parts) {
   // x * 0 + acc stays 0 for finite x and turns NaN for the others: two
   // elements per instruction (one warp checks a stage in 0.2 us; comparing the
   // exponents of every element took 1.75 us, longer than the stage's MMAs)
   const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
   __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll 8
-  for (int i = lane; i < kABytes / 16; i += 32) {
+  for (int i = part * 32 + lane; i < kABytes / 16; i += 32 * parts) {
     const uint4 v = reinterpret_cast<const uint4*>(st)[i];
     const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
@@ -749,16 +751,19 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* st, int lane) {
   const __nv_bfloat162 any = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
   const bool found = __hisnan(any.x) || __hisnan(any.y);
   if (!__any_sync(0xffffffffu, found)) return false;
-  for (int i = lane; i < kABytes / 2; i += 32) {
-    uint16_t* e = reinterpret_cast<uint16_t*>(st) + i;
-    if ((*e & 0x7f80u) == 0x7f80u) *e = 0;
+  for (int i = part * 32 + lane; i < kABytes / 16; i += 32 * parts) {
+    uint16_t* e = reinterpret_cast<uint16_t*>(st) + 8 * i;
+    for (int c = 0; c < 8; ++c)
+      if ((e[c] & 0x7f80u) == 0x7f80u) e[c] = 0;
   }
+  fence_async_smem();   // the MMA reads what was written here
   return true;
 }
 
 // Few tiles: a cluster of kS CTAs per tile, each taking a share of the K
 // stages; the partial tiles meet in shared memory and are added in rank order.
 constexpr int kSplitOther = 1024;    // SplitShared
+constexpr int kGuards = 5;           // all warps but the producer and the MMA warp
 template <int kNB>
 struct SplitCfg {
   static constexpr int kTmemCols = kNB < 32 ? 32 : kNB;
@@ -772,10 +777,13 @@ struct SplitCfg {
 // since the guard follows the adapters' stages only.
 struct SplitShared {
   uint64_t full[kMaxStages], empty[kMaxStages], loaded[kMaxStages], ready[kMaxStages];
+  alignas(16) uint16_t list[kMaxEntries];
   uint64_t acc_full, drain;
   uint32_t tmem_base;
   int abort;
 };
+
+static_assert(sizeof(SplitShared) <= kSplitOther, "shared block");
 
 template <int kNB, bool kKMajor, int kS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -800,7 +808,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 1);
       mbar_init(&sh->loaded[s], 1);
-      mbar_init(&sh->ready[s], 1);
+      mbar_init(&sh->ready[s], kGuards);
     }
     mbar_init(&sh->acc_full, 1);
     mbar_init(&sh->drain, 1);
@@ -839,14 +847,14 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     pdl_trigger();          // and so they are for the kernel that follows
     fence_async_global();
     const int q_all = plan->n_ent * a.R;
-    const uint4 list = load_list(plan, lane);
+    store_list(sh->list, load_list(plan, lane), lane);
     const int ne = (q_all + kK - 1) / kK;
     ok = __all_sync(0xffffffffu, ok);
     for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
       ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      load_ext<>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, list, q_all, j, mt,
-                 row0, pol_w, pol_v, leader);
+      load_ext<>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, sh->list, q_all, j,
+                 mt, row0, pol_w, pol_v, leader);
       at.next();
       ext.next();
     }
@@ -900,7 +908,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       if (!mbar_wait(&sh->drain, 0, nullptr, kWaitLimitNs))
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
-  } else if (warp == 2) {
+  } else {   // the guards, warps 2 .. 6
     Place at(stages), ext(stages);
     for (int kb = kb0; kb < kb1; ++kb) at.next();
     pdl_wait();
@@ -909,8 +917,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     for (int j = ne * rank / kS; j < ne * (rank + 1) / kS; ++j) {
       const bool got = mbar_wait(&sh->loaded[ext.stage], ext.phase, abort_flag, kWaitLimitNs);
       if (!__all_sync(0xffffffffu, got)) break;
-      found |= clear_nonfinite(smem + at.stage * stage_bytes, lane);
-      fence_async_smem();
+      found |= clear_nonfinite(smem + at.stage * stage_bytes, lane, warp - 2, kGuards);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ready[ext.stage]);
       at.next();
@@ -967,10 +974,13 @@ struct FullCfg {
 };
 struct FullShared {
   uint64_t full[kMaxStages], empty[kMaxStages], loaded[kMaxStages], ready[kMaxStages];   // as in SplitShared
+  alignas(16) uint16_t list[kMaxEntries];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort;
 };
+
+static_assert(sizeof(FullShared) <= 1024, "shared block");
 
 template <bool kKMajor>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1053,11 +1063,12 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         list = load_list(plan, lane);
       }
       const int q_all = n_ent * a.R;
+      store_list(sh->list, list, lane);
       for (int j = 0; j * kK < q_all; ++j) {
         ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        load_ext<true>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, list, q_all,
-                       j, mt, row0, pol_w, pol_v, leader, rank);
+        load_ext<true>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, sh->list,
+                       q_all, j, mt, row0, pol_w, pol_v, leader, rank);
         at.next();
         ext.next();
       }
@@ -1137,8 +1148,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       for (int j = 0; j * kK < q_all; ++j) {
         const bool got = mbar_wait(&sh->loaded[ext.stage], ext.phase, abort_flag, kWaitLimitNs);
         if (!(ok = __all_sync(0xffffffffu, got))) break;
-        found |= clear_nonfinite(smem + at.stage * stage_bytes, lane);
-        fence_async_smem();
+        found |= clear_nonfinite(smem + at.stage * stage_bytes, lane, 0, 1);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ready[ext.stage]);
         at.next();
@@ -1218,7 +1228,7 @@ struct WgradArgs {
 template <int kCols>
 struct WgradCfg {
   static constexpr int kStageBytes = kABytes + kCols * 64 * kK * 2;
-  static constexpr int kStages = 4;      // two CTAs per SM at kCols = 1
+  static constexpr int kStages = 3;      // three CTAs per SM at kCols = 1
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kSmemBytes = kRing + 1024 + 1024;
   static constexpr int kTmemCols = 64 * kCols;
