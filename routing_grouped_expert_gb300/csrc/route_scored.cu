@@ -56,14 +56,6 @@ template <int L>
 __device__ __forceinline__ float seg_max(float v) {
   return route_key_value(seg_max<L>(route_key(v)));
 }
-// This token's bits of a warp-wide ballot.
-template <int L>
-__device__ __forceinline__ unsigned seg_ballot(bool p) {
-  const unsigned m = __ballot_sync(0xffffffffu, p);
-  if constexpr (L == 32) return m;
-  else return (m >> (threadIdx.x & 31 & ~(L - 1))) & ((1u << L) - 1u);
-}
-
 // hi + lo += x without losing bits (Knuth's two-sum).
 __device__ __forceinline__ void pair_add(float& hi, float& lo, float x) {
   const float s = __fadd_rn(hi, x);
@@ -152,157 +144,201 @@ __device__ __forceinline__ int select_best(uint32_t (&key)[kPerLane], int k, int
   }
 }
 
-// One token per L lanes, kPerLane logits per lane (expert lane + L i).  Bound by
-// instruction issue, not memory: about 25 instructions per score (exp and a
-// correctly rounded reciprocal or quotient) and 25 per selection round; so a
-// token's candidates are compacted to the kept groups before the selection
-// (8 groups of 32, 4 kept: four keys per lane to sort instead of eight).
+// As route_key, in fewer instructions: -0 + 0 is +0, and the sign spread over
+// the word flips the rest of a negative number.  A NaN gets a key like any
+// other, which keeps the order total (the status reports it).
+__device__ __forceinline__ uint32_t rank_key(float x) {
+  const int b = __float_as_int(__fadd_rn(x, 0.f));
+  return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
+}
+
+// One token per L lanes, kPerLane logits per lane (expert lane + L i); the warps
+// go through the tokens in strides, the next token's logits on their way.
+// Bound by instruction issue, not memory (8192 tokens of 256 experts read 8.4
+// MB, 1.3 us): about 25 instructions per score (exp and a correctly rounded
+// reciprocal or quotient) and 20 per selection round.  So a token's candidates
+// are compacted to the kept groups before the selection (8 groups of 32, 4
+// kept: four keys per lane to sort instead of eight), everything but the scores
+// is done on integer keys, and what depends on the expert alone (bias, place
+// in shared memory) is worked out once per warp.
 template <int kPerLane, int L, bool kGroups>
 __global__ void __launch_bounds__(32 * kMaxWarps)
 route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, RouteCfg c,
                     int T, int E, int k, int tpc, int group_pad, int32_t* __restrict__ topk_idx,
                     float* __restrict__ topk_w, int32_t* __restrict__ chunk_hist,
                     int* __restrict__ status, bool whole) {
-  // per token of the block: n_group * (group size + pad) values, n_group kept groups
-  extern __shared__ float stage[];
+  // per token of the block: n_group * (group size + pad) keys, n_group kept groups
+  extern __shared__ uint32_t stage[];
   pdl_trigger();
   const int lane = threadIdx.x & (L - 1), seg = threadIdx.x / L;   // seg: the block's token
-  const int t0 = blockIdx.x * (blockDim.x / L) + seg;
-  const bool live = t0 < T;
-  // a warp without a token leaves, unless the grid reports together
-  if (!whole && !__any_sync(0xffffffffu, live)) return;
-  const int t = live ? t0 : T - 1;
-  const float* row = logits + (size_t)t * E;
-  float v[kPerLane];
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int e = lane + L * i;
-    v[i] = e < E ? __ldg(row + e) : -INFINITY;
-    bad |= e < E && !isfinite(v[i]);
-  }
-  // softmax: the row's maximum and the sum of exp(l - m)
+  const int per_block = blockDim.x / L, stride = gridDim.x * per_block;
   const bool two = kGroups && c.group_top == 2;
-  const bool scored = bias != nullptr || two;   // the scores take part in the choice
-  float m = 0.f, S = 1.f;
-  float ex[kPerLane];
-  if (c.softmax && (scored || !c.renorm)) {
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) mx = fmaxf(mx, v[i]);
-    m = seg_max<L>(mx);
-    float hi = 0.f, lo = 0.f;
+  const bool scored = bias != nullptr;       // all scores take part in the choice
+  const bool need_s = scored || (two && c.softmax);   // the scores' exact sum decides
+  const int gsz = kGroups ? E / c.n_group : E, pitch = gsz + group_pad;
+  uint32_t* st = kGroups ? stage + (size_t)seg * c.n_group * (pitch + 1) : nullptr;
+  int* list = kGroups ? reinterpret_cast<int*>(st) + c.n_group * pitch : nullptr;
+  // kept in registers across tokens: this lane's biases
+  constexpr bool kKeep = kPerLane <= 8;
+  float be[kKeep ? kPerLane : 1];
+  float nan = 0.f;     // turns NaN with the first value that is not finite
+  bool bad = false;
+  if constexpr (kKeep) {
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      ex[i] = lane + L * i < E ? expf(v[i] - m) : 0.f;
-      pair_add(hi, lo, ex[i]);
+      be[i] = scored && lane + L * i < E ? __ldg(bias + lane + L * i) : 0.f;
+      bad |= !(be[i] < INFINITY);   // NaN or +inf: -inf switches an expert off
     }
-    S = seg_sum_rounded<L>(hi, lo);
   }
-  // b: score (+ bias), the value that the two best of a group add up;
-  // r: the value that ranks
-  uint32_t key[kPerLane];
-  const int gsz = kGroups ? E / c.n_group : E;
-  float* st = kGroups ? stage + (size_t)seg * c.n_group * (gsz + group_pad + 1) : nullptr;
+  float next[kPerLane];
+  auto fetch = [&](int t) {
+    const float* row = logits + (size_t)(t < T ? t : T - 1) * E;
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int e = lane + L * i;
-    float r = v[i], b = v[i];
-    if (scored && e < E) {
-      b = c.softmax ? __fdiv_rn(ex[i], S) : sigmoid_rn(v[i]);
-      if (bias != nullptr) {
-        const float be = __ldg(bias + e);
-        bad |= !(be < INFINITY);   // NaN or +inf: -inf switches an expert off
-        b = __fadd_rn(b, be);
-        r = b;
+    for (int i = 0; i < kPerLane; ++i)
+      next[i] = lane + L * i < E ? __ldg(row + lane + L * i) : -INFINITY;
+  };
+  // the warp's tokens stay together: its first one decides
+  const int first = blockIdx.x * per_block + (seg & ~(32 / L - 1)), own = seg & (32 / L - 1);
+  if (first < T) fetch(first + own);
+  for (int tw = first; tw < T; tw += stride) {
+    const bool live = tw + own < T;
+    const int t = live ? tw + own : T - 1;
+    const float* row = logits + (size_t)t * E;
+    float v[kPerLane];
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      v[i] = next[i];
+      if (lane + L * i < E) nan = fmaf(v[i], 0.f, nan);
+    }
+    if (tw + stride < T) fetch(tw + stride + own);
+    // softmax: the row's maximum and the sum of exp(l - m), rounded once where
+    // the scores decide
+    float m = 0.f, S = 1.f;
+    if (c.softmax && (need_s || !c.renorm)) {
+      float mx = v[0];
+#pragma unroll
+      for (int i = 1; i < kPerLane; ++i) mx = fmaxf(mx, v[i]);
+      m = seg_max<L>(mx);
+      if (need_s) {
+        float hi = 0.f, lo = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+          pair_add(hi, lo, lane + L * i < E ? expf(v[i] - m) : 0.f);
+        S = seg_sum_rounded<L>(hi, lo);
+      } else {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) sum += lane + L * i < E ? expf(v[i] - m) : 0.f;
+        S = seg_sum<L>(sum);
       }
     }
-    if (isnan(r)) r = -INFINITY;   // keep the order total; the status reports it
-    key[i] = e < E ? route_key(r) : 0u;
-    if (kGroups && e < E) {
-      const int g = (int)((uint32_t)e * c.group_magic >> 20);
-      st[e + g * group_pad] = two ? (isnan(b) ? -INFINITY : b) : r;
-    }
-  }
-  int idx;
-  if constexpr (!kGroups) {
-    idx = select_best<kPerLane, L>(key, k, lane);
-  } else {
-    __syncwarp();
-    // lpg lanes scan one group: its two largest values
-    const int lpg = c.lanes_per_group / (32 / L), sub = lane & (lpg - 1), g = lane / lpg;
-    float a1 = -INFINITY, a2 = -INFINITY;
-    if (g < c.n_group) {
-      const float* gs = st + g * (gsz + group_pad);
-      for (int j = sub; j < gsz; j += lpg) {
-        const float x = gs[j];
-        a2 = fmaxf(a2, fminf(a1, x));
-        a1 = fmaxf(a1, x);
-      }
-    }
-    for (int off = 1; off < lpg; off <<= 1) {
-      const float o1 = __shfl_xor_sync(0xffffffffu, a1, off);
-      const float o2 = __shfl_xor_sync(0xffffffffu, a2, off);
-      a2 = fmaxf(fmaxf(a2, o2), fminf(a1, o1));
-      a1 = fmaxf(a1, o1);
-    }
-    const uint32_t gk = route_key(two ? __fadd_rn(a1, a2) : a1);
-    // a group's place among the groups: how many come before it
-    int before = 0;
-    for (int o = 0; o < c.n_group; ++o) {
-      const uint32_t ok = __shfl_sync(0xffffffffu, gk, o * lpg, L);
-      before += ok > gk || (ok == gk && o < g);
-    }
-    // the kept groups, ascending
-    const bool keep = sub == 0 && g < c.n_group && before < c.topk_group;
-    const unsigned kept = seg_ballot<L>(keep);
-    __syncwarp();   // every lane has scanned its group
-    int* list = reinterpret_cast<int*>(st) + c.n_group * (gsz + group_pad);
-    if (keep) list[__popc(kept & ((1u << lane) - 1u))] = g;
-    // The keys of all experts take the place of the group values: candidate j,
-    // the j-th expert of the kept groups in ascending order, is read from them.
+    auto score = [&](float l) { return c.softmax ? __fdiv_rn(expf(l - m), S) : sigmoid_rn(l); };
+    uint32_t key[kPerLane];
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
       const int e = lane + L * i;
-      const int ge = (int)((uint32_t)e * c.group_magic >> 20);
-      if (e < E) reinterpret_cast<uint32_t*>(st)[e + ge * group_pad] = key[i];
+      float r = v[i];
+      if (scored && e < E) {
+        float b;
+        if constexpr (kKeep) {
+          b = be[i];
+        } else {
+          b = __ldg(bias + e);
+          bad |= !(b < INFINITY);
+        }
+        r = __fadd_rn(score(r), b);
+      }
+      key[i] = e < E ? rank_key(r) : 0u;
+      if constexpr (kGroups) {
+        const int g = (int)((uint32_t)e * c.group_magic >> 20);
+        if (e < E) st[e + g * group_pad] = key[i];
+      }
     }
-    __syncwarp();
-    const int n_cand = c.topk_group * gsz;
-    auto expert_of = [&](int j) {
-      const int cg = (int)((uint32_t)j * c.group_magic >> 20);
-      return list[cg] * gsz + (j - cg * gsz);
-    };
-    auto load = [&](int j) {
-      if (j >= n_cand) return 0u;
-      const int cg = (int)((uint32_t)j * c.group_magic >> 20);
-      return reinterpret_cast<const uint32_t*>(st)[list[cg] * (gsz + group_pad) + j - cg * gsz];
-    };
-    int pick;
-    if (kPerLane > 1 && n_cand <= L * (kPerLane / 2)) {
-      constexpr int kHalf = kPerLane > 1 ? kPerLane / 2 : 1;
-      uint32_t half[kHalf];
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i) half[i] = load(lane + L * i);
-      pick = select_best<kHalf, L>(half, k, lane);
+    int idx;
+    if constexpr (!kGroups) {
+      idx = select_best<kPerLane, L>(key, k, lane);
     } else {
+      __syncwarp();
+      // lpg lanes scan one group: its two largest keys
+      const int lpg = c.lanes_per_group / (32 / L), sub = lane & (lpg - 1), g = lane / lpg;
+      uint32_t a1 = 0u, a2 = 0u;
+      if (g < c.n_group) {
+        const uint32_t* gs = st + g * pitch;
+#pragma unroll 4
+        for (int j = sub; j < gsz; j += lpg) {
+          const uint32_t x = gs[j];
+          a2 = max(a2, min(a1, x));
+          a1 = max(a1, x);
+        }
+      }
+      for (int off = 1; off < lpg; off <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, a1, off);
+        const uint32_t o2 = __shfl_xor_sync(0xffffffffu, a2, off);
+        a2 = max(max(a2, o2), min(a1, o1));
+        a1 = max(a1, o1);
+      }
+      uint32_t gk = a1;
+      if (two) {   // the sum of two values: of the biased scores, or of the scores themselves
+        float x1 = route_key_value(a1), x2 = route_key_value(a2);
+        if (!scored) {
+          x1 = score(x1);
+          x2 = score(x2);
+        }
+        gk = rank_key(__fadd_rn(x1, x2));
+      }
+      if (sub != 0 || g >= c.n_group) gk = 0u;
+      // the best groups, one after the other (equal ones: the lower first)
+      unsigned kept = 0u;
+      for (int j = 0; j < c.topk_group; ++j) {
+        const uint32_t top = seg_max<L>(gk);
+        const uint32_t win = seg_min<L>(gk == top && top != 0u ? (uint32_t)lane : 31u);
+        kept |= 1u << win;
+        if ((int)win == lane) gk = 0u;
+      }
+      if ((kept >> lane) & 1u) list[__popc(kept & ((1u << lane) - 1u))] = g * pitch;
+      __syncwarp();
+      // candidate j: the j-th expert of the kept groups in ascending order
+      const int n_cand = c.topk_group * gsz;
+      auto place_of = [&](int j) {
+        const int cg = (int)((uint32_t)j * c.group_magic >> 20);
+        return list[cg] + (j - cg * gsz);
+      };
+      int pick;
+      if (kPerLane > 1 && n_cand <= L * (kPerLane / 2)) {
+        constexpr int kHalf = kPerLane > 1 ? kPerLane / 2 : 1;
+        uint32_t half[kHalf];
 #pragma unroll
-      for (int i = 0; i < kPerLane; ++i) key[i] = load(lane + L * i);
-      pick = select_best<kPerLane, L>(key, k, lane);
+        for (int i = 0; i < kHalf; ++i) {
+          const int j = lane + L * i;
+          half[i] = j < n_cand ? st[place_of(j)] : 0u;
+        }
+        pick = select_best<kHalf, L>(half, k, lane);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const int j = lane + L * i;
+          key[i] = j < n_cand ? st[place_of(j)] : 0u;
+        }
+        pick = select_best<kPerLane, L>(key, k, lane);
+      }
+      pick = (int)min((uint32_t)pick, (uint32_t)(n_cand - 1));
+      const int cg = (int)((uint32_t)pick * c.group_magic >> 20);
+      idx = lane < k ? list[cg] / pitch * gsz + (pick - cg * gsz) : 0;
+      __syncwarp();   // the next token's keys take this one's place
     }
-    idx = lane < k ? expert_of(pick) : 0;
+    // the picks' logits, and whether the bias switched the expert off
+    const bool have = lane < k;
+    idx = have ? (int)min((uint32_t)idx, (uint32_t)(E - 1)) : 0;
+    const float l = have ? __ldg(row + idx) : 0.f;
+    const bool on = have && (!scored || __ldg(bias + idx) != -INFINITY);
+    const float w = pick_weight<L>(c.softmax, c.renorm, c.scale, l, on, m, S);
+    if (have && live) {
+      topk_idx[(size_t)t * k + lane] = idx;
+      topk_w[(size_t)t * k + lane] = w;
+      if (chunk_hist) atomicAdd(&chunk_hist[(size_t)(t / tpc) * E + idx], 1);
+    }
   }
-  // the picks' logits, and whether the bias switched the expert off
-  const bool have = lane < k;
-  if (!have) idx = 0;
-  const float l = have ? __ldg(row + idx) : 0.f;
-  const bool on = have && (bias == nullptr || __ldg(bias + idx) != -INFINITY);
-  const float w = pick_weight<L>(c.softmax, c.renorm, c.scale, l, on, m, S);
-  if (have && live) {
-    topk_idx[(size_t)t * k + lane] = idx;
-    topk_w[(size_t)t * k + lane] = w;
-    if (chunk_hist) atomicAdd(&chunk_hist[(size_t)(t / tpc) * E + idx], 1);
-  }
+  bad |= isnan(nan);
   if (whole) {
     // a batch that one block routes: it writes the status itself
     const int any = __syncthreads_or(bad);
@@ -383,6 +419,12 @@ route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __rest
   if (__any_sync(0xffffffffu, lane < k && !in) && lane == 0) set_status(status, MOE_ERR_INVALID_ARG);
 }
 
+// Four blocks of eight warps per SM, about what the registers allow at once.
+int grid_of(int T, int per_block) {
+  const int blocks = (T + per_block - 1) / per_block, most = 4 * device_sm_count();
+  return blocks < most ? blocks : most;
+}
+
 template <int kPerLane, int L>
 cudaError_t launch_t(const float* logits, const float* bias, const RouteCfg& c, int T, int E, int k,
                      int32_t* topk_idx, float* topk_w, int32_t* chunk_hist, int* status, bool whole,
@@ -398,13 +440,13 @@ cudaError_t launch_t(const float* logits, const float* bias, const RouteCfg& c, 
     const int warps = bytes * kMaxWarps <= 48 * 1024 ? kMaxWarps : kMaxWarps / 2;
     const int per_block = warps * per_warp;
     route_scored_kernel<kPerLane, L, true>
-        <<<(T + per_block - 1) / per_block, 32 * warps, bytes * warps, s>>>(
+        <<<grid_of(T, per_block), 32 * warps, bytes * warps, s>>>(
             logits, bias, c, T, E, k, tpc, pad, topk_idx, topk_w, chunk_hist, status,
             whole && T <= per_block);
   } else {
     const int per_block = kMaxWarps * per_warp;
     route_scored_kernel<kPerLane, L, false>
-        <<<(T + per_block - 1) / per_block, 32 * kMaxWarps, 0, s>>>(
+        <<<grid_of(T, per_block), 32 * kMaxWarps, 0, s>>>(
             logits, bias, c, T, E, k, tpc, 0, topk_idx, topk_w, chunk_hist, status,
             whole && T <= per_block);
   }
