@@ -238,10 +238,11 @@ moe_status moe_route_scored(const float* logits, const float* bias, const moe_ro
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* status = static_cast<int*>(ws);
   // a few tokens are one block's work, which writes the status itself
-  const bool whole = route_scored_whole(T, E);
+  const RouteCfg cfg = make_route_cfg(*config, E);
+  const bool whole = route_scored_whole(T, E, k, cfg);
   if (!whole) MOE_TRY(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
-  return cuda_status(launch_route_scored(logits, bias, make_route_cfg(*config, E), T, E, k,
-                                         topk_idx, topk_w, nullptr, status, s, whole));
+  return cuda_status(launch_route_scored(logits, bias, cfg, T, E, k, topk_idx, topk_w, nullptr,
+                                         status, s, whole));
 }
 
 moe_status moe_route_scored_backward(const float* dtopk_w, const int32_t* topk_idx,

@@ -250,7 +250,7 @@ RouteCfg make_route_cfg(const moe_route_config& a, int E);
 // bias: [E] or null.  chunk_hist as for launch_route.  With `whole` (allowed when
 // route_scored_whole) the launch writes the status word itself, which then need
 // not be zero.
-bool route_scored_whole(int T, int E);
+bool route_scored_whole(int T, int E, int k, const RouteCfg& c);
 cudaError_t launch_route_scored(const float* logits, const float* bias, const RouteCfg& c, int T,
                                 int E, int k, int32_t* topk_idx, float* topk_w,
                                 int32_t* chunk_hist, int* status, cudaStream_t s,

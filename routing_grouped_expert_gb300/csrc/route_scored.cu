@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kMaxWarps = 8;
 
-// Lanes per token L: 8 or 16 where the experts fit (a warp then routes four or
-// two tokens), else 32.  Reductions over a token's lanes:
+// L lanes route one token, so a warp routes 32 / L.  Reductions over a token's
+// lanes:
 template <int L>
 __device__ __forceinline__ uint32_t seg_max(uint32_t v) {
   if constexpr (L == 32) {
@@ -102,46 +102,82 @@ __device__ __forceinline__ float pick_weight(bool softmax, bool renorm, float sc
   return sum > 0.f ? scale * (s / sum) : 0.f;
 }
 
-// The k largest of a token's candidates: lane i's keys are those of candidates
-// lane + L i (0: none); lane j < k returns slot j's candidate.  A larger key wins,
-// equal keys go to the lower candidate.  Up to eight keys per lane are sorted
-// once (route_select); with more, each round rescans the winner's keys instead:
-// 4 n instructions a round against 5 n (n - 1) / 2 for the sort.
-template <int kPerLane, int L>
-__device__ __forceinline__ int select_best(uint32_t (&key)[kPerLane], int k, int lane) {
-  if constexpr (L == 32 && kPerLane <= 8) {
-    uint32_t sel_key;
-    int sel;
-    route_select<kPerLane>(key, k, lane, &sel_key, &sel);
-    return sel;
-  } else {
-    uint32_t best = 0u;
-    int slot = 0, mine = 0;
-    auto scan = [&]() {
-      best = key[0];
-      slot = 0;
+// The lanes of this token whose `p` holds, as bits of its lanes.
+template <int L>
+__device__ __forceinline__ unsigned seg_ballot(bool p) {
+  const unsigned m = __ballot_sync(0xffffffffu, p);
+  if constexpr (L == 32) return m;
+  else return (m >> (threadIdx.x & 31 & ~(L - 1))) & ((1u << L) - 1u);
+}
+
+// The k largest of a token's candidates: lane i's keys are n candidates of it
+// (key 0: none), id[] their numbers, ascending; lane j < k returns slot j's
+// number.  A larger key wins, equal keys go to the lower number.  Up to eight
+// keys per lane are sorted once; with more, each round rescans the winner's keys
+// instead: 4 n instructions a round against 5 n (n - 1) / 2 for the sort.  A round
+// finds the largest head by one reduction and its lane by a vote; only where
+// several lanes hold the same key a second reduction finds the lowest number.
+template <int n, int L>
+__device__ __forceinline__ int select_best(uint32_t (&key)[n], int (&id)[n], int k, int lane) {
+  constexpr bool kSort = n <= 8;
+  if constexpr (kSort) {
+    // odd-even transposition, swapping only on a strictly smaller key
 #pragma unroll
-      for (int i = 1; i < kPerLane; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          slot = i;
-        }
-    };
-    scan();
-    for (int j = 0; j < k; ++j) {
-      const uint32_t m = seg_max<L>(best);
-      const uint32_t win =
-          seg_min<L>(best == m && m != 0u ? (uint32_t)(lane + L * slot) : ~0u);
-      if (lane == j) mine = (int)win;
-      if (m != 0u && (int)(win & (L - 1)) == lane) {
+    for (int pass = 0; pass < n; ++pass) {
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-          if (i == slot) key[i] = 0u;
-        scan();
+      for (int i = pass & 1; i + 1 < n; i += 2) {
+        const bool swap = key[i] < key[i + 1];
+        const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
+        const int x = swap ? id[i + 1] : id[i], y = swap ? id[i] : id[i + 1];
+        key[i] = hi;
+        key[i + 1] = lo;
+        id[i] = x;
+        id[i + 1] = y;
       }
     }
-    return mine;
   }
+  uint32_t best = 0u;
+  int head = 0, mine = 0;
+  auto scan = [&]() {   // this lane's largest key
+    best = key[0];
+    head = id[0];
+    if constexpr (!kSort) {
+#pragma unroll
+      for (int i = 1; i < n; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          head = id[i];
+        }
+    }
+  };
+  scan();
+  for (int j = 0; j < k; ++j) {
+    const bool top = best == seg_max<L>(best);
+    const unsigned who = seg_ballot<L>(top);
+    int win = __ffs(who) - 1;   // the lane that holds it
+    if (__any_sync(0xffffffffu, (who & (who - 1)) != 0u)) {
+      const uint32_t low = seg_min<L>(top ? (uint32_t)head : ~0u);
+      win = __ffs(seg_ballot<L>(top && (uint32_t)head == low)) - 1;
+    }
+    const int cand = __shfl_sync(0xffffffffu, head, win, L);
+    if (lane == j) mine = cand;
+    if (win == lane) {
+      if constexpr (kSort) {
+#pragma unroll
+        for (int i = 0; i + 1 < n; ++i) {
+          key[i] = key[i + 1];
+          id[i] = id[i + 1];
+        }
+        key[n - 1] = 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+          if (id[i] == head) key[i] = 0u;
+      }
+      scan();
+    }
+  }
+  return mine;
 }
 
 // As route_key, in fewer instructions: -0 + 0 is +0, and the sign spread over
@@ -152,111 +188,167 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
 }
 
-// One token per L lanes, kPerLane logits per lane (expert lane + L i); the warps
-// go through the tokens in strides, the next token's logits on their way.
+
+// Blocks of eight warps per SM for n logits per lane: what hides the fixed
+// latencies of a token's dependent steps.
+template <int n>
+constexpr int kBlocks = n <= 8 ? 4 : n <= 20 ? 3 : 1;
+
+// V consecutive values of global or shared memory by one access.
+template <int V, typename Tp>
+__device__ __forceinline__ void load_chunk(Tp (&x)[V], const Tp* p, bool global) {
+  if constexpr (V == 4) {
+    const uint4 v = global ? __ldg(reinterpret_cast<const uint4*>(p)) : *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if constexpr (sizeof(Tp) == 4) x[c] = *reinterpret_cast<const Tp*>(&w[c]);
+  } else {
+    x[0] = global ? __ldg(p) : *p;
+  }
+}
+
+// One token per L lanes; lane l holds kC chunks of V experts, chunk q = l + L i
+// being experts V q .. V q + V - 1.  The warps go through the tokens in strides.
 // Bound by instruction issue, not memory (8192 tokens of 256 experts read 8.4
-// MB, 1.3 us): about 25 instructions per score (exp and a correctly rounded
-// reciprocal or quotient) and 20 per selection round.  So a token's candidates
-// are compacted to the kept groups before the selection (8 groups of 32, 4
-// kept: four keys per lane to sort instead of eight), everything but the scores
-// is done on integer keys, and what depends on the expert alone (bias, place
-// in shared memory) is worked out once per warp.
-template <int kPerLane, int L, bool kGroups>
-__global__ void __launch_bounds__(32 * kMaxWarps)
+// MB, 1.3 us; 40001 of 160 25.6 MB, 3.8 us): so experts go in chunks of four
+// wherever E and the groups allow it (one load, one check and one group index
+// for four), everything but the scores is done on integer keys, a token's
+// candidates are compacted to the kept groups before the selection, and in a
+// large batch one warp routes two or four tokens, which share the instructions
+// of the groups, the rounds and the weights.
+template <int V, int kC, int L, bool kGroups>
+__global__ void __launch_bounds__(32 * kMaxWarps, kBlocks<V * kC>)
 route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, RouteCfg c,
-                    int T, int E, int k, int tpc, int group_pad, int32_t* __restrict__ topk_idx,
-                    float* __restrict__ topk_w, int32_t* __restrict__ chunk_hist,
-                    int* __restrict__ status, bool whole) {
-  // per token of the block: n_group * (group size + pad) keys, n_group kept groups
-  extern __shared__ uint32_t stage[];
+                    int T, int E, int k, int tpc, int group_pad, int region,
+                    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
+                    int32_t* __restrict__ chunk_hist, int* __restrict__ status, bool whole) {
+  // per token of the block `region` words: n_group * (group size + pad) keys, then
+  // the kept groups
+  extern __shared__ __align__(16) uint32_t stage[];
   pdl_trigger();
+  constexpr int n = V * kC;
   const int lane = threadIdx.x & (L - 1), seg = threadIdx.x / L;   // seg: the block's token
   const int per_block = blockDim.x / L, stride = gridDim.x * per_block;
   const bool two = kGroups && c.group_top == 2;
-  const bool scored = bias != nullptr;       // all scores take part in the choice
-  const bool need_s = scored || (two && c.softmax);   // the scores' exact sum decides
+  const bool scored = bias != nullptr;                  // all scores take part in the choice
+  const bool need_s = scored || (two && c.softmax);     // the scores' exact sum decides
   const int gsz = kGroups ? E / c.n_group : E, pitch = gsz + group_pad;
-  uint32_t* st = kGroups ? stage + (size_t)seg * c.n_group * (pitch + 1) : nullptr;
+  const int nq = E / V;                                 // chunks of a row
+  uint32_t* st = kGroups ? stage + (size_t)seg * region : nullptr;
   int* list = kGroups ? reinterpret_cast<int*>(st) + c.n_group * pitch : nullptr;
-  // kept in registers across tokens: this lane's biases
-  constexpr bool kKeep = kPerLane <= 8;
-  float be[kKeep ? kPerLane : 1];
+  // few logits per lane: this lane's biases are kept across tokens, and the
+  // next token's logits are on their way while one is routed
+  constexpr bool kKeep = n <= 8;
+  float be[kKeep ? kC : 1][V];
   float nan = 0.f;     // turns NaN with the first value that is not finite
   bool bad = false;
   if constexpr (kKeep) {
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      be[i] = scored && lane + L * i < E ? __ldg(bias + lane + L * i) : 0.f;
-      bad |= !(be[i] < INFINITY);   // NaN or +inf: -inf switches an expert off
+    for (int i = 0; i < kC; ++i) {
+#pragma unroll
+      for (int x = 0; x < V; ++x) be[i][x] = 0.f;
+      if (scored && lane + L * i < nq) load_chunk<V>(be[i], bias + V * (lane + L * i), true);
+#pragma unroll
+      for (int x = 0; x < V; ++x) bad |= !(be[i][x] < INFINITY);   // -inf switches an expert off
     }
   }
-  float next[kPerLane];
+  float next[kC][V];
   auto fetch = [&](int t) {
-    const float* row = logits + (size_t)(t < T ? t : T - 1) * E;
+    const float* row = logits + (size_t)(t < T ? t : T - 1) * E + V * lane;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
-      next[i] = lane + L * i < E ? __ldg(row + lane + L * i) : -INFINITY;
+    for (int i = 0; i < kC; ++i) {
+#pragma unroll
+      for (int x = 0; x < V; ++x) next[i][x] = -INFINITY;
+      if (lane + L * i < nq) load_chunk<V>(next[i], row + V * L * i, true);
+    }
   };
   // the warp's tokens stay together: its first one decides
   const int first = blockIdx.x * per_block + (seg & ~(32 / L - 1)), own = seg & (32 / L - 1);
-  if (first < T) fetch(first + own);
+  if (kKeep && first < T) fetch(first + own);
   for (int tw = first; tw < T; tw += stride) {
     const bool live = tw + own < T;
     const int t = live ? tw + own : T - 1;
     const float* row = logits + (size_t)t * E;
-    float v[kPerLane];
+    float v[kC][V];
+    if (!kKeep) fetch(t);
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      v[i] = next[i];
-      if (lane + L * i < E) nan = fmaf(v[i], 0.f, nan);
-    }
-    if (tw + stride < T) fetch(tw + stride + own);
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int x = 0; x < V; ++x) v[i][x] = next[i][x];
+    if (kKeep && tw + stride < T) fetch(tw + stride + own);
     // softmax: the row's maximum and the sum of exp(l - m), rounded once where
     // the scores decide
     float m = 0.f, S = 1.f;
     if (c.softmax && (need_s || !c.renorm)) {
-      float mx = v[0];
+      float mx = -INFINITY;
 #pragma unroll
-      for (int i = 1; i < kPerLane; ++i) mx = fmaxf(mx, v[i]);
+      for (int i = 0; i < kC; ++i)
+#pragma unroll
+        for (int x = 0; x < V; ++x) mx = fmaxf(mx, v[i][x]);
       m = seg_max<L>(mx);
       if (need_s) {
         float hi = 0.f, lo = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-          pair_add(hi, lo, lane + L * i < E ? expf(v[i] - m) : 0.f);
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+          for (int x = 0; x < V; ++x) pair_add(hi, lo, expf(v[i][x] - m));   // exp(-inf) = 0
         S = seg_sum_rounded<L>(hi, lo);
       } else {
+        // a factor of the weights only: the short exp, whose error of 2 ulp + |l - m|
+        // 2^-23 stands on terms of size exp(l - m)
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) sum += lane + L * i < E ? expf(v[i] - m) : 0.f;
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+          for (int x = 0; x < V; ++x) sum += __expf(v[i][x] - m);
         S = seg_sum<L>(sum);
       }
     }
     auto score = [&](float l) { return c.softmax ? __fdiv_rn(expf(l - m), S) : sigmoid_rn(l); };
-    uint32_t key[kPerLane];
+    uint32_t key[n];
+    int id[n];
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + L * i;
-      float r = v[i];
-      if (scored && e < E) {
-        float b;
-        if constexpr (kKeep) {
-          b = be[i];
-        } else {
-          b = __ldg(bias + e);
-          bad |= !(b < INFINITY);
-        }
-        r = __fadd_rn(score(r), b);
+    for (int i = 0; i < kC; ++i) {
+      const int q = lane + L * i;
+      const bool in = q < nq;
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        key[i * V + x] = 0u;
+        id[i * V + x] = V * q + x;
       }
-      key[i] = e < E ? rank_key(r) : 0u;
-      if constexpr (kGroups) {
-        const int g = (int)((uint32_t)e * c.group_magic >> 20);
-        if (e < E) st[e + g * group_pad] = key[i];
+      if (in) {
+        float b[V];
+        if (scored) {
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int x = 0; x < V; ++x) b[x] = be[i][x];
+          } else {
+            load_chunk<V>(b, bias + V * q, true);
+#pragma unroll
+            for (int x = 0; x < V; ++x) bad |= !(b[x] < INFINITY);
+          }
+        }
+        uint32_t kx[V];
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          nan = fmaf(v[i][x], 0.f, nan);
+          const float r = scored ? __fadd_rn(score(v[i][x]), b[x]) : v[i][x];
+          kx[x] = key[i * V + x] = rank_key(r);
+        }
+        if constexpr (kGroups) {
+          const int g = (int)((uint32_t)(V * q) * c.group_magic >> 20);
+          uint32_t* at = st + V * q + g * group_pad;
+          if constexpr (V == 4)
+            *reinterpret_cast<uint4*>(at) = make_uint4(kx[0], kx[1], kx[2], kx[3]);
+          else
+            *at = kx[0];
+        }
       }
     }
     int idx;
     if constexpr (!kGroups) {
-      idx = select_best<kPerLane, L>(key, k, lane);
+      idx = select_best<n, L>(key, id, k, lane);
     } else {
       __syncwarp();
       // lpg lanes scan one group: its two largest keys
@@ -264,11 +356,15 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
       uint32_t a1 = 0u, a2 = 0u;
       if (g < c.n_group) {
         const uint32_t* gs = st + g * pitch;
-#pragma unroll 4
-        for (int j = sub; j < gsz; j += lpg) {
-          const uint32_t x = gs[j];
-          a2 = max(a2, min(a1, x));
-          a1 = max(a1, x);
+#pragma unroll 2
+        for (int j = V * sub; j < gsz; j += V * lpg) {
+          uint32_t x[V];
+          load_chunk<V>(x, gs + j, false);
+#pragma unroll
+          for (int y = 0; y < V; ++y) {
+            a2 = max(a2, min(a1, x[y]));
+            a1 = max(a1, x[y]);
+          }
         }
       }
       for (int off = 1; off < lpg; off <<= 1) {
@@ -290,36 +386,40 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
       // the best groups, one after the other (equal ones: the lower first)
       unsigned kept = 0u;
       for (int j = 0; j < c.topk_group; ++j) {
-        const uint32_t top = seg_max<L>(gk);
-        const uint32_t win = seg_min<L>(gk == top && top != 0u ? (uint32_t)lane : 31u);
+        const int win = __ffs(seg_ballot<L>(gk == seg_max<L>(gk))) - 1;
         kept |= 1u << win;
-        if ((int)win == lane) gk = 0u;
+        if (win == lane) gk = 0u;
       }
       if ((kept >> lane) & 1u) list[__popc(kept & ((1u << lane) - 1u))] = g * pitch;
       __syncwarp();
       // candidate j: the j-th expert of the kept groups in ascending order
       const int n_cand = c.topk_group * gsz;
-      auto place_of = [&](int j) {
-        const int cg = (int)((uint32_t)j * c.group_magic >> 20);
-        return list[cg] + (j - cg * gsz);
+      auto candidates = [&](auto& ck, auto& ci, int chunks) {
+#pragma unroll
+        for (int i = 0; i < chunks; ++i) {
+          const int j = V * (lane + L * i);
+          const int cg = (int)((uint32_t)j * c.group_magic >> 20);
+          uint32_t x[V];
+#pragma unroll
+          for (int y = 0; y < V; ++y) x[y] = 0u;
+          if (j < n_cand) load_chunk<V>(x, st + list[cg] + (j - cg * gsz), false);
+#pragma unroll
+          for (int y = 0; y < V; ++y) {
+            ck[i * V + y] = x[y];
+            ci[i * V + y] = j + y;
+          }
+        }
       };
       int pick;
-      if (kPerLane > 1 && n_cand <= L * (kPerLane / 2)) {
-        constexpr int kHalf = kPerLane > 1 ? kPerLane / 2 : 1;
-        uint32_t half[kHalf];
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) {
-          const int j = lane + L * i;
-          half[i] = j < n_cand ? st[place_of(j)] : 0u;
-        }
-        pick = select_best<kHalf, L>(half, k, lane);
+      constexpr int kH = kC > 1 ? kC / 2 : 1;
+      if (kC > 1 && n_cand <= L * kH * V) {
+        uint32_t hk[kH * V];
+        int hi[kH * V];
+        candidates(hk, hi, kH);
+        pick = select_best<kH * V, L>(hk, hi, k, lane);
       } else {
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-          const int j = lane + L * i;
-          key[i] = j < n_cand ? st[place_of(j)] : 0u;
-        }
-        pick = select_best<kPerLane, L>(key, k, lane);
+        candidates(key, id, kC);
+        pick = select_best<n, L>(key, id, k, lane);
       }
       pick = (int)min((uint32_t)pick, (uint32_t)(n_cand - 1));
       const int cg = (int)((uint32_t)pick * c.group_magic >> 20);
@@ -419,42 +519,56 @@ route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __rest
   if (__any_sync(0xffffffffu, lane < k && !in) && lane == 0) set_status(status, MOE_ERR_INVALID_ARG);
 }
 
-// Four blocks of eight warps per SM, about what the registers allow at once.
-int grid_of(int T, int per_block) {
-  const int blocks = (T + per_block - 1) / per_block, most = 4 * device_sm_count();
-  return blocks < most ? blocks : most;
+// How a batch is routed: lanes per token, and experts per chunk.
+struct Shape {
+  int L, V;
+};
+// The slots and the groups need a lane each.  A few tokens are routed one per
+// warp, for the shortest chain of steps; from 2048 on (three warps per
+// scheduler) the instructions bound, and a warp shares them among as many tokens
+// as can be.  Chunks of four where neither a row nor a group splits one.
+constexpr int kManyTokens = 2048;
+Shape shape_of(int T, int E, int k, int n_group) {
+  const int need = k > n_group ? k : n_group;
+  const int V = E % 4 == 0 && E / n_group % 4 == 0 && E > 16 ? 4 : 1;
+  if (T >= kManyTokens || E <= 16) {
+    if (need <= 8 && E <= 160) return {8, V};
+    if (need <= 16 && E <= 256) return {16, V};
+  }
+  return {32, V};
 }
 
-template <int kPerLane, int L>
+template <int V, int kC, int L>
 cudaError_t launch_t(const float* logits, const float* bias, const RouteCfg& c, int T, int E, int k,
                      int32_t* topk_idx, float* topk_w, int32_t* chunk_hist, int* status, bool whole,
                      cudaStream_t s) {
   const int tpc = tokens_per_chunk(k);
-  const int per_warp = 32 / L;
-  if (c.n_group > 1) {
-    // a group starts as many banks after the one before it as lanes scan it, so
-    // the lanes that scan the groups of a token read different banks
-    const int gsz = E / c.n_group, lpg = c.lanes_per_group / per_warp;
-    const int pad = (lpg - gsz % 32 + 32) % 32;
-    const size_t bytes = (size_t)c.n_group * (gsz + pad + 1) * 4 * per_warp;
-    const int warps = bytes * kMaxWarps <= 48 * 1024 ? kMaxWarps : kMaxWarps / 2;
+  constexpr int per_warp = 32 / L;
+  int warps = kMaxWarps;
+  auto grid_of = [&]() {   // as many blocks as the SMs take at once
     const int per_block = warps * per_warp;
-    route_scored_kernel<kPerLane, L, true>
-        <<<grid_of(T, per_block), 32 * warps, bytes * warps, s>>>(
-            logits, bias, c, T, E, k, tpc, pad, topk_idx, topk_w, chunk_hist, status,
-            whole && T <= per_block);
+    const int blocks = (T + per_block - 1) / per_block, most = kBlocks<V * kC> * device_sm_count();
+    return blocks < most ? blocks : most;
+  };
+  if (c.n_group > 1) {
+    // A group starts as many chunks' banks after the one before it as lanes scan
+    // it, and a token L chunks after the one before it, so that a warp's lanes
+    // read different banks; every group starts on a chunk.
+    const int gsz = E / c.n_group, lpg = c.lanes_per_group / per_warp;
+    const int pad = (V * lpg - gsz % 32 + 64) % 32;
+    int region = c.n_group * (gsz + pad + 1);
+    region += (V * L % 32 - region % 32 + 32) % 32;
+    const size_t bytes = (size_t)region * 4 * per_warp;
+    if (bytes * warps > 48 * 1024) warps /= 2;
+    if (bytes * warps > 48 * 1024) warps /= 2;
+    route_scored_kernel<V, kC, L, true><<<grid_of(), 32 * warps, bytes * warps, s>>>(
+        logits, bias, c, T, E, k, tpc, pad, region, topk_idx, topk_w, chunk_hist, status, whole);
   } else {
-    const int per_block = kMaxWarps * per_warp;
-    route_scored_kernel<kPerLane, L, false>
-        <<<grid_of(T, per_block), 32 * kMaxWarps, 0, s>>>(
-            logits, bias, c, T, E, k, tpc, 0, topk_idx, topk_w, chunk_hist, status,
-            whole && T <= per_block);
+    route_scored_kernel<V, kC, L, false><<<grid_of(), 32 * warps, 0, s>>>(
+        logits, bias, c, T, E, k, tpc, 0, 0, topk_idx, topk_w, chunk_hist, status, whole);
   }
   return cudaGetLastError();
 }
-
-// Lanes per token for E experts (k <= E, and at most E groups).
-int lanes_of(int E) { return E <= 8 ? 8 : E <= 16 ? 16 : 32; }
 
 }  // namespace
 
@@ -474,31 +588,42 @@ RouteCfg make_route_cfg(const moe_route_config& a, int E) {
   return c;
 }
 
-// Tokens that one block routes: the block writes the status itself.
-bool route_scored_whole(int T, int E) {
-  const int per_warp = 32 / lanes_of(E);
-  return T <= kMaxWarps / 2 * per_warp;
+// A quarter of a block's tokens at most (the block may have two warps): it
+// writes the status itself.
+bool route_scored_whole(int T, int E, int k, const RouteCfg& c) {
+  return T <= kMaxWarps / 4 * (32 / shape_of(T, E, k, c.n_group).L);
 }
 
 cudaError_t launch_route_scored(const float* logits, const float* bias, const RouteCfg& c, int T,
                                 int E, int k, int32_t* topk_idx, float* topk_w,
                                 int32_t* chunk_hist, int* status, cudaStream_t s, bool whole) {
   if (T == 0) return cudaSuccess;
-#define MOE_ROUTE_CASE(most, n, lanes) \
-  if (E <= most)                       \
-    return launch_t<n, lanes>(logits, bias, c, T, E, k, topk_idx, topk_w, chunk_hist, status, whole, s)
-  MOE_ROUTE_CASE(8, 1, 8);
-  MOE_ROUTE_CASE(16, 1, 16);
-  MOE_ROUTE_CASE(32, 1, 32);
-  MOE_ROUTE_CASE(64, 2, 32);
-  MOE_ROUTE_CASE(96, 3, 32);
-  MOE_ROUTE_CASE(128, 4, 32);
-  MOE_ROUTE_CASE(160, 5, 32);
-  MOE_ROUTE_CASE(192, 6, 32);
-  MOE_ROUTE_CASE(256, 8, 32);
-  MOE_ROUTE_CASE(384, 12, 32);
-  MOE_ROUTE_CASE(512, 16, 32);
-  MOE_ROUTE_CASE(MOE_MAX_EXPERTS, 32, 32);
+  const Shape f = shape_of(T, E, k, c.n_group);
+#define MOE_ROUTE_CASE(v, n, lanes)                      \
+  if (f.V == v && f.L == lanes && E <= v * n * lanes)    \
+    return launch_t<v, n, lanes>(logits, bias, c, T, E, k, topk_idx, topk_w, chunk_hist, status, whole, s)
+  MOE_ROUTE_CASE(1, 1, 8);
+  MOE_ROUTE_CASE(1, 2, 8);
+  MOE_ROUTE_CASE(1, 8, 8);
+  MOE_ROUTE_CASE(1, 20, 8);
+  MOE_ROUTE_CASE(1, 1, 16);
+  MOE_ROUTE_CASE(1, 8, 16);
+  MOE_ROUTE_CASE(1, 16, 16);
+  MOE_ROUTE_CASE(1, 2, 32);
+  MOE_ROUTE_CASE(1, 4, 32);
+  MOE_ROUTE_CASE(1, 8, 32);
+  MOE_ROUTE_CASE(1, 16, 32);
+  MOE_ROUTE_CASE(1, 32, 32);
+  MOE_ROUTE_CASE(4, 1, 8);
+  MOE_ROUTE_CASE(4, 2, 8);
+  MOE_ROUTE_CASE(4, 4, 8);
+  MOE_ROUTE_CASE(4, 5, 8);
+  MOE_ROUTE_CASE(4, 2, 16);
+  MOE_ROUTE_CASE(4, 4, 16);
+  MOE_ROUTE_CASE(4, 1, 32);
+  MOE_ROUTE_CASE(4, 2, 32);
+  MOE_ROUTE_CASE(4, 4, 32);
+  MOE_ROUTE_CASE(4, 8, 32);
 #undef MOE_ROUTE_CASE
   return cudaErrorInvalidValue;
 }
