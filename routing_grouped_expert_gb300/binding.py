@@ -127,6 +127,14 @@ def _need(t: torch.Tensor, dtype, shape, name: str, cuda: bool = True):
         raise ValueError(f"{name}: must be contiguous")
 
 
+def _out(t: torch.Tensor | None, dtype, shape, like: torch.Tensor, name: str) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one on `like`'s device."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, dtype, shape, name)
+    return t
+
+
 class Workspace:
     """A reusable device workspace (grows on demand, 256-byte aligned)."""
 
@@ -241,15 +249,11 @@ def moe_route_scored(logits: torch.Tensor, k: int, config: RouteConfig, bias=Non
     T, E = logits.shape
     _need(logits, torch.float32, (T, E), "logits")
     _need_bias(bias, E)
-    topk_idx = torch.empty(T, k, dtype=torch.int32, device=logits.device) \
-        if topk_idx is None else topk_idx
-    topk_w = torch.empty(T, k, dtype=torch.float32, device=logits.device) \
-        if topk_w is None else topk_w
-    _need(topk_idx, torch.int32, (T, k), "topk_idx")
-    _need(topk_w, torch.float32, (T, k), "topk_w")
-    ws = _ws(ws, 256)
+    topk_idx = _out(topk_idx, torch.int32, (T, k), logits, "topk_idx")
+    topk_w = _out(topk_w, torch.float32, (T, k), logits, "topk_w")
+    buf = _ws(ws, 256).buf
     _check(load_library().moe_route_scored(_p(logits), _p(bias), config._ptr, T, E, k,
-                                           _p(topk_idx), _p(topk_w), ws.ptr, ws.nbytes,
+                                           _p(topk_idx), _p(topk_w), _p(buf), buf.numel(),
                                            _stream()), "moe_route_scored")
     return topk_idx, topk_w
 
@@ -264,13 +268,11 @@ def moe_route_scored_backward(dtopk_w: torch.Tensor, topk_idx: torch.Tensor, log
     _need(dtopk_w, torch.float32, (T, k), "dtopk_w")
     _need(topk_idx, torch.int32, (T, k), "topk_idx")
     _need_bias(bias, E)
-    dlogits = torch.empty(T, E, dtype=torch.float32, device=logits.device) \
-        if dlogits is None else dlogits
-    _need(dlogits, torch.float32, (T, E), "dlogits")
-    ws = _ws(ws, 256)
+    dlogits = _out(dlogits, torch.float32, (T, E), logits, "dlogits")
+    buf = _ws(ws, 256).buf
     _check(load_library().moe_route_scored_backward(_p(dtopk_w), _p(topk_idx), _p(logits),
                                                     _p(bias), config._ptr, T, E, k, _p(dlogits),
-                                                    ws.ptr, ws.nbytes, _stream()),
+                                                    _p(buf), buf.numel(), _stream()),
            "moe_route_scored_backward")
     return dlogits
 
@@ -582,12 +584,11 @@ def moe_adapter_project(x, W, A, B, scale, adapter_idx, y=None, ws: Workspace | 
     """y [T, N] = x W + scale_a (x A_a^T) B_a, a = adapter_idx[t] (-1: none);
     A [n, R, H], B [n, R, N]."""
     T, H, N, n, R = _need_adapters(x, W, A, B, scale, adapter_idx)
-    y = torch.empty(T, N, dtype=torch.bfloat16, device=x.device) if y is None else y
-    _need(y, torch.bfloat16, (T, N), "y")
+    y = _out(y, torch.bfloat16, (T, N), x, "y")
     lib = load_library()
-    ws = _ws(ws, lib.moe_adapter_workspace_size(T, H, N, n, R))
+    buf = _ws(ws, lib.moe_adapter_workspace_size(T, H, N, n, R)).buf
     _check(lib.moe_adapter_project(_p(x), _p(W), _p(A), _p(B), _p(scale), _p(adapter_idx), T, H,
-                                   N, n, R, _p(y), ws.ptr, ws.nbytes, _stream()),
+                                   N, n, R, _p(y), _p(buf), buf.numel(), _stream()),
            "moe_adapter_project")
     return y
 
@@ -599,10 +600,10 @@ def moe_adapter_project_backward(dy, x, W, A, B, scale, adapter_idx,
     _need(dy, torch.bfloat16, (T, N), "dy")
     dx, dA, dB = torch.empty_like(x), torch.empty_like(A), torch.empty_like(B)
     lib = load_library()
-    ws = _ws(ws, lib.moe_adapter_workspace_size_backward(T, H, N, n, R))
+    buf = _ws(ws, lib.moe_adapter_workspace_size_backward(T, H, N, n, R)).buf
     _check(lib.moe_adapter_project_backward(_p(dy), _p(x), _p(W), _p(A), _p(B), _p(scale),
                                             _p(adapter_idx), T, H, N, n, R, _p(dx), _p(dA),
-                                            _p(dB), ws.ptr, ws.nbytes, _stream()),
+                                            _p(dB), _p(buf), buf.numel(), _stream()),
            "moe_adapter_project_backward")
     return dx, dA, dB
 

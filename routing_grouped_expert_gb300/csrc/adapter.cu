@@ -18,6 +18,8 @@
 // bf16 once, as an MMA operand; y, dx, dA and dB are rounded once on output.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "moe_common.cuh"
 #include "ptx.cuh"
 
@@ -1517,11 +1519,17 @@ ExpandPlan plan_expand(int T, int K, int M) {
   return best;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, int smem, bool pdl,
-                           cudaStream_t s, Args&&... args) {
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Launches kKern as clusters of `cluster` CTAs.  Its shared-memory limit is raised
+// once per device (half a microsecond a call otherwise), and again should a
+// launch find it back at its default, as after a device reset.
+template <auto kKern, typename... Args>
+cudaError_t launch_cluster(dim3 grid, int cluster, int smem, bool pdl, cudaStream_t s,
+                           Args&&... args) {
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  const uint64_t bit = 1ull << (dev & 63);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
@@ -1543,7 +1551,15 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, int s
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (raised.load(std::memory_order_relaxed) & bit) {
+    err = cudaLaunchKernelEx(&cfg, kKern, args...);
+    if (err != cudaErrorInvalidValue) return err;
+    (void)cudaGetLastError();
+  }
+  err = cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  raised.fetch_or(bit, std::memory_order_relaxed);
+  return cudaLaunchKernelEx(&cfg, kKern, args...);
 }
 
 template <int kNB>
@@ -1552,10 +1568,10 @@ cudaError_t launch_shrink_nb(int cluster, int gy, const ShrinkMaps& m, const Shr
   const dim3 grid(n_tt * cluster, gy);
   constexpr int smem = ShrinkCfg<kNB>::kSmemBytes;
   switch (cluster) {
-    case 1: return launch_cluster(adapter_shrink_kernel<kNB, 1>, grid, 1, smem, !a.first, s, m, a);
-    case 2: return launch_cluster(adapter_shrink_kernel<kNB, 2>, grid, 2, smem, !a.first, s, m, a);
-    case 4: return launch_cluster(adapter_shrink_kernel<kNB, 4>, grid, 4, smem, !a.first, s, m, a);
-    default: return launch_cluster(adapter_shrink_kernel<kNB, 8>, grid, 8, smem, !a.first, s, m, a);
+    case 1: return launch_cluster<adapter_shrink_kernel<kNB, 1>>(grid, 1, smem, !a.first, s, m, a);
+    case 2: return launch_cluster<adapter_shrink_kernel<kNB, 2>>(grid, 2, smem, !a.first, s, m, a);
+    case 4: return launch_cluster<adapter_shrink_kernel<kNB, 4>>(grid, 4, smem, !a.first, s, m, a);
+    default: return launch_cluster<adapter_shrink_kernel<kNB, 8>>(grid, 8, smem, !a.first, s, m, a);
   }
 }
 
@@ -1608,16 +1624,16 @@ cudaError_t launch_split_nb(int split, const ExpandMaps& m, const ExpandArgs& a,
   constexpr int smem = SplitCfg<kNB>::kSmemBytes;
   switch (split) {
     case 1:
-      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 1>, grid, 1, smem, true, s, m,
+      return launch_cluster<adapter_expand_split_kernel<kNB, kKMajor, 1>>(grid, 1, smem, true, s, m,
                             a);
     case 2:
-      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 2>, grid, 2, smem, true, s, m,
+      return launch_cluster<adapter_expand_split_kernel<kNB, kKMajor, 2>>(grid, 2, smem, true, s, m,
                             a);
     case 4:
-      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 4>, grid, 4, smem, true, s, m,
+      return launch_cluster<adapter_expand_split_kernel<kNB, kKMajor, 4>>(grid, 4, smem, true, s, m,
                             a);
     default:
-      return launch_cluster(adapter_expand_split_kernel<kNB, kKMajor, 8>, grid, 8, smem, true, s, m,
+      return launch_cluster<adapter_expand_split_kernel<kNB, kKMajor, 8>>(grid, 8, smem, true, s, m,
                             a);
   }
 }
@@ -1625,7 +1641,7 @@ cudaError_t launch_split_nb(int split, const ExpandMaps& m, const ExpandArgs& a,
 template <bool kKMajor>
 cudaError_t launch_expand_t(int split, const ExpandMaps& m, const ExpandArgs& a, cudaStream_t s) {
   if (split == 0)
-    return launch_cluster(adapter_expand_kernel<kKMajor>, dim3(device_sm_count() / 2 * 2), 2,
+    return launch_cluster<adapter_expand_kernel<kKMajor>>(dim3(device_sm_count() / 2 * 2), 2,
                           FullCfg::kSmemBytes, true, s, m, a);
   if (a.nb <= 32) return launch_split_nb<32, kKMajor>(split, m, a, s);
   if (a.nb <= 64) return launch_split_nb<64, kKMajor>(split, m, a, s);
@@ -1723,8 +1739,8 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, plan, masks, {dA, dB}, status};
   const dim3 grid((unsigned)(z.n * ((z.H + z.N) / kM)));
   if (z.R > 64)
-    return launch_cluster(adapter_wgrad_kernel<2>, grid, 1, WgradCfg<2>::kSmemBytes, true, s, m, a);
-  return launch_cluster(adapter_wgrad_kernel<1>, grid, 1, WgradCfg<1>::kSmemBytes, true, s, m, a);
+    return launch_cluster<adapter_wgrad_kernel<2>>(grid, 1, WgradCfg<2>::kSmemBytes, true, s, m, a);
+  return launch_cluster<adapter_wgrad_kernel<1>>(grid, 1, WgradCfg<1>::kSmemBytes, true, s, m, a);
 }
 
 }  // namespace moe

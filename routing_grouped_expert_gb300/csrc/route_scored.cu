@@ -192,7 +192,7 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
 // Blocks of eight warps per SM for n logits per lane: what hides the fixed
 // latencies of a token's dependent steps.
 template <int n>
-constexpr int kBlocks = n <= 8 ? 4 : n <= 20 ? 3 : 1;
+constexpr int kBlocks = n <= 20 ? 4 : 1;
 
 // V consecutive values of global or shared memory by one access.
 template <int V, typename Tp>
