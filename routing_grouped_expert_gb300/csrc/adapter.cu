@@ -136,6 +136,58 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const vo
       : "memory");
   return ok ? true : wait_slow(bar, parity, abort_flag);
 }
+// The role loops' instructions on shared addresses (no generic pointers to
+// convert at every stage).
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, int z, int w, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+      : "memory");
+}
+// A load that lands, and counts, at the same place in every CTA of `mask`.
+__device__ __forceinline__ void load_2d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                  int x, int y, uint16_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
+      : "memory");
+}
+// Arrive once on `bar`'s place in every CTA of `mask` when this thread's
+// tcgen05 operations so far have completed.
+__device__ __forceinline__ void commit_multicast(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
 // A 128-byte-swizzled operand descriptor from its two words (see
 // ptx::sdesc_sw128): the first word moves with the address >> 4.
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
@@ -481,6 +533,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       const uint64_t pol_p = policy_evict_normal(), pol_v = policy_evict_last();
       const bool leader = elect_lane();
       const int from = at.count;
+      const uint32_t sbase = smem_u32(smem);
       const uint32_t bytes = (uint32_t)((q_end + (gather ? 0 : a.nb)) * kK * 2);
       // this warp's boxes: at most 16 of 8 rows over four warps
       int row[4], ad[4];
@@ -496,17 +549,16 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
         if (!ok) break;
-        uint64_t* fb = &sh->full[at.stage];
-        uint8_t* st = smem + at.stage * stage_bytes;
+        const uint32_t fb = full0 + at.stage * 8, st = sbase + at.stage * stage_bytes;
         if (loader == 0 && leader) {
-          mbar_arrive_expect_tx(fb, bytes);
-          if (!gather) tma_load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
+          expect_tx(fb, bytes);
+          if (!gather) load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (box[i] && leader)
-            tma_load_3d(st + (loader + 4 * i) * a.rb * (kK * 2), &maps.p, fb, kb * kK, row[i], ad[i],
-                        pol_p);
+            load_3d(st + (loader + 4 * i) * a.rb * (kK * 2), &maps.p, fb, kb * kK, row[i], ad[i],
+                    pol_p);
         at.next();
       }
       if (leader && !ok) {
@@ -536,7 +588,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
           for (int kk = 0; kk < kK / 16; ++kk)
             mma_bf16_ss(tmem, desc_of(la + 2 * kk, desc_hi(1024)), desc_of(lb + 2 * kk, desc_hi(1024)),
                         idesc, (kb > kb0 || kk) ? 1u : 0u);
-          mma_commit(&sh->empty[at.stage]);
+          commit(empty0 + at.stage * 8);
         }
         at.next();
       }
@@ -632,48 +684,26 @@ struct ExpandArgs {
   int* status;
 };
 
-// A TMA load of this CTA that lands, and counts, at the same place in every
-// CTA of the cluster in `mask`.
-__device__ __forceinline__ void tma_load_2d_multicast(void* dst, const CUtensorMap* map,
-                                                      uint64_t* bar, int x, int y, uint16_t mask,
-                                                      uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "h"(mask),
-      "l"(policy)
-      : "memory");
-}
-// Arrive once on `bar`'s place in every CTA of `mask` when this thread's
-// tcgen05 operations so far have completed.
-__device__ __forceinline__ void mma_commit_multicast(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(mask)
-      : "memory");
-}
 // Columns x .. x + 64 of a block's rows; in a pair, rank r loads the r-th half
 // for both CTAs.
 template <bool kPair>
-__device__ __forceinline__ void load_tokens(uint8_t* dst, uint64_t* fb, const CUtensorMap* map, int nb,
+__device__ __forceinline__ void load_tokens(uint32_t dst, uint32_t fb, const CUtensorMap* map, int nb,
                                             int x, int row0, uint64_t pol, int rank) {
   if constexpr (kPair)
-    tma_load_2d_multicast(dst + rank * (nb / 2 * kK * 2), map, fb, x, row0 + rank * (nb / 2), 0x3,
-                          pol);
+    load_2d_multicast(dst + rank * (nb / 2 * kK * 2), map, fb, x, row0 + rank * (nb / 2), 0x3, pol);
   else
-    tma_load_2d(dst, map, fb, x, row0, pol);
+    load_2d(dst, map, fb, x, row0, pol);
 }
 // The weight operand of one stage and its token rows.
 template <bool kKMajor, bool kPair = false>
-__device__ __forceinline__ void load_base(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
+__device__ __forceinline__ void load_base(uint32_t st, uint32_t fb, const ExpandMaps& maps,
                                           int nb, int kb, int mt, int row0, uint64_t pol_w, uint64_t pol_v,
                                           int rank = 0) {
-  mbar_arrive_expect_tx(fb, (uint32_t)(kABytes + nb * kK * 2));
+  expect_tx(fb, (uint32_t)(kABytes + nb * kK * 2));
   if constexpr (kKMajor)
-    tma_load_2d(st, &maps.w, fb, kb * kK, mt * kM, pol_w);
+    load_2d(st, &maps.w, fb, kb * kK, mt * kM, pol_w);
   else
-    tma_load_3d(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
+    load_3d(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
   load_tokens<kPair>(st + kABytes, fb, &maps.v, nb, kb * kK, row0, pol_v, rank);
 }
 // A block's entry list, copied to shared memory by the warp that uses it.
@@ -689,19 +719,19 @@ __device__ __forceinline__ uint4 load_list(const BlockPlan* plan, int lane) {
 // the block's entries, in boxes of rb rows, each [2 feature atoms][rb rows][128
 // bytes].
 template <bool kPair = false>
-__device__ __forceinline__ void load_ext(uint8_t* st, uint64_t* fb, const ExpandMaps& maps,
+__device__ __forceinline__ void load_ext(uint32_t st, uint32_t fb, const ExpandMaps& maps,
                                          const ExpandArgs& a, const uint16_t* list, int q_all, int j,
                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v,
                                          bool leader, int rank = 0) {
   if (leader) {
-    mbar_arrive_expect_tx(fb, (uint32_t)(kABytes + a.nb * kK * 2));
+    expect_tx(fb, (uint32_t)(kABytes + a.nb * kK * 2));
     load_tokens<kPair>(st + kABytes, fb, &maps.z, a.nb, j * kK, row0, pol_v, rank);
   }
   int e = j * kK / a.R, row = j * kK - e * a.R;
   for (int q = 0; q < kK; q += a.rb) {
     // past the last entry: an adapter that does not exist, read as zeros
     const int ad = j * kK + q < q_all ? (int)list[e] : a.n;
-    if (leader) tma_load_4d(st + q * (kM * 2), &maps.p, fb, 0, row, mt * 2, ad, pol_w);
+    if (leader) load_4d(st + q * (kM * 2), &maps.p, fb, 0, row, mt * 2, ad, pol_w);
     row += a.rb;
     if (row == a.R) {
       row = 0;
@@ -827,7 +857,8 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
   const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty);
-  const uint32_t ready0 = smem_u32(sh->ready);
+  const uint32_t ready0 = smem_u32(sh->ready), loaded0 = smem_u32(sh->loaded);
+  const uint32_t sbase = smem_u32(smem);
 
   if (warp == 0) {
     // a weight tile read by one block is streamed past L2
@@ -839,7 +870,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
       if (leader)
-        load_base<kKMajor>(smem + at.stage * stage_bytes, &sh->full[base.stage], maps, a.nb, kb, mt,
+        load_base<kKMajor>(sbase + at.stage * stage_bytes, full0 + base.stage * 8, maps, a.nb, kb, mt,
                            row0, pol_w, pol_v);
       at.next();
       base.next();
@@ -855,7 +886,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
       ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      load_ext<>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, sh->list, q_all, j,
+      load_ext<>(sbase + at.stage * stage_bytes, loaded0 + ext.stage * 8, maps, a, sh->list, q_all, j,
                  mt, row0, pol_w, pol_v, leader);
       at.next();
       ext.next();
@@ -870,7 +901,6 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       drain_loads(sh->loaded, stages, 0, ext.count);
     }
   } else if (warp == 1) {
-    const uint32_t sbase = smem_u32(smem);
     const uint32_t id_base = idesc_bf16(kM, a.nb, /*a_mn=*/!kKMajor, false);
     const uint32_t id_ext = idesc_bf16(kM, a.nb, /*a_mn=*/true, false);
     const bool leader = elect_lane();
@@ -882,7 +912,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       if (leader) {
         mma_base<kKMajor>(tmem, sbase + (uint32_t)(at.stage * stage_bytes), id_base,
                           kb > kb0 ? 1u : 0u);
-        mma_commit(&sh->empty[at.stage]);
+        commit(empty0 + at.stage * 8);
       }
       at.next();
       base.next();
@@ -895,7 +925,7 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
       tc_fence_after();
       if (leader) {
         mma_ext(tmem, sbase + (uint32_t)(at.stage * stage_bytes), id_ext, a.rb);
-        mma_commit(&sh->empty[at.stage]);
+        commit(empty0 + at.stage * 8);
       }
       at.next();
       ext.next();
@@ -1032,7 +1062,8 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   };
 
   const uint32_t full0 = smem_u32(sh->full), empty0 = smem_u32(sh->empty);
-  const uint32_t ready0 = smem_u32(sh->ready);
+  const uint32_t ready0 = smem_u32(sh->ready), loaded0 = smem_u32(sh->loaded);
+  const uint32_t sbase = smem_u32(smem);
 
   if (warp == 0) {
     const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
@@ -1050,7 +1081,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       for (int kb = 0; kb < nk; ++kb) {
         if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
         if (leader)
-          load_base<kKMajor, true>(smem + at.stage * stage_bytes, &sh->full[base.stage], maps, a.nb,
+          load_base<kKMajor, true>(sbase + at.stage * stage_bytes, full0 + base.stage * 8, maps, a.nb,
                                    kb, mt, row0, pol_w, pol_v, rank);
         at.next();
         base.next();
@@ -1069,7 +1100,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       for (int j = 0; j * kK < q_all; ++j) {
         ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        load_ext<true>(smem + at.stage * stage_bytes, &sh->loaded[ext.stage], maps, a, sh->list,
+        load_ext<true>(sbase + at.stage * stage_bytes, loaded0 + ext.stage * 8, maps, a, sh->list,
                        q_all, j, mt, row0, pol_w, pol_v, leader, rank);
         at.next();
         ext.next();
@@ -1086,7 +1117,6 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       drain_loads(sh->loaded, stages, 0, ext.count);
     }
   } else if (warp == 1) {
-    const uint32_t sbase = smem_u32(smem);
     const uint32_t id_base = idesc_bf16(kM, a.nb, /*a_mn=*/!kKMajor, false);
     const uint32_t id_ext = idesc_bf16(kM, a.nb, /*a_mn=*/true, false);
     const bool leader = elect_lane();
@@ -1106,7 +1136,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         tc_fence_after();
         if (leader) {
           mma_base<kKMajor>(d, sbase + (uint32_t)(at.stage * stage_bytes), id_base, kb ? 1u : 0u);
-          mma_commit_multicast(&sh->empty[at.stage], 0x3);
+          commit_multicast(empty0 + at.stage * 8, 0x3);
         }
         at.next();
         base.next();
@@ -1122,7 +1152,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         tc_fence_after();
         if (leader) {
           mma_ext(d, sbase + (uint32_t)(at.stage * stage_bytes), id_ext, a.rb);
-          mma_commit_multicast(&sh->empty[at.stage], 0x3);
+          commit_multicast(empty0 + at.stage * 8, 0x3);
         }
         at.next();
         ext.next();
@@ -1285,7 +1315,8 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
     const uint64_t pol = policy_evict_normal();
     const bool leader = elect_lane();
     fence_async_global();   // Z and dZ were written by ordinary stores
-    const uint32_t empty0 = smem_u32(sh->empty);
+    const uint32_t empty0 = smem_u32(sh->empty), full0 = smem_u32(sh->full);
+    const uint32_t sbase = smem_u32(smem);
     Place at(C::kStages);
     bool ok = true;
     for (int tb = 0; ok && tb < a.n_tt; tb += 32) {
@@ -1318,17 +1349,15 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
           ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (ok && leader) {
-            uint8_t* st = smem + at.stage * C::kStageBytes;
-            uint64_t* fb = &sh->full[at.stage];
+            const uint32_t st = sbase + at.stage * C::kStageBytes, fb = full0 + at.stage * 8;
             sh->mask[at.stage][0] = ml;
             sh->mask[at.stage][1] = mh;
             sh->rows[at.stage] = min(64, a.nb - g * kK);
-            mbar_arrive_expect_tx(fb, C::kStageBytes);
-            tma_load_3d(st, &maps.v[which], fb, 0, t0, d0 >> 6, pol);
+            expect_tx(fb, C::kStageBytes);
+            load_3d(st, &maps.v[which], fb, 0, t0, d0 >> 6, pol);
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
-              tma_load_2d(st + kABytes + c * 64 * kK * 2, &maps.z[which], fb, eb * a.R + 64 * c, t0,
-                          pol);
+              load_2d(st + kABytes + c * 64 * kK * 2, &maps.z[which], fb, eb * a.R + 64 * c, t0, pol);
           }
           if (ok) at.next();
         }
