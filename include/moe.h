@@ -409,6 +409,11 @@ moe_status moe_forward_gated(const void* x, const void* Wg,
  *   dB [n, R, N] bf16: dB[a] = sum of z[t]^T dy[t], z[t] = scale[a] * (x[t] A[a]^T)
  * with exact zeros for adapters without a token.  Sums run in a fixed order.
  *
+ * Requests do not see each other's infinities and NaN: a token or an adapter
+ * that holds one spoils its own results only.  Where the weights enter the
+ * product that a whole block of tokens shares -- B in y, A in dx -- such a
+ * weight counts as zero and sets MOE_ERR_NONFINITE in the device status.
+ *
  * ws: moe_adapter_workspace_size bytes (.._backward for the backward, which
  * covers both).  Limits: H and N positive multiples of 128, T < 2^30,
  * 1 <= n <= MOE_MAX_ADAPTERS, R a multiple of 8 up to MOE_MAX_RANK.

@@ -14,7 +14,7 @@
 // once, s + b, the sum of two group members): the picks are a function of the
 // inputs, not of a reduction order.  S is accumulated as an unevaluated pair
 // of floats (error-free additions), so it is the correctly rounded sum for any
-// order of the lanes.
+// order of the lanes, but for sums within 2^-15 ulp of a rounding boundary.
 #include <math.h>
 
 #include "route_token.cuh"
@@ -229,7 +229,8 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
   pdl_trigger();
   constexpr int n = V * kC;
   const int lane = threadIdx.x & (L - 1), seg = threadIdx.x / L;   // seg: the block's token
-  const int per_block = blockDim.x / L, stride = gridDim.x * per_block;
+  const int per_block = blockDim.x / L;
+  const uint32_t stride = gridDim.x * per_block;   // token numbers stay below 2^32
   const bool two = kGroups && c.group_top == 2;
   const bool scored = bias != nullptr;                  // all scores take part in the choice
   const bool need_s = scored || (two && c.softmax);     // the scores' exact sum decides
@@ -254,8 +255,8 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
     }
   }
   float next[kC][V];
-  auto fetch = [&](int t) {
-    const float* row = logits + (size_t)(t < T ? t : T - 1) * E + V * lane;
+  auto fetch = [&](uint32_t t) {
+    const float* row = logits + (size_t)(t < (uint32_t)T ? t : T - 1) * E + V * lane;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
 #pragma unroll
@@ -264,11 +265,11 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
     }
   };
   // the warp's tokens stay together: its first one decides
-  const int first = blockIdx.x * per_block + (seg & ~(32 / L - 1)), own = seg & (32 / L - 1);
-  if (kKeep && first < T) fetch(first + own);
-  for (int tw = first; tw < T; tw += stride) {
-    const bool live = tw + own < T;
-    const int t = live ? tw + own : T - 1;
+  const uint32_t first = blockIdx.x * per_block + (seg & ~(32 / L - 1)), own = seg & (32 / L - 1);
+  if (kKeep && first < (uint32_t)T) fetch(first + own);
+  for (uint32_t tw = first; tw < (uint32_t)T; tw += stride) {
+    const bool live = tw + own < (uint32_t)T;
+    const int t = live ? (int)(tw + own) : T - 1;
     const float* row = logits + (size_t)t * E;
     float v[kC][V];
     if (!kKeep) fetch(t);
@@ -276,7 +277,7 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
     for (int i = 0; i < kC; ++i)
 #pragma unroll
       for (int x = 0; x < V; ++x) v[i][x] = next[i][x];
-    if (kKeep && tw + stride < T) fetch(tw + stride + own);
+    if (kKeep && tw + stride < (uint32_t)T) fetch(tw + stride + own);
     // softmax: the row's maximum and the sum of exp(l - m), rounded once where
     // the scores decide
     float m = 0.f, S = 1.f;
@@ -454,8 +455,9 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
 //   softmax, renormalised:  dl_j = scale w_j (dw_j - sum_i w_i dw_i)
 //   softmax (kDense):       dl_e = s_e (scale dw_e - D), D = sum_j scale dw_j s_j
 // The first three are zero at every expert that was not chosen; they are bound
-// by writing dlogits.  kDense > 0: that many logits per lane are kept from the
-// first read to the last write.
+// by writing dlogits (8192 x 256: 6.1 us, 8.9 MB).  kDense > 0: that many logits
+// per lane are kept from the first read to the last write (40001 x 64: 12.5 us,
+// 24 MB; bound by the latency of one row's steps).
 template <int kDense>
 __global__ void __launch_bounds__(32 * kMaxWarps)
 route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __restrict__ topk_idx,
@@ -523,15 +525,18 @@ route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __rest
 struct Shape {
   int L, V;
 };
-// The slots and the groups need a lane each.  A few tokens are routed one per
-// warp, for the shortest chain of steps; from 2048 on (three warps per
-// scheduler) the instructions bound, and a warp shares them among as many tokens
-// as can be.  Chunks of four where neither a row nor a group splits one.
-constexpr int kManyTokens = 2048;
+// The slots and the groups need a lane each.  Up to 2048 tokens (three warps per
+// scheduler) are routed one per warp, for the shortest chain of steps; above, the
+// instructions bound, and a warp shares them among as many tokens as can be.
+// One per warp against several, with the launch's clearing of the status: 2048 x
+// 256 in 8 groups 8.2 / 10.3 us, 8192 x 256 16.4 / 14.3, 8192 x 160 13.5 / 9.3,
+// 40001 x 160 39.3 / 20.5, 40001 x 64 26.6 / 14.3.  Chunks of four where neither
+// a row nor a group splits one: 40001 x 160 34.6 us by single experts.
+constexpr int kFewTokens = 2048;
 Shape shape_of(int T, int E, int k, int n_group) {
   const int need = k > n_group ? k : n_group;
   const int V = E % 4 == 0 && E / n_group % 4 == 0 && E > 16 ? 4 : 1;
-  if (T >= kManyTokens || E <= 16) {
+  if (T > kFewTokens || E <= 16) {
     if (need <= 8 && E <= 160) return {8, V};
     if (need <= 16 && E <= 256) return {16, V};
   }

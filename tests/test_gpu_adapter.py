@@ -215,3 +215,52 @@ def test_binding_checks_types_and_shapes():
                           ("adapter_idx", good["adapter_idx"][:3], ValueError)):
         with pytest.raises(err):
             moe.moe_adapter_project(**{**good, key: bad})
+
+
+def test_output_given_and_default_workspace():
+    v = dev(make((70, 256, 128, 3, 16, "shuffled"))[0])
+    y = torch.empty(70, 128, dtype=torch.bfloat16, device="cuda")
+    assert moe.moe_adapter_project(**v, y=y) is y
+    assert torch.equal(y, moe.moe_adapter_project(**v, ws=moe.Workspace()))
+    with pytest.raises(ValueError):
+        moe.moe_adapter_project(**v, y=y[:69])
+    with pytest.raises(moe.MoeError):     # a rank that is no multiple of 8
+        moe.moe_adapter_project(v["x"], v["W"], v["A"][:, :12].contiguous(),
+                                v["B"][:, :12].contiguous(), v["scale"], v["adapter_idx"])
+
+
+@pytest.mark.parametrize("T,N", [(40, 256), (2600, 2048)])     # split tiles, persistent pairs
+def test_captured_in_a_graph(T, N):
+    d, dy = make((T, 256, N, 4, 16, "shuffled"))
+    v, dy = dev(d), dy.cuda()
+    ws = moe.Workspace()
+    moe.moe_adapter_project(**v, ws=ws)
+    moe.moe_adapter_project_backward(dy, **v, ws=ws)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        y = moe.moe_adapter_project(**v, ws=ws)
+        grads = moe.moe_adapter_project_backward(dy, **v, ws=ws)
+    other, _ = make((T, 256, N, 4, 16, "shuffled"), seed=9)
+    for k in ("x", "adapter_idx", "scale"):
+        v[k].copy_(other[k])
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, moe.moe_adapter_project(**v))
+    for a, b in zip(grads, moe.moe_adapter_project_backward(dy, **v)):
+        assert torch.equal(a, b)
+
+
+def test_operands_of_the_layers_own_calls_share_a_workspace():
+    """An adapter projection between two layer calls on one workspace changes
+    neither."""
+    from routing_grouped_expert_gb300 import inputs as I
+    d = I.make_inputs(I.small("tiny", T=64, H=256, F=128, E=8, k=2), "cuda")
+    args = (d["x"], d["logits"], d["W1"], d["W3"], d["W2"], 2)
+    ws = moe.Workspace()
+    want = moe.moe_forward(*args, ws=ws)
+    v = dev(make((64, 256, 128, 3, 16, "shuffled"))[0])
+    y = moe.moe_adapter_project(**v, ws=ws)
+    assert torch.equal(want, moe.moe_forward(*args, ws=ws))
+    assert moe.moe_get_device_status(ws) == 0
+    assert torch.equal(y, moe.moe_adapter_project(**v, ws=ws))

@@ -307,3 +307,75 @@ def test_layer_empty_batch_and_other_workspaces():
     assert torch.equal(plain, moe.moe_forward(d["x"], d["logits"], d["W1"], d["W3"], d["W2"], 2))
     empty = moe.moe_forward_scored(d["x"][:0], d["logits"][:0], d["W1"], d["W3"], d["W2"], 2, cfg)
     assert empty.shape == (0, 128)
+
+
+LARGE = [  # several tokens per warp, chunks of four and single experts
+    (2049, 256, 8, "sigmoid", True, 8, 4, 2, True, 2.5),
+    (3001, 160, 6, "softmax", False, 8, 3, 1, False, 16.0),
+    (2500, 100, 8, "sigmoid", True, 5, 2, 2, True, 1.0),
+    (5000, 64, 8, "softmax", True, 1, 1, 1, True, 1.0),
+    (2050, 24, 16, "softmax", True, 2, 2, 2, False, 1.0),
+    (2700, 250, 12, "sigmoid", False, 10, 7, 2, True, 1.0),
+    (4111, 12, 3, "sigmoid", True, 3, 2, 1, True, 1.0),
+    (2100, 16, 9, "softmax", False, 16, 9, 1, True, 1.0),
+    (2048, 384, 6, "softmax", True, 8, 3, 2, True, 1.0),
+    (20000, 32, 4, "sigmoid", True, 4, 2, 1, True, 1.0),
+]
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties"])
+@pytest.mark.parametrize("case", LARGE, ids=str)
+def test_route_large_batches(case, kind):
+    l, b, cfg = make(case, kind)
+    ws = moe.Workspace()
+    idx, w = moe.moe_route_scored(l.cuda(), case[2], cfg, bias=None if b is None else b.cuda(),
+                                  ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    check(case, l, b, cfg, idx, w)
+    # the first tokens of the batch, one per warp: the same bits
+    few = moe.moe_route_scored(l[:70].cuda(), case[2], cfg, bias=None if b is None else b.cuda())
+    assert torch.equal(few[0], idx[:70])
+    torch.testing.assert_close(few[1], w[:70], rtol=2.0 ** -20, atol=0)
+
+
+def test_outputs_given_and_refused():
+    l = torch.randn(40, 16, generator=torch.Generator().manual_seed(3)).cuda()
+    cfg = moe.RouteConfig("sigmoid")
+    idx, w = moe.moe_route_scored(l, 4, cfg)
+    i2 = torch.empty(40, 4, dtype=torch.int32, device="cuda")
+    w2 = torch.empty(40, 4, device="cuda")
+    got = moe.moe_route_scored(l, 4, cfg, topk_idx=i2, topk_w=w2)
+    assert got[0] is i2 and got[1] is w2 and torch.equal(i2, idx) and torch.equal(w2, w)
+    with pytest.raises(ValueError):
+        moe.moe_route_scored(l, 4, cfg, topk_idx=i2[:, :3])
+    with pytest.raises(TypeError):
+        moe.moe_route_scored(l, 4, cfg, bias=torch.zeros(16, dtype=torch.float64, device="cuda"))
+    with pytest.raises(TypeError):
+        moe.moe_route_scored(l.half(), 4, cfg)
+    with pytest.raises(ValueError):
+        moe.moe_route_scored(l.t(), 4, cfg)
+    with pytest.raises(ValueError):
+        moe.moe_route_scored_backward(w[:, :3].contiguous(), idx, l, cfg)
+    with pytest.raises(moe.MoeError):
+        moe.moe_route_scored(l, 17, cfg)
+
+
+def test_captured_in_a_graph():
+    """Route and gradient replayed from a CUDA graph on refilled inputs."""
+    cfg = moe.RouteConfig("sigmoid", 8, 4, 2, True, 2.5)
+    l = torch.zeros(300, 64, device="cuda")
+    dw = torch.randn(300, 6, generator=torch.Generator().manual_seed(4)).cuda()
+    ws = moe.Workspace()
+    moe.moe_route_scored(l, 6, cfg, ws=ws)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        idx, w = moe.moe_route_scored(l, 6, cfg, ws=ws)
+        d = moe.moe_route_scored_backward(dw, idx, l, cfg, ws=ws)
+    for seed in (1, 2):
+        l.copy_(torch.randn(300, 64, generator=torch.Generator().manual_seed(seed)))
+        g.replay()
+        torch.cuda.synchronize()
+        ref = moe.moe_route_scored(l, 6, cfg)
+        assert torch.equal(idx, ref[0]) and torch.equal(w, ref[1])
+        assert torch.equal(d, moe.moe_route_scored_backward(dw, idx, l, cfg))
