@@ -236,13 +236,9 @@ moe_status moe_route_scored(const float* logits, const float* bias, const moe_ro
   if (check_ws(ws, ws_bytes, 256) != MOE_OK) return MOE_ERR_WORKSPACE;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int* status = static_cast<int*>(ws);
-  // a few tokens are one block's work, which writes the status itself
-  const RouteCfg cfg = make_route_cfg(*config, E);
-  const bool whole = route_scored_whole(T, E, k, cfg);
-  if (!whole) MOE_TRY(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
-  return cuda_status(launch_route_scored(logits, bias, cfg, T, E, k, topk_idx, topk_w, nullptr,
-                                         status, s, whole));
+  return cuda_status(launch_route_scored(logits, bias, make_route_cfg(*config, E), T, E, k,
+                                         topk_idx, topk_w, nullptr, static_cast<int*>(ws), s,
+                                         /*clear=*/true));
 }
 
 moe_status moe_route_scored_backward(const float* dtopk_w, const int32_t* topk_idx,
@@ -257,11 +253,9 @@ moe_status moe_route_scored_backward(const float* dtopk_w, const int32_t* topk_i
   if (check_ws(ws, ws_bytes, 256) != MOE_OK) return MOE_ERR_WORKSPACE;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int* status = static_cast<int*>(ws);
-  MOE_TRY(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
   return cuda_status(launch_route_scored_backward(dtopk_w, topk_idx, logits, bias,
                                                   make_route_cfg(*config, E), T, E, k, dlogits,
-                                                  status, s));
+                                                  static_cast<int*>(ws), s, /*clear=*/true));
 }
 
 moe_status moe_permute(const int32_t* topk_idx, int T, int E, int k, int32_t* counts,

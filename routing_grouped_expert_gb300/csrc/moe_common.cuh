@@ -247,19 +247,17 @@ struct RouteCfg {
   uint32_t group_magic;    // expert e is in group e * group_magic >> 20
 };
 RouteCfg make_route_cfg(const moe_route_config& a, int E);
-// bias: [E] or null.  chunk_hist as for launch_route.  With `whole` (allowed when
-// route_scored_whole) the launch writes the status word itself, which then need
-// not be zero.
-bool route_scored_whole(int T, int E, int k, const RouteCfg& c);
+// bias: [E] or null.  chunk_hist as for launch_route.  With `clear` the launch
+// clears the status (its first 16 bytes) before anything is reported.
 cudaError_t launch_route_scored(const float* logits, const float* bias, const RouteCfg& c, int T,
                                 int E, int k, int32_t* topk_idx, float* topk_w,
                                 int32_t* chunk_hist, int* status, cudaStream_t s,
-                                bool whole = false);
+                                bool clear = false);
 // dlogits [T, E] of the weights' gradient dw [T, k].
 cudaError_t launch_route_scored_backward(const float* dw, const int32_t* topk_idx,
                                          const float* logits, const float* bias, const RouteCfg& c,
                                          int T, int E, int k, float* dlogits, int* status,
-                                         cudaStream_t s);
+                                         cudaStream_t s, bool clear = false);
 cudaError_t launch_count(const int32_t* topk_idx, int T, int E, int k, int32_t* chunk_hist,
                          int* status, cudaStream_t s);
 cudaError_t launch_scan(int32_t* chunk_hist, int C, int E, int32_t* counts, int32_t* offsets,

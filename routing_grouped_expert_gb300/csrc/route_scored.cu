@@ -17,12 +17,40 @@
 // order of the lanes, but for sums within 2^-15 ulp of a rounding boundary.
 #include <math.h>
 
+#include <atomic>
+#include <chrono>
+
+#include "ptx.cuh"
 #include "route_token.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kMaxWarps = 8;
+
+// The status word of a launch that clears it itself (a memset ahead of it costs 2
+// us on the host and as much on the device): block 0 clears the word and then
+// publishes the launch's own number beside it; a block that has something to
+// report, which is rare, first waits for that number.  Block 0 is among the first
+// to start and waits for nobody; the wait is bounded all the same.
+__device__ __forceinline__ void status_begin(int* status, uint64_t launch) {
+  if (launch != 0 && blockIdx.x == 0 && threadIdx.x == 0) {
+    status[0] = 0;
+    status[1] = 0;
+    __threadfence();
+    *reinterpret_cast<volatile uint64_t*>(status + 2) = launch;
+  }
+}
+__device__ __noinline__ void status_report(int* status, uint64_t launch, int code) {
+  if (launch != 0) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (*reinterpret_cast<volatile uint64_t*>(status + 2) != launch &&
+           ptx::globaltimer_ns() - t0 < 1000000000ull) {
+    }
+    __threadfence();
+  }
+  set_status(status, code);
+}
 
 // L lanes route one token, so a warp routes 32 / L.  Reductions over a token's
 // lanes:
@@ -222,11 +250,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kBlocks<V * kC>)
 route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, RouteCfg c,
                     int T, int E, int k, int tpc, int group_pad, int region,
                     int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
-                    int32_t* __restrict__ chunk_hist, int* __restrict__ status, bool whole) {
+                    int32_t* __restrict__ chunk_hist, int* __restrict__ status, uint64_t launch,
+                    bool whole) {
   // per token of the block `region` words: n_group * (group size + pad) keys, then
   // the kept groups
   extern __shared__ __align__(16) uint32_t stage[];
   pdl_trigger();
+  status_begin(status, launch);
   constexpr int n = V * kC;
   const int lane = threadIdx.x & (L - 1), seg = threadIdx.x / L;   // seg: the block's token
   const int per_block = blockDim.x / L;
@@ -445,7 +475,7 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
     const int any = __syncthreads_or(bad);
     if (threadIdx.x < 2) status[threadIdx.x] = threadIdx.x == 0 && any ? MOE_ERR_NONFINITE : 0;
   } else if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) {
-    set_status(status, MOE_ERR_NONFINITE);
+    status_report(status, launch, MOE_ERR_NONFINITE);
   }
 }
 
@@ -463,7 +493,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __restrict__ topk_idx,
                              const float* __restrict__ logits, const float* __restrict__ bias,
                              RouteCfg c, int T, int E, int k, float* __restrict__ dlogits,
-                             int* __restrict__ status) {
+                             int* __restrict__ status, uint64_t launch) {
+  status_begin(status, launch);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= T) return;
@@ -517,8 +548,10 @@ route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __rest
   }
   __syncwarp();   // the row's first values before the picks' own
   if (on) out[idx] = d;
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(status, MOE_ERR_NONFINITE);
-  if (__any_sync(0xffffffffu, lane < k && !in) && lane == 0) set_status(status, MOE_ERR_INVALID_ARG);
+  const bool nonfinite = __any_sync(0xffffffffu, bad);
+  const bool outside = __any_sync(0xffffffffu, lane < k && !in);
+  if ((nonfinite || outside) && lane == 0)
+    status_report(status, launch, outside ? MOE_ERR_INVALID_ARG : MOE_ERR_NONFINITE);
 }
 
 // How a batch is routed: lanes per token, and experts per chunk.
@@ -545,8 +578,8 @@ Shape shape_of(int T, int E, int k, int n_group) {
 
 template <int V, int kC, int L>
 cudaError_t launch_t(const float* logits, const float* bias, const RouteCfg& c, int T, int E, int k,
-                     int32_t* topk_idx, float* topk_w, int32_t* chunk_hist, int* status, bool whole,
-                     cudaStream_t s) {
+                     int32_t* topk_idx, float* topk_w, int32_t* chunk_hist, int* status,
+                     uint64_t launch, bool whole, cudaStream_t s) {
   const int tpc = tokens_per_chunk(k);
   constexpr int per_warp = 32 / L;
   int warps = kMaxWarps;
@@ -567,10 +600,11 @@ cudaError_t launch_t(const float* logits, const float* bias, const RouteCfg& c, 
     if (bytes * warps > 48 * 1024) warps /= 2;
     if (bytes * warps > 48 * 1024) warps /= 2;
     route_scored_kernel<V, kC, L, true><<<grid_of(), 32 * warps, bytes * warps, s>>>(
-        logits, bias, c, T, E, k, tpc, pad, region, topk_idx, topk_w, chunk_hist, status, whole);
+        logits, bias, c, T, E, k, tpc, pad, region, topk_idx, topk_w, chunk_hist, status, launch,
+        whole);
   } else {
     route_scored_kernel<V, kC, L, false><<<grid_of(), 32 * warps, 0, s>>>(
-        logits, bias, c, T, E, k, tpc, 0, 0, topk_idx, topk_w, chunk_hist, status, whole);
+        logits, bias, c, T, E, k, tpc, 0, 0, topk_idx, topk_w, chunk_hist, status, launch, whole);
   }
   return cudaGetLastError();
 }
@@ -593,20 +627,44 @@ RouteCfg make_route_cfg(const moe_route_config& a, int E) {
   return c;
 }
 
-// A quarter of a block's tokens at most (the block may have two warps): it
-// writes the status itself.
-bool route_scored_whole(int T, int E, int k, const RouteCfg& c) {
-  return T <= kMaxWarps / 4 * (32 / shape_of(T, E, k, c.n_group).L);
+namespace {
+// A number no launch before it had, in this process or (from the clock it starts
+// at) in what an earlier one left in memory.
+uint64_t next_launch() {
+  static std::atomic<uint64_t> n{
+      (uint64_t)std::chrono::system_clock::now().time_since_epoch().count() | 1};
+  return n.fetch_add(2, std::memory_order_relaxed);
 }
+// The launch's number, or 0 after a memset of the status: a captured launch runs
+// many times under one number.
+cudaError_t begin_status(int* status, cudaStream_t s, uint64_t* launch) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  const cudaError_t err = cudaStreamIsCapturing(s, &cs);
+  if (err != cudaSuccess) return err;
+  *launch = 0;
+  if (cs != cudaStreamCaptureStatusNone) return cudaMemsetAsync(status, 0, 2 * sizeof(int), s);
+  *launch = next_launch();
+  return cudaSuccess;
+}
+}  // namespace
 
 cudaError_t launch_route_scored(const float* logits, const float* bias, const RouteCfg& c, int T,
                                 int E, int k, int32_t* topk_idx, float* topk_w,
-                                int32_t* chunk_hist, int* status, cudaStream_t s, bool whole) {
+                                int32_t* chunk_hist, int* status, cudaStream_t s, bool clear) {
   if (T == 0) return cudaSuccess;
   const Shape f = shape_of(T, E, k, c.n_group);
+  // A quarter of a block's tokens at most (the block may have two warps) are one
+  // block's work, which writes the status itself at its end.
+  const bool whole = clear && T <= kMaxWarps / 4 * (32 / f.L);
+  uint64_t launch = 0;
+  if (clear && !whole) {
+    const cudaError_t err = begin_status(status, s, &launch);
+    if (err != cudaSuccess) return err;
+  }
 #define MOE_ROUTE_CASE(v, n, lanes)                      \
   if (f.V == v && f.L == lanes && E <= v * n * lanes)    \
-    return launch_t<v, n, lanes>(logits, bias, c, T, E, k, topk_idx, topk_w, chunk_hist, status, whole, s)
+    return launch_t<v, n, lanes>(logits, bias, c, T, E, k, topk_idx, topk_w, chunk_hist, status, launch, \
+                                 whole, s)
   MOE_ROUTE_CASE(1, 1, 8);
   MOE_ROUTE_CASE(1, 2, 8);
   MOE_ROUTE_CASE(1, 8, 8);
@@ -636,12 +694,17 @@ cudaError_t launch_route_scored(const float* logits, const float* bias, const Ro
 cudaError_t launch_route_scored_backward(const float* dw, const int32_t* topk_idx,
                                          const float* logits, const float* bias, const RouteCfg& c,
                                          int T, int E, int k, float* dlogits, int* status,
-                                         cudaStream_t s) {
+                                         cudaStream_t s, bool clear) {
   if (T == 0) return cudaSuccess;
+  uint64_t launch = 0;
+  if (clear) {
+    const cudaError_t err = begin_status(status, s, &launch);
+    if (err != cudaSuccess) return err;
+  }
   const int grid = (T + kMaxWarps - 1) / kMaxWarps;
 #define MOE_ROUTE_BWD(n)                                                                       \
   route_scored_backward_kernel<n><<<grid, 32 * kMaxWarps, 0, s>>>(dw, topk_idx, logits, bias, c, T, \
-                                                                  E, k, dlogits, status)
+                                                                  E, k, dlogits, status, launch)
   if (!c.softmax || c.renorm) MOE_ROUTE_BWD(0);
   else if (E <= 32) MOE_ROUTE_BWD(1);
   else if (E <= 64) MOE_ROUTE_BWD(2);

@@ -379,3 +379,28 @@ def test_captured_in_a_graph():
         ref = moe.moe_route_scored(l, 6, cfg)
         assert torch.equal(idx, ref[0]) and torch.equal(w, ref[1])
         assert torch.equal(d, moe.moe_route_scored_backward(dw, idx, l, cfg))
+
+
+@pytest.mark.parametrize("T", [1, 40, 3000])
+def test_status_of_a_reused_workspace(T):
+    """A report of the last token; the next call clears it, whatever the
+    workspace held before."""
+    cfg = moe.RouteConfig("sigmoid", 8, 4, 2, True, 2.5)
+    dense = moe.RouteConfig("softmax", renormalize=False)   # its gradient reads every logit
+    ws = moe.Workspace()
+    ws.ensure(256).fill_(0xff)
+    good = torch.randn(T, 64, generator=torch.Generator().manual_seed(6)).cuda()
+    bad = good.clone()
+    bad[T - 1, 63] = float("nan")
+    dw = torch.randn(T, 6, generator=torch.Generator().manual_seed(7)).cuda()
+    idx, _ = moe.moe_route_scored(good, 6, cfg, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    for _ in range(3):
+        moe.moe_route_scored(bad, 6, cfg, ws=ws)
+        assert moe.moe_get_device_status(ws) == 2
+        moe.moe_route_scored_backward(dw, idx, good, dense, ws=ws)
+        assert moe.moe_get_device_status(ws) == 0
+        moe.moe_route_scored_backward(dw, idx, bad, dense, ws=ws)
+        assert moe.moe_get_device_status(ws) == 2
+        moe.moe_route_scored(good, 6, cfg, ws=ws)
+        assert moe.moe_get_device_status(ws) == 0
