@@ -260,23 +260,26 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int from
 // by 16-byte asynchronous copies into the swizzled operand.  (TMA
 // tile::gather4 took about 16 ns a row: 777 tokens of 24 adapters of rank 64
 // spent 31 us on the gathers.)
+//
+// The gradient's two products, x A^T and dy B^T, are one launch: blockIdx.z says
+// which.  While both fit the SMs they run side by side, otherwise one after the other.
 struct ShrinkMaps {
-  CUtensorMap p;     // the adapters' rank rows [n, R, K], boxes of 64 K x rb rows
-  CUtensorMap v;     // token rows [T, K], boxes of 64 K x nb rows
+  CUtensorMap p[2];  // the adapters' rank rows [n, R, K], boxes of 64 K x rb rows
+  CUtensorMap v[2];  // token rows [T, K], boxes of 64 K x nb rows
 };
 struct ShrinkArgs {
-  int T, nb, K, n, R, rb, zc;   // nb: tokens per block; rb: rank rows per box, a power
-                                // of two that divides R
-  const __nv_bfloat16* rows;   // the token rows
+  int T, nb, n, R, rb, zc;   // nb: tokens per block; rb: rank rows per box, a power
+                             // of two that divides R
+  int K[2];
+  const __nv_bfloat16* rows[2];   // the token rows
   const char* next;         // the adapters' matrices [n][next_bytes] of the expand launch, or null
   long long next_bytes;
   const int32_t* adapter_idx;
   const float* scale;
-  __nv_bfloat16* z;         // [T, zc]
+  __nv_bfloat16* z[2];      // [T, zc]
   void* plan;
   uint32_t* masks;          // [n_tt][256][8]: the tokens of every entry, as bits; or null
   int* status;
-  bool first;               // the first kernel of the call: clears the status, writes the plan
 };
 constexpr int kGatherRows = 64;   // most tokens of a unit that gathers
 constexpr int kRowWarps = 2;      // warps 2 and 3 copy them
@@ -397,7 +400,7 @@ __device__ __forceinline__ void write_plan(ShrinkShared* sh, const ShrinkArgs& a
 // This CTA's tokens of a finished unit: Z rows of 128 columns, a warp per token.
 template <int kS>
 __device__ __forceinline__ void store_unit(const ShrinkShared* sh, const ShrinkArgs& a,
-                                           const uint8_t* smem, int row0, int rows, int u,
+                                           __nv_bfloat16* z, const uint8_t* smem, int row0, int rows, int u,
                                            int q_end, bool gather, int first, int r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this lane's four rank rows belong to one entry (R is a multiple of 8)
@@ -412,7 +415,7 @@ __device__ __forceinline__ void store_unit(const ShrinkShared* sh, const ShrinkA
       s = cluster_sum<kS>(mine + (uint32_t)j * (kM * 4), first);
       s = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
     }
-    *reinterpret_cast<uint2*>(a.z + (size_t)(row0 + t) * a.zc + u * kM + 4 * lane) = pack4(s);
+    *reinterpret_cast<uint2*>(z + (size_t)(row0 + t) * a.zc + u * kM + 4 * lane) = pack4(s);
   }
 }
 
@@ -428,17 +431,22 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   const int rank = kC > 1 ? (int)cluster_ctarank() : 0;
   const int tt = (int)blockIdx.x / kC;
   const int row0 = tt * a.nb, rows = min(a.nb, a.T - row0);
-  const int nk = a.K / kK;
+  const int job = (int)blockIdx.z;   // 0 or 1; no indexing of the parameters with it
+  const int K = job ? a.K[1] : a.K[0], nk = K / kK;
+  const CUtensorMap* map_p = job ? &maps.p[1] : &maps.p[0];
+  const CUtensorMap* map_v = job ? &maps.v[1] : &maps.v[0];
+  __nv_bfloat16* z = job ? a.z[1] : a.z[0];
 
   pdl_trigger();
   // the call's status starts clean: this is its first kernel, and nothing is
   // reported before a later kernel of the call or a wait of a second
-  if (a.first && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
+  if (job == 0 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
   build_list<C::kGather>(sh, a, row0, rows);
-  if (a.first && rank == 0 && blockIdx.y == 0) write_plan(sh, a, tt, rows, reinterpret_cast<uint32_t*>(smem));
+  if (job == 0 && rank == 0 && blockIdx.y == 0)
+    write_plan(sh, a, tt, rows, reinterpret_cast<uint32_t*>(smem));
   const int q_all = sh->n_ent * a.R;
   const int units = (q_all + kM - 1) / kM;
-  if (a.next != nullptr && warp == 3) {
+  if (a.next != nullptr && warp == 3 && blockIdx.z + 1 == gridDim.z) {
     // the expand launch's adapter rows start on their way into L2
     const int parts = (int)gridDim.y * kC;
     const long long step = 16384, per = (a.next_bytes + step - 1) / step;
@@ -455,12 +463,7 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
   while (s > 1 && units * s > (int)gridDim.y * kC) s >>= 1;
   const int groups = kC / s, sub = rank / s, r = rank - sub * s;
   const int u_step = (int)gridDim.y * groups, u_first = (int)blockIdx.y * groups;
-  // A second shrink of a call starts while the first one runs (neither reads
-  // what the other writes) but does not end before it.
-  if (u_first >= units) {   // the same for the whole cluster
-    pdl_wait();
-    return;
-  }
+  if (u_first >= units) return;   // the same for the whole cluster
   const int kb0 = nk * r / s, kb1 = nk * (r + 1) / s;
   bool gather = false;
   if constexpr (C::kGather) {
@@ -552,12 +555,12 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
         const uint32_t fb = full0 + at.stage * 8, st = sbase + at.stage * stage_bytes;
         if (loader == 0 && leader) {
           expect_tx(fb, bytes);
-          if (!gather) load_2d(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
+          if (!gather) load_2d(st + kABytes, map_v, fb, kb * kK, row0, pol_v);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (box[i] && leader)
-            load_3d(st + (loader + 4 * i) * a.rb * (kK * 2), &maps.p, fb, kb * kK, row[i], ad[i],
+            load_3d(st + (loader + 4 * i) * a.rb * (kK * 2), map_p, fb, kb * kK, row[i], ad[i],
                     pol_p);
         at.next();
       }
@@ -614,7 +617,8 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
         const int piece = (int)threadIdx.x - 64 + i * (32 * kRowWarps), j = piece >> 3, c = piece & 7;
         dst[i] = piece < n_piece ? (uint32_t)(kABytes + j * 128 + ((c ^ (j & 7)) << 4)) : 0u;
         // rows up to a multiple of 16 repeat the last token
-        src[i] = a.rows + (size_t)(row0 + (int)sh->tok[min(j, n_tok - 1)]) * a.K + c * 8;
+        src[i] = (job ? a.rows[1] : a.rows[0]) + (size_t)(row0 + (int)sh->tok[min(j, n_tok - 1)]) * K +
+                 c * 8;
       }
       const uint32_t sbase = smem_u32(smem);
       // every thread arrives when its copies land (64 arrivals a stage; 160, of
@@ -648,13 +652,15 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
     if (have && !*abort_flag) {
       const int first = sub * s;
       if (kC == 1 || s == 1)
-        store_unit<1>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
+        store_unit<1>(sh, a, z, smem, row0, rows, u, q_end, gather, first, r);
       else if (kC == 2 || s == 2)
-        store_unit<2>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
+        store_unit<2>(sh, a, z, smem, row0, rows, u, q_end, gather, first, r);
+      else if (kC == 3)
+        store_unit<3>(sh, a, z, smem, row0, rows, u, q_end, gather, first, r);
       else if (kC == 4 || s == 4)
-        store_unit<4>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
+        store_unit<4>(sh, a, z, smem, row0, rows, u, q_end, gather, first, r);
       else
-        store_unit<8>(sh, a, smem, row0, rows, u, q_end, gather, first, r);
+        store_unit<8>(sh, a, z, smem, row0, rows, u, q_end, gather, first, r);
     }
     // no CTA loads the next unit (by TMA, over a tile that ordinary stores
     // wrote), or leaves, while another reads its tile; after a wait that ran out
@@ -665,7 +671,6 @@ adapter_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const ShrinkArgs 
     tc_fence_after();
     if (have) parity ^= 1u;
   }
-  pdl_wait();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
@@ -1241,7 +1246,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
 // group that holds one of adapter a, ascending.  Both gradients in one launch:
 // dA from (x, dZ), then dB from (dy, Z).  Bound by reading x and dy once more.
 // It may start while the expand launch before it still runs: expand lets it go
-// once it has itself seen both shrinks complete, so everything read here (past
+// once it has itself seen the shrink launch complete, so everything read here (past
 // the L1 cache) is complete, and nothing that expand writes is read; but it does
 // not end before expand.
 struct WgradMaps {
@@ -1592,37 +1597,62 @@ cudaError_t launch_cluster(dim3 grid, int cluster, int smem, bool pdl, cudaStrea
 }
 
 template <int kNB>
-cudaError_t launch_shrink_nb(int cluster, int gy, const ShrinkMaps& m, const ShrinkArgs& a,
-                             int n_tt, cudaStream_t s) {
-  const dim3 grid(n_tt * cluster, gy);
+cudaError_t launch_shrink_nb(int cluster, int gy, int jobs, const ShrinkMaps& m,
+                             const ShrinkArgs& a, int n_tt, cudaStream_t s) {
+  const dim3 grid(n_tt * cluster, gy, jobs);
   constexpr int smem = ShrinkCfg<kNB>::kSmemBytes;
   switch (cluster) {
-    case 1: return launch_cluster<adapter_shrink_kernel<kNB, 1>>(grid, 1, smem, !a.first, s, m, a);
-    case 2: return launch_cluster<adapter_shrink_kernel<kNB, 2>>(grid, 2, smem, !a.first, s, m, a);
-    case 4: return launch_cluster<adapter_shrink_kernel<kNB, 4>>(grid, 4, smem, !a.first, s, m, a);
-    default: return launch_cluster<adapter_shrink_kernel<kNB, 8>>(grid, 8, smem, !a.first, s, m, a);
+    case 1: return launch_cluster<adapter_shrink_kernel<kNB, 1>>(grid, 1, smem, false, s, m, a);
+    case 2: return launch_cluster<adapter_shrink_kernel<kNB, 2>>(grid, 2, smem, false, s, m, a);
+    case 3: return launch_cluster<adapter_shrink_kernel<kNB, 3>>(grid, 3, smem, false, s, m, a);
+    case 4: return launch_cluster<adapter_shrink_kernel<kNB, 4>>(grid, 4, smem, false, s, m, a);
+    default: return launch_cluster<adapter_shrink_kernel<kNB, 8>>(grid, 8, smem, false, s, m, a);
   }
 }
 
-// Z of the rows v [T, D] and the adapters' matrices P [n, R, D].  `first`: the
-// first launch of a call; `ctas`: the expand launch that follows has so many;
-// `next` [n, R, next_cols]: the adapters' matrices that it reads.
-cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* P,
-                          int D, const float* scale, const int32_t* adapter_idx, void* plan,
-                          uint32_t* masks, __nv_bfloat16* Z, int* status, bool first,
-                          long long ctas, const __nv_bfloat16* next, int next_cols,
+// One product: Z [T, zc] of the rows v [T, K] and the adapters' matrices P [n, R, K].
+struct ShrinkJob {
+  const __nv_bfloat16 *v, *P;
+  int K;
+  __nv_bfloat16* z;
+};
+// One or two of them, the first launch of a call.  `next` [n, R, next_cols]: the
+// adapters' matrices that the expand launch reads; `v_map`: the map of the last
+// job's rows, which is the expand launch's too if its boxes are equal.
+cudaError_t launch_shrink(const AdapterSizes& z, int jobs, const ShrinkJob* job, const float* scale,
+                          const int32_t* adapter_idx, void* plan, uint32_t* masks, int* status,
+                          const __nv_bfloat16* next, int next_cols, CUtensorMap* v_map,
                           cudaStream_t s) {
   ShrinkMaps m;
+  ShrinkArgs a{};
   const int rb = rank_box(z.R);
-  if (!map_rank_rows(&m.p, P, z.n, z.R, D, rb) || !map_rows(&m.v, v, z.T, D, z.nb))
-    return cudaErrorInvalidValue;
+  int least = job[0].K;
+  for (int i = 0; i < jobs; ++i) {
+    if (!map_rank_rows(&m.p[i], job[i].P, z.n, z.R, job[i].K, rb) ||
+        !map_rows(&m.v[i], job[i].v, z.T, job[i].K, z.nb))
+      return cudaErrorInvalidValue;
+    a.K[i] = job[i].K;
+    a.rows[i] = job[i].v;
+    a.z[i] = job[i].z;
+    if (job[i].K < least) least = job[i].K;
+  }
+  *v_map = m.v[jobs - 1];
   // few blocks: the expand's tiles meet their adapters' rows cold, after the
   // projection's weights; with many blocks most of those reads hit L2 anyway
-  const bool ahead = next != nullptr && z.n_tt <= 4;
-  const ShrinkArgs a{z.T, z.nb, D, z.n, z.R, rb, z.zc, v,
-                     ahead ? reinterpret_cast<const char*>(next) : nullptr,
-                     (long long)z.R * next_cols * 2, adapter_idx, scale, Z, plan, masks, status,
-                     first};
+  const bool ahead = z.n_tt <= 4;
+  a.T = z.T;
+  a.nb = z.nb;
+  a.n = z.n;
+  a.R = z.R;
+  a.rb = rb;
+  a.zc = z.zc;
+  a.next = ahead ? reinterpret_cast<const char*>(next) : nullptr;
+  a.next_bytes = (long long)z.R * next_cols * 2;
+  a.adapter_idx = adapter_idx;
+  a.scale = scale;
+  a.plan = plan;
+  a.masks = masks;
+  a.status = status;
   // as many clusters per block as the SMs take in one round and the block can
   // have units for; the CTAs share them out once they know its adapters
   int sms = device_sm_count();
@@ -1630,21 +1660,30 @@ cudaError_t launch_shrink(const AdapterSizes& z, const __nv_bfloat16* v, const _
   // shrink keeps to the SMs that are left, since the expand's weights stream
   // meanwhile and a tile that waited for shrink's SMs came out last (8 of 128
   // tiles, 18 us late).
-  if (z.n_tt == 1 && ctas < sms && sms - ctas >= 8) sms -= (int)ctas;
+  if (z.n_tt == 1 && z.ctas < sms && sms - z.ctas >= 8) sms -= (int)z.ctas;
   // clusters of eight do not tile the GPU's processing clusters: more than
   // three quarters of the SMs' worth of them run in two rounds (16 blocks of
   // 4096 tokens: 30 us against 18)
   int cluster = 8;
   while (cluster > 1 && (z.n_tt * cluster > (cluster == 8 ? sms * 3 / 4 : sms) ||
-                         D / kK / cluster < 4))
+                         least / kK / cluster < 4))
     cluster /= 2;
+  // s of the kernel for as many units as a block can have
+  auto share = [&](int c) {
+    const int per = sms / (jobs * z.n_tt * c) * c;
+    int n = c;
+    while (n > 1 && z.zc / kM * n > per) n >>= 1;
+    return n;
+  };
+  // three CTAs per unit where a power of two leaves a third of the SMs idle
+  if (cluster > 3 && share(cluster) == 2 && share(3) == 3) cluster = 3;
   const int most = (z.zc / kM * 8 + cluster - 1) / cluster;   // up to eight CTAs per unit
-  int gy = sms / (z.n_tt * cluster);
+  int gy = sms / (jobs * z.n_tt * cluster);
   gy = gy < 1 ? 1 : gy > most ? most : gy;
-  if (z.nb <= 32) return launch_shrink_nb<32>(cluster, gy, m, a, z.n_tt, s);
-  if (z.nb <= 64) return launch_shrink_nb<64>(cluster, gy, m, a, z.n_tt, s);
-  if (z.nb <= 128) return launch_shrink_nb<128>(cluster, gy, m, a, z.n_tt, s);
-  return launch_shrink_nb<256>(cluster, gy, m, a, z.n_tt, s);
+  if (z.nb <= 32) return launch_shrink_nb<32>(cluster, gy, jobs, m, a, z.n_tt, s);
+  if (z.nb <= 64) return launch_shrink_nb<64>(cluster, gy, jobs, m, a, z.n_tt, s);
+  if (z.nb <= 128) return launch_shrink_nb<128>(cluster, gy, jobs, m, a, z.n_tt, s);
+  return launch_shrink_nb<256>(cluster, gy, jobs, m, a, z.n_tt, s);
 }
 
 template <int kNB, bool kKMajor>
@@ -1679,7 +1718,8 @@ cudaError_t launch_expand_t(int split, const ExpandMaps& m, const ExpandArgs& a,
 }
 
 // out [T, M] = v [T, K] W + Z P, with P [n, R, M]; W [K, M] or (k_major) [M, K].
-cudaError_t launch_expand(const AdapterSizes& z, const __nv_bfloat16* v, const __nv_bfloat16* W,
+cudaError_t launch_expand(const AdapterSizes& z, const CUtensorMap& v_map,
+                          const __nv_bfloat16* v, const __nv_bfloat16* W,
                           bool k_major, const __nv_bfloat16* Z, const __nv_bfloat16* P, int K,
                           int M, const void* plan, __nv_bfloat16* out, int* status,
                           cudaStream_t s) {
@@ -1687,9 +1727,10 @@ cudaError_t launch_expand(const AdapterSizes& z, const __nv_bfloat16* v, const _
   const int rb = rank_box(z.R);
   const int box = z.split == 0 ? z.nb / 2 : z.nb;
   if (!(k_major ? map_rows(&m.w, W, M, K, kM) : map_atoms(&m.w, W, K, M)) ||
-      !map_rows(&m.v, v, z.T, K, box) || !map_rank_atoms(&m.p, P, z.n, z.R, M, rb) ||
+      (box != z.nb && !map_rows(&m.v, v, z.T, K, box)) || !map_rank_atoms(&m.p, P, z.n, z.R, M, rb) ||
       !map_rows(&m.z, Z, z.T, z.zc, box))
     return cudaErrorInvalidValue;
+  if (box == z.nb) m.v = v_map;
   const ExpandArgs a{z.T, z.nb, K, M, z.n, z.R, rb, z.n_tt, out, plan, status};
   return k_major ? launch_expand_t<true>(z.split, m, a, s)
                  : launch_expand_t<false>(z.split, m, a, s);
@@ -1736,10 +1777,12 @@ cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x
   int* status = static_cast<int*>(ws);
   void* plan = ws_ptr<void>(ws, z.plan);
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, nullptr, Z, status,
-                                  true, z.ctas, B, z.N, s);
+  const ShrinkJob job{x, A, z.H, Z};
+  CUtensorMap v_map;
+  const cudaError_t err =
+      launch_shrink(z, 1, &job, scale, adapter_idx, plan, nullptr, status, B, z.N, &v_map, s);
   if (err != cudaSuccess) return err;
-  return launch_expand(z, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
+  return launch_expand(z, v_map, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
 }
 
 cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* dy,
@@ -1753,13 +1796,12 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   __nv_bfloat16* Z = ws_ptr<__nv_bfloat16>(ws, z.z);
   __nv_bfloat16* dZ = ws_ptr<__nv_bfloat16>(ws, z.dz);
   uint32_t* masks = ws_ptr<uint32_t>(ws, z.masks);
-  const int sms = device_sm_count();
-  cudaError_t err = launch_shrink(z, x, A, z.H, scale, adapter_idx, plan, masks, Z, status,
-                                  true, sms, nullptr, 0, s);
+  const ShrinkJob job[2] = {{x, A, z.H, Z}, {dy, B, z.N, dZ}};
+  CUtensorMap v_map;
+  cudaError_t err =
+      launch_shrink(z, 2, job, scale, adapter_idx, plan, masks, status, A, z.H, &v_map, s);
   if (err == cudaSuccess)
-    err = launch_shrink(z, dy, B, z.N, scale, adapter_idx, plan, nullptr, dZ, status, false,
-                        z.ctas, A, z.H, s);
-  if (err == cudaSuccess) err = launch_expand(z, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
+    err = launch_expand(z, v_map, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
   if (err != cudaSuccess) return err;
   WgradMaps m;
   if (!map_atoms(&m.v[0], x, z.T, z.H) || !map_rows(&m.z[0], dZ, z.T, z.zc, 64) ||

@@ -43,6 +43,7 @@ CASES = [  # T, H, N, n, R, order
     (2049, 512, 2432, 8, 16, "shuffled"),      # an odd number of feature tiles in pairs
     (1025, 256, 5120, 9, 8, "segments"),       # blocks that are no multiple of 64 tokens
     (140, 512, 128, 20, 32, "distinct"),
+    (777, 1024, 128, 24, 64, "shuffled"),      # three CTAs per unit of rank rows
 ]
 
 
