@@ -1242,8 +1242,10 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
 
 // ------------------------------------------------------- weight gradients
 // G[a][r][d] = sum over the tokens t of adapter a of Z[t, entry(a) R + r] V[t, d]:
-// one CTA per (adapter, 128 columns of V), K = the tokens of every 64-token
-// group that holds one of adapter a, ascending.  Both gradients in one launch:
+// one cluster of kS CTAs per (adapter, 128 columns of V), K = the tokens of every
+// 64-token group that holds one of adapter a, ascending, the groups dealt to the
+// CTAs in turn; their tiles meet in shared memory and are added in rank order.
+// Both gradients in one launch:
 // dA from (x, dZ), then dB from (dy, Z).  Bound by reading x and dy once more.
 // It may start while the expand launch before it still runs: expand lets it go
 // once it has itself seen the shrink launch complete, so everything read here (past
@@ -1270,6 +1272,8 @@ struct WgradCfg {
   static constexpr int kSmemBytes = kRing + 1024 + 1024;
   static constexpr int kTmemCols = 64 * kCols;
 };
+static_assert(WgradCfg<1>::kRing >= 64 * kM * 4 && WgradCfg<2>::kRing >= 128 * kM * 4,
+              "a CTA's fp32 tile is staged in the ring");
 struct WgradShared {
   uint64_t full[4], empty[4], ready[4];
   uint64_t acc_full, drain;
@@ -1280,7 +1284,7 @@ struct WgradShared {
   volatile int rows[4];           // rows of the stage that belong to its block
 };
 
-template <int kCols>
+template <int kCols, int kS>
 __global__ void __launch_bounds__(kThreads, 1)
 adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) {
   using C = WgradCfg<kCols>;
@@ -1290,8 +1294,9 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   WgradShared* sh = reinterpret_cast<WgradShared*>(smem + C::kRing);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int units0 = a.n * (a.D[0] / kM);
-  const int which = (int)blockIdx.x < units0 ? 0 : 1;
-  const int unit = (int)blockIdx.x - (which ? units0 : 0);
+  const int rank = kS > 1 ? (int)cluster_ctarank() : 0;
+  const int which = (int)blockIdx.x / kS < units0 ? 0 : 1;
+  const int unit = (int)blockIdx.x / kS - (which ? units0 : 0);
   const int D = a.D[which], n_dt = D / kM;
   const int ad = unit / n_dt, d0 = (unit - ad * n_dt) * kM;
   const int N = (a.R + 15) & ~15;
@@ -1324,6 +1329,7 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
     const uint32_t sbase = smem_u32(smem);
     Place at(C::kStages);
     bool ok = true;
+    int group = 0;   // of the adapter's
     for (int tb = 0; ok && tb < a.n_tt; tb += 32) {
       // lane: block tb + lane, ad's entry in it and its tokens there
       int e = 0;
@@ -1350,6 +1356,7 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
           const uint32_t ml = __shfl_sync(0xffffffffu, lo[g], src);
           const uint32_t mh = __shfl_sync(0xffffffffu, hi[g], src);
           if (!ok || (ml | mh) == 0u) continue;   // no token of ad in this group
+          if (kS > 1 && (group++ & (kS - 1)) != rank) continue;
           const int t0 = (tb + src) * a.nb + g * kK;
           ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
@@ -1451,24 +1458,43 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
       if (lane == 0) mbar_arrive(&sh->ready[at.stage]);
       at.next();
     }
-  } else {
+  } else {   // warps 3 to 6, TMEM lanes 32 (warp % 4) ..
     const bool got = mbar_wait(&sh->acc_full, 0, abort_flag, kWaitLimitNs);
     if (__all_sync(0xffffffffu, got) && !*abort_flag) {
       tc_fence_after();
       const bool none = sh->stages == 0;   // no token: a zero gradient
       const int q = warp & 3;
       __nv_bfloat16* o = a.out[which] + (size_t)ad * a.R * D + d0 + q * 32 + lane;
+      float* st = reinterpret_cast<float*>(smem) + q * 32 + lane;   // the ring: every load was read
       for (int c0 = 0; c0 < a.R; c0 += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c0 + c < a.R)
-            o[(size_t)(c0 + c) * D] = __float2bfloat16_rn(none ? 0.f : __uint_as_float(v[c]));
+        for (int c = 0; c < 16; ++c) {
+          const float f = none ? 0.f : __uint_as_float(v[c]);
+          if constexpr (kS > 1) {
+            if (c0 + c < a.R) st[(c0 + c) * kM] = f;
+          } else {
+            if (c0 + c < a.R) o[(size_t)(c0 + c) * D] = __float2bfloat16_rn(f);
+          }
+        }
       }
     }
     tc_fence_before();
+  }
+  if constexpr (kS > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (!*abort_flag) {
+      const uint32_t tile = smem_u32(smem);
+      __nv_bfloat16* o = a.out[which] + (size_t)ad * a.R * D + d0;
+      for (int i = rank * kThreads + (int)threadIdx.x; i < a.R * (kM / 4); i += kS * kThreads)
+        *reinterpret_cast<uint2*>(o + (size_t)(i >> 5) * D + (i & 31) * 4) =
+            pack4(cluster_sum<kS>(tile + (uint32_t)i * 16));
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while another reads its tile
   }
   __syncwarp();
   __syncthreads();
@@ -1736,6 +1762,29 @@ cudaError_t launch_expand(const AdapterSizes& z, const CUtensorMap& v_map,
                  : launch_expand_t<false>(z.split, m, a, s);
 }
 
+template <int kCols>
+cudaError_t launch_wgrad(const AdapterSizes& z, const WgradMaps& m, const WgradArgs& a,
+                         cudaStream_t s) {
+  // Few units (one adapter trained alone: 72 of them with H 7168, N 2048) are
+  // split until there are about two CTAs per SM, with 8 stages or more each.
+  // 8192 tokens, one adapter, the whole gradient call: 221 us unsplit, 200, 194
+  // and 203 us with 2, 4 and 8; two adapters 199, 193, 198 and 209 us; at eight
+  // a split only adds (195 us, 203 with 2).  1000 tokens x 2048 x 1024, one adapter:
+  // 22.6, 22.0, 26.7 and 27.9 us.
+  const int units = z.n * ((z.H + z.N) / kM);
+  const int groups = (z.T + kK - 1) / kK / z.n;   // of an adapter, on average
+  int split = 1;
+  while (split < 8 && units * split <= device_sm_count() && groups / split >= 16) split *= 2;
+  const dim3 grid((unsigned)(units * split));
+  constexpr int smem = WgradCfg<kCols>::kSmemBytes;
+  switch (split) {
+    case 1: return launch_cluster<adapter_wgrad_kernel<kCols, 1>>(grid, 1, smem, true, s, m, a);
+    case 2: return launch_cluster<adapter_wgrad_kernel<kCols, 2>>(grid, 2, smem, true, s, m, a);
+    case 4: return launch_cluster<adapter_wgrad_kernel<kCols, 4>>(grid, 4, smem, true, s, m, a);
+    default: return launch_cluster<adapter_wgrad_kernel<kCols, 8>>(grid, 8, smem, true, s, m, a);
+  }
+}
+
 }  // namespace
 
 AdapterSizes adapter_sizes(int T, int H, int N, int n, int R, bool backward) {
@@ -1808,10 +1857,7 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
       !map_atoms(&m.v[1], dy, z.T, z.N) || !map_rows(&m.z[1], Z, z.T, z.zc, 64))
     return cudaErrorInvalidValue;
   const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, plan, masks, {dA, dB}, status};
-  const dim3 grid((unsigned)(z.n * ((z.H + z.N) / kM)));
-  if (z.R > 64)
-    return launch_cluster<adapter_wgrad_kernel<2>>(grid, 1, WgradCfg<2>::kSmemBytes, true, s, m, a);
-  return launch_cluster<adapter_wgrad_kernel<1>>(grid, 1, WgradCfg<1>::kSmemBytes, true, s, m, a);
+  return z.R > 64 ? launch_wgrad<2>(z, m, a, s) : launch_wgrad<1>(z, m, a, s);
 }
 
 }  // namespace moe

@@ -44,6 +44,10 @@ CASES = [  # T, H, N, n, R, order
     (1025, 256, 5120, 9, 8, "segments"),       # blocks that are no multiple of 64 tokens
     (140, 512, 128, 20, 32, "distinct"),
     (777, 1024, 128, 24, 64, "shuffled"),      # three CTAs per unit of rank rows
+    (1000, 128, 256, 1, 8, "one"),             # the tokens of a gradient split by 2, 4 and 8
+    (2100, 256, 128, 1, 40, "one"),
+    (4100, 128, 128, 1, 128, "shuffled"),
+    (2100, 128, 128, 2, 72, "none"),
 ]
 
 
