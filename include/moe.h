@@ -53,7 +53,8 @@ extern "C" {
 typedef enum {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = 1,  /* bad size, null or misaligned pointer       */
-  MOE_ERR_NONFINITE = 2,    /* a router logit is NaN or +-inf (device)    */
+  MOE_ERR_NONFINITE = 2,    /* a router logit is NaN or +-inf, a balance bias NaN
+                             or +inf, or an adapter weight either (device) */
   MOE_ERR_TIMEOUT = 3,      /* a bounded device wait ran out (device)     */
   MOE_ERR_WORKSPACE = 4,    /* ws is NULL, too small or misaligned        */
   MOE_ERR_CUDA = 5,         /* a CUDA runtime call or launch failed       */

@@ -859,7 +859,7 @@ const char* moe_status_string(moe_status st) {
   switch (st) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID_ARG: return "invalid argument (size, null or misaligned pointer, expert index)";
-    case MOE_ERR_NONFINITE: return "a router logit is NaN or infinite";
+    case MOE_ERR_NONFINITE: return "a router logit, balance bias or adapter weight is NaN or infinite";
     case MOE_ERR_TIMEOUT: return "a bounded device wait ran out";
     case MOE_ERR_WORKSPACE: return "workspace is null, misaligned or too small";
     case MOE_ERR_CUDA: return "a CUDA runtime call or kernel launch failed";

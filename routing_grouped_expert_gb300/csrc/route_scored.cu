@@ -238,8 +238,9 @@ __device__ __forceinline__ void load_chunk(Tp (&x)[V], const Tp* p, bool global)
 
 // One token per L lanes; lane l holds kC chunks of V experts, chunk q = l + L i
 // being experts V q .. V q + V - 1.  The warps go through the tokens in strides.
-// Bound by instruction issue, not memory (8192 tokens of 256 experts read 8.4
-// MB, 1.3 us; 40001 of 160 25.6 MB, 3.8 us): so experts go in chunks of four
+// Bound by instruction issue, not memory (8192 tokens of 256 experts in 8 groups
+// read 8.4 MB, 1.3 us, in 12.3 us; 40001 of 160 25.6 MB, 3.8 us, in 18.5 us, 1.5
+// TB/s; one token of 256: 3.9 us, its chain of steps): so experts go in chunks of four
 // wherever E and the groups allow it (one load, one check and one group index
 // for four), everything but the scores is done on integer keys, a token's
 // candidates are compacted to the kept groups before the selection, and in a
@@ -485,9 +486,10 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
 //   softmax, renormalised:  dl_j = scale w_j (dw_j - sum_i w_i dw_i)
 //   softmax (kDense):       dl_e = s_e (scale dw_e - D), D = sum_j scale dw_j s_j
 // The first three are zero at every expert that was not chosen; they are bound
-// by writing dlogits (8192 x 256: 6.1 us, 8.9 MB).  kDense > 0: that many logits
-// per lane are kept from the first read to the last write (40001 x 64: 12.5 us,
-// 24 MB; bound by the latency of one row's steps).
+// by writing dlogits (8192 x 256: 6.1 us, 9.2 MB, 1.5 TB/s into L2).  kDense > 0: that
+// many logits per lane are kept from the first read to the last write (40001 x 64:
+// 11.0 us, 22.4 MB; bound by the latency of one row's steps).  With one slot the
+// renormalised weight is the constant `scale`: its gradient comes out exactly zero.
 template <int kDense>
 __global__ void __launch_bounds__(32 * kMaxWarps)
 route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __restrict__ topk_idx,
@@ -561,7 +563,7 @@ struct Shape {
 // The slots and the groups need a lane each.  Up to 2048 tokens (three warps per
 // scheduler) are routed one per warp, for the shortest chain of steps; above, the
 // instructions bound, and a warp shares them among as many tokens as can be.
-// One per warp against several, with the launch's clearing of the status: 2048 x
+// One per warp against several, with 2 us of a memset ahead of each: 2048 x
 // 256 in 8 groups 8.2 / 10.3 us, 8192 x 256 16.4 / 14.3, 8192 x 160 13.5 / 9.3,
 // 40001 x 160 39.3 / 20.5, 40001 x 64 26.6 / 14.3.  Chunks of four where neither
 // a row nor a group splits one: 40001 x 160 34.6 us by single experts.

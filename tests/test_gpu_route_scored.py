@@ -404,3 +404,14 @@ def test_status_of_a_reused_workspace(T):
         assert moe.moe_get_device_status(ws) == 2
         moe.moe_route_scored(good, 6, cfg, ws=ws)
         assert moe.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_renormalised_slot_has_no_gradient(score):
+    """Its weight is the constant scale."""
+    cfg = moe.RouteConfig(score, scale=2.5)
+    l = torch.randn(37, 24, generator=torch.Generator().manual_seed(8)).cuda()
+    dw = torch.randn(37, 1, generator=torch.Generator().manual_seed(9)).cuda()
+    idx, w = moe.moe_route_scored(l, 1, cfg)
+    assert torch.equal(w, torch.full_like(w, 2.5))
+    assert not moe.moe_route_scored_backward(dw, idx, l, cfg).any()
