@@ -1566,17 +1566,34 @@ struct ExpandPlan {
 int block_rows(int T, int blocks) { return ((T + blocks - 1) / blocks + 15) & ~15; }
 // The cheapest of both by a cost in microseconds: a K stage of 64 takes 0.3 us
 // at 256 tokens (measured alone; its MMAs 0.27), in proportion to the tokens
-// down to 0.12 us, and a CTA's set-up, first loads and epilogue 6 us, which the
-// persistent CTAs pay once.
-ExpandPlan plan_expand(int T, int K, int M) {
+// down to 0.15 us, a CTA's set-up, first loads and epilogue 6 us, which the
+// persistent CTAs pay once, and joining s partial tiles of 256 tokens 6 + 3 log2 s
+// us.  More blocks are more work for shrink, whose K stages (shrink_k in all) take
+// 0.25 us per unit (777 x 7168 x 2048, 24 adapters of rank 64: 60 us in six blocks
+// of pairs, 44 in four blocks of clusters of two).  Over 370 calls (1 to 8192 tokens, H and N from 512 to 16384, both directions)
+// every form was timed: the choice is 1.7% slower than the best on average, at
+// most 31%; without the join's cost and the limit on clusters of eight it was 6%
+// and 59% (1024 x 2048 x 1024: 20.8 us in clusters of four, 13.1 in pairs; 128 x
+// 7168 x 2048: 30.2 us in clusters of eight, 19.1 in clusters of four).
+ExpandPlan plan_expand(int T, int K, int M, int n, int R, int shrink_k) {
   const int nk = K / kK, sms = device_sm_count();
-  auto stage = [](int nb) { return nb > 102 ? 0.3 * nb / 256 : 0.12; };
+  auto stage = [](int nb) { return nb > 128 ? 0.3 * nb / 256 : 0.15; };
   const int least = (T + 255) / 256;
+  auto shrink = [&](int blocks, int nb) {
+    const int units = ((n < nb ? n : nb) * R + kM - 1) / kM;
+    return 0.25 * blocks * units * (shrink_k / kK) / sms;
+  };
   ExpandPlan best{least, block_rows(T, least), 1};
   double cost = 1e30;
   for (int s = 1; s <= 8 && (s == 1 || nk / s >= 4); s *= 2) {
     const long long ctas = (long long)least * (M / kM) * s;
-    const double c = (double)((ctas + sms - 1) / sms) * (nk * stage(best.nb) / s + 6.0);
+    // clusters of eight do not tile the GPU's processing clusters, and shrink's
+    // take some of their places: above three quarters of the SMs the last of
+    // them start when shrink ends
+    const int room = s == 8 ? sms * 3 / 4 : sms;
+    const double join = s == 1 ? 0.0 : best.nb / 256.0 * (s == 2 ? 9 : s == 4 ? 12 : 15);
+    const double c = (double)((ctas + room - 1) / room) * (nk * stage(best.nb) / s + 6.0 + join) +
+                     shrink(least, best.nb);
     if (c < cost) {
       cost = c;
       best.split = s;
@@ -1587,7 +1604,7 @@ ExpandPlan plan_expand(int T, int K, int M) {
     const int nb = block_rows(T, blocks);
     if (nb <= 128) break;
     const long long tiles = (long long)blocks * ((M / kM + 1) / 2);
-    const double c = (double)((tiles + pairs - 1) / pairs) * (nk * stage(nb) + 0.5) + 6.0;
+    const double c = (double)((tiles + pairs - 1) / pairs) * nk * stage(nb) + 6.0 + shrink(blocks, nb);
     if (c < cost) {
       cost = c;
       best = ExpandPlan{blocks, nb, 0};
@@ -1811,7 +1828,8 @@ AdapterSizes adapter_sizes(int T, int H, int N, int n, int R, bool backward) {
   z.N = N;
   z.n = n;
   z.R = R;
-  const ExpandPlan e = T > 0 ? (backward ? plan_expand(T, N, H) : plan_expand(T, H, N))
+  const ExpandPlan e = T > 0 ? (backward ? plan_expand(T, N, H, n, R, H + N)
+                                       : plan_expand(T, H, N, n, R, H))
                              : ExpandPlan{0, 16, 1};
   z.nb = e.nb;
   z.n_tt = (T + e.nb - 1) / e.nb;

@@ -18,6 +18,13 @@ CASES = [  # T, H, N, n, R, order
     (1, 128, 128, 1, 8, "one"),
     (1, 512, 1024, 4, 8, "shuffled"),
     (1, 2048, 128, 3, 128, "one"),
+    (1, 7168, 256, 2, 40, "one"),
+    (1, 512, 128, 2, 16, "none"),
+    (2, 640, 384, 4, 16, "distinct"),
+    (3, 1152, 256, 5, 8, "distinct"),
+    (4, 2048, 640, 3, 128, "shuffled"),
+    (1, 16384, 128, 3, 16, "one"),
+    (1, 128, 20480, 3, 8, "one"),
     (7, 256, 384, 5, 24, "shuffled"),
     (31, 2048, 256, 40, 16, "distinct"),
     (32, 384, 128, 32, 40, "distinct"),
@@ -234,7 +241,7 @@ def test_output_given_and_default_workspace():
                                 v["B"][:, :12].contiguous(), v["scale"], v["adapter_idx"])
 
 
-@pytest.mark.parametrize("T,N", [(40, 256), (2600, 2048)])     # split tiles, persistent pairs
+@pytest.mark.parametrize("T,N", [(1, 256), (40, 256), (2600, 2048)])   # one token, split tiles, pairs
 def test_captured_in_a_graph(T, N):
     d, dy = make((T, 256, N, 4, 16, "shuffled"))
     v, dy = dev(d), dy.cuda()
@@ -269,3 +276,41 @@ def test_operands_of_the_layers_own_calls_share_a_workspace():
     assert torch.equal(want, moe.moe_forward(*args, ws=ws))
     assert moe.moe_get_device_status(ws) == 0
     assert torch.equal(y, moe.moe_adapter_project(**v, ws=ws))
+
+
+@pytest.mark.parametrize("T", [1, 2, 3])
+def test_few_tokens_keep_to_themselves_and_report(T):
+    """Non-finite values, bad indices and a status left by an
+    earlier call."""
+    d, _ = make((T, 256, 384, 5, 16, "distinct"))
+    d["adapter_idx"] = torch.arange(T, dtype=torch.int32)
+    ws = moe.Workspace()
+    ws.ensure(1 << 16).fill_(0xff)
+    clean = moe.moe_adapter_project(**dev(d), ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    last = T - 1
+    others = torch.arange(T) != last
+    for value in (float("nan"), float("inf"), -float("inf")):
+        bad = {**d, "B": d["B"].clone()}
+        bad["B"][last, 3, 200] = value
+        zeroed = {**d, "B": d["B"].clone()}
+        zeroed["B"][last, 3, 200] = 0.
+        y = moe.moe_adapter_project(**dev(bad), ws=ws)
+        assert moe.moe_get_device_status(ws) == 2
+        assert torch.equal(y, moe.moe_adapter_project(**dev(zeroed), ws=ws))
+        assert moe.moe_get_device_status(ws) == 0
+        for key in ("A", "x"):
+            bad = {**d, key: d[key].clone()}
+            bad[key][(last, 5, 77) if key == "A" else (last, 77)] = value
+            y = moe.moe_adapter_project(**dev(bad), ws=ws)
+            assert moe.moe_get_device_status(ws) == 0
+            assert torch.equal(y.cpu()[others], clean.cpu()[others])
+            assert not y.cpu()[last].isfinite().all()
+    none = {**d, "adapter_idx": d["adapter_idx"].clone()}
+    for index in (5, -2):
+        none["adapter_idx"][last] = index
+        y = moe.moe_adapter_project(**dev(none), ws=ws)
+        assert moe.moe_get_device_status(ws) == 1
+    none["adapter_idx"][last] = -1
+    assert torch.equal(y, moe.moe_adapter_project(**dev(none), ws=ws))
+    assert moe.moe_get_device_status(ws) == 0
