@@ -59,6 +59,33 @@ __device__ __forceinline__ const BlockPlan* plan_of(const void* plan, int tt) {
                                             (size_t)tt * kAdapterPlanBytes);
 }
 
+// The hand-over of what shrink wrote to a kernel that starts before expand ends: a
+// thread of expand, once its own griddepcontrol.wait has made shrink's results
+// visible to it, publishes the call's number with release order; the kernel after
+// it reads nothing of shrink's before it has read that number with acquire order
+// (starting early makes no writes visible).  The word is in the workspace, beside
+// the status.
+__device__ __forceinline__ uint64_t* hand_over_word(int* status) {
+  return reinterpret_cast<uint64_t*>(status + 4);
+}
+__device__ __forceinline__ void hand_over(int* status, uint64_t call) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(hand_over_word(status)), "l"(call)
+               : "memory");
+}
+// Bounded: expand publishes before it lets the next kernel start, unless it gave up.
+__device__ __forceinline__ bool take_over(int* status, uint64_t call) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (true) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];"
+                 : "=l"(v)
+                 : "l"(hand_over_word(status))
+                 : "memory");
+    if (v == call) return true;
+    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
 __device__ __forceinline__ void fence_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
@@ -693,6 +720,7 @@ struct ExpandArgs {
   __nv_bfloat16* out;       // [T, M]
   const void* plan;
   int* status;
+  uint64_t call;            // the call's number where a kernel follows that starts early, or 0
 };
 
 // Columns x .. x + 64 of a block's rows; in a pair, rank r loads the r-th half
@@ -893,7 +921,8 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     }
     __syncwarp();
     pdl_wait();             // the plan and Z are complete
-    pdl_trigger();          // and so they are for the kernel that follows
+    if (a.call != 0 && blockIdx.x == 0 && leader) hand_over(a.status, a.call);
+    pdl_trigger();
     fence_async_global();
     const int q_all = plan->n_ent * a.R;
     store_list(sh->list, load_list(plan, lane), lane);
@@ -1109,7 +1138,8 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (!later) {
         pdl_wait();             // the plan and Z are complete
-        pdl_trigger();          // and so they are for the kernel that follows
+        if (a.call != 0 && blockIdx.x == 0 && leader) hand_over(a.status, a.call);
+        pdl_trigger();
         fence_async_global();
         n_ent = plan->n_ent;
         list = load_list(plan, lane);
@@ -1264,10 +1294,10 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
 // 8192 tokens, 7168 + 2048 columns, 8 adapters in 40 us by itself, 3.8 TB/s (the
 // 576 CTAs are a round and a quarter of three per SM, of unequal lengths), 33 us
 // of it after expand has ended.
-// It may start while the expand launch before it still runs: expand lets it go
-// once it has itself seen the shrink launch complete, so everything read here (past
-// the L1 cache) is complete, and nothing that expand writes is read; but it does
-// not end before expand.
+// It may start while the expand launch before it still runs, since nothing that
+// expand writes is read: expand hands shrink's results over (see take_over), and
+// this kernel does not end before expand.  In a captured launch, whose number would
+// be the same in every replay, it waits for the end of expand before it reads.
 struct WgradMaps {
   CUtensorMap v[2];   // [T, D] as (64 features, tokens, D / 64)
   CUtensorMap z[2];   // [T, zc], boxes of 64 columns x 64 tokens
@@ -1279,6 +1309,7 @@ struct WgradArgs {
   const uint32_t* masks;       // [n_tt][256][8]: the tokens of every entry, as bits
   __nv_bfloat16* out[2];       // [n, R, D]
   int* status;
+  uint64_t call;               // the number that expand hands shrink's results over with, or 0
 };
 // kCols: 64-column boxes of Z per stage (ranks up to 64, or up to 128).
 template <int kCols>
@@ -1338,14 +1369,16 @@ adapter_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) 
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
+  if (a.call == 0) pdl_wait();
   if (warp == 0) {
     const uint64_t pol = policy_evict_normal();
     const bool leader = elect_lane();
+    bool ok = a.call == 0 || take_over(a.status, a.call);
+    ok = __all_sync(0xffffffffu, ok);
     fence_async_global();   // Z and dZ were written by ordinary stores
     const uint32_t empty0 = smem_u32(sh->empty), full0 = smem_u32(sh->full);
     const uint32_t sbase = smem_u32(smem);
     Place at(C::kStages);
-    bool ok = true;
     int group = 0;   // of the adapter's
     for (int tb = 0; ok && tb < a.n_tt; tb += 32) {
       // lane: block tb + lane, ad's entry in it and its tokens there
@@ -1781,7 +1814,7 @@ cudaError_t launch_expand_t(int split, const ExpandMaps& m, const ExpandArgs& a,
 cudaError_t launch_expand(const AdapterSizes& z, const CUtensorMap& v_map,
                           const __nv_bfloat16* v, const __nv_bfloat16* W,
                           bool k_major, const __nv_bfloat16* Z, const __nv_bfloat16* P, int K,
-                          int M, const void* plan, __nv_bfloat16* out, int* status,
+                          int M, const void* plan, __nv_bfloat16* out, int* status, uint64_t call,
                           cudaStream_t s) {
   ExpandMaps m;
   const int rb = rank_box(z.R);
@@ -1791,7 +1824,7 @@ cudaError_t launch_expand(const AdapterSizes& z, const CUtensorMap& v_map,
       !map_rows(&m.z, Z, z.T, z.zc, box))
     return cudaErrorInvalidValue;
   if (box == z.nb) m.v = v_map;
-  const ExpandArgs a{z.T, z.nb, K, M, z.n, z.R, rb, z.n_tt, out, plan, status};
+  const ExpandArgs a{z.T, z.nb, K, M, z.n, z.R, rb, z.n_tt, out, plan, status, call};
   return k_major ? launch_expand_t<true>(z.split, m, a, s)
                  : launch_expand_t<false>(z.split, m, a, s);
 }
@@ -1866,7 +1899,7 @@ cudaError_t launch_adapter_project(const AdapterSizes& z, const __nv_bfloat16* x
   const cudaError_t err =
       launch_shrink(z, 1, &job, scale, adapter_idx, plan, nullptr, status, B, z.N, &v_map, s);
   if (err != cudaSuccess) return err;
-  return launch_expand(z, v_map, x, W, false, Z, B, z.H, z.N, plan, y, status, s);
+  return launch_expand(z, v_map, x, W, false, Z, B, z.H, z.N, plan, y, status, 0, s);
 }
 
 cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* dy,
@@ -1882,16 +1915,18 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
   uint32_t* masks = ws_ptr<uint32_t>(ws, z.masks);
   const ShrinkJob job[2] = {{x, A, z.H, Z}, {dy, B, z.N, dZ}};
   CUtensorMap v_map;
-  cudaError_t err =
-      launch_shrink(z, 2, job, scale, adapter_idx, plan, masks, status, A, z.H, &v_map, s);
+  uint64_t call = 0;
+  cudaError_t err = launch_number(s, &call);
   if (err == cudaSuccess)
-    err = launch_expand(z, v_map, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, s);
+    err = launch_shrink(z, 2, job, scale, adapter_idx, plan, masks, status, A, z.H, &v_map, s);
+  if (err == cudaSuccess)
+    err = launch_expand(z, v_map, dy, W, true, dZ, A, z.N, z.H, plan, dx, status, call, s);
   if (err != cudaSuccess) return err;
   WgradMaps m;
   if (!map_atoms(&m.v[0], x, z.T, z.H) || !map_rows(&m.z[0], dZ, z.T, z.zc, 64) ||
       !map_atoms(&m.v[1], dy, z.T, z.N) || !map_rows(&m.z[1], Z, z.T, z.zc, 64))
     return cudaErrorInvalidValue;
-  const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, plan, masks, {dA, dB}, status};
+  const WgradArgs a{z.T, z.n, z.R, z.nb, z.n_tt, {z.H, z.N}, plan, masks, {dA, dB}, status, call};
   return z.R > 64 ? launch_wgrad<2>(z, m, a, s) : launch_wgrad<1>(z, m, a, s);
 }
 

@@ -238,6 +238,9 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
 // launches with programmatic stream serialisation (see above).
 cudaError_t launch_route(const float* logits, int T, int E, int k, int32_t* topk_idx,
                          float* topk_w, int32_t* chunk_hist, int* status, cudaStream_t s);
+// A number no launch before it had, in any process; 0 while `s` is being captured (a
+// captured launch runs many times under the number it was captured with).
+cudaError_t launch_number(cudaStream_t s, uint64_t* launch);
 // A scored routing's configuration as the kernels take it.
 struct RouteCfg {
   bool softmax, renorm;

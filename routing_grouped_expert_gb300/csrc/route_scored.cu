@@ -629,24 +629,24 @@ RouteCfg make_route_cfg(const moe_route_config& a, int E) {
   return c;
 }
 
-namespace {
-// A number no launch before it had, in this process or (from the clock it starts
-// at) in what an earlier one left in memory.
-uint64_t next_launch() {
+// From the clock on, so that no number an earlier process left in memory comes again.
+cudaError_t launch_number(cudaStream_t s, uint64_t* launch) {
   static std::atomic<uint64_t> n{
       (uint64_t)std::chrono::system_clock::now().time_since_epoch().count() | 1};
-  return n.fetch_add(2, std::memory_order_relaxed);
-}
-// The launch's number, or 0 after a memset of the status: a captured launch runs
-// many times under one number.
-cudaError_t begin_status(int* status, cudaStream_t s, uint64_t* launch) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   const cudaError_t err = cudaStreamIsCapturing(s, &cs);
+  *launch = err == cudaSuccess && cs == cudaStreamCaptureStatusNone
+                ? n.fetch_add(2, std::memory_order_relaxed)
+                : 0;
+  return err;
+}
+
+namespace {
+// The launch's number, or 0 after a memset of the status.
+cudaError_t begin_status(int* status, cudaStream_t s, uint64_t* launch) {
+  const cudaError_t err = launch_number(s, launch);
   if (err != cudaSuccess) return err;
-  *launch = 0;
-  if (cs != cudaStreamCaptureStatusNone) return cudaMemsetAsync(status, 0, 2 * sizeof(int), s);
-  *launch = next_launch();
-  return cudaSuccess;
+  return *launch == 0 ? cudaMemsetAsync(status, 0, 2 * sizeof(int), s) : cudaSuccess;
 }
 }  // namespace
 

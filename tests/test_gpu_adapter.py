@@ -314,3 +314,27 @@ def test_few_tokens_keep_to_themselves_and_report(T):
     none["adapter_idx"][last] = -1
     assert torch.equal(y, moe.moe_adapter_project(**dev(none), ws=ws))
     assert moe.moe_get_device_status(ws) == 0
+
+
+def test_gradients_of_changing_requests_repeat_bit_for_bit():
+    """Long gradients whose weight-gradient launch starts while the one before it
+    runs, on one workspace that still holds the last call's rows, masks and plan:
+    each call's results are those of a workspace of its own."""
+    T, H, N, n, R = 4096, 2048, 2048, 6, 16
+    base, dy = make((T, H, N, n, R, "segments"))
+    v, dy = dev(base), dy.cuda()
+    orders = []
+    for seed in range(3):
+        g = torch.Generator().manual_seed(100 + seed)
+        cuts = torch.randint(0, T, (2 + 5 * seed,), generator=g)
+        of = torch.randint(-1, n, (len(cuts) + 1,), generator=g)
+        orders.append(of[(cuts[None] <= torch.arange(T)[:, None]).sum(1)].to(torch.int32).cuda())
+    want = [moe.moe_adapter_project_backward(dy, **{**v, "adapter_idx": i}, ws=moe.Workspace())
+            for i in orders]
+    ws = moe.Workspace()
+    for rep in range(20):
+        i = (rep * 2) % 3
+        got = moe.moe_adapter_project_backward(dy, **{**v, "adapter_idx": orders[i]}, ws=ws)
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b), rep
+    assert moe.moe_get_device_status(ws) == 0

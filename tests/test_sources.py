@@ -1,0 +1,33 @@
+"""What the device sources keep to, read as text (nothing here needs a GPU)."""
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "routing_grouped_expert_gb300", "csrc")
+
+
+def kernel_body(name, path):
+    """The body of a __global__ function, comments taken out."""
+    src = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, path)).read())
+    start = src.index("{", src.index(name + "("))
+    depth = 0
+    for i in range(start, len(src)):
+        depth += {"{": 1, "}": -1}.get(src[i], 0)
+        if depth == 0:
+            return src[start:i]
+    raise AssertionError(f"{name}: no end")
+
+
+def test_weight_gradients_read_nothing_before_it_is_handed_over():
+    """The kernel starts while the one before it runs.  Starting early makes no
+    writes visible: both of its ways to wait come before the first read of the
+    plan, the masks and Z."""
+    body = kernel_body("adapter_wgrad_kernel", "adapter.cu")
+    first = min(body.index(what) for what in ("plan_of(", "a.masks", "load_2d(", "load_3d("))
+    assert "if (a.call == 0) pdl_wait();" in body[:first]
+    assert "take_over(a.status, a.call)" in body[:first]
+    # and expand hands over after its own wait, in both of its forms
+    for name in ("adapter_expand_split_kernel", "adapter_expand_kernel"):
+        expand = kernel_body(name, "adapter.cu")
+        at = expand.index("hand_over(a.status, a.call)")
+        assert "pdl_wait();" in expand[:at] and "pdl_trigger();" not in expand[:at]
