@@ -137,31 +137,40 @@ __device__ __forceinline__ bool elect_lane() {
       : "=r"(p));
   return p != 0;
 }
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    uint32_t ok;
+// kCluster: the barrier counts arrivals of the pair's other CTA too, whose writes
+// are to be seen.
+template <bool kCluster>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
-    if (ok) return true;
+  return ok != 0;
+}
+template <bool kCluster>
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (try_wait<kCluster>(bar, parity)) return true;
     if ((i & 15) == 0 && (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) return false;
   }
 }
 // Wait for the phase with `parity` of the barrier at shared address `bar`;
 // bounded as ptx::mbar_wait.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok ? true : wait_slow(bar, parity, abort_flag);
+  return try_wait<kCluster>(bar, parity) ? true : wait_slow<kCluster>(bar, parity, abort_flag);
 }
 // The role loops' instructions on shared addresses (no generic pointers to
 // convert at every stage).
@@ -173,21 +182,38 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
 }
+// kPair: `bar` may be a barrier of the pair's other CTA (a cluster address).
+template <bool kPair = false>
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                         int y, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
 }
+template <bool kPair = false>
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                         int y, int z, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
 }
 __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                         int y, int z, int w, uint64_t policy) {
@@ -197,22 +223,13 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, ui
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
       : "memory");
 }
-// A load that lands, and counts, at the same place in every CTA of `mask`.
-__device__ __forceinline__ void load_2d_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                                  int x, int y, uint16_t mask, uint64_t policy) {
+// Arrive once on `bar`'s place in both CTAs of a pair when the pair's tcgen05
+// operations that this thread issued so far have completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
-      : "memory");
-}
-// Arrive once on `bar`'s place in every CTA of `mask` when this thread's
-// tcgen05 operations so far have completed.
-__device__ __forceinline__ void commit_multicast(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(bar),
-      "h"(mask)
+      "h"((uint16_t)0x3)
       : "memory");
 }
 // A 128-byte-swizzled operand descriptor from its two words (see
@@ -723,27 +740,15 @@ struct ExpandArgs {
   uint64_t call;            // the call's number where a kernel follows that starts early, or 0
 };
 
-// Columns x .. x + 64 of a block's rows; in a pair, rank r loads the r-th half
-// for both CTAs.
-template <bool kPair>
-__device__ __forceinline__ void load_tokens(uint32_t dst, uint32_t fb, const CUtensorMap* map, int nb,
-                                            int x, int row0, uint64_t pol, int rank) {
-  if constexpr (kPair)
-    load_2d_multicast(dst + rank * (nb / 2 * kK * 2), map, fb, x, row0 + rank * (nb / 2), 0x3, pol);
-  else
-    load_2d(dst, map, fb, x, row0, pol);
-}
-// The weight operand of one stage and its token rows.
+// The weight operand of one stage and its `nb` token rows from row0 on.
 template <bool kKMajor, bool kPair = false>
-__device__ __forceinline__ void load_base(uint32_t st, uint32_t fb, const ExpandMaps& maps,
-                                          int nb, int kb, int mt, int row0, uint64_t pol_w, uint64_t pol_v,
-                                          int rank = 0) {
-  expect_tx(fb, (uint32_t)(kABytes + nb * kK * 2));
+__device__ __forceinline__ void load_base(uint32_t st, uint32_t fb, const ExpandMaps& maps, int kb,
+                                          int mt, int row0, uint64_t pol_w, uint64_t pol_v) {
   if constexpr (kKMajor)
-    load_2d(st, &maps.w, fb, kb * kK, mt * kM, pol_w);
+    load_2d<kPair>(st, &maps.w, fb, kb * kK, mt * kM, pol_w);
   else
-    load_3d(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
-  load_tokens<kPair>(st + kABytes, fb, &maps.v, nb, kb * kK, row0, pol_v, rank);
+    load_3d<kPair>(st, &maps.w, fb, 0, kb * kK, mt * 2, pol_w);
+  load_2d<kPair>(st + kABytes, &maps.v, fb, kb * kK, row0, pol_v);
 }
 // A block's entry list, copied to shared memory by the warp that uses it.
 __device__ __forceinline__ void store_list(uint16_t* list, const uint4& v, int lane) {
@@ -757,14 +762,13 @@ __device__ __forceinline__ uint4 load_list(const BlockPlan* plan, int lane) {
 // Stage j of the adapters' part, by the whole producer warp: 64 rank rows of
 // the block's entries, in boxes of rb rows, each [2 feature atoms][rb rows][128
 // bytes].
-template <bool kPair = false>
 __device__ __forceinline__ void load_ext(uint32_t st, uint32_t fb, const ExpandMaps& maps,
                                          const ExpandArgs& a, const uint16_t* list, int q_all, int j,
-                                         int mt, int row0, uint64_t pol_w, uint64_t pol_v,
-                                         bool leader, int rank = 0) {
+                                         int mt, int nb, int row0, uint64_t pol_w, uint64_t pol_v,
+                                         bool leader) {
   if (leader) {
-    expect_tx(fb, (uint32_t)(kABytes + a.nb * kK * 2));
-    load_tokens<kPair>(st + kABytes, fb, &maps.z, a.nb, j * kK, row0, pol_v, rank);
+    expect_tx(fb, (uint32_t)(kABytes + nb * kK * 2));
+    load_2d(st + kABytes, &maps.z, fb, j * kK, row0, pol_v);
   }
   int e = j * kK / a.R, row = j * kK - e * a.R;
   for (int q = 0; q < kK; q += a.rb) {
@@ -778,8 +782,17 @@ __device__ __forceinline__ void load_ext(uint32_t st, uint32_t fb, const ExpandM
     }
   }
 }
+// One MMA of a CTA, or of a pair.
+template <bool kPair>
+__device__ __forceinline__ void mma_of(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (kPair)
+    mma_bf16_ss_pair(tmem, a, b, idesc, accumulate);
+  else
+    mma_bf16_ss(tmem, a, b, idesc, accumulate);
+}
 // The four MMAs of a stage at shared address a0 (one lane).
-template <bool kKMajor>
+template <bool kKMajor, bool kPair = false>
 __device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, uint32_t idesc, uint32_t first) {
   // MN-major weights: 64-feature atoms 8 KB apart, 16 K rows = 2 KB; K-major
   // operands: 8-row groups 1 KB apart, 16 K = 32 bytes
@@ -787,10 +800,11 @@ __device__ __forceinline__ void mma_base(uint32_t tmem, uint32_t a0, uint32_t id
   const uint32_t lb = desc_lo(a0 + kABytes, 16);
 #pragma unroll
   for (int kk = 0; kk < kK / 16; ++kk)
-    mma_bf16_ss(tmem, desc_of(la + (kKMajor ? 2 : 128) * kk, desc_hi(1024)),
-                desc_of(lb + 2 * kk, desc_hi(1024)), idesc, kk ? 1u : first);
+    mma_of<kPair>(tmem, desc_of(la + (kKMajor ? 2 : 128) * kk, desc_hi(1024)),
+                  desc_of(lb + 2 * kk, desc_hi(1024)), idesc, kk ? 1u : first);
 }
 // The same of an adapters' stage: MN-major boxes of rb rank rows.
+template <bool kPair = false>
 __device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, uint32_t idesc, int rb) {
   const uint32_t lb = desc_lo(a0 + kABytes, 16);
   const uint32_t lbo = (uint32_t)rb * 128, hi = desc_hi(rb == 8 ? 2048u : 1024u);
@@ -798,7 +812,7 @@ __device__ __forceinline__ void mma_ext(uint32_t tmem, uint32_t a0, uint32_t ide
   for (int kk = 0; kk < kK / 16; ++kk) {
     const uint32_t q = 16u * kk, in = q & (uint32_t)(rb - 1);   // rb: a power of two
     const uint32_t la = desc_lo(a0 + (q - in) * 256 + in * 128, lbo);
-    mma_bf16_ss(tmem, desc_of(la, hi), desc_of(lb + 2 * kk, desc_hi(1024)), idesc, 1u);
+    mma_of<kPair>(tmem, desc_of(la, hi), desc_of(lb + 2 * kk, desc_hi(1024)), idesc, 1u);
   }
 }
 // A guard's pass over the 64 x 128 adapter weights of a stage: every
@@ -913,9 +927,11 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
-      if (leader)
-        load_base<kKMajor>(sbase + at.stage * stage_bytes, full0 + base.stage * 8, maps, a.nb, kb, mt,
-                           row0, pol_w, pol_v);
+      if (leader) {
+        expect_tx(full0 + base.stage * 8, (uint32_t)stage_bytes);
+        load_base<kKMajor>(sbase + at.stage * stage_bytes, full0 + base.stage * 8, maps, kb, mt, row0,
+                           pol_w, pol_v);
+      }
       at.next();
       base.next();
     }
@@ -931,8 +947,8 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
     for (int j = ne * rank / kS; ok && j < ne * (rank + 1) / kS; ++j) {
       ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      load_ext<>(sbase + at.stage * stage_bytes, loaded0 + ext.stage * 8, maps, a, sh->list, q_all, j,
-                 mt, row0, pol_w, pol_v, leader);
+      load_ext(sbase + at.stage * stage_bytes, loaded0 + ext.stage * 8, maps, a, sh->list, q_all, j,
+               mt, a.nb, row0, pol_w, pol_v, leader);
       at.next();
       ext.next();
     }
@@ -1039,9 +1055,12 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
 
 // Many tiles: persistent CTAs, two accumulators of 256 tokens in TMEM, so the
 // epilogue of one tile runs under the main loop of the next.  Two CTAs of a
-// cluster take neighbouring feature tiles of the same token block: each loads
-// half of the block's rows and multicasts it to both, so a stage reads 32 KB
-// from L2 instead of 48 KB.
+// cluster take neighbouring feature tiles of the same token block as one tile of
+// 256 features (.cta_group::2): each stages its own weights and half of the
+// block's rows, 32 KB a stage instead of 48 KB, in a ring of six stages instead of
+// four.  Rank 0 issues the MMAs: its `full` counts both CTAs' loads, its `ready`
+// both guards, its acc_empty both epilogues; each CTA's own `loaded` counts what
+// its guard has to pass, and `empty` and acc_full are announced to both.
 // Bound by the tensor cores under the power limit: 4096 x 6144 x 10752 in 314 us,
 // 1.72 PFLOP/s (0.99 of what cuBLAS sustains, 0.88 of its burst rate); the
 // gradient's 8192 x 2048 x 7168 in 139 us, 1.73 PFLOP/s.
@@ -1058,6 +1077,7 @@ struct FullShared {
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort;
+  uint32_t issued;   // rank 0: the projection's stages that rank 1 has loaded
 };
 
 static_assert(sizeof(FullShared) <= 1024, "shared block");
@@ -1065,14 +1085,16 @@ static_assert(sizeof(FullShared) <= 1024, "shared block");
 template <bool kKMajor>
 __global__ void __launch_bounds__(kThreads, 1)
 adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs a) {
-  // maps.v and maps.z: boxes of half a block's rows
+  // maps.v and maps.z: boxes of half a block's rows (a.nb: a multiple of 32, as the
+  // pair's MMAs need)
   using C = FullCfg;
   constexpr int kNB = C::kNB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   FullShared* sh = reinterpret_cast<FullShared*>(smem + C::kRing);
-  const int stage_bytes = stage_bytes_of(a.nb), stages = ring_stages(stage_bytes, C::kOther);
+  const int half = a.nb / 2;   // a multiple of 16
+  const int stage_bytes = stage_bytes_of(half), stages = ring_stages(stage_bytes, C::kOther);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int nk = a.K / kK;
   const int rank = (int)cluster_ctarank();
@@ -1082,27 +1104,33 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], 2);    // both CTAs' MMAs have read the slot
+      mbar_init(&sh->empty[s], 1);
       mbar_init(&sh->loaded[s], 1);
-      mbar_init(&sh->ready[s], 1);
+      mbar_init(&sh->ready[s], 2);    // both CTAs' guards
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->acc_full[b], 1);
-      mbar_init(&sh->acc_empty[b], 4);
+      mbar_init(&sh->acc_empty[b], 8);   // both CTAs' epilogue warps
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&sh->tmem_base, 2 * kNB);
-    tmem_relinquish();
+    tmem_alloc_pair(&sh->tmem_base, 2 * kNB);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   cluster_sync();   // both CTAs' barriers are set before either signals the other's
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort_flag = &sh->abort;
+  int issued0 = -1;   // rank 0's producer: the projection's stages it has loaded
+  // arrive on rank 0's barrier
+  auto arrive_rank0 = [=](uint64_t* bar) {
+    if (rank == 0) mbar_arrive(bar);
+    else mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
+  };
   // a role that gives up stops the roles of both CTAs
   auto raise_abort = [=]() {
     *abort_flag = 1;
@@ -1116,10 +1144,12 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
   if (warp == 0) {
     const uint64_t pol_w = policy_evict_normal(), pol_v = policy_evict_last();
     const bool leader = elect_lane();
+    const uint32_t counted0 = mapa_shared(full0, 0);   // rank 0's barriers
     Place at(stages), base(stages), ext(stages);
     bool ok = true;
     for (int tile = first; ok && tile < total; tile += step) {
-      const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank, row0 = tt * a.nb;
+      // row0: of this CTA's half of the block
+      const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank, row0 = tt * a.nb + rank * half;
       const BlockPlan* plan = plan_of(a.plan, tt);
       // from the second tile on the plan is known to be complete: its words
       // are on their way while the projection's stages are loaded
@@ -1128,9 +1158,11 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       uint4 list = later ? load_list(plan, lane) : make_uint4(0, 0, 0, 0);
       for (int kb = 0; kb < nk; ++kb) {
         if (!(ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag))) break;
-        if (leader)
-          load_base<kKMajor, true>(sbase + at.stage * stage_bytes, full0 + base.stage * 8, maps, a.nb,
-                                   kb, mt, row0, pol_w, pol_v, rank);
+        if (leader) {
+          if (rank == 0) expect_tx(full0 + base.stage * 8, 2u * (uint32_t)stage_bytes);
+          load_base<kKMajor, true>(sbase + at.stage * stage_bytes, counted0 + base.stage * 8, maps, kb,
+                                   mt, row0, pol_w, pol_v);
+        }
         at.next();
         base.next();
       }
@@ -1149,8 +1181,8 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       for (int j = 0; j * kK < q_all; ++j) {
         ok = wait_bar(empty0 + at.stage * 8, at.phase ^ 1u, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        load_ext<true>(sbase + at.stage * stage_bytes, loaded0 + ext.stage * 8, maps, a, sh->list,
-                       q_all, j, mt, row0, pol_w, pol_v, leader, rank);
+        load_ext(sbase + at.stage * stage_bytes, loaded0 + ext.stage * 8, maps, a, sh->list, q_all, j,
+                 mt, half, row0, pol_w, pol_v, leader);
         at.next();
         ext.next();
       }
@@ -1162,30 +1194,35 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailProducer);
         raise_abort();
       }
-      drain_loads(sh->full, stages, 0, base.count);
+      if (rank == 0) {
+        issued0 = base.count;
+        if (ok) drain_loads(sh->full, stages, 0, base.count);   // both CTAs' loads
+      } else {
+        st_cluster_u32(mapa_shared(smem_u32(&sh->issued), 0), (uint32_t)base.count);
+      }
       drain_loads(sh->loaded, stages, 0, ext.count);
     }
-  } else if (warp == 1) {
-    const uint32_t id_base = idesc_bf16(kM, a.nb, /*a_mn=*/!kKMajor, false);
-    const uint32_t id_ext = idesc_bf16(kM, a.nb, /*a_mn=*/true, false);
+  } else if (warp == 1 && rank == 0) {
+    const uint32_t id_base = idesc_bf16(2 * kM, a.nb, /*a_mn=*/!kKMajor, false);
+    const uint32_t id_ext = idesc_bf16(2 * kM, a.nb, /*a_mn=*/true, false);
     const bool leader = elect_lane();
+    const uint32_t acc_full0 = smem_u32(sh->acc_full), acc_empty0 = smem_u32(sh->acc_empty);
     Place at(stages), base(stages), ext(stages);
     Place buf(2);
     bool ok = true;
     for (int tile = first; ok && tile < total; tile += step) {
-      if (!(ok = mbar_wait(&sh->acc_empty[buf.stage], buf.phase ^ 1u, abort_flag, kWaitLimitNs)))
-        break;
+      if (!(ok = wait_bar<true>(acc_empty0 + buf.stage * 8, buf.phase ^ 1u, abort_flag))) break;
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(buf.stage * kNB);
       const BlockPlan* plan = plan_of(a.plan, tile % a.n_tt);
       const bool later = tile != first;
       int n_ent = later ? plan->n_ent : 0;   // early, as the producer's
       for (int kb = 0; kb < nk; ++kb) {
-        if (!(ok = wait_bar(full0 + base.stage * 8, base.phase, abort_flag))) break;
+        if (!(ok = wait_bar<true>(full0 + base.stage * 8, base.phase, abort_flag))) break;
         tc_fence_after();
         if (leader) {
-          mma_base<kKMajor>(d, sbase + (uint32_t)(at.stage * stage_bytes), id_base, kb ? 1u : 0u);
-          commit_multicast(empty0 + at.stage * 8, 0x3);
+          mma_base<kKMajor, true>(d, sbase + (uint32_t)(at.stage * stage_bytes), id_base, kb ? 1u : 0u);
+          commit_pair(empty0 + at.stage * 8);
         }
         at.next();
         base.next();
@@ -1197,17 +1234,17 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       }
       const int q_all = n_ent * a.R;
       for (int j = 0; ok && j * kK < q_all; ++j) {
-        if (!(ok = wait_bar(ready0 + ext.stage * 8, ext.phase, abort_flag))) break;
+        if (!(ok = wait_bar<true>(ready0 + ext.stage * 8, ext.phase, abort_flag))) break;
         tc_fence_after();
         if (leader) {
-          mma_ext(d, sbase + (uint32_t)(at.stage * stage_bytes), id_ext, a.rb);
-          commit_multicast(empty0 + at.stage * 8, 0x3);
+          mma_ext<true>(d, sbase + (uint32_t)(at.stage * stage_bytes), id_ext, a.rb);
+          commit_pair(empty0 + at.stage * 8);
         }
         at.next();
         ext.next();
       }
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      if (leader) mma_commit(&sh->acc_full[buf.stage]);
+      if (leader) commit_pair(acc_full0 + buf.stage * 8);
       buf.next();
     }
     if (leader) {
@@ -1215,7 +1252,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailMma);
         raise_abort();
       }
-      mma_commit(&sh->drain);
+      commit_pair(smem_u32(&sh->drain));
       if (!mbar_wait(&sh->drain, 0, nullptr, kWaitLimitNs))
         set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
     }
@@ -1231,13 +1268,13 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
         if (!(ok = __all_sync(0xffffffffu, got))) break;
         found |= clear_nonfinite(smem + at.stage * stage_bytes, lane, 0, 1);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->ready[ext.stage]);
+        if (lane == 0) arrive_rank0(&sh->ready[ext.stage]);
         at.next();
         ext.next();
       }
     }
     if (found) set_status(a.status, MOE_ERR_NONFINITE);
-  } else {
+  } else if (warp >= 3) {
     const int q = warp & 3;
     __nv_bfloat16* stg =
         reinterpret_cast<__nv_bfloat16*>(smem + C::kRing + 1024 + (warp - 3) * C::kStgBytes);
@@ -1271,16 +1308,30 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->acc_empty[buf.stage]);
+      if (lane == 0) arrive_rank0(&sh->acc_empty[buf.stage]);
       buf.next();
     }
+    // rank 1's last announcements have arrived: `drain` is the last of them
+    if (rank == 1 && warp == 3 && lane == 0 && !mbar_wait(&sh->drain, 0, nullptr, kWaitLimitNs))
+      set_status(a.status, MOE_ERR_TIMEOUT, kWaitDetailDrain);
   }
   __syncwarp();
   tc_fence_before();
   cluster_sync();   // neither CTA leaves while the other may still write to it
+  if (*abort_flag) {
+    // a wait ran out: the loads on rank 0's `full` that no drain has waited for,
+    // rank 1's beyond rank 0's among them, which nothing has announced
+    if (rank == 0 && issued0 >= 0) {
+      const int issued1 = (int)sh->issued;
+      for (int i = issued0; i < issued1; ++i) expect_tx(full0 + (i % stages) * 8, (uint32_t)stage_bytes);
+      drain_loads(sh->full, stages, 0, issued0 > issued1 ? issued0 : issued1);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * kNB);
+    tmem_dealloc_pair(tmem, 2 * kNB);
   }
 }
 
@@ -1595,8 +1646,11 @@ bool map_rank_atoms(CUtensorMap* m, const void* p, int n, int R, int cols, int r
 struct ExpandPlan {
   int blocks, nb, split;
 };
-// Tokens per block for a number of blocks: equal blocks, whole MMA columns.
-int block_rows(int T, int blocks) { return ((T + blocks - 1) / blocks + 15) & ~15; }
+// Tokens per block for a number of blocks: equal blocks, whole MMA columns (16,
+// for a pair of CTAs 32).
+int block_rows(int T, int blocks, int step = 16) {
+  return ((T + blocks - 1) / blocks + step - 1) / step * step;
+}
 // The cheapest of both by a cost in microseconds: a K stage of 64 takes 0.3 us
 // at 256 tokens (measured alone; its MMAs 0.27), in proportion to the tokens
 // down to 0.15 us, a CTA's set-up, first loads and epilogue 6 us, which the
@@ -1634,7 +1688,7 @@ ExpandPlan plan_expand(int T, int K, int M, int n, int R, int shrink_k) {
   }
   const int pairs = sms / 2;
   for (int blocks = least; blocks < least + 8; ++blocks) {
-    const int nb = block_rows(T, blocks);
+    const int nb = block_rows(T, blocks, 32);
     if (nb <= 128) break;
     const long long tiles = (long long)blocks * ((M / kM + 1) / 2);
     const double c = (double)((tiles + pairs - 1) / pairs) * nk * stage(nb) + 6.0 + shrink(blocks, nb);

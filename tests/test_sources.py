@@ -1,9 +1,18 @@
 """What the device sources keep to, read as text (nothing here needs a GPU)."""
+import glob
 import os
 import re
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "routing_grouped_expert_gb300", "csrc")
+SOURCES = sorted(glob.glob(os.path.join(CSRC, "*.cu*")) +
+                 glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
+def asm_statements(src):
+    """Every asm statement, its string literals joined."""
+    for m in re.finditer(r"\basm\s+volatile\s*\((.*?)\);", src, flags=re.S):
+        yield "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', m.group(1)))
 
 
 def kernel_body(name, path):
@@ -31,3 +40,16 @@ def test_weight_gradients_read_nothing_before_it_is_handed_over():
         expand = kernel_body(name, "adapter.cu")
         at = expand.index("hand_over(a.status, a.call)")
         assert "pdl_wait();" in expand[:at] and "pdl_trigger();" not in expand[:at]
+
+
+def test_every_copy_lands_in_one_cta():
+    """The library serves several GPUs as well as one, so no tensor or bulk copy
+    is sent to more than one CTA of a cluster: each CTA loads what it stages
+    (a pair shares operands through its MMAs)."""
+    seen = 0
+    for path in SOURCES:
+        for text in asm_statements(open(path).read()):
+            if "cp.async.bulk" in text:
+                seen += 1
+                assert "multicast" not in text, (os.path.basename(path), text)
+    assert seen >= 10
