@@ -3,11 +3,16 @@ torch tensors.  This layer only checks shapes, dtypes and devices and passes
 raw pointers, sizes and the current CUDA stream; all computation runs in the
 library's kernels.  A missing or unloadable library raises MoeError: there is
 no CPU or PyTorch fallback.
+
+Every call takes a Workspace, `ws`.  Without one it uses a default that belongs
+to the calling thread and the current stream, so such calls may run beside each
+other; calls that are given one must not overlap on it.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -136,7 +141,9 @@ def _out(t: torch.Tensor | None, dtype, shape, like: torch.Tensor, name: str) ->
 
 
 class Workspace:
-    """A reusable device workspace (grows on demand, 256-byte aligned)."""
+    """A reusable device workspace (grows on demand, 256-byte aligned).  Calls
+    on one workspace must not overlap in time: a stream or a thread that runs
+    beside others takes one of its own."""
 
     def __init__(self, device=None):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
@@ -145,6 +152,9 @@ class Workspace:
 
     def ensure(self, nbytes: int) -> torch.Tensor:
         if self.buf.numel() < nbytes:
+            if self.buf.numel():
+                # calls on this stream may still use it when it is freed
+                self.buf.record_stream(torch.cuda.current_stream(self.device))
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         return self.buf
 
@@ -157,13 +167,24 @@ class Workspace:
         return self.buf.numel()
 
 
-_default_ws: dict = {}
+# The calling thread's own workspaces, by (device, stream): calls without one on
+# other streams or in other threads may overlap in time.
+_default_ws = threading.local()
 
 
 def _ws(ws: Workspace | None, nbytes: int) -> Workspace:
+    """`ws`, or without one the default of this thread and stream, with room for
+    `nbytes`.  A call that is being captured into a CUDA graph without a
+    workspace gets one in the graph's own memory, as its outputs do."""
     if ws is None:
         dev = torch.cuda.current_device()
-        ws = _default_ws.setdefault(dev, Workspace(torch.device("cuda", dev)))
+        if torch.cuda.is_current_stream_capturing():
+            ws = Workspace(torch.device("cuda", dev))
+        else:
+            key = (dev, _stream())
+            ws = _default_ws.__dict__.get(key)
+            if ws is None:
+                ws = _default_ws.__dict__[key] = Workspace(torch.device("cuda", dev))
     ws.ensure(nbytes)
     return ws
 
