@@ -258,6 +258,10 @@ class RouteConfig:
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ptr", ctypes.c_void_p(ctypes.addressof(c)))
 
+    def __reduce__(self):   # copies and pickles are made from the fields
+        return type(self), (self.score, self.n_group, self.topk_group, self.group_top,
+                            self.renormalize, self.scale)
+
 
 def _need_bias(bias, E: int):
     if bias is not None:
