@@ -1663,7 +1663,8 @@ int block_rows(int T, int blocks, int step = 16) {
 // and 59% (1024 x 2048 x 1024: 20.8 us in clusters of four, 13.1 in pairs; 128 x
 // 7168 x 2048: 30.2 us in clusters of eight, 19.1 in clusters of four).
 ExpandPlan plan_expand(int T, int K, int M, int n, int R, int shrink_k) {
-  const int nk = K / kK, sms = device_sm_count();
+  // sizes are asked for on hosts without a device too: there the count is 1
+  const int nk = K / kK, sms = device_sm_count() > 1 ? device_sm_count() : 2;
   auto stage = [](int nb) { return nb > 128 ? 0.3 * nb / 256 : 0.15; };
   const int least = (T + 255) / 256;
   auto shrink = [&](int blocks, int nb) {

@@ -1,0 +1,35 @@
+"""The adapters' workspace sizes (nothing here needs a GPU)."""
+import os
+import subprocess
+import sys
+
+from tests.conftest import ROOT
+
+SHAPES = [  # H, N, n, R
+    (512, 1024, 4, 16), (6144, 10752, 16, 16), (256, 256, 300, 16), (4096, 4096, 1024, 64),
+    (7168, 2048, 24, 64), (128, 128, 1, 8), (2048, 128, 1024, 128),
+]
+
+
+def test_sizes_and_refusals_on_a_host_without_a_device():
+    """More tokens than one small block: sizes are given, and a call is refused,
+    where there is no device at all (in a process of its own, with none)."""
+    code = """
+import ctypes
+import routing_grouped_expert_gb300 as moe
+from routing_grouped_expert_gb300 import binding
+for T in (1, 128, 129, 300, 5000):
+    for shape in %r:
+        assert moe.moe_adapter_workspace_size(T, *shape) > 0
+        assert moe.moe_adapter_workspace_size_backward(T, *shape) > 0
+p = ctypes.c_void_p(4096)    # never dereferenced
+lib = binding.load_library()
+size = (300, 512, 1024, 4, 16)
+assert lib.moe_adapter_project(*[p] * 6, *size, p, p, 1 << 40, None) == 6
+assert lib.moe_adapter_project_backward(*[p] * 7, *size, p, p, p, p, 1 << 40, None) == 6
+print("done")
+""" % SHAPES
+    env = {**os.environ, "CUDA_VISIBLE_DEVICES": ""}
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=env, capture_output=True,
+                       text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "done", (r.returncode, r.stderr[-2000:])
