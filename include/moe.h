@@ -416,7 +416,11 @@ moe_status moe_forward_gated(const void* x, const void* Wg,
  * weight counts as zero and sets MOE_ERR_NONFINITE in the device status.
  *
  * ws: moe_adapter_workspace_size bytes (.._backward for the backward, which
- * covers both).  Limits: H and N positive multiples of 128, T < 2^30,
+ * covers both): about T * min(n, 256) * R * 2 for the low-rank activations,
+ * which are kept with R columns for every adapter that a block of up to 256
+ * tokens can meet, twice in the backward (8192 tokens, 1024 adapters of rank
+ * 128: 0.54 and 1.07 GB).  It grows with T, so a workspace for the largest batch
+ * serves smaller ones.  Limits: H and N positive multiples of 128, T < 2^30,
  * 1 <= n <= MOE_MAX_ADAPTERS, R a multiple of 8 up to MOE_MAX_RANK.
  */
 #define MOE_MAX_ADAPTERS 1024

@@ -1646,6 +1646,7 @@ bool map_rank_atoms(CUtensorMap* m, const void* p, int n, int R, int cols, int r
 struct ExpandPlan {
   int blocks, nb, split;
 };
+constexpr int kMoreBlocks = 7;   // token blocks tried beyond the fewest
 // Tokens per block for a number of blocks: equal blocks, whole MMA columns (16,
 // for a pair of CTAs 32).
 int block_rows(int T, int blocks, int step = 16) {
@@ -1688,7 +1689,7 @@ ExpandPlan plan_expand(int T, int K, int M, int n, int R, int shrink_k) {
     }
   }
   const int pairs = sms / 2;
-  for (int blocks = least; blocks < least + 8; ++blocks) {
+  for (int blocks = least; blocks <= least + kMoreBlocks; ++blocks) {
     const int nb = block_rows(T, blocks, 32);
     if (nb <= 128) break;
     const long long tiles = (long long)blocks * ((M / kM + 1) / 2);
@@ -1924,18 +1925,26 @@ AdapterSizes adapter_sizes(int T, int H, int N, int n, int R, bool backward) {
   z.split = e.split;
   // CTAs of the expand launch, of which one block's shrink keeps clear
   z.ctas = e.split ? (long long)z.n_tt * ((backward ? H : N) / kM) * e.split : device_sm_count();
-  const int entries = n < z.nb ? n : z.nb;
-  z.zc = (int)align_up((size_t)entries * R, kM);
+  auto columns = [&](int nb) {
+    const int entries = n < nb ? n : nb;
+    return (int)align_up((size_t)entries * R, kM);
+  };
+  z.zc = columns(z.nb);
+  // The layout has room for every launch shape that plan_expand may choose for T
+  // tokens, and so for fewer tokens too: a caller sizes its workspace once, for its
+  // largest batch.
+  const size_t most_blocks = (size_t)(T + 255) / 256 + kMoreBlocks;
+  const size_t z_bytes = (size_t)T * columns(T < 256 ? (T + 31) & ~31 : 256) * 2;
   size_t o = 1024;   // the status word
   z.plan = o;
-  o += (size_t)z.n_tt * kAdapterPlanBytes;
+  o += most_blocks * kAdapterPlanBytes;
   z.z = o;
-  o = align_up(o + (size_t)T * z.zc * 2, 1024);
+  o = align_up(o + z_bytes, 1024);
   if (backward) {
     z.dz = o;
-    o = align_up(o + (size_t)T * z.zc * 2, 1024);
+    o = align_up(o + z_bytes, 1024);
     z.masks = o;
-    o = align_up(o + (size_t)z.n_tt * kMaxEntries * 8 * 4, 1024);
+    o = align_up(o + most_blocks * kMaxEntries * 8 * 4, 1024);
   }
   z.total = o;
   return z;

@@ -771,9 +771,7 @@ size_t moe_adapter_workspace_size(int T, int H, int N, int n, int R) {
 
 size_t moe_adapter_workspace_size_backward(int T, int H, int N, int n, int R) {
   if (!ok_adapter_sizes(T, H, N, n, R)) return 0;
-  const size_t forward = adapter_sizes(T, H, N, n, R, false).total;
-  const size_t backward = adapter_sizes(T, H, N, n, R, true).total;
-  return forward > backward ? forward : backward;
+  return adapter_sizes(T, H, N, n, R, true).total;
 }
 
 moe_status moe_adapter_project(const void* x, const void* W, const void* A, const void* B,

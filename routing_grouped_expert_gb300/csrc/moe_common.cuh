@@ -425,6 +425,7 @@ struct AdapterSizes {
   int split;          // CTAs per tile of the expand launch; 0: persistent pairs
   long long ctas;     // CTAs of the expand launch
   int zc;             // columns of Z: R for every adapter a block can meet, rounded up to 128
+  // workspace offsets; the room for each does not depend on nb
   size_t plan;        // [n_tt][kAdapterPlanBytes]  the adapters of each block
   size_t z, dz;       // bf16[T][zc]
   size_t masks;       // uint32[n_tt][256][8]  the tokens of each block's adapters, as bits

@@ -3,6 +3,7 @@ import os
 import subprocess
 import sys
 
+import routing_grouped_expert_gb300 as moe
 from tests.conftest import ROOT
 
 SHAPES = [  # H, N, n, R
@@ -33,3 +34,19 @@ print("done")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=env, capture_output=True,
                        text=True)
     assert r.returncode == 0 and r.stdout.strip() == "done", (r.returncode, r.stderr[-2000:])
+
+
+def test_a_workspace_for_a_batch_serves_smaller_ones():
+    for H, N, n, R in SHAPES:
+        for size in (moe.moe_adapter_workspace_size, moe.moe_adapter_workspace_size_backward):
+            last = 0
+            for T in [*range(0, 1200), *range(1200, 20000, 37), 1 << 20]:
+                now = size(T, H, N, n, R)
+                assert now >= last, (size.__name__, H, N, n, R, T)
+                last = now
+            # a number of adapters or a rank that grows needs no less either
+            assert size(700, H, N, n, R) >= size(700, H, N, max(1, n - 1), R)
+            assert size(700, H, N, n, R) >= size(700, H, N, n, max(8, R - 8))
+        for T in (0, 1, 200, 5000):
+            assert (moe.moe_adapter_workspace_size_backward(T, H, N, n, R) >=
+                    moe.moe_adapter_workspace_size(T, H, N, n, R))
