@@ -1279,6 +1279,7 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
     __nv_bfloat16* stg =
         reinterpret_cast<__nv_bfloat16*>(smem + C::kRing + 1024 + (warp - 3) * C::kStgBytes);
     Place buf(2);
+    pdl_wait();   // the limit of the first wait does not run while shrink does
     for (int tile = first; tile < total; tile += step) {
       const int tt = tile % a.n_tt, mt = 2 * (tile / a.n_tt) + rank;
       const int row0 = tt * a.nb, rows = min(a.nb, a.T - row0);

@@ -53,3 +53,16 @@ def test_every_copy_lands_in_one_cta():
                 seen += 1
                 assert "multicast" not in text, (os.path.basename(path), text)
     assert seen >= 10
+
+
+def test_no_bounded_wait_runs_while_an_earlier_launch_does():
+    """A wait that depends on the launch before this one starts after that launch
+    has ended: a low-rank product of more than a second is no time-out."""
+    body = kernel_body("adapter_expand_kernel", "adapter.cu")
+    epilogue = body[body.index("else if (warp >= 3)"):]
+    assert "pdl_wait();" in epilogue[:epilogue.index("sh->acc_full")]
+    guard = body[body.index("else if (warp == 2)"):body.index("else if (warp >= 3)")]
+    assert "pdl_wait();" in guard[:guard.index("sh->loaded")]
+    split = kernel_body("adapter_expand_split_kernel", "adapter.cu")
+    split = split[:split.index("mbar_wait(&sh->loaded")]
+    assert "pdl_wait();" in split[split.rindex("else {"):]
