@@ -338,3 +338,54 @@ def test_gradients_of_changing_requests_repeat_bit_for_bit():
         for a, b in zip(got, want[i]):
             assert torch.equal(a, b), rep
     assert moe.moe_get_device_status(ws) == 0
+
+
+PAIRS = [  # persistent pairs of CTAs in both directions, every box of rank rows
+    (3000, 384, 2176, 7, 8, "shuffled"),
+    (2333, 640, 2432, 4, 128, "shuffled"),
+    (2200, 2176, 384, 5, 24, "segments"),
+    (2117, 2432, 640, 3, 64, "shuffled"),
+    (2500, 2304, 2304, 200, 16, "distinct"),     # many entries per block
+]
+# more than 32 token blocks: the weight gradients look at blocks 32 at a time
+MANY_BLOCKS = [  # T, H, N, n, R: one adapter (its tokens split over a cluster) and several
+    (9001, 128, 128, 1, 16),
+    (9001, 128, 128, 10, 24),
+    (8700, 256, 128, 4, 128),
+    (17000, 128, 128, 20, 8),
+]
+
+
+@pytest.mark.parametrize("case", PAIRS, ids=str)
+def test_pairs_of_ctas(case):
+    test_project(case)
+    test_backward(case)
+
+
+@pytest.mark.parametrize("case", MANY_BLOCKS, ids=str)
+def test_gradients_over_many_blocks(case):
+    """Adapters with tokens on both sides of the 32nd block (of up to 256
+    tokens), only before it, only after it, and none."""
+    T, H, N, n, R = case
+    d, dy = make((*case, "none"))
+    g = torch.Generator().manual_seed(T)
+    idx = torch.randint(-1, n, (T,), generator=g) if n == 1 else torch.full((T,), n - 1)
+    if n > 1:
+        idx[:5000] = torch.randint(0, max(1, n // 3), (5000,), generator=g)     # only before
+        idx[3000:3400] = -1
+        idx[T - 300:] = n // 2                                                  # only after
+        if n > 4:
+            idx[100], idx[T - 1] = n // 3 + 1, n // 3 + 1                       # one token on each side
+    d["adapter_idx"] = idx.to(torch.int32)
+    ws = moe.Workspace()
+    got = moe.moe_adapter_project_backward(dy.cuda(), **dev(d), ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    ref, mag = P.backward(dy, *d.values(), magnitudes=True)
+    for key, v in zip(("dx", "dA", "dB"), got):
+        assert_close(v, ref[key], mag[key], key)
+    for a in range(n):
+        if not (idx == a).any():
+            assert (got[1][a] == 0).all() and (got[2][a] == 0).all()
+    y = moe.moe_adapter_project(**dev(d), ws=ws)
+    ref, mag = P.project(*d.values(), magnitudes=True)
+    assert_close(y, ref, mag, "y")

@@ -415,3 +415,108 @@ def test_one_renormalised_slot_has_no_gradient(score):
     idx, w = moe.moe_route_scored(l, 1, cfg)
     assert torch.equal(w, torch.full_like(w, 2.5))
     assert not moe.moe_route_scored_backward(dw, idx, l, cfg).any()
+
+
+DENSE = [  # softmax without renormalisation: 1, 2, 4, 8, 16 and 32 logits per lane
+    (70, 20, 3, "softmax", False, 1, 1, 1, False, 1.0),
+    (300, 64, 6, "softmax", False, 1, 1, 1, False, 1.0),
+    (131, 33, 4, "softmax", True, 1, 1, 1, False, 2.5),
+    (257, 100, 5, "softmax", True, 5, 2, 2, False, 1.0),
+    (90, 128, 8, "softmax", False, 4, 2, 1, False, 1.0),
+    (75, 250, 7, "softmax", True, 10, 4, 2, False, 1.0),
+    (60, 511, 8, "softmax", False, 7, 3, 1, False, 16.0),
+    (50, 1000, 8, "softmax", True, 8, 2, 2, False, 1.0),
+    (33, 1024, 32, "softmax", False, 32, 8, 1, False, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", DENSE, ids=str)
+def test_dense_gradient(case):
+    test_backward(case)
+
+
+MANY_TOKENS = [  # more tokens than the grid takes at once; more than 8 logits per lane but in the last
+    (40001, 160, 6, "softmax", False, 8, 3, 1, False, 16.0),
+    (20011, 250, 12, "sigmoid", True, 10, 4, 2, True, 1.0),
+    (24001, 160, 4, "sigmoid", True, 1, 1, 1, True, 2.5),
+    (6007, 384, 6, "softmax", True, 8, 3, 2, True, 1.0),
+    (2501, 1000, 8, "sigmoid", True, 8, 2, 2, True, 1.0),
+    (12011, 256, 8, "sigmoid", True, 8, 4, 2, True, 2.5),
+]
+
+
+@pytest.mark.parametrize("case", MANY_TOKENS, ids=str)
+def test_route_and_gradient_of_many_tokens(case):
+    """Every warp routes several tokens one after the other.  The choice is
+    checked against the oracle at tokens of every pass, and all of it against
+    the same tokens routed in batches that the grid takes at once."""
+    T, E, k = case[:3]
+    l, b, cfg = make(case)
+    dev_l, dev_b = l.cuda(), None if b is None else b.cuda()
+    ws = moe.Workspace()
+    idx, w = moe.moe_route_scored(dev_l, k, cfg, bias=dev_b, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    rows = torch.arange(0, T, max(1, T // 1500))
+    rows = torch.cat([rows, torch.arange(T - 40, T)]).unique()
+    check((len(rows), *case[1:]), l[rows], b, cfg, idx[rows.cuda()], w[rows.cuda()])
+    for t0 in range(0, T, 1000):
+        part = moe.moe_route_scored(dev_l[t0:t0 + 1000], k, cfg, bias=dev_b)
+        assert torch.equal(part[0], idx[t0:t0 + 1000])
+        torch.testing.assert_close(part[1], w[t0:t0 + 1000], rtol=2.0 ** -20, atol=0)
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(5)).cuda()
+    d = moe.moe_route_scored_backward(dw, idx, dev_l, cfg, bias=dev_b, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    i, wn = to_np(idx[rows.cuda()]), np.abs(to_np(w[rows.cuda()])).astype(np.float64)
+    g = np.abs(to_np(dw[rows.cuda()])).astype(np.float64)
+    bn = None if b is None else b.numpy()
+    score, renorm, scale = case[3], case[8], case[9]
+    ref = S.backward(to_np(dw[rows.cuda()]), l[rows].numpy(), i, bn, score, renorm, scale)
+    size = np.zeros_like(ref)
+    mean = (wn * g).sum(axis=1, keepdims=True) / (scale if renorm else 1.0)
+    np.put_along_axis(size, i.astype(np.int64), wn * (g + mean), axis=1)
+    if score == "softmax" and not renorm:
+        size += S.scores(l[rows].numpy(), score) * mean
+    assert (np.abs(to_np(d[rows.cuda()]) - ref) <= 2.0 ** -18 * size + 1e-30).all()
+
+
+@pytest.mark.parametrize("T", [60, 2100])     # a token per warp, several tokens per warp
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_experts_masked_by_the_lowest_logit(score, T):
+    """Logits of the type's lowest value, which some routers mask with: never
+    chosen while others are left, no weight and no gradient, and finite where a
+    whole row is masked."""
+    low = torch.finfo(torch.float32).min
+    l, _, _ = make((T, 64, 6, score, False, 1, 1, 1, True, 1.0))
+    masked = torch.arange(64) % 4 == 1
+    l[:, masked] = low
+    l[3, :] = low                      # a row whose mask leaves nothing
+    l[5, 4:] = low                     # fewer experts than slots
+    for renorm in (True, False):
+        cfg = moe.RouteConfig(score, 8, 8, 1, renorm)
+        ws = moe.Workspace()
+        idx, w = moe.moe_route_scored(l.cuda(), 6, cfg, ws=ws)
+        assert moe.moe_get_device_status(ws) == 0
+        i, ln = to_np(idx), l.numpy()
+        np.testing.assert_array_equal(i, S.choose(ln, 6, None, score, 8, 8, 1))
+        want = S.weights(ln, i, None, score, renorm, 1.0)
+        dw = torch.randn(T, 6, generator=torch.Generator().manual_seed(5))
+        ref = S.backward(dw.numpy(), ln, i, None, score, renorm, 1.0)
+        if score == "sigmoid" and renorm:
+            # sigmoid(low) is zero in 64 bits too, but the ratio of equal scores
+            # is one: each of the six has a sixth, and 1 - s is one
+            want[3] = 1 / 6
+            g3 = dw[3].double().numpy()
+            np.put(ref[3], i[3], (g3 - g3.mean()) / 6)
+        # as above; the logits that are left are at most 8 apart
+        np.testing.assert_allclose(to_np(w), want, rtol=2.0 ** -18, atol=1e-30)
+        d = to_np(moe.moe_route_scored_backward(dw.cuda(), idx, l.cuda(), cfg, ws=ws))
+        assert moe.moe_get_device_status(ws) == 0 and np.isfinite(d).all()
+        rows = np.delete(np.arange(T), 3)
+        assert (d[rows][:, masked.numpy()] == 0).all()
+        size = np.zeros_like(ref)
+        g = np.abs(dw.numpy()).astype(np.float64)
+        mean = (want * g).sum(axis=1, keepdims=True)
+        np.put_along_axis(size, i.astype(np.int64), want * (g + mean), axis=1)
+        if score == "softmax" and not renorm:
+            size += S.scores(ln, score) * mean
+        assert (np.abs(d - ref) <= 2.0 ** -18 * size + 1e-30).all()
