@@ -452,7 +452,8 @@ moe_status moe_adapter_project_backward(const void* dy, const void* x, const voi
  *   dlogits [T, E] fp32 (softmax Jacobian over the k selected logits;
  *           zero for unselected experts),
  *   dW1, dW3 [E, H, F] bf16, dW2 [E, F, H] bf16 (fp32 accumulation; zero
- *           for experts that received no token).
+ *           for experts that received no token, and so all of it when
+ *           T == 0, where null pointers are left alone).
  * The two calls must use the same ws, sizes, logits and weights, with no
  * other call on that ws in between; moe_backward leaves the saved state
  * intact, so it may be repeated (e.g. for another dout).

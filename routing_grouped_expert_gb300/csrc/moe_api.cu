@@ -686,7 +686,15 @@ moe_status backward_device(const void* dout, const float* router_logits, const v
                            void* dx, float* dlogits, void* dW1, void* dW3, void* dW2, void* ws,
                            size_t ws_bytes, void* stream, const ScoredRoute* scored) {
   if (!ok_sizes(T, H, F, E, k)) return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
+  if (T == 0) {   // no token: zero weight gradients, where there are any
+    for (void* dW : {dW1, dW3, dW2}) {
+      if (dW == nullptr) continue;
+      if (!ok_ptr(dW)) return MOE_ERR_INVALID_ARG;
+      if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+      MOE_TRY(cudaMemsetAsync(dW, 0, (size_t)E * H * F * 2, static_cast<cudaStream_t>(stream)));
+    }
+    return MOE_OK;
+  }
   if (!ok_ptr(dout) || !ok_ptr(router_logits) || !ok_ptr(W1) || !ok_ptr(W3) || !ok_ptr(W2) ||
       !ok_ptr(dx) || !ok_ptr(dlogits) || !ok_ptr(dW1) || !ok_ptr(dW3) || !ok_ptr(dW2))
     return MOE_ERR_INVALID_ARG;

@@ -520,3 +520,24 @@ def test_experts_masked_by_the_lowest_logit(score, T):
         if score == "softmax" and not renorm:
             size += S.scores(ln, score) * mean
         assert (np.abs(d - ref) <= 2.0 ** -18 * size + 1e-30).all()
+
+
+@pytest.mark.parametrize("scored", [False, True])
+def test_layer_gradients_of_an_empty_batch_are_zero(scored):
+    d = I.make_inputs(I.small("tiny", T=32, H=128, F=256, E=8, k=2), "cuda")
+    weights = (d["W1"], d["W3"], d["W2"])
+    empty = d["x"][:0], d["logits"][:0], *weights, 2
+    ws = moe.Workspace()
+    # what the allocator hands out next is not zero
+    leftovers = [torch.full_like(w, float("nan")) for w in (*weights, *weights)]
+    del leftovers
+    if scored:
+        cfg = moe.RouteConfig("sigmoid", 2, 1, 2)
+        moe.moe_forward_scored_train(*empty, cfg, ws)
+        dx, dl, *dW = moe.moe_backward_scored(d["x"][:0], *empty[1:], cfg, ws)
+    else:
+        moe.moe_forward_train(*empty, ws)
+        dx, dl, *dW = moe.moe_backward(d["x"][:0], *empty[1:], ws)
+    assert dx.shape == (0, 128) and dl.shape == (0, 8)
+    for got, w in zip(dW, weights):
+        assert got.shape == w.shape and (got == 0).all()
