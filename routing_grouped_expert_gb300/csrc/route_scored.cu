@@ -556,6 +556,9 @@ route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __rest
     status_report(status, launch, outside ? MOE_ERR_INVALID_ARG : MOE_ERR_NONFINITE);
 }
 
+// Blocks of `per` tokens each; T may be the largest int.
+int blocks_of(int T, int per) { return T / per + (T % per != 0); }
+
 // How a batch is routed: lanes per token, and experts per chunk.
 struct Shape {
   int L, V;
@@ -586,8 +589,7 @@ cudaError_t launch_t(const float* logits, const float* bias, const RouteCfg& c, 
   constexpr int per_warp = 32 / L;
   int warps = kMaxWarps;
   auto grid_of = [&]() {   // as many blocks as the SMs take at once
-    const int per_block = warps * per_warp;
-    const int blocks = (T + per_block - 1) / per_block, most = kBlocks<V * kC> * device_sm_count();
+    const int blocks = blocks_of(T, warps * per_warp), most = kBlocks<V * kC> * device_sm_count();
     return blocks < most ? blocks : most;
   };
   if (c.n_group > 1) {
@@ -703,7 +705,7 @@ cudaError_t launch_route_scored_backward(const float* dw, const int32_t* topk_id
     const cudaError_t err = begin_status(status, s, &launch);
     if (err != cudaSuccess) return err;
   }
-  const int grid = (T + kMaxWarps - 1) / kMaxWarps;
+  const int grid = blocks_of(T, kMaxWarps);
 #define MOE_ROUTE_BWD(n)                                                                       \
   route_scored_backward_kernel<n><<<grid, 32 * kMaxWarps, 0, s>>>(dw, topk_idx, logits, bias, c, T, \
                                                                   E, k, dlogits, status, launch)

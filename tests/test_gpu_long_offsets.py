@@ -72,3 +72,20 @@ def test_adapters(H, N):
     ref, mag = P.backward(dy[at].cpu(), *few, magnitudes=True)
     for key, got in (("dx", dx[at]), ("dA", dA), ("dB", dB)):
         assert_close(got, ref[key], mag[key], key)
+
+
+def test_route_the_most_tokens_that_are_accepted():
+    T = 2 ** 31 - 1                    # T * k < 2^31
+    l = torch.randn(1, device="cuda").expand(T).reshape(T, 1).contiguous()
+    l[-1, 0], l[-2, 0] = 0.5, -1.5
+    cfg = moe.RouteConfig("sigmoid", renormalize=False)
+    ws = moe.Workspace()
+    idx, w = moe.moe_route_scored(l, 1, cfg, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    want = torch.sigmoid(l[[0, 5, T // 2, T - 2, T - 1], 0].double())
+    rows = torch.tensor([0, 5, T // 2, T - 2, T - 1], device="cuda")
+    torch.testing.assert_close(w[rows, 0].double(), want, rtol=2.0 ** -20, atol=0)
+    assert int(idx.max()) == 0 and int(idx.min()) == 0 and torch.equal(w[3], w[T - 3])
+    d = moe.moe_route_scored_backward(torch.ones_like(w), idx, l, cfg, ws=ws)
+    assert moe.moe_get_device_status(ws) == 0
+    torch.testing.assert_close(d[rows, 0].double(), want * (1 - want), rtol=2.0 ** -18, atol=0)
