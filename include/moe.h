@@ -97,7 +97,8 @@ moe_status moe_route_topk(const float* logits, int T, int E, int k,
  *
  * The choice is made in fp32, each operation rounded to nearest (the softmax's
  * sum rounded once); with softmax scores, no bias, one group and renormalize
- * it is moe_route_topk.
+ * it is moe_route_topk.  Weights are within 2^-24 (16 + 2 max |l_e - max l|) of
+ * themselves; renormalised ones are ratios, kept where every score underflows.
  *
  *   logits [T, E] fp32, finite; bias [E] fp32 or null, finite or -inf.  -inf
  *     switches an expert off: it is chosen only where the candidates that are

@@ -7,9 +7,12 @@
 // of Z holds R columns per entry, zero but for the token's own one.  Then
 //   shrink: Z = mask(x [A_a0; A_a1; ..]^T)   one product, masked in its epilogue
 //   expand: y = [x | Z] [W; B_a0; B_a1; ..]  the K loop of x W runs on over Z
-// so the adapters' part is a few more K stages of the projection's own tiles,
-// whatever the order of the tokens: no rows are gathered or scattered, and a
-// block of one request pays for one adapter.  dx = dy W^T + dz A is the same
+// so the adapters' part is more K stages of the projection's own tiles: no rows
+// are gathered or scattered, and a block of one request pays for one adapter.  A
+// block pays for every adapter it meets: few in any order cost little, many in random
+// order cost more than the projection (4096 x 4096 x 4096, rank 16: 90 us with one
+// adapter, 116 with 16 in random order, 304 with 256; rank 64: 986 with 256, 200 when
+// their tokens stand together).  dx = dy W^T + dz A is the same
 // pair of products with the roles of A and B exchanged and W read K-major.
 //   weight gradients: dA_a = dZ_a^T x, dB_a = Z_a^T dy over the blocks that meet a.
 //
@@ -848,7 +851,7 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* st, int lane, int part,
 // Few tiles: a cluster of kS CTAs per tile, each taking a share of the K
 // stages; the partial tiles meet in shared memory and are added in rank order.
 // Bound by reading W while there are few tokens (128 x 6144 x 16384, 128 tiles
-// unsplit: 39 us for the whole call, 5.9 TB/s of its 230 MB, 0.87 of a copy's
+// unsplit: 42 us for the whole call, 5.4 TB/s of its 230 MB, 0.80 of a copy's
 // rate; shrink runs on the SMs that are left), and by the length of a tile's K
 // loop otherwise (777 x 7168 x 2048 and 24 stages of adapters, 64 tiles split in
 // two: 26 us of the call's 44 after shrink; the tensor pipe is busy 42% of it).
@@ -1061,9 +1064,11 @@ adapter_expand_split_kernel(const __grid_constant__ ExpandMaps maps, const Expan
 // four.  Rank 0 issues the MMAs: its `full` counts both CTAs' loads, its `ready`
 // both guards, its acc_empty both epilogues; each CTA's own `loaded` counts what
 // its guard has to pass, and `empty` and acc_full are announced to both.
-// Bound by the tensor cores under the power limit: 4096 x 6144 x 10752 in 314 us,
-// 1.72 PFLOP/s (0.99 of what cuBLAS sustains, 0.88 of its burst rate); the
-// gradient's 8192 x 2048 x 7168 in 139 us, 1.73 PFLOP/s.
+// Bound by the tensor cores: 4096 x 6144 x 10752 in 287 us by itself, 1.89 PFLOP/s
+// (0.97 of cuBLAS's burst rate, tensor pipe 88%), about 300 in calls one after the
+// other, under the power limit; the gradient's 8192 x 2048 x 7168 in 138 us, 1.74
+// PFLOP/s (79%).  With each CTA staging the whole block's rows for an MMA of its own,
+// sent to both, the two calls took 338 and 211 us; they take 320 and 207.
 struct FullCfg {
   static constexpr int kNB = 256;
   static constexpr int kStgBytes = 16 * 32 * 2;            // 16 tokens x 32 features per warp
@@ -1343,13 +1348,16 @@ adapter_expand_kernel(const __grid_constant__ ExpandMaps maps, const ExpandArgs 
 // CTAs in turn; their tiles meet in shared memory and are added in rank order.
 // Both gradients in one launch:
 // dA from (x, dZ), then dB from (dy, Z).  Bound by reading x and dy once more:
-// 8192 tokens, 7168 + 2048 columns, 8 adapters in 40 us by itself, 3.8 TB/s (the
-// 576 CTAs are a round and a quarter of three per SM, of unequal lengths), 33 us
-// of it after expand has ended.
+// 8192 tokens, 7168 + 2048 columns, 8 adapters in 42 us by itself, 3.6 TB/s (the
+// 576 CTAs are a round and a quarter of three per SM, of unequal lengths).  Adapters in
+// random order share most 64-token groups, and each reads those it shares: 4096 x
+// 4096 x 4096, 256 adapters of rank 16, 1.41 ms for the gradient call, 0.36 where
+// their tokens stand together.
 // It may start while the expand launch before it still runs, since nothing that
 // expand writes is read: expand hands shrink's results over (see take_over), and
 // this kernel does not end before expand.  In a captured launch, whose number would
-// be the same in every replay, it waits for the end of expand before it reads.
+// be the same in every replay, it waits for the end of expand before it reads (4 to 5
+// us of a gradient call).
 struct WgradMaps {
   CUtensorMap v[2];   // [T, D] as (64 features, tokens, D / 64)
   CUtensorMap z[2];   // [T, zc], boxes of 64 columns x 64 tokens
@@ -1658,12 +1666,13 @@ int block_rows(int T, int blocks, int step = 16) {
 // down to 0.15 us, a CTA's set-up, first loads and epilogue 6 us, which the
 // persistent CTAs pay once, and joining s partial tiles of 256 tokens 6 + 3 log2 s
 // us.  More blocks are more work for shrink, whose K stages (shrink_k in all) take
-// 0.25 us per unit (777 x 7168 x 2048, 24 adapters of rank 64: 60 us in six blocks
-// of pairs, 44 in four blocks of clusters of two).  Over 370 calls (1 to 8192 tokens, H and N from 512 to 16384, both directions)
-// every form was timed: the choice is 1.7% slower than the best on average, at
-// most 31%; without the join's cost and the limit on clusters of eight it was 6%
-// and 59% (1024 x 2048 x 1024: 20.8 us in clusters of four, 13.1 in pairs; 128 x
-// 7168 x 2048: 30.2 us in clusters of eight, 19.1 in clusters of four).
+// 0.25 us per unit (777 x 7168 x 2048, 24 adapters of rank 64: 70 us in pairs, 44 in
+// four blocks of clusters of two).  Over 379 calls (1 to 8192 tokens, H and N from 512
+// to 16384, both directions) every form was timed: the choice is 1.9% slower than the
+// best on average, at most 33% (1024 x 4096 x 1024, 16 adapters in random order: 29.8 us
+// in pairs, 22.5 in clusters of two); without the join's cost and the limit on clusters
+// of eight it would be 8% and 85% (1024 x 2048 x 1024: 21.2 us in clusters of four, 13.9
+// in pairs; 128 x 7168 x 2048: 27.0 us in clusters of eight, 18.4 in clusters of four).
 ExpandPlan plan_expand(int T, int K, int M, int n, int R, int shrink_k) {
   // sizes are asked for on hosts without a device too: there the count is 1
   const int nk = K / kK, sms = device_sm_count() > 1 ? device_sm_count() : 2;
@@ -1891,10 +1900,10 @@ cudaError_t launch_wgrad(const AdapterSizes& z, const WgradMaps& m, const WgradA
                          cudaStream_t s) {
   // Few units (one adapter trained alone: 72 of them with H 7168, N 2048) are
   // split until there are about two CTAs per SM, with 8 stages or more each.
-  // 8192 tokens, one adapter, the whole gradient call: 221 us unsplit, 200, 194
-  // and 203 us with 2, 4 and 8; two adapters 199, 193, 198 and 209 us; at eight
-  // a split only adds (195 us, 203 with 2).  1000 tokens x 2048 x 1024, one adapter:
-  // 22.6, 22.0, 26.7 and 27.9 us.
+  // 8192 tokens, one adapter, the whole gradient call: 228 us unsplit, 206, 200
+  // and 212 us with 2, 4 and 8; two adapters 206, 202, 207 and 218 us; at eight a split
+  // only adds (200 us, 207 with 2).  1000 tokens x 2048 x 1024, one adapter, replayed
+  // from a graph: 31.5, 27.3, 26.1 and 25.5 us.
   const int units = z.n * ((z.H + z.N) / kM);
   const int groups = (z.T + kK - 1) / kK / z.n;   // of an adapter, on average
   int split = 1;

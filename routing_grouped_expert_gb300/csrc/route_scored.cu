@@ -238,14 +238,17 @@ __device__ __forceinline__ void load_chunk(Tp (&x)[V], const Tp* p, bool global)
 
 // One token per L lanes; lane l holds kC chunks of V experts, chunk q = l + L i
 // being experts V q .. V q + V - 1.  The warps go through the tokens in strides.
-// Bound by instruction issue, not memory (8192 tokens of 256 experts in 8 groups
-// read 8.4 MB, 1.3 us, in 12.3 us; 40001 of 160 25.6 MB, 3.8 us, in 18.5 us, 1.5
-// TB/s; one token of 256: 3.9 us, its chain of steps): so experts go in chunks of four
-// wherever E and the groups allow it (one load, one check and one group index
-// for four), everything but the scores is done on integer keys, a token's
-// candidates are compacted to the kept groups before the selection, and in a
-// large batch one warp routes two or four tokens, which share the instructions
-// of the groups, the rounds and the weights.
+// Bound by the latency of a token's chain of dependent steps and the instructions in
+// it, not by memory: 8192 tokens of 256 experts in 8 groups read 8.4 MB, 1.3 us, in
+// 13.4 us by itself (DRAM 8% busy); the schedulers issue in 61% of their active cycles
+// and 43% of the launch's, with 6 warps each that mostly wait out fixed latencies.  40001
+// of 160: 25.6 MB, 3.8 us, in 20.8 us, 18.5 in calls one after the other, issue 65% and
+// 51%; one token of 256, replayed from a graph: 4.1 us.
+// So experts go in chunks of four wherever E and the groups allow it (one load, one
+// check and one group index for four), everything but the scores is done on integer
+// keys, a token's candidates are compacted to the kept groups before the selection,
+// and in a large batch one warp routes two or four tokens, which share the
+// instructions of the groups, the rounds and the weights.
 template <int V, int kC, int L, bool kGroups>
 __global__ void __launch_bounds__(32 * kMaxWarps, kBlocks<V * kC>)
 route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, RouteCfg c,
@@ -485,11 +488,13 @@ route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ 
 //   sigmoid:                dl_j = scale dw_j s_j (1 - s_j)
 //   softmax, renormalised:  dl_j = scale w_j (dw_j - sum_i w_i dw_i)
 //   softmax (kDense):       dl_e = s_e (scale dw_e - D), D = sum_j scale dw_j s_j
-// The first three are zero at every expert that was not chosen; they are bound
-// by writing dlogits (8192 x 256: 6.1 us, 9.2 MB, 1.5 TB/s into L2).  kDense > 0: that
-// many logits per lane are kept from the first read to the last write (40001 x 64:
-// 11.0 us, 22.4 MB; bound by the latency of one row's steps).  With one slot the
-// renormalised weight is the constant `scale`: its gradient comes out exactly zero.
+// The first three are zero at every expert that was not chosen.  kDense > 0: that
+// many logits per lane are kept from the first read to the last write.  Both are bound
+// by the latency of one row's steps, each warp waiting on loads that depend on one
+// another (8192 x 256: 7.0 us by itself for 9.2 MB, 1.35 at the copy rate; 40001 x 64,
+// dense: 14.2 us, 12.0 in calls one after the other, for 22.4 MB, 3.3; the schedulers
+// issue in 47 and 62% of their active cycles).  With one slot the renormalised weight is
+// the constant `scale`: its gradient comes out exactly zero.
 template <int kDense>
 __global__ void __launch_bounds__(32 * kMaxWarps)
 route_scored_backward_kernel(const float* __restrict__ dw, const int32_t* __restrict__ topk_idx,
@@ -568,7 +573,11 @@ struct Shape {
 // instructions bound, and a warp shares them among as many tokens as can be.
 // One per warp against several, with 2 us of a memset ahead of each: 2048 x
 // 256 in 8 groups 8.2 / 10.3 us, 8192 x 256 16.4 / 14.3, 8192 x 160 13.5 / 9.3,
-// 40001 x 160 39.3 / 20.5, 40001 x 64 26.6 / 14.3.  Chunks of four where neither
+// 40001 x 160 39.3 / 20.5, 40001 x 64 26.6 / 14.3.  Eight lanes hold up to 20 logits
+// each and sixteen up to 16; with more a lane's registers leave one block per SM.  40001
+// tokens by 8, 16 and 32 lanes, memset included: 128 experts in 8 groups 22.8, 28.8 and
+// 39.3 us, 160 35.0, 37.3 and 49.3, 192 55.9, 37.1 and 49.2, 256 67.8, 41.1 and 47.5; without
+// groups 160 25.1, 37.3 and 35.0, 192 35.0, 37.2 and 35.0.  Chunks of four where neither
 // a row nor a group splits one: 40001 x 160 34.6 us by single experts.
 constexpr int kFewTokens = 2048;
 Shape shape_of(int T, int E, int k, int n_group) {
