@@ -54,7 +54,8 @@ typedef enum {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = 1,  /* bad size, null or misaligned pointer       */
   MOE_ERR_NONFINITE = 2,    /* a router logit is NaN or +-inf, a balance bias NaN
-                             or +inf, or an adapter weight either (device) */
+                             or +inf, or an adapter weight or an optimizer's
+                             gradient either (device)                     */
   MOE_ERR_TIMEOUT = 3,      /* a bounded device wait ran out (device)     */
   MOE_ERR_WORKSPACE = 4,    /* ws is NULL, too small or misaligned        */
   MOE_ERR_CUDA = 5,         /* a CUDA runtime call or launch failed       */
@@ -486,6 +487,158 @@ moe_status moe_backward_scored(const void* dout, const float* router_logits, con
                                int T, int H, int F, int E, int k,
                                void* dx, float* dlogits, void* dW1, void* dW3, void* dW2,
                                void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * What a training step runs around the layer.
+ *
+ * Layer norm, ahead of the router and the experts, with the residual add:
+ *   h[t] = x[t] + residual[t], rounded to the tensors' type; x itself without
+ *          a residual
+ *   mean, rstd = 1 / sqrt(var + eps) over the H values of h[t], var their
+ *          variance around the mean (divided by H)
+ *   y[t] = (h[t] - mean) * rstd * weight + bias
+ * x, residual, h, y [T, H] of `type`; weight, bias [H] of `weight_type`; stats
+ * [T, 2] fp32 out: mean and rstd of each token.  bias, residual and stats may
+ * be null; h is written where there is a residual, and null otherwise.  x or
+ * residual may be h (the sum takes its place), and x may be y where there is
+ * no residual.
+ *
+ * The backward, given dy = dL/dy and, where the sum is used past the norm too,
+ * dh = dL/dh [T, H] (or null):
+ *   dx[t] = rstd (w dy - mean(w dy) - xhat mean(w dy xhat)) + dh[t],
+ *           xhat = (h[t] - mean) rstd: the gradient of x and of the residual
+ *   dweight = sum_t dy xhat,  dbias = sum_t dy   (dbias may be null)
+ * dx of `type`, dweight and dbias of `weight_type`.  dx may be dy or dh.  With
+ * T == 0 dweight and dbias are zero.
+ *
+ * Statistics and sums are fp32 in a fixed order; every output is rounded once.
+ * A NaN or infinity spoils its own token, and what is summed over tokens.
+ * type: MOE_BF16 or MOE_F32; weight_type: MOE_F32, or MOE_BF16 beside bf16
+ * tensors.  eps > 0, finite.  1 <= H <= MOE_MAX_NORM_WIDTH; any H is taken,
+ * multiples of 8 by wide accesses.  ws (backward):
+ * moe_layer_norm_workspace_size bytes; the forward takes none.
+ */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+#define MOE_MAX_NORM_WIDTH 16384
+moe_status moe_layer_norm(const void* x, const void* residual, const void* weight,
+                          const void* bias, float eps, int T, int H, int type, int weight_type,
+                          void* y, void* h, float* stats, void* stream);
+size_t moe_layer_norm_workspace_size(int T, int H);
+moe_status moe_layer_norm_backward(const void* dy, const void* h, const float* stats,
+                                   const void* weight, const void* dh, int T, int H, int type,
+                                   int weight_type, void* dx, void* dweight, void* dbias,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The loss that keeps the experts' loads even, and the loads.  The batch holds
+ * S sequences one after the other, tokens seq_offsets[s] .. seq_offsets[s + 1]
+ * - 1 each; a token counts where its mask is not zero.  With n_s counted
+ * tokens in sequence s and c_se of their choices (topk_idx) expert e:
+ *
+ *   p_t = softmax(l_t), or sigmoid(l_t) / sum_i sigmoid(l_ti)
+ *   loss = alpha / S * sum_s sum_e (E c_se / (k n_s)) (sum_t p_te / n_s)
+ *
+ * (alpha where the loads are even); a sequence in which no token counts adds
+ * nothing.  The choices are constants:
+ *
+ *   dlogits_te = dloss * alpha E / (S k n_s^2) * p_te f_te (c_se - sum_i p_ti c_si)
+ *
+ * with f = 1 for softmax and 1 - sigmoid(l_te) for sigmoid.  Tokens that are
+ * masked, or ahead of the first or behind the last sequence, have gradient zero.
+ *
+ *   logits [T, E] fp32; topk_idx [T, k] int32, of any routing;
+ *   score: moe_score;
+ *   seq_offsets [S + 1] int32, ascending, within 0 .. T; null (then S == 1):
+ *     all tokens are one sequence;
+ *   mask [T] bytes, or null: every token counts;
+ *   loss [1] fp32, counts [S, E] int32, tokens [S] int32 (n_s) out.
+ * moe_balance_loss_backward takes counts and tokens as the forward wrote them,
+ * and dloss [1] fp32 on the device (null: 1).  `accumulate`: the gradient is
+ * added onto dlogits [T, E] fp32 (onto the layer's own, say), and rows with
+ * gradient zero are left as they were; otherwise all of dlogits is written.
+ *
+ * Sums are fp32 in a fixed order: results are the same from run to run.  Where
+ * the loads are even the gradient is exactly zero.  The forward reports in the
+ * device status: a logit of a counted token that is not finite
+ * (MOE_ERR_NONFINITE; loss and that row's gradient are then unspecified), a
+ * choice outside [0, E) or offsets that do not ascend within 0 .. T
+ * (MOE_ERR_INVALID_ARG; such a choice is not counted).  Masked tokens' logits
+ * and choices are not looked at.  ws (forward): moe_balance_workspace_size
+ * bytes; the backward takes none.  Limits: 1 <= S <= MOE_MAX_SEQUENCES, alpha
+ * finite.
+ */
+#define MOE_MAX_SEQUENCES 65536
+size_t moe_balance_workspace_size(int T, int E, int S);
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, int score, float alpha,
+                            const int32_t* seq_offsets, const uint8_t* mask, int T, int E, int k,
+                            int S, float* loss, int32_t* counts, int32_t* tokens,
+                            void* ws, size_t ws_bytes, void* stream);
+moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
+                                     const int32_t* tokens, const float* logits, int score,
+                                     float alpha, const int32_t* seq_offsets, const uint8_t* mask,
+                                     int T, int E, int k, int S, int accumulate, float* dlogits,
+                                     void* stream);
+
+/*
+ * One AdamW step over many tensors, in place.  For each element, at step t:
+ *
+ *   g' = grad_scale g
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ *
+ * p is the fp32 master weight where there are masters, and the parameter its
+ * rounding to bf16; otherwise the parameter itself, rounded once.  Arithmetic
+ * is fp32.
+ *
+ * The tensors (param, and grads[i] of tensor i: device pointers, each to n values
+ * one after the other) are listed in host memory, which may be reused after the
+ * call.  Their moments and masters lie in arrays that all of them share, tensor i at
+ * elements start .. start + n - 1, start a multiple of MOE_ADAMW_BLOCK, so that
+ * no block of that many elements belongs to two tensors:
+ *   master         fp32, or null;
+ *   exp_avg        m, fp32 or e4m3 values (state_bits 32 or 8);
+ *   exp_avg_sq     v in fp32, or its square root in e4m3;
+ *   exp_avg_scale, exp_avg_sq_scale   (8 bits) fp32 [one per block]: what the
+ *                  block's e4m3 values are multiplied by.
+ * A block's scale is its largest magnitude over 448 (0 where that is below the
+ * normal fp32 range: the block is then zero), and a value is rounded to the
+ * nearest e4m3 one; the step itself uses m and v before that rounding.  8-bit
+ * arrays hold whole blocks, zero past a tensor's end.  State arrays that are
+ * zero are those of step 0.
+ *
+ * step: the number t of this step (1 for the first); or step_at, device int64,
+ * read when the step runs (so that a captured step can count), where not null.
+ * lr_at: device fp32, in the place of config->lr where not null.  grad_scale:
+ * device fp32, 1 where null (a clipping or unscaling factor).
+ *
+ * An element whose moments would not be finite (a gradient that is NaN or
+ * infinite, or too large to be squared) is left as it was, and
+ * MOE_ERR_NONFINITE is set in the device status: a grad_scale that is not
+ * finite skips the whole step.
+ *
+ * param_type, grad_type: moe_dtype, of all tensors of the call; masters only
+ * beside bf16 parameters.  Tensors and scales are 16-byte aligned, the other
+ * state arrays 32-byte.  No tensor may appear twice.
+ * 0 <= beta < 1, eps > 0, weight_decay, decay and
+ * lr finite, step >= 1 (with step_at it is not looked at).  ws: 256 bytes.
+ */
+#define MOE_ADAMW_BLOCK 256
+typedef struct {
+  void* param;
+  int64_t n;        /* elements                                             */
+  int64_t start;    /* first element in the state arrays                    */
+  double decay;     /* factor on the weight decay (0: none, 1: the config's) */
+} moe_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t state_bits;   /* 32 or 8 */
+} moe_adamw_config;
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, const void* const* grads, int count,
+                          int param_type, int grad_type, const moe_adamw_config* config, int64_t step,
+                          const int64_t* step_at, const float* lr_at, const float* grad_scale,
+                          float* master, void* exp_avg, void* exp_avg_sq, float* exp_avg_scale,
+                          float* exp_avg_sq_scale, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * moe_forward with timing marks: records events[0] on `stream` before the

@@ -74,6 +74,18 @@ SIGNATURES = {
                                  _VP]),
     "moe_adapter_project_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I,
                                           _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_layer_norm": (_I, [_VP, _VP, _VP, _VP, ctypes.c_float, _I, _I, _I, _I, _VP, _VP, _VP,
+                            _VP]),
+    "moe_layer_norm_workspace_size": (_SZ, [_I, _I]),
+    "moe_layer_norm_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP,
+                                     _SZ, _VP]),
+    "moe_balance_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_balance_loss": (_I, [_VP, _VP, _I, ctypes.c_float, _VP, _VP, _I, _I, _I, _I, _VP, _VP,
+                              _VP, _VP, _SZ, _VP]),
+    "moe_balance_loss_backward": (_I, [_VP, _VP, _VP, _VP, _I, ctypes.c_float, _VP, _VP, _I, _I,
+                                       _I, _I, _I, _VP, _VP]),
+    "moe_adamw_step": (_I, [_VP, _VP, _I, _I, _I, _VP, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP,
+                            _VP, _VP, _VP, _VP, _SZ, _VP]),
     "moe_plan_workspace_size": (_SZ, [_I, _I]),
     "moe_plan_replicas": (_I, [_VP, _I, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
 }
@@ -702,6 +714,298 @@ def moe_backward_scored(dout, router_logits, W1, W3, W2, k: int, config: RouteCo
         _p(dx), _p(dl), _p(dW1), _p(dW3), _p(dW2), ws.ptr, ws.nbytes, _stream()),
            "moe_backward_scored")
     return dx, dl, dW1, dW3, dW2
+
+
+# --------------------------------- around the layer in a training step
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return d
+
+
+def _on_current(t: torch.Tensor, *others):
+    """The tensors' device has to be the one whose stream the call runs on."""
+    d = t.get_device()
+    if d != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current CUDA device")
+    for o in others:
+        if o is not None and o.get_device() != d:
+            raise ValueError(f"tensors on {t.device} and {o.device} in one call")
+
+
+def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float = 1e-5,
+                   residual=None, y=None, h=None, stats=None, want_stats: bool = True):
+    """(y [T, H], h, stats [T, 2]): layer norm of h = x + residual, or of x, which
+    is then h.  stats (mean and 1 / std of each token, for the backward) is None
+    unless wanted or given."""
+    T, H = x.shape
+    dt, wt = _dtype(x, "x"), _dtype(weight, "weight")
+    _need(x, x.dtype, (T, H), "x")
+    _need(weight, weight.dtype, (H,), "weight")
+    if dt == 1 and wt == 0:
+        raise TypeError("weight: expected torch.float32 beside float32 tensors")
+    if bias is not None:
+        _need(bias, weight.dtype, (H,), "bias")
+    y = _out(y, x.dtype, (T, H), x, "y")
+    if residual is not None:
+        _need(residual, x.dtype, (T, H), "residual")
+        h = _out(h, x.dtype, (T, H), x, "h")
+    elif h is not None and h is not x:
+        raise ValueError("h: x itself without a residual")
+    if want_stats or stats is not None:
+        stats = _out(stats, torch.float32, (T, 2), x, "stats")
+    _on_current(x, weight, bias, residual, y, h, stats)
+    _check(load_library().moe_layer_norm(_p(x), _p(residual), _p(weight), _p(bias), eps, T, H, dt,
+                                         wt, _p(y), None if residual is None else _p(h), _p(stats),
+                                         _stream()), "moe_layer_norm")
+    return y, x if residual is None else h, stats
+
+
+def moe_layer_norm_workspace_size(T: int, H: int) -> int:
+    return int(load_library().moe_layer_norm_workspace_size(T, H))
+
+
+def moe_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, stats: torch.Tensor,
+                            weight: torch.Tensor, has_bias: bool = True, dh=None, dx=None,
+                            ws: Workspace | None = None):
+    """(dx, dweight, dbias) of moe_layer_norm, given dy and, where h is used past
+    the norm too, its gradient dh; dx is x's and the residual's gradient.  dbias
+    is None unless has_bias."""
+    T, H = dy.shape
+    dt, wt = _dtype(dy, "dy"), _dtype(weight, "weight")
+    _need(dy, dy.dtype, (T, H), "dy")
+    _need(h, dy.dtype, (T, H), "h")
+    _need(stats, torch.float32, (T, 2), "stats")
+    _need(weight, weight.dtype, (H,), "weight")
+    if dt == 1 and wt == 0:
+        raise TypeError("weight: expected torch.float32 beside float32 tensors")
+    if dh is not None:
+        _need(dh, dy.dtype, (T, H), "dh")
+    dx = _out(dx, dy.dtype, (T, H), dy, "dx")
+    _on_current(dy, h, stats, weight, dh, dx)
+    dw = torch.empty_like(weight)
+    db = torch.empty_like(weight) if has_bias else None
+    lib = load_library()
+    buf = _ws(ws, lib.moe_layer_norm_workspace_size(T, H)).buf
+    _check(lib.moe_layer_norm_backward(_p(dy), _p(h), _p(stats), _p(weight), _p(dh), T, H, dt, wt,
+                                       _p(dx), _p(dw), _p(db), _p(buf), buf.numel(), _stream()),
+           "moe_layer_norm_backward")
+    return dx, dw, db
+
+
+def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
+    return int(load_library().moe_balance_workspace_size(T, E, S))
+
+
+def _balance_shape(logits, score, seq_offsets, mask):
+    T, E = logits.shape
+    _need(logits, torch.float32, (T, E), "logits")
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score: expected one of {sorted(ROUTE_SCORES)}, got {score!r}")
+    S = 1
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        _need(seq_offsets, torch.int32, (S + 1,), "seq_offsets")
+    if mask is not None:
+        _need(mask, torch.bool, (T,), "mask")
+    return T, E, S
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
+                     score: str = "softmax", seq_offsets=None, mask=None,
+                     ws: Workspace | None = None):
+    """(loss [], counts [S, E], tokens [S]): the experts' balance loss of the
+    sequences seq_offsets [S + 1] (without: all tokens are one), over the tokens
+    whose mask [T] is set; the choices of each expert and the counted tokens."""
+    T, E, S = _balance_shape(logits, score, seq_offsets, mask)
+    k = topk_idx.shape[1]
+    _need(topk_idx, torch.int32, (T, k), "topk_idx")
+    _on_current(logits, topk_idx, seq_offsets, mask)
+    dev = logits.device
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    tokens = torch.empty((S,), dtype=torch.int32, device=dev)
+    lib = load_library()
+    buf = _ws(ws, lib.moe_balance_workspace_size(T, E, S)).buf
+    _check(lib.moe_balance_loss(_p(logits), _p(topk_idx), ROUTE_SCORES[score], alpha,
+                                _p(seq_offsets), _p(mask), T, E, k, S, _p(loss), _p(counts),
+                                _p(tokens), _p(buf), buf.numel(), _stream()), "moe_balance_loss")
+    return loss, counts, tokens
+
+
+def moe_balance_loss_backward(dloss, counts: torch.Tensor, tokens: torch.Tensor,
+                              logits: torch.Tensor, k: int, alpha: float, score: str = "softmax",
+                              seq_offsets=None, mask=None, onto=None):
+    """dlogits [T, E] of moe_balance_loss, given its counts and tokens and dloss
+    (a device scalar, or None: 1); onto: dlogits to which it is added, in place."""
+    T, E, S = _balance_shape(logits, score, seq_offsets, mask)
+    _need(counts, torch.int32, (S, E), "counts")
+    _need(tokens, torch.int32, (S,), "tokens")
+    if dloss is not None and (dloss.numel() != 1 or dloss.dtype != torch.float32):
+        raise ValueError("dloss: expected one float32 value")
+    dlogits = _out(onto, torch.float32, (T, E), logits, "onto")
+    _on_current(logits, counts, tokens, dloss, seq_offsets, mask, dlogits)
+    _check(load_library().moe_balance_loss_backward(
+        _p(dloss), _p(counts), _p(tokens), _p(logits), ROUTE_SCORES[score], alpha,
+        _p(seq_offsets), _p(mask), T, E, k, S, int(onto is not None), _p(dlogits), _stream()),
+        "moe_balance_loss_backward")
+    return dlogits
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("n", ctypes.c_int64), ("start", ctypes.c_int64),
+                ("decay", ctypes.c_double)]
+
+
+class _AdamWConfigStruct(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("state_bits", ctypes.c_int32)]
+
+
+ADAMW_BLOCK = 256    # elements of a block that shares one scale of an 8-bit moment
+
+
+@dataclass(frozen=True)
+class AdamWConfig:
+    """The factors of an AdamW step (see moe_adamw_step in include/moe.h)."""
+    lr: float = 1e-3
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 1e-2
+
+
+class AdamWState:
+    """The moments of a list of parameters (all bf16 or all fp32, on one device),
+    and their fp32 master weights where wanted: bits is 32 (fp32 moments) or 8
+    (e4m3 in blocks of 256 elements with an fp32 scale each, the second moment as
+    its square root).  decay: a factor on the weight decay for each parameter.
+
+    exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale (8 bits; else None) and
+    master (or None) are flat tensors that hold all parameters' values, each
+    parameter's from a block of its own on: `of(flat, i)` is parameter i's part of
+    a flat one of values.  To save a state, keep these; to load one, copy into
+    them.  The parameters are kept alive and updated where they lie."""
+
+    def __init__(self, params, bits: int = 32, master: bool = False, decay=None):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("params: no tensor given")
+        if bits not in (8, 32):
+            raise ValueError(f"bits: expected 8 or 32, got {bits}")
+        first = self.params[0]
+        self.param_type = _dtype(first, "params[0]")
+        if master and self.param_type == 1:
+            raise ValueError("master: float32 parameters are their own")
+        decay = [1.0] * len(self.params) if decay is None else [float(d) for d in decay]
+        if len(decay) != len(self.params):
+            raise ValueError("decay: one factor for each parameter")
+        self.starts, at, spans = [], 0, []
+        for i, p in enumerate(self.params):
+            _need(p, first.dtype, p.shape, f"params[{i}]")
+            if p.device != first.device:
+                raise ValueError(f"params[{i}]: on {p.device}, not {first.device}")
+            if p.data_ptr() % 16:
+                raise ValueError(f"params[{i}]: must be 16-byte aligned")
+            self.starts.append(at)
+            at += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+            if p.numel():
+                spans.append((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size(), i))
+        spans.sort()
+        for (_, end, i), (begin, _, j) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError(f"params[{min(i, j)}] and params[{max(i, j)}] share memory")
+        self.bits, self.size, dev = bits, at, first.device
+        kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        zeros = lambda n, dtype: torch.zeros(n, dtype=dtype, device=dev)  # noqa: E731
+        self.exp_avg, self.exp_avg_sq = zeros(at, kind), zeros(at, kind)
+        self.exp_avg_scale = self.exp_avg_sq_scale = self.master = None
+        if bits == 8:
+            self.exp_avg_scale = zeros(at // ADAMW_BLOCK, torch.float32)
+            self.exp_avg_sq_scale = zeros(at // ADAMW_BLOCK, torch.float32)
+        if master:
+            self.master = zeros(at, torch.float32)
+            for i, p in enumerate(self.params):
+                self.of(self.master, i).copy_(p)
+        self.decay = tuple(decay)
+        self._bind()
+
+    def _bind(self):
+        """What a step compares with and hands over, for all parameters at once."""
+        first, count = self.params[0], len(self.params)
+        self._shapes = [p.shape for p in self.params]
+        self._ptrs = [p.data_ptr() for p in self.params]
+        self._devices = [first.get_device()] * count
+        self._table = (_AdamWTensor * count)(*[
+            (p.data_ptr(), p.numel(), o, d)
+            for p, o, d in zip(self.params, self.starts, self.decay)])
+        self._grad_table = ctypes.c_void_p * count
+
+    def __getstate__(self):   # copies and pickles have parameters, and places, of their own
+        return {k: v for k, v in self.__dict__.items()
+                if k not in ("_table", "_grad_table", "_ptrs", "_devices", "_shapes")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._bind()
+
+    def of(self, flat: torch.Tensor, i: int) -> torch.Tensor:
+        """Parameter i's part of a flat tensor of this state, in its shape."""
+        p = self.params[i]
+        return flat[self.starts[i]:self.starts[i] + p.numel()].view(p.shape)
+
+
+def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None, grad_scale=None,
+                   ws: Workspace | None = None) -> None:
+    """One AdamW step on the state's parameters, in place, by gradients of their
+    shapes (all bf16 or all fp32).  step: its number (1 for the first), or an
+    int64 tensor of one element that holds it on the device; lr, grad_scale:
+    device scalars, in the place of config.lr and 1."""
+    grads, n = list(grads), len(state.params)
+    if len(grads) != n:
+        raise ValueError(f"grads: {len(grads)} for {n} parameters")
+    gt = _dtype(grads[0], "grads[0]")
+    _on_current(state.exp_avg, lr, grad_scale)
+    # all at once: per tensor it would cost the host more than the step costs the device
+    dtype = grads[0].dtype
+    if ([g.dtype for g in grads] != [dtype] * n or [g.shape for g in grads] != state._shapes or
+            [g.get_device() for g in grads] != state._devices or
+            not all([g.is_contiguous() for g in grads])):
+        for i, (g, shape) in enumerate(zip(grads, state._shapes)):
+            _need(g, dtype, shape, f"grads[{i}]")
+        raise ValueError(f"grads: must be on {state.exp_avg.device}")
+    if [p.data_ptr() for p in state.params] != state._ptrs:
+        raise ValueError("params: one lies elsewhere than where the state was made for it")
+    kind = torch.float32 if state.bits == 32 else torch.float8_e4m3fn
+    for name, dtype, size in (("exp_avg", kind, state.size), ("exp_avg_sq", kind, state.size),
+                              ("exp_avg_scale", torch.float32, state.size // ADAMW_BLOCK),
+                              ("exp_avg_sq_scale", torch.float32, state.size // ADAMW_BLOCK),
+                              ("master", torch.float32, state.size)):
+        t = getattr(state, name)
+        if t is not None:
+            _need(t, dtype, (size,), f"state.{name}")
+    step_at = None
+    if isinstance(step, torch.Tensor):
+        if step.dtype != torch.int64 or step.numel() != 1 or not step.is_cuda:
+            raise ValueError("step: expected an int, or one int64 value on the device")
+        _on_current(step)
+        step_at, step = step, 1
+    for name, t in (("lr", lr), ("grad_scale", grad_scale)):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+            raise ValueError(f"{name}: expected one float32 value")
+    c = _AdamWConfigStruct(config.lr, config.beta1, config.beta2, config.eps, config.weight_decay,
+                           state.bits)
+    buf = _ws(ws, 256).buf
+    _check(load_library().moe_adamw_step(
+        state._table, state._grad_table(*[g.data_ptr() for g in grads]), n, state.param_type, gt,
+        ctypes.byref(c), step, _p(step_at), _p(lr), _p(grad_scale), _p(state.master),
+        _p(state.exp_avg), _p(state.exp_avg_sq), _p(state.exp_avg_scale),
+        _p(state.exp_avg_sq_scale), _p(buf), buf.numel(), _stream()), "moe_adamw_step")
 
 
 def moe_plan_workspace_size(E: int, G: int) -> int:

@@ -851,6 +851,153 @@ moe_status moe_plan_replicas(const int32_t* counts, int E, int G, int beta, int 
                                           static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+bool is_finite(double v) { return v - v == 0.0; }
+bool ok_norm_sizes(int T, int H) { return T >= 0 && H >= 1 && H <= MOE_MAX_NORM_WIDTH; }
+bool ok_norm_types(int type, int weight_type) {
+  return (type == MOE_F32 && weight_type == MOE_F32) ||
+         (type == MOE_BF16 && (weight_type == MOE_F32 || weight_type == MOE_BF16));
+}
+bool ok_balance_sizes(int T, int E, int k, int S, int score, float alpha) {
+  return ok_route_sizes(T, E, k) && S >= 1 && S <= MOE_MAX_SEQUENCES &&
+         (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID) && is_finite(alpha);
+}
+BalanceArgs balance_args(const float* logits, int score, float alpha, const int32_t* seq_offsets,
+                         const uint8_t* mask, int T, int E, int k, int S) {
+  BalanceArgs a{};
+  a.logits = logits;
+  a.seq_offsets = seq_offsets;
+  a.mask = mask;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.S = S;
+  a.softmax = score == MOE_SCORE_SOFTMAX;
+  a.factor = (float)((double)alpha * E / ((double)S * k));
+  return a;
+}
+}  // namespace
+
+moe_status moe_layer_norm(const void* x, const void* residual, const void* weight,
+                          const void* bias, float eps, int T, int H, int type, int weight_type,
+                          void* y, void* h, float* stats, void* stream) {
+  if (!ok_norm_sizes(T, H) || !ok_norm_types(type, weight_type) || !is_finite(eps) || !(eps > 0.f))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(weight) || !ok_ptr(y) || !aligned16(residual) || !aligned16(bias) ||
+      !aligned16(h) || !aligned16(stats) || (residual == nullptr) != (h == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  return cuda_status(launch_norm(x, residual, weight, bias, eps, T, H, type, weight_type, y, h,
+                                 stats, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_layer_norm_workspace_size(int T, int H) {
+  if (!ok_norm_sizes(T, H)) return 0;
+  return kNormHeader + (size_t)norm_backward_blocks(T, H) * 2 * H * sizeof(float);
+}
+
+moe_status moe_layer_norm_backward(const void* dy, const void* h, const float* stats,
+                                   const void* weight, const void* dh, int T, int H, int type,
+                                   int weight_type, void* dx, void* dweight, void* dbias,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  if (!ok_norm_sizes(T, H) || !ok_norm_types(type, weight_type)) return MOE_ERR_INVALID_ARG;
+  if (!ok_ptr(dweight) || !aligned16(dbias)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!ok_ptr(dy) || !ok_ptr(h) || !ok_ptr(stats) || !ok_ptr(weight) || !ok_ptr(dx) ||
+                !aligned16(dh)))
+    return MOE_ERR_INVALID_ARG;
+  if (check_ws(ws, ws_bytes, moe_layer_norm_workspace_size(T, H)) != MOE_OK)
+    return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  return cuda_status(launch_norm_backward(dy, h, stats, weight, dh, T, H, type, weight_type, dx,
+                                          dweight, dbias, ws_ptr<float>(ws, kNormHeader),
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_balance_workspace_size(int T, int E, int S) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || S < 1 || S > MOE_MAX_SEQUENCES) return 0;
+  return balance_layout(T, E, S, nullptr, nullptr);
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, int score, float alpha,
+                            const int32_t* seq_offsets, const uint8_t* mask, int T, int E, int k,
+                            int S, float* loss, int32_t* counts, int32_t* tokens, void* ws,
+                            size_t ws_bytes, void* stream) {
+  if (!ok_balance_sizes(T, E, k, S, score, alpha)) return MOE_ERR_INVALID_ARG;
+  if (!ok_ptr(loss) || !ok_ptr(counts) || !ok_ptr(tokens) || !aligned16(seq_offsets) ||
+      !aligned16(mask) || (seq_offsets == nullptr && S != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!ok_ptr(logits) || !ok_ptr(topk_idx))) return MOE_ERR_INVALID_ARG;
+  if (check_ws(ws, ws_bytes, moe_balance_workspace_size(T, E, S)) != MOE_OK)
+    return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  BalanceArgs a = balance_args(logits, score, alpha, seq_offsets, mask, T, E, k, S);
+  a.topk_idx = topk_idx;
+  a.loss = loss;
+  a.counts = counts;
+  a.tokens = tokens;
+  balance_layout(T, E, S, &a, ws);
+  return cuda_status(launch_balance(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
+                                     const int32_t* tokens, const float* logits, int score,
+                                     float alpha, const int32_t* seq_offsets, const uint8_t* mask,
+                                     int T, int E, int k, int S, int accumulate, float* dlogits,
+                                     void* stream) {
+  if (!ok_balance_sizes(T, E, k, S, score, alpha)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!ok_ptr(counts) || !ok_ptr(tokens) || !ok_ptr(logits) || !ok_ptr(dlogits) ||
+      !aligned16(dloss) || !aligned16(seq_offsets) || !aligned16(mask) ||
+      (seq_offsets == nullptr && S != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  BalanceArgs a = balance_args(logits, score, alpha, seq_offsets, mask, T, E, k, S);
+  balance_layout(T, E, S, &a, nullptr);
+  return cuda_status(launch_balance_backward(a, dloss, counts, tokens, accumulate != 0, dlogits,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, const void* const* grads, int count,
+                          int param_type, int grad_type, const moe_adamw_config* config, int64_t step,
+                          const int64_t* step_at, const float* lr_at, const float* grad_scale,
+                          float* master, void* exp_avg, void* exp_avg_sq, float* exp_avg_scale,
+                          float* exp_avg_sq_scale, void* ws, size_t ws_bytes, void* stream) {
+  const auto type_ok = [](int t) { return t == MOE_BF16 || t == MOE_F32; };
+  if (count < 0 || config == nullptr || (count > 0 && (tensors == nullptr || grads == nullptr)) ||
+      !type_ok(param_type) || !type_ok(grad_type) || (master != nullptr && param_type == MOE_F32))
+    return MOE_ERR_INVALID_ARG;
+  const moe_adamw_config& c = *config;
+  const auto beta_ok = [](double b) { return b >= 0.0 && b < 1.0; };
+  if (!is_finite(c.lr) || !beta_ok(c.beta1) || !beta_ok(c.beta2) || !is_finite(c.eps) ||
+      !(c.eps > 0.0) || !is_finite(c.weight_decay) || (c.state_bits != 32 && c.state_bits != 8) ||
+      (step_at == nullptr && step < 1))
+    return MOE_ERR_INVALID_ARG;
+  const auto aligned32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };
+  if ((reinterpret_cast<uintptr_t>(step_at) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lr_at) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(grad_scale) & 3u) != 0)
+    return MOE_ERR_INVALID_ARG;
+  bool any = false;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.start < 0 || t.start % MOE_ADAMW_BLOCK != 0 ||
+        t.start / MOE_ADAMW_BLOCK > 0xffffffffLL || t.n >= (1LL << 40) || !is_finite(t.decay) ||
+        (t.n > 0 && (!ok_ptr(t.param) || !ok_ptr(grads[i]))))
+      return MOE_ERR_INVALID_ARG;
+    any |= t.n > 0;
+  }
+  if (any && (exp_avg == nullptr || exp_avg_sq == nullptr || !aligned32(exp_avg) ||
+              !aligned32(exp_avg_sq) || !aligned32(master) ||
+              (c.state_bits == 8 && (!ok_ptr(exp_avg_scale) || !ok_ptr(exp_avg_sq_scale)))))
+    return MOE_ERR_INVALID_ARG;
+  if (check_ws(ws, ws_bytes, 256) != MOE_OK) return MOE_ERR_WORKSPACE;
+  if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
+  const AdamwArgs a{tensors, grads, count, config, step, step_at, lr_at, grad_scale, param_type,
+                    grad_type, master, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale};
+  return cuda_status(launch_adamw(a, static_cast<int*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
 moe_status moe_get_device_status(const void* ws, void* stream) {
   if (ws == nullptr) return MOE_ERR_WORKSPACE;
   int word = 0;
@@ -865,7 +1012,7 @@ const char* moe_status_string(moe_status st) {
   switch (st) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID_ARG: return "invalid argument (size, null or misaligned pointer, expert index)";
-    case MOE_ERR_NONFINITE: return "a router logit, balance bias or adapter weight is NaN or infinite";
+    case MOE_ERR_NONFINITE: return "a router logit, balance bias, adapter weight or gradient is NaN or infinite";
     case MOE_ERR_TIMEOUT: return "a bounded device wait ran out";
     case MOE_ERR_WORKSPACE: return "workspace is null, misaligned or too small";
     case MOE_ERR_CUDA: return "a CUDA runtime call or kernel launch failed";

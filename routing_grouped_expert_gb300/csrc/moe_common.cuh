@@ -24,6 +24,8 @@ constexpr int kBlockRows = 128;
 constexpr int kBlockRowsLarge = 256;
 constexpr int kTileM = 128;
 constexpr int kTileK = 64;           // one 128-byte swizzle atom of bf16
+constexpr int kSms = 152;            // of a GB300: launch shapes that a workspace's size follows
+                                     // from do not depend on the device that is current
 constexpr int kRowBox = 32;          // token rows per TMA box of the N operand
 constexpr int kGroupBlocks = 16;     // blocks of one expert rastered together
 
@@ -443,6 +445,60 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
                                     const float* scale, const int32_t* adapter_idx,
                                     __nv_bfloat16* dx, __nv_bfloat16* dA, __nv_bfloat16* dB,
                                     void* ws, cudaStream_t s);
+
+// Layer norm (norm.cu).  type, weight_type: moe_dtype.
+constexpr int kNormHeader = 1024;   // bytes ahead of the shares in the backward's workspace
+int norm_backward_blocks(int rows, int H);
+cudaError_t launch_norm(const void* x, const void* residual, const void* weight, const void* bias,
+                        float eps, int rows, int H, int type, int weight_type, void* y, void* h,
+                        float* stats, cudaStream_t s);
+// part: float[norm_backward_blocks][2][H].  db may be null.
+cudaError_t launch_norm_backward(const void* dy, const void* h, const float* stats,
+                                 const void* weight, const void* dh, int rows, int H, int type,
+                                 int weight_type, void* dx, void* dw, void* db, float* part,
+                                 cudaStream_t s);
+
+// The balance loss (balance.cu).
+struct BalanceArgs {
+  const float* logits;          // [T, E]
+  const int32_t* topk_idx;      // [T, k]
+  const int32_t* seq_offsets;   // [S + 1] or null: one sequence of all tokens
+  const uint8_t* mask;          // [T] or null
+  int T, E, k, S;
+  bool softmax;
+  float factor;                 // alpha E / (S k)
+  int chunk, blocks;            // tokens per block, blocks
+  int* status;                  // workspace: the status word,
+  int* flags;                   // [blocks]  what a block has to report,
+  int* part_n;                  // [blocks + S]  tokens,
+  float* part_p;                // [blocks + S][E]  sums of probabilities,
+  int* part_c;                  // [blocks + S][E]  and counts of a block's part of a sequence
+  float* loss;                  // outputs
+  int32_t* counts;              // [S, E]
+  int32_t* tokens;              // [S]
+};
+// Workspace bytes; fills in the workspace pointers and the launch shape of `a`.
+size_t balance_layout(int T, int E, int S, BalanceArgs* a, void* ws);
+cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s);
+cudaError_t launch_balance_backward(const BalanceArgs& a, const float* dloss, const int32_t* counts,
+                                    const int32_t* tokens, bool onto, float* out, cudaStream_t s);
+
+// AdamW (adamw.cu).
+struct AdamwArgs {
+  const moe_adamw_tensor* tensors;   // host
+  const void* const* grads;          // host
+  int count;
+  const moe_adamw_config* config;    // host
+  int64_t step;
+  const int64_t* step_at;            // device, or null
+  const float* lr_at;                // device, or null
+  const float* grad_scale;           // device, or null
+  int param_type, grad_type;         // moe_dtype
+  float* master;
+  void *exp_avg, *exp_avg_sq;
+  float *exp_avg_scale, *exp_avg_sq_scale;
+};
+cudaError_t launch_adamw(const AdamwArgs& a, int* status, cudaStream_t s);
 
 // bf16 TMA tensor map with a 128-byte swizzle; dims/strides innermost first.
 bool make_tensor_map_bf16(void* map /* CUtensorMap* */, const void* base, int rank,
