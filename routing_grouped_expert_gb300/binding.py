@@ -10,6 +10,7 @@ other; calls that are given one must not overlap on it.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -944,11 +945,10 @@ class AdamWState:
         self._table = (_AdamWTensor * count)(*[
             (p.data_ptr(), p.numel(), o, d)
             for p, o, d in zip(self.params, self.starts, self.decay)])
-        self._grad_table = ctypes.c_void_p * count
 
     def __getstate__(self):   # copies and pickles have parameters, and places, of their own
         return {k: v for k, v in self.__dict__.items()
-                if k not in ("_table", "_grad_table", "_ptrs", "_devices", "_shapes")}
+                if k not in ("_table", "_ptrs", "_devices", "_shapes")}
 
     def __setstate__(self, state):
         self.__dict__.update(state)
@@ -974,13 +974,14 @@ def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None,
     # all at once: per tensor it would cost the host more than the step costs the device
     dtype = grads[0].dtype
     if ([g.dtype for g in grads] != [dtype] * n or [g.shape for g in grads] != state._shapes or
-            [g.get_device() for g in grads] != state._devices or
-            not all([g.is_contiguous() for g in grads])):
+            list(map(torch.Tensor.get_device, grads)) != state._devices or
+            not all(map(torch.Tensor.is_contiguous, grads))):
         for i, (g, shape) in enumerate(zip(grads, state._shapes)):
             _need(g, dtype, shape, f"grads[{i}]")
         raise ValueError(f"grads: must be on {state.exp_avg.device}")
-    if [p.data_ptr() for p in state.params] != state._ptrs:
+    if list(map(torch.Tensor.data_ptr, state.params)) != state._ptrs:
         raise ValueError("params: one lies elsewhere than where the state was made for it")
+    table = array.array("Q", map(torch.Tensor.data_ptr, grads))
     kind = torch.float32 if state.bits == 32 else torch.float8_e4m3fn
     for name, dtype, size in (("exp_avg", kind, state.size), ("exp_avg_sq", kind, state.size),
                               ("exp_avg_scale", torch.float32, state.size // ADAMW_BLOCK),
@@ -1002,7 +1003,7 @@ def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None,
                            state.bits)
     buf = _ws(ws, 256).buf
     _check(load_library().moe_adamw_step(
-        state._table, state._grad_table(*[g.data_ptr() for g in grads]), n, state.param_type, gt,
+        state._table, table.buffer_info()[0], n, state.param_type, gt,
         ctypes.byref(c), step, _p(step_at), _p(lr), _p(grad_scale), _p(state.master),
         _p(state.exp_avg), _p(state.exp_avg_sq), _p(state.exp_avg_scale),
         _p(state.exp_avg_sq_scale), _p(buf), buf.numel(), _stream()), "moe_adamw_step")

@@ -14,6 +14,8 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "moe_common.cuh"
 #include "status.cuh"
 
@@ -22,9 +24,11 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kThreads = 256;
-constexpr int kPerThread = 2;                          // groups of eight elements
-constexpr int kChunk = kThreads * 8 * kPerThread;      // elements per block
+constexpr int kThreads = 128;
+constexpr int kTurns = 2;                   // groups of eight elements per thread
+constexpr int kTurn = kThreads * 8;
+constexpr int kChunk = kTurn * kTurns;     // elements per block
+constexpr int kB8 = 8, kB32 = 4;
 
 struct Entry {
   void* param;
@@ -58,107 +62,259 @@ struct Hyper {
   const float* grad_scale;             // where not null
 };
 
-__device__ __forceinline__ void load8(const bf16* p, float (&f)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __bfloat1622float2(q[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0];
-  const float4 b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_fp8_e4m3* p, float (&f)[8]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? v.x : v.y;
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (i & 1))), __NV_E4M3);
-    const float2 t = __half22float2(__half2(h));
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-__device__ __forceinline__ void store8(bf16* p, const float (&f)[8]) {
+// Eight consecutive values of a type: as they lie in memory, and as four pairs of fp32, on
+// which one instruction works at a time.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<bf16> {
   uint4 v;
-  __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-  *reinterpret_cast<uint4*>(p) = v;
-}
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float (&f)[8]) {
-  uint2 v = make_uint2(0u, 0u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    if (i < 2) v.x |= w << (16 * (i & 1));
-    else v.y |= w << (16 * (i & 1));
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ float2 get(int i) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
   }
-  *reinterpret_cast<uint2*>(p) = v;
-}
-__device__ __forceinline__ float get(const bf16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float get(const float* p) { return *p; }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<__nv_bfloat162&>(w[i]) = __float22bfloat162_rn(f[i]);
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Eight<float> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = reinterpret_cast<const float4*>(p)[0];
+    v[1] = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = v[0];
+    reinterpret_cast<float4*>(p)[1] = v[1];
+  }
+  __device__ __forceinline__ float2 get(int i) const {
+    return i & 1 ? make_float2(v[i / 2].z, v[i / 2].w) : make_float2(v[i / 2].x, v[i / 2].y);
+  }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x, f[2 * i + 1].y);
+  }
+};
+template <>
+struct Eight<__nv_fp8_e4m3> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_fp8_e4m3* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void store(__nv_fp8_e4m3* p) const { *reinterpret_cast<uint2*>(p) = v; }
+  __device__ __forceinline__ float2 get(int i) const {
+    const uint32_t w = (i < 2 ? v.x : v.y) >> (16 * (i & 1));
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3)));
+  }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __nv_cvt_float2_to_fp8x2(f[i], __NV_SATFINITE, __NV_E4M3);
+    v = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  }
+};
+
+__device__ __forceinline__ float one(const bf16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float one(const float* p) { return *p; }
 __device__ __forceinline__ void put(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
-// `left` of the eight elements from p on: all of them by wide accesses.
-template <typename T>
-__device__ __forceinline__ void read8(const T* p, long long left, float (&f)[8]) {
-  if (left >= 8) {
-    load8(p, f);
+// The eight elements from p on, or `left` of them.
+template <bool kAll, typename T>
+__device__ __forceinline__ void read(Eight<T>& e, const T* p, int left) {
+  if constexpr (kAll) {
+    e.load(p);
+  } else if (left >= 8) {
+    e.load(p);
   } else {
+    float2 f[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = j < left ? get(p + j) : 0.f;
+    for (int j = 0; j < 4; ++j)
+      f[j] = make_float2(2 * j < left ? one(p + 2 * j) : 0.f, 2 * j + 1 < left ? one(p + 2 * j + 1) : 0.f);
+    e.set(f);
   }
 }
-template <typename T>
-__device__ __forceinline__ void write8(T* p, long long left, const float (&f)[8]) {
-  if (left >= 8) {
-    store8(p, f);
-  } else {
+template <bool kAll, typename T>
+__device__ __forceinline__ void write(T* p, int left, const float2 (&f)[4]) {
+  if (kAll || left >= 8) {
+    Eight<T> e;
+    e.set(f);
+    e.store(p);
+    return;
+  }
+  if constexpr (!kAll) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) put(p + j, f[j]);
+    for (int j = 0; j < 4; ++j) {
+      if (2 * j < left) put(p + 2 * j, f[j].x);
+      if (2 * j + 1 < left) put(p + 2 * j + 1, f[j].y);
+    }
   }
 }
 
-__device__ __forceinline__ float sqrt_approx(float x) {   // 1 ulp
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// A sum of products, each operation rounded to nearest.  Added one by one: the compiler
+// fuses a pair's addition with the multiplication before it.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
+// The square root, correctly rounded: a Newton step from the reciprocal root, whose last
+// operation rounds a value that is exact to 2^-45 (below the normal range: inexact).
+__device__ __forceinline__ float2 root2(float2 v) {
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 1.17549435e-38f)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 1.17549435e-38f)));
+  const float2 g = __fmul2_rn(v, y), h = __fmul2_rn(y, both(0.5f));
+  const float2 rest = __ffma2_rn(__fmul2_rn(g, both(-1.f)), g, v);
+  return __ffma2_rn(rest, h, g);
+}
+__device__ __forceinline__ float rcp_approx(float x) {   // of normal numbers
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-
-// The largest of eight values of each lane of the warp (none negative).
-__device__ __forceinline__ float block_max(const float (&f)[8]) {
-  float m = fabsf(f[0]);
+// The largest magnitude of the warp's 32 times eight values.
+__device__ __forceinline__ float block_max(const float2 (&f)[4]) {
+  float m = 0.f;
 #pragma unroll
-  for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+  for (int i = 0; i < 4; ++i)
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(f[i].x), "f"(f[i].y));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
-// Scales f so that its largest magnitude, `most` over the block, is 448, and returns what
-// a unit of the result stands for.  Magnitudes that cannot be told from zero become zero.
-__device__ __forceinline__ float to_units(float (&f)[8], float most) {
-  const float scale = most / 448.f;
+// f / scale with scale = `most` / 448, most the block's largest magnitude; returns the
+// scale.  Quotients are correctly rounded (Markstein: with the correctly rounded
+// reciprocal, one correction of the quotient by its remainder).  Blocks whose scale is
+// below the normal range become zero.
+__device__ __forceinline__ float to_units(float2 (&f)[4], float most) {
+  const float scale = __fmul_rn(most, 1.f / 448.f);
   const bool some = scale >= 1.17549435e-38f;
-  const float inv = some ? 1.f / scale : 0.f;
+  const float inv = some ? __frcp_rn(scale) : 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] *= inv;
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = __fmul2_rn(f[i], both(inv));
+    const float2 rest = __ffma2_rn(q, both(-scale), f[i]);
+    f[i] = __ffma2_rn(rest, both(inv), q);
+  }
   return some ? scale : 0.f;
 }
 
 // P, G: types of the parameters and gradients.  k8: 8-bit moments.
+//
+// What an 8-bit moment is rounded to is a function of the inputs: m, v, the root, the scale
+// and the quotient are fp32 with each operation rounded to nearest, none of them fused.
+// Eight elements of a thread, as they lie in memory.
+template <typename P, typename G, bool kMaster, bool k8>
+struct Group {
+  using M = typename std::conditional<k8, __nv_fp8_e4m3, float>::type;
+  using W = typename std::conditional<kMaster, float, P>::type;
+  const G* grad;
+  W* from;
+  P* param;
+  M *ms, *vs;
+  float *m_scale, *v_scale;   // of the warp's block
+  Eight<W> rp;
+  Eight<G> rg;
+  Eight<M> rm, rv;
+  float sm, sv;
+
+  // kWhole: all of the block's elements are there; else `left` of these are.  8-bit arrays
+  // hold whole blocks.
+  template <bool kWhole>
+  __device__ __forceinline__ void load(int left) {
+    read<kWhole>(rg, grad, left);
+    read<k8 || kWhole>(rm, ms, left);
+    read<k8 || kWhole>(rv, vs, left);
+    read<kWhole>(rp, from, left);
+    sm = sv = 1.f;
+    if constexpr (k8) {
+      sm = *m_scale;
+      sv = *v_scale;
+    }
+  }
+  // Their step; returns whether an element was left as it was.
+  template <bool kWhole>
+  __device__ __forceinline__ bool step(int left, float rate, float keep, float root, float gs,
+                                       const Hyper& h);
+};
+
+template <typename P, typename G, bool kMaster, bool k8>
+template <bool kWhole>
+__device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float rate, float keep,
+                                                               float root, float gs,
+                                                               const Hyper& h) {
+  float2 m[4], v[4], p[4];
+  float2 nan = both(0.f);   // turns NaN with the first moment that is not finite
+  // the pairs' moments before and after the step
+  auto old = [&](int i, float2& m, float2& v) {
+    m = rm.get(i);
+    v = rv.get(i);
+    if constexpr (k8) {
+      m = __fmul2_rn(m, both(sm));
+      v = __fmul2_rn(v, both(sv));
+      v = __fmul2_rn(v, v);
+    }
+  };
+  auto moments = [&](int i, float2& m, float2& v) {
+    const float2 g = __fmul2_rn(rg.get(i), both(gs));
+    old(i, m, v);
+    m = add2(__fmul2_rn(m, both(h.b1)), __fmul2_rn(g, both(h.omb1)));
+    v = add2(__fmul2_rn(v, both(h.b2)), __fmul2_rn(__fmul2_rn(g, both(h.omb2)), g));
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    moments(i, m[i], v[i]);
+    nan = __ffma2_rn(m[i], both(0.f), nan);
+    nan = __ffma2_rn(v[i], both(0.f), nan);
+    const float2 r = root2(v[i]);
+    const float2 d = __ffma2_rn(r, both(root), both(h.eps));
+    const float2 s = __fmul2_rn(m[i], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+    p[i] = __ffma2_rn(s, both(rate), __fmul2_rn(rp.get(i), both(keep)));
+    if constexpr (k8) v[i] = r;
+  }
+  const bool bad = isnan(nan.x + nan.y);
+  if (bad) {
+    // rare: elements whose moments are not finite stay as they were.  Read again: kept, the
+    // values would cost every block registers.
+    asm volatile("" ::: "memory");
+    load<kWhole>(left);
+    auto stay = [&](float& p, float& m, float& v, float op, float om, float ov, float nm, float nv) {
+      if (fabsf(nm) < INFINITY && fabsf(nv) < INFINITY) return;
+      p = op;
+      m = om;
+      v = k8 ? root2(both(ov)).x : ov;
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 om, ov, nm, nv;
+      old(i, om, ov);
+      moments(i, nm, nv);
+      const float2 op = rp.get(i);
+      stay(p[i].x, m[i].x, v[i].x, op.x, om.x, ov.x, nm.x, nv.x);
+      stay(p[i].y, m[i].y, v[i].y, op.y, om.y, ov.y, nm.y, nv.y);
+    }
+  }
+  if constexpr (kMaster) write<kWhole>(from, left, p);
+  write<kWhole>(param, left, p);
+  if constexpr (k8) {
+    // v: its roots.  Places past the tensor's end hold zeros and stay so.
+    sm = to_units(m, block_max(m));
+    sv = to_units(v, block_max(v));
+    if ((threadIdx.x & 31) == 0) {
+      *m_scale = sm;
+      *v_scale = sv;
+    }
+  }
+  write<k8 || kWhole>(ms, left, m);
+  write<k8 || kWhole>(vs, left, v);
+  return bad;
+}
+
 template <typename P, typename G, bool kMaster, bool k8, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, k8 ? kB8 : kB32)
 adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* status,
              uint64_t launch) {
   status_begin(status, launch);
@@ -169,9 +325,30 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
     else hi = mid - 1;
   }
   const Entry& t = table.entry[lo];
-  P* param = static_cast<P*>(t.param);
-  const G* grad = static_cast<const G*>(t.grad);
-  const size_t base = (size_t)t.start * MOE_ADAMW_BLOCK;
+  const size_t chunk = blockIdx.x - table.first[lo];
+  const size_t at = chunk * kChunk, state = (size_t)t.start * MOE_ADAMW_BLOCK + at;
+  Group<P, G, kMaster, k8> group[kTurns];
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    const unsigned i = u * kTurn + threadIdx.x * 8;
+    using Gr = Group<P, G, kMaster, k8>;
+    group[u].grad = static_cast<const G*>(t.grad) + at + i;
+    group[u].param = static_cast<P*>(t.param) + at + i;
+    if constexpr (kMaster) group[u].from = st.master + state + i;
+    else group[u].from = group[u].param;
+    group[u].ms = static_cast<typename Gr::M*>(st.m) + state + i;
+    group[u].vs = static_cast<typename Gr::M*>(st.v) + state + i;
+    group[u].m_scale = st.m_scale + (state + i) / MOE_ADAMW_BLOCK;
+    group[u].v_scale = st.v_scale + (state + i) / MOE_ADAMW_BLOCK;
+  }
+  const long long rest = t.n - (long long)at;    // of the tensor, from this block on
+  const bool whole = rest >= kChunk;
+  // everything is on its way before anything is waited for
+  if (whole) {
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) group[u].template load<true>(8);
+  }
+
   const float lr = h.lr_at != nullptr ? __ldg(h.lr_at) : h.lr;
   float inv1 = h.inv1, root = h.root;
   if (h.step != nullptr) {
@@ -179,67 +356,29 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
     inv1 = 1.f / -expm1f(s * h.log_b1);
     root = rsqrtf(-expm1f(s * h.log_b2));
   }
-  const float rate = lr * inv1;
+  const float rate = -lr * inv1, keep = 1.f - lr * t.decay;
   const float gs = h.grad_scale != nullptr ? __ldg(h.grad_scale) : 1.f;
-  const float keep = 1.f - lr * t.decay;
   bool bad = false;
+  if (whole) {
 #pragma unroll
-  for (int u = 0; u < kPerThread; ++u) {
-    const long long at = (long long)(blockIdx.x - table.first[lo]) * kChunk +
-                         (u * kThreads + threadIdx.x) * 8;
-    const long long left = t.n - at;
-    if (k8 ? at - (threadIdx.x & 31) * 8 >= t.n : left <= 0) continue;   // k8: whole warps
-    float p[8], g[8], m[8], v[8];
-    float ms = 0.f, vs = 0.f;
-    const size_t i = base + at, q = i / MOE_ADAMW_BLOCK;
-    read8(grad + at, left, g);
-    if constexpr (kMaster) read8(st.master + i, left, p);
-    else read8(param + at, left, p);
-    if constexpr (k8) {
-      // the state arrays hold whole blocks
-      load8(static_cast<const __nv_fp8_e4m3*>(st.m) + i, m);
-      load8(static_cast<const __nv_fp8_e4m3*>(st.v) + i, v);
-      ms = st.m_scale[q];
-      vs = st.v_scale[q];
-    } else {
-      read8(static_cast<const float*>(st.m) + i, left, m);
-      read8(static_cast<const float*>(st.v) + i, left, v);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (k8) {
-        m[j] *= ms;
-        v[j] *= vs;
-        v[j] *= v[j];
-      }
-      const float x = g[j] * gs;
-      const float nm = fmaf(h.b1, m[j], h.omb1 * x), nv = fmaf(h.b2, v[j], h.omb2 * x * x);
-      const bool fine = fabsf(nm) < INFINITY && nv < INFINITY;
-      const float r = sqrt_approx(nv);
-      const float np = fmaf(p[j], keep, -rate * __fdividef(nm, fmaf(r, root, h.eps)));
-      bad |= !fine;
-      if (fine) {
-        p[j] = np;
-        m[j] = nm;
-        v[j] = nv;
-      }
-      if (k8) v[j] = fine ? r : sqrt_approx(v[j]);
-    }
-    if constexpr (kMaster) write8(st.master + i, left, p);
-    write8(param + at, left, p);
-    if constexpr (k8) {
-      // places past the tensor's end hold zeros and stay so
-      ms = to_units(m, block_max(m));
-      vs = to_units(v, block_max(v));
-      store8(static_cast<__nv_fp8_e4m3*>(st.m) + i, m);
-      store8(static_cast<__nv_fp8_e4m3*>(st.v) + i, v);
-      if ((threadIdx.x & 31) == 0) {
-        st.m_scale[q] = ms;
-        st.v_scale[q] = vs;
-      }
-    } else {
-      write8(static_cast<float*>(st.m) + i, left, m);
-      write8(static_cast<float*>(st.v) + i, left, v);
+    for (int u = 0; u < kTurns; ++u)
+      bad |= group[u].template step<true>(8, rate, keep, root, gs, h);
+  } else {
+#pragma unroll 1
+    for (int u = 0; u < kTurns; ++u) {
+      const int left = (int)rest - u * kTurn - (int)threadIdx.x * 8;
+      // an 8-bit block is worked on by a whole warp
+      if (k8 ? left + (int)(threadIdx.x & 31) * 8 <= 0 : left <= 0) break;
+      Group<P, G, kMaster, k8> part = group[0];
+      part.grad += u * kTurn;
+      part.param += u * kTurn;
+      part.from += u * kTurn;
+      part.ms += u * kTurn;
+      part.vs += u * kTurn;
+      part.m_scale += u * (kTurn / MOE_ADAMW_BLOCK);
+      part.v_scale += u * (kTurn / MOE_ADAMW_BLOCK);
+      part.template load<false>(left);
+      bad |= part.template step<false>(left, rate, keep, root, gs, h);
     }
   }
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0)
