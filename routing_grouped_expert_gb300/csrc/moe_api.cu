@@ -910,7 +910,7 @@ moe_status moe_layer_norm_backward(const void* dy, const void* h, const float* s
     return MOE_ERR_WORKSPACE;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;
   return cuda_status(launch_norm_backward(dy, h, stats, weight, dh, T, H, type, weight_type, dx,
-                                          dweight, dbias, ws_ptr<float>(ws, kNormHeader),
+                                          dweight, dbias, ws,
                                           static_cast<cudaStream_t>(stream)));
 }
 

@@ -447,15 +447,16 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
                                     void* ws, cudaStream_t s);
 
 // Layer norm (norm.cu).  type, weight_type: moe_dtype.
-constexpr int kNormHeader = 1024;   // bytes ahead of the shares in the backward's workspace
+constexpr int kNormHeader = 16384;   // bytes ahead of the shares in the backward's workspace:
+                                    // the status word, then a flag for each block
 int norm_backward_blocks(int rows, int H);
 cudaError_t launch_norm(const void* x, const void* residual, const void* weight, const void* bias,
                         float eps, int rows, int H, int type, int weight_type, void* y, void* h,
                         float* stats, cudaStream_t s);
-// part: float[norm_backward_blocks][2][H].  db may be null.
+// ws: kNormHeader bytes, then float[norm_backward_blocks][2][H].  db may be null.
 cudaError_t launch_norm_backward(const void* dy, const void* h, const float* stats,
                                  const void* weight, const void* dh, int rows, int H, int type,
-                                 int weight_type, void* dx, void* dw, void* db, float* part,
+                                 int weight_type, void* dx, void* dw, void* db, void* ws,
                                  cudaStream_t s);
 
 // The balance loss (balance.cu).
