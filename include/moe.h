@@ -511,7 +511,9 @@ moe_status moe_backward_scored(const void* dout, const float* router_logits, con
  * dx of `type`, dweight and dbias of `weight_type`.  dx may be dy or dh.  With
  * T == 0 dweight and dbias are zero.
  *
- * Statistics and sums are fp32 in a fixed order; every output is rounded once.
+ * Statistics and sums are fp32 in a fixed order, which goes by the sizes and,
+ * where H is no multiple of 8, by the place of a row between 16-byte boundaries;
+ * every output is rounded once.  The backward sets the device status of ws.
  * A NaN or infinity spoils its own token, and what is summed over tokens.
  * type: MOE_BF16 or MOE_F32; weight_type: MOE_F32, or MOE_BF16 beside bf16
  * tensors.  eps > 0, finite.  1 <= H <= MOE_MAX_NORM_WIDTH; any H is taken,
@@ -620,7 +622,7 @@ moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
  * param_type, grad_type: moe_dtype, of all tensors of the call; masters only
  * beside bf16 parameters.  Tensors and scales are 16-byte aligned, the other
  * state arrays 32-byte.  No tensor may appear twice.
- * 0 <= beta < 1, eps > 0, weight_decay, decay and
+ * 0 <= beta < 1, eps a normal fp32 number, weight_decay, decay and
  * lr finite, step >= 1 (with step_at it is not looked at).  ws: 256 bytes.
  */
 #define MOE_ADAMW_BLOCK 256

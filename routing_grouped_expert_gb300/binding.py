@@ -728,14 +728,30 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return d
 
 
-def _on_current(t: torch.Tensor, *others):
-    """The tensors' device has to be the one whose stream the call runs on."""
+def _beside(t: torch.Tensor, dtype, shape, dev: int, name: str):
+    """_need, and on device `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name}: on {t.device}, not on the current CUDA device of the other tensors")
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """A call's device, that of its first tensor: it has to be the current one, on whose
+    stream the call runs, and that of the other tensors."""
     d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name}: must be a CUDA tensor")
     if d != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on {t.device}, which is not the current CUDA device")
-    for o in others:
-        if o is not None and o.get_device() != d:
-            raise ValueError(f"tensors on {t.device} and {o.device} in one call")
+        raise ValueError(f"{name}: on {t.device}, which is not the current CUDA device")
+    return d
+
+
+def _norm_types(x, weight, name):
+    dt, wt = _dtype(x, name), _dtype(weight, "weight")
+    if dt == 1 and wt == 0:
+        raise TypeError("weight: expected torch.float32 beside float32 tensors")
+    return dt, wt
 
 
 def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float = 1e-5,
@@ -743,23 +759,30 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float 
     """(y [T, H], h, stats [T, 2]): layer norm of h = x + residual, or of x, which
     is then h.  stats (mean and 1 / std of each token, for the backward) is None
     unless wanted or given."""
-    T, H = x.shape
-    dt, wt = _dtype(x, "x"), _dtype(weight, "weight")
-    _need(x, x.dtype, (T, H), "x")
-    _need(weight, weight.dtype, (H,), "weight")
-    if dt == 1 and wt == 0:
-        raise TypeError("weight: expected torch.float32 beside float32 tensors")
+    shape, dtype, wtype = x.shape, x.dtype, weight.dtype
+    T, H = shape
+    dt, wt = _norm_types(x, weight, "x")
+    dev = _device_of(x, "x")
+    _beside(x, dtype, shape, dev, "x")
+    _beside(weight, wtype, (H,), dev, "weight")
     if bias is not None:
-        _need(bias, weight.dtype, (H,), "bias")
-    y = _out(y, x.dtype, (T, H), x, "y")
+        _beside(bias, wtype, (H,), dev, "bias")
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _beside(y, dtype, shape, dev, "y")
     if residual is not None:
-        _need(residual, x.dtype, (T, H), "residual")
-        h = _out(h, x.dtype, (T, H), x, "h")
+        _beside(residual, dtype, shape, dev, "residual")
+        if h is None:
+            h = torch.empty_like(x)
+        else:
+            _beside(h, dtype, shape, dev, "h")
     elif h is not None and h is not x:
         raise ValueError("h: x itself without a residual")
-    if want_stats or stats is not None:
-        stats = _out(stats, torch.float32, (T, 2), x, "stats")
-    _on_current(x, weight, bias, residual, y, h, stats)
+    if stats is not None:
+        _beside(stats, torch.float32, (T, 2), dev, "stats")
+    elif want_stats:
+        stats = torch.empty((T, 2), dtype=torch.float32, device=x.device)
     _check(load_library().moe_layer_norm(_p(x), _p(residual), _p(weight), _p(bias), eps, T, H, dt,
                                          wt, _p(y), None if residual is None else _p(h), _p(stats),
                                          _stream()), "moe_layer_norm")
@@ -776,18 +799,20 @@ def moe_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, stats: torch.Tens
     """(dx, dweight, dbias) of moe_layer_norm, given dy and, where h is used past
     the norm too, its gradient dh; dx is x's and the residual's gradient.  dbias
     is None unless has_bias."""
-    T, H = dy.shape
-    dt, wt = _dtype(dy, "dy"), _dtype(weight, "weight")
-    _need(dy, dy.dtype, (T, H), "dy")
-    _need(h, dy.dtype, (T, H), "h")
-    _need(stats, torch.float32, (T, 2), "stats")
-    _need(weight, weight.dtype, (H,), "weight")
-    if dt == 1 and wt == 0:
-        raise TypeError("weight: expected torch.float32 beside float32 tensors")
+    shape, dtype = dy.shape, dy.dtype
+    T, H = shape
+    dt, wt = _norm_types(dy, weight, "dy")
+    dev = _device_of(dy, "dy")
+    _beside(dy, dtype, shape, dev, "dy")
+    _beside(h, dtype, shape, dev, "h")
+    _beside(stats, torch.float32, (T, 2), dev, "stats")
+    _beside(weight, weight.dtype, (H,), dev, "weight")
     if dh is not None:
-        _need(dh, dy.dtype, (T, H), "dh")
-    dx = _out(dx, dy.dtype, (T, H), dy, "dx")
-    _on_current(dy, h, stats, weight, dh, dx)
+        _beside(dh, dtype, shape, dev, "dh")
+    if dx is None:
+        dx = torch.empty_like(dy)
+    else:
+        _beside(dx, dtype, shape, dev, "dx")
     dw = torch.empty_like(weight)
     db = torch.empty_like(weight) if has_bias else None
     lib = load_library()
@@ -803,17 +828,19 @@ def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
 
 
 def _balance_shape(logits, score, seq_offsets, mask):
-    T, E = logits.shape
-    _need(logits, torch.float32, (T, E), "logits")
+    shape = logits.shape
+    T, E = shape
     if score not in ROUTE_SCORES:
         raise ValueError(f"score: expected one of {sorted(ROUTE_SCORES)}, got {score!r}")
+    dev = _device_of(logits, "logits")
+    _beside(logits, torch.float32, shape, dev, "logits")
     S = 1
     if seq_offsets is not None:
         S = seq_offsets.numel() - 1
-        _need(seq_offsets, torch.int32, (S + 1,), "seq_offsets")
+        _beside(seq_offsets, torch.int32, (S + 1,), dev, "seq_offsets")
     if mask is not None:
-        _need(mask, torch.bool, (T,), "mask")
-    return T, E, S
+        _beside(mask, torch.bool, (T,), dev, "mask")
+    return T, E, S, dev
 
 
 def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
@@ -822,14 +849,13 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
     """(loss [], counts [S, E], tokens [S]): the experts' balance loss of the
     sequences seq_offsets [S + 1] (without: all tokens are one), over the tokens
     whose mask [T] is set; the choices of each expert and the counted tokens."""
-    T, E, S = _balance_shape(logits, score, seq_offsets, mask)
+    T, E, S, dev = _balance_shape(logits, score, seq_offsets, mask)
     k = topk_idx.shape[1]
-    _need(topk_idx, torch.int32, (T, k), "topk_idx")
-    _on_current(logits, topk_idx, seq_offsets, mask)
-    dev = logits.device
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    tokens = torch.empty((S,), dtype=torch.int32, device=dev)
+    _beside(topk_idx, torch.int32, (T, k), dev, "topk_idx")
+    device = logits.device
+    loss = torch.empty((), dtype=torch.float32, device=device)
+    counts = torch.empty((S, E), dtype=torch.int32, device=device)
+    tokens = torch.empty((S,), dtype=torch.int32, device=device)
     lib = load_library()
     buf = _ws(ws, lib.moe_balance_workspace_size(T, E, S)).buf
     _check(lib.moe_balance_loss(_p(logits), _p(topk_idx), ROUTE_SCORES[score], alpha,
@@ -843,13 +869,18 @@ def moe_balance_loss_backward(dloss, counts: torch.Tensor, tokens: torch.Tensor,
                               seq_offsets=None, mask=None, onto=None):
     """dlogits [T, E] of moe_balance_loss, given its counts and tokens and dloss
     (a device scalar, or None: 1); onto: dlogits to which it is added, in place."""
-    T, E, S = _balance_shape(logits, score, seq_offsets, mask)
-    _need(counts, torch.int32, (S, E), "counts")
-    _need(tokens, torch.int32, (S,), "tokens")
-    if dloss is not None and (dloss.numel() != 1 or dloss.dtype != torch.float32):
-        raise ValueError("dloss: expected one float32 value")
-    dlogits = _out(onto, torch.float32, (T, E), logits, "onto")
-    _on_current(logits, counts, tokens, dloss, seq_offsets, mask, dlogits)
+    T, E, S, dev = _balance_shape(logits, score, seq_offsets, mask)
+    _beside(counts, torch.int32, (S, E), dev, "counts")
+    _beside(tokens, torch.int32, (S,), dev, "tokens")
+    if dloss is not None:
+        if dloss.numel() != 1:
+            raise ValueError("dloss: expected one float32 value")
+        _beside(dloss, torch.float32, dloss.shape, dev, "dloss")
+    if onto is None:
+        dlogits = torch.empty_like(logits)
+    else:
+        _beside(onto, torch.float32, (T, E), dev, "onto")
+        dlogits = onto
     _check(load_library().moe_balance_loss_backward(
         _p(dloss), _p(counts), _p(tokens), _p(logits), ROUTE_SCORES[score], alpha,
         _p(seq_offsets), _p(mask), T, E, k, S, int(onto is not None), _p(dlogits), _stream()),
@@ -969,8 +1000,7 @@ def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None,
     grads, n = list(grads), len(state.params)
     if len(grads) != n:
         raise ValueError(f"grads: {len(grads)} for {n} parameters")
-    gt = _dtype(grads[0], "grads[0]")
-    _on_current(state.exp_avg, lr, grad_scale)
+    gt, dev = _dtype(grads[0], "grads[0]"), _device_of(state.exp_avg, "state")
     # all at once: per tensor it would cost the host more than the step costs the device
     dtype = grads[0].dtype
     if ([g.dtype for g in grads] != [dtype] * n or [g.shape for g in grads] != state._shapes or
@@ -989,16 +1019,16 @@ def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None,
                               ("master", torch.float32, state.size)):
         t = getattr(state, name)
         if t is not None:
-            _need(t, dtype, (size,), f"state.{name}")
+            _beside(t, dtype, (size,), dev, f"state.{name}")
     step_at = None
     if isinstance(step, torch.Tensor):
-        if step.dtype != torch.int64 or step.numel() != 1 or not step.is_cuda:
+        if step.dtype != torch.int64 or step.numel() != 1 or step.get_device() != dev:
             raise ValueError("step: expected an int, or one int64 value on the device")
-        _on_current(step)
         step_at, step = step, 1
     for name, t in (("lr", lr), ("grad_scale", grad_scale)):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
-            raise ValueError(f"{name}: expected one float32 value")
+        if t is not None and (t.dtype != torch.float32 or t.numel() != 1 or
+                              t.get_device() != dev):
+            raise ValueError(f"{name}: expected one float32 value on the device")
     c = _AdamWConfigStruct(config.lr, config.beta1, config.beta2, config.eps, config.weight_decay,
                            state.bits)
     buf = _ws(ws, 256).buf

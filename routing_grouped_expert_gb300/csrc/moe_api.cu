@@ -970,7 +970,7 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, const void* const* gr
   const moe_adamw_config& c = *config;
   const auto beta_ok = [](double b) { return b >= 0.0 && b < 1.0; };
   if (!is_finite(c.lr) || !beta_ok(c.beta1) || !beta_ok(c.beta2) || !is_finite(c.eps) ||
-      !(c.eps > 0.0) || !is_finite(c.weight_decay) || (c.state_bits != 32 && c.state_bits != 8) ||
+      !(c.eps >= 1.17549435e-38) || !is_finite(c.weight_decay) || (c.state_bits != 32 && c.state_bits != 8) ||
       (step_at == nullptr && step < 1))
     return MOE_ERR_INVALID_ARG;
   const auto aligned32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };

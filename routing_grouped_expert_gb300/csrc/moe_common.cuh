@@ -235,12 +235,21 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// Allows a kernel `smem` bytes of dynamic shared memory; up to 48 KB it has them anyway.
+template <typename... KArgs>
+inline cudaError_t allow_smem(void (*kern)(KArgs...), int smem) {
+  if (smem <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 // ------------------------------------------------------------ launchers
 // Each returns cudaSuccess or the launch error.  All enqueue on `s`; `pdl`
 // launches with programmatic stream serialisation (see above).
 cudaError_t launch_route(const float* logits, int T, int E, int k, int32_t* topk_idx,
                          float* topk_w, int32_t* chunk_hist, int* status, cudaStream_t s);
-// A number no launch before it had, in any process; 0 while `s` is being captured (a
+// A number that no launch before had, in any process.
+uint64_t unique_number();
+// The same for a launch on `s`; 0 while `s` is being captured (a
 // captured launch runs many times under the number it was captured with).
 cudaError_t launch_number(cudaStream_t s, uint64_t* launch);
 // A scored routing's configuration as the kernels take it.
@@ -469,8 +478,12 @@ struct BalanceArgs {
   bool softmax;
   float factor;                 // alpha E / (S k)
   int chunk, blocks;            // tokens per block, blocks
+  int adders, share;            // blocks that add the slots (the last ones), warps that share some
+  uint64_t launch;              // this launch's number, a multiple of 4
   int* status;                  // workspace: the status word,
-  int* flags;                   // [blocks]  what a block has to report,
+  uint64_t* done;               // [blocks + adders]  `launch` from the blocks and adders that are
+                                // done, and in its lowest bits what they have to report,
+  float* shares;                // [adders]  the adders' shares of the loss,
   int* part_n;                  // [blocks + S]  tokens,
   float* part_p;                // [blocks + S][E]  sums of probabilities,
   int* part_c;                  // [blocks + S][E]  and counts of a block's part of a sequence
@@ -480,7 +493,7 @@ struct BalanceArgs {
 };
 // Workspace bytes; fills in the workspace pointers and the launch shape of `a`.
 size_t balance_layout(int T, int E, int S, BalanceArgs* a, void* ws);
-cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s);
+cudaError_t launch_balance(BalanceArgs a, cudaStream_t s);
 cudaError_t launch_balance_backward(const BalanceArgs& a, const float* dloss, const int32_t* counts,
                                     const int32_t* tokens, bool onto, float* out, cudaStream_t s);
 

@@ -269,7 +269,8 @@ norm_kernel(const T* __restrict__ x, const T* __restrict__ residual, const W* __
   s.y = lanes_sum<kLanes>(s.y);
   if constexpr (kBlock) s = join_moments(H, count, u, s, sh);
   else s = make_float2(u + s.x / H, fmaf(-s.x / H, s.x, s.y));
-  const float mean = s.x, rstd = rsqrtf(s.y / H + eps);
+  // rounding may leave a constant row a little below zero
+  const float mean = s.x, rstd = rsqrtf((s.y < 0.f ? 0.f : s.y / H) + eps);
   if (t.me == 0 && there && stats != nullptr) stats[row] = make_float2(mean, rstd);
 #pragma unroll
   for (int i = 0; i < n; ++i) {
@@ -636,8 +637,7 @@ cudaError_t backward_t(const void* dy, const void* h, const float* stats, const 
     const auto kern = norm_backward_ring_kernel<T, W, f.n, kVec, team, f.per>;                    \
     int stages = ring_bytes(f.per) / stage;                                                       \
     stages = stages < kMaxStages ? stages : kMaxStages;                                           \
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                                               stages * stage);                                   \
+    const cudaError_t e = allow_smem(kern, stages * stage);                                       \
     if (e != cudaSuccess) return e;                                                               \
     kern<<<blocks, team_of(H, f.n), stages * stage, s>>>(gt, ht, st, wt, rt, rows, H, stages, xt, part, \
                                                          flags);                                  \

@@ -618,13 +618,16 @@ RouteCfg make_route_cfg(const moe_route_config& a, int E) {
 }
 
 // From the clock on, so that no number an earlier process left in memory comes again.
-cudaError_t launch_number(cudaStream_t s, uint64_t* launch) {
+uint64_t unique_number() {
   static std::atomic<uint64_t> n{
       (uint64_t)std::chrono::system_clock::now().time_since_epoch().count() | 1};
+  return n.fetch_add(2, std::memory_order_relaxed);
+}
+cudaError_t launch_number(cudaStream_t s, uint64_t* launch) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   const cudaError_t err = cudaStreamIsCapturing(s, &cs);
   *launch = err == cudaSuccess && cs == cudaStreamCaptureStatusNone
-                ? n.fetch_add(2, std::memory_order_relaxed)
+                ? unique_number()
                 : 0;
   return err;
 }
