@@ -555,7 +555,7 @@ moe_status moe_layer_norm_backward(const void* dy, const void* h, const float* s
  *   mask [T] bytes, or null: every token counts;
  *   loss [1] fp32, counts [S, E] int32, tokens [S] int32 (n_s) out.
  * moe_balance_loss_backward takes counts and tokens as the forward wrote them,
- * and dloss [1] fp32 on the device (null: 1).  `accumulate`: the gradient is
+ * and dloss [1] fp32 on the device (null: 1; 4-byte aligned).  `accumulate`: the gradient is
  * added onto dlogits [T, E] fp32 (onto the layer's own, say), and rows with
  * gradient zero are left as they were; otherwise all of dlogits is written.
  *
@@ -566,7 +566,8 @@ moe_status moe_layer_norm_backward(const void* dy, const void* h, const float* s
  * choice outside [0, E) or offsets that do not ascend within 0 .. T
  * (MOE_ERR_INVALID_ARG; such a choice is not counted).  Masked tokens' logits
  * and choices are not looked at.  ws (forward): moe_balance_workspace_size
- * bytes; the backward takes none.  Limits: 1 <= S <= MOE_MAX_SEQUENCES, alpha
+ * bytes, about 8 E for each sequence and each block of up to T / 304 tokens; the
+ * backward takes none.  Limits: 1 <= S <= MOE_MAX_SEQUENCES, alpha
  * finite.
  */
 #define MOE_MAX_SEQUENCES 65536
@@ -610,7 +611,8 @@ moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
  * zero are those of step 0.
  *
  * step: the number t of this step (1 for the first); or step_at, device int64,
- * read when the step runs (so that a captured step can count), where not null.
+ * read when the step runs (so that a captured step can count; below 1 it counts
+ * as 1), where not null.
  * lr_at: device fp32, in the place of config->lr where not null.  grad_scale:
  * device fp32, 1 where null (a clipping or unscaling factor).
  *

@@ -352,7 +352,7 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
   const float lr = h.lr_at != nullptr ? __ldg(h.lr_at) : h.lr;
   float inv1 = h.inv1, root = h.root;
   if (h.step != nullptr) {
-    const float s = (float)__ldg(h.step);
+    const float s = fmaxf((float)__ldg(h.step), 1.f);
     inv1 = 1.f / -expm1f(s * h.log_b1);
     root = rsqrtf(-expm1f(s * h.log_b2));
   }

@@ -948,7 +948,7 @@ moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
   if (!ok_balance_sizes(T, E, k, S, score, alpha)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!ok_ptr(counts) || !ok_ptr(tokens) || !ok_ptr(logits) || !ok_ptr(dlogits) ||
-      !aligned16(dloss) || !aligned16(seq_offsets) || !aligned16(mask) ||
+      (reinterpret_cast<uintptr_t>(dloss) & 3u) != 0 || !aligned16(seq_offsets) || !aligned16(mask) ||
       (seq_offsets == nullptr && S != 1))
     return MOE_ERR_INVALID_ARG;
   if (!device_is_sm103()) return MOE_ERR_UNSUPPORTED;

@@ -149,6 +149,33 @@ def test_device_scalars_and_a_captured_step(bits):
         torch.testing.assert_close(a, b, rtol=2 ** -6, atol=1e-3)
 
 
+def test_a_captured_step_of_many_tensors():
+    """More tensors than one launch takes, replayed: the bits of the same steps called."""
+    sizes = [1 + 37 * (i % 9) for i in range(600)]
+    c = moe.AdamWConfig(lr=0.01)
+    sets = [make(sizes, BF, F32, 8, True) for _ in range(2)]
+    (a, ga, _), (b, gb, _) = sets
+    steps = [torch.full((1,), t, device="cuda") for t in (1, 2, 3)]
+    at = steps[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_adamw_step(a, ga, c, at)
+    for t in steps:
+        at.copy_(t)
+        graph.replay()
+        moe.moe_adamw_step(b, gb, c, t)
+    torch.cuda.synchronize()
+    for x, y in ((a.master, b.master), (a.exp_avg, b.exp_avg), (a.exp_avg_sq, b.exp_avg_sq),
+                 (a.exp_avg_scale, b.exp_avg_scale)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert all(torch.equal(x, y) for x, y in zip(a.params, b.params))
+    # a number below 1 counts as 1
+    (a, ga, _), (b, gb, _) = [make([300], F32, F32, 32, False) for _ in range(2)]
+    moe.moe_adamw_step(a, ga, c, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    moe.moe_adamw_step(b, gb, c, torch.ones(1, dtype=torch.int64, device="cuda"))
+    assert torch.equal(a.params[0], b.params[0])
+
+
 def test_long_run_of_steps_is_torchs():
     """fp32 parameters and moments: a hundred steps beside torch's own optimizer."""
     g = torch.Generator(device="cuda").manual_seed(1)

@@ -89,7 +89,11 @@ def check(case, l, idx, kw, rows=slice(None)):
         off[rows] = False
     assert (got.cpu().numpy()[off] == 0).all()
     assert torch.equal(onto.cpu()[off], base[off])
-    # None stands for 1, and 2 dloss for twice the gradient, bit for bit
+    # None stands for 1, a gradient may lie anywhere,
+    inside = moe.moe_balance_loss_backward(torch.full((4,), 1.75, device="cuda")[1], counts, tokens,
+                                           l.cuda(), k, ALPHA, **dev)
+    assert torch.equal(inside, got)
+    # and 2 dloss for twice the gradient, bit for bit
     one = moe.moe_balance_loss_backward(None, counts, tokens, l.cuda(), k, ALPHA, **dev)
     two = moe.moe_balance_loss_backward(torch.tensor([2.0], device="cuda"), counts, tokens,
                                         l.cuda(), k, ALPHA, **dev)

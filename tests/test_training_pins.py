@@ -159,7 +159,7 @@ def test_balance_refuses():
         assert call(**bad) == WS, bad
     good = dict(d=P, c=P, n=P, l=P, sc=0, al=0.1, o=P, m=P, T=4, E=8, k=2, S=3, acc=0, out=P)
     call = lambda **kw: lib.moe_balance_loss_backward(*{**good, **kw}.values(), None)  # noqa: E731
-    for bad in (dict(d=ODD), dict(c=None), dict(n=None), dict(l=None), dict(sc=-1), dict(o=None),
+    for bad in (dict(d=ctypes.c_void_p(4098)), dict(c=None), dict(n=None), dict(l=None), dict(sc=-1), dict(o=None),
                 dict(m=ODD), dict(S=0), dict(k=33, E=64), dict(out=None)):
         assert call(**bad) == INVALID, bad
     assert call(T=0, c=None, n=None, l=None, out=None) == OK
