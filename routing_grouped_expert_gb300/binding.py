@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -789,6 +790,7 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float 
     return y, x if residual is None else h, stats
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_layer_norm_workspace_size(T: int, H: int) -> int:
     return int(load_library().moe_layer_norm_workspace_size(T, H))
 
@@ -815,14 +817,14 @@ def moe_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, stats: torch.Tens
         _beside(dx, dtype, shape, dev, "dx")
     dw = torch.empty_like(weight)
     db = torch.empty_like(weight) if has_bias else None
-    lib = load_library()
-    buf = _ws(ws, lib.moe_layer_norm_workspace_size(T, H)).buf
-    _check(lib.moe_layer_norm_backward(_p(dy), _p(h), _p(stats), _p(weight), _p(dh), T, H, dt, wt,
-                                       _p(dx), _p(dw), _p(db), _p(buf), buf.numel(), _stream()),
-           "moe_layer_norm_backward")
+    buf = _ws(ws, moe_layer_norm_workspace_size(T, H)).buf
+    _check(load_library().moe_layer_norm_backward(
+        _p(dy), _p(h), _p(stats), _p(weight), _p(dh), T, H, dt, wt, _p(dx), _p(dw), _p(db),
+        _p(buf), buf.numel(), _stream()), "moe_layer_norm_backward")
     return dx, dw, db
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
     return int(load_library().moe_balance_workspace_size(T, E, S))
 
@@ -856,11 +858,10 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
     loss = torch.empty((), dtype=torch.float32, device=device)
     counts = torch.empty((S, E), dtype=torch.int32, device=device)
     tokens = torch.empty((S,), dtype=torch.int32, device=device)
-    lib = load_library()
-    buf = _ws(ws, lib.moe_balance_workspace_size(T, E, S)).buf
-    _check(lib.moe_balance_loss(_p(logits), _p(topk_idx), ROUTE_SCORES[score], alpha,
-                                _p(seq_offsets), _p(mask), T, E, k, S, _p(loss), _p(counts),
-                                _p(tokens), _p(buf), buf.numel(), _stream()), "moe_balance_loss")
+    buf = _ws(ws, moe_balance_workspace_size(T, E, S)).buf
+    _check(load_library().moe_balance_loss(
+        _p(logits), _p(topk_idx), ROUTE_SCORES[score], alpha, _p(seq_offsets), _p(mask), T, E, k, S,
+        _p(loss), _p(counts), _p(tokens), _p(buf), buf.numel(), _stream()), "moe_balance_loss")
     return loss, counts, tokens
 
 
