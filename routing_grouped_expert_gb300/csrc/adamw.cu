@@ -9,8 +9,16 @@
 // which halves the range its exponents have to span.  The step itself uses m and v before
 // they are rounded.
 //
-// Bound by memory: every array is read and written once.  The tensors' table is a kernel
-// argument, so a call makes no copy and keeps nothing on the device.
+// Every array is read and written once, which bounds it: 704 M bf16 parameters in 2.77 ms
+// with fp32 moments and masters (19.7 GB, 1.05 of the rate of a plain copy) and in 1.15 ms
+// with 8-bit moments (7.1 GB, 0.91; the schedulers issue in two thirds of their cycles).
+// 150 ragged tensors of 15.3 M parameters: 68 us (0.93) and, gradients in fp32, 62 us.
+//
+// Blocks of 2048 elements in launch order: what is in flight then lies close together in
+// each array.  A block that went on to further chunks, with its loads ahead in registers or
+// in a ring of shared memory, was slower for that reason: fp32 moments 2.76 -> 2.91 and
+// 4.24 ms, 8-bit ones 1.42 -> 2.24 and 1.47 at the same point.  The tensors' table is a
+// kernel argument, so a call makes no copy and keeps nothing on the device.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -24,11 +32,14 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
+// Groups of eight elements per thread, all on their way at once, and blocks per SM.  8-bit
+// moments, ms: 128 threads of one group 1.27, of two 1.13 (8 blocks) 1.16 (6) 1.25 (5), of
+// three 1.20; 256 threads of one 1.33; 64 of two 1.15.  fp32 moments: 2.76 to 2.77 in all.
 constexpr int kThreads = 128;
-constexpr int kTurns = 2;                   // groups of eight elements per thread
+constexpr int kTurns = 2;
 constexpr int kTurn = kThreads * 8;
 constexpr int kChunk = kTurn * kTurns;     // elements per block
-constexpr int kB8 = 8, kB32 = 4;
+constexpr int kB8 = 8, kB32 = 4;     // for 8-bit and fp32 moments
 
 struct Entry {
   void* param;
@@ -202,11 +213,11 @@ __device__ __forceinline__ float to_units(float2 (&f)[4], float most) {
   return some ? scale : 0.f;
 }
 
-// P, G: types of the parameters and gradients.  k8: 8-bit moments.
+// Eight elements of a thread, as they lie in memory.  P, G: types of the parameters and
+// gradients.  k8: 8-bit moments.
 //
 // What an 8-bit moment is rounded to is a function of the inputs: m, v, the root, the scale
 // and the quotient are fp32 with each operation rounded to nearest, none of them fused.
-// Eight elements of a thread, as they lie in memory.
 template <typename P, typename G, bool kMaster, bool k8>
 struct Group {
   using M = typename std::conditional<k8, __nv_fp8_e4m3, float>::type;

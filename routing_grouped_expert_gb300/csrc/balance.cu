@@ -18,6 +18,14 @@
 // the last ones wait for all of them, the very last for the others' sums.  Blocks start in
 // order, so a block that waits holds up none that it waits for; waits are bounded all the
 // same.  No atomics on floats: results are the same from run to run.
+//
+// 40001 x 256 logits: 17.7 us in one sequence, 22.7 in 24 with a mask (42 MB, 6.2 us at the
+// rate of a plain copy).  Of a call's time, rows are done after 11 us (median; memory from a
+// cold start), announced by 14, the slots added by 17.4: the last part is a chain of loads
+// through L2, each waiting for the one before.  131072 x 256: 35.5 us (0.57).  One token: 6.3.
+// Two launches, the second one cluster: 24 and 33 us.
+// The gradient: 40001 x 256 in 13.7 us (0.88), onto dlogits, 24 sequences, 22.5 (0.80),
+// 131072 x 256 in 47.9 (0.83); 8192 x 64 in 3.5, latency.
 #include <math.h>
 
 #include "moe_common.cuh"
@@ -27,7 +35,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMinChunk = 64, kPerSm = 2, kRound = 4;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // Over the L lanes of a row, for R rows at once.
@@ -455,7 +462,7 @@ __device__ __forceinline__ float add_slots(const BalanceArgs& a, int rank, Balan
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads, S::n <= 8 ? kPerSm : S::n <= 16 ? 2 : 1) balance_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(BalanceArgs a) {
   __shared__ BalanceShared sh;
   extern __shared__ float sums[];   // [kWarps * 32 / L][E]
   const int block = blockIdx.x, blocks = a.blocks;
@@ -626,9 +633,11 @@ balance_backward_kernel(BalanceArgs a, const float* __restrict__ dloss,
   if (at < end) rows(-1, at, end);
 }
 
-// Tokens per block: two blocks for each SM where there are many.
+// Tokens per block: two blocks for each SM where there are many (three: 40001 x 256 23.6 us
+// in the place of 20.6), at least 64 (8192 x 256 12.6 us, and 13.7 from 16 on).
+constexpr int kMinChunk = 64, kRound = 4;
 int chunk_of(int T) {
-  const long long c = ((long long)T + kPerSm * kSms - 1) / (kPerSm * kSms);
+  const long long c = ((long long)T + 2 * kSms - 1) / (2 * kSms);
   return (int)(c < kMinChunk ? kMinChunk : (c + kRound - 1) / kRound * kRound);
 }
 // Warps that share a sequence's 32 experts, each adding up to 20 of their slots, and the

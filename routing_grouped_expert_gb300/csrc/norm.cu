@@ -7,6 +7,11 @@
 // A row is held in registers between its statistics and its output, so memory is read once;
 // the variance is taken around the mean (a second pass over the registers), not as a
 // difference of two large sums.  Sums are fp32 in a fixed order.
+//
+// Bound by memory: 8192 x 7168 bf16 with a residual in 71.0 us (470 MB, 0.98 of the rate of a
+// plain copy; DRAM read 235 MB), 12000 x 4096 in 58.5 (0.99), 40001 x 512 in 25.9 (0.93),
+// without a residual 47 (0.73: half the bytes in flight).  Rows of 7170 113 us (0.61): their
+// weights are taken one by one.
 #include "norm.cuh"
 
 namespace moe {
@@ -130,7 +135,7 @@ norm_kernel(const T* __restrict__ x, const T* __restrict__ residual, const W* __
   }
 }
 
-constexpr int kFewRows = kSms;
+constexpr int kFewRows = kSms;   // up to here a row has as many threads as it can use: one row 2.6 us
 template <typename T, typename W, bool kVec, bool kResidual>
 cudaError_t forward_r(const T* x, const T* residual, const W* weight, const W* bias, float eps,
                       int rows, int H, T* y, T* h, float2* stats, cudaStream_t s) {
@@ -140,6 +145,10 @@ cudaError_t forward_r(const T* x, const T* residual, const W* weight, const W* b
 #define MOE_NORM_BLOCK(n, team, per)                                                              \
   norm_kernel<T, W, n, kVec, kResidual, 0, team, per><<<rows, team_of(H, n), 0, s>>>(             \
       x, residual, weight, bias, eps, rows, H, y, h, stats)
+  // Few threads with several groups each, which are on their way at once, and few rows: all
+  // of an SM's threads on one, for the shortest time.  us, threads x groups: 8192 x 7168 with a
+  // residual 896 x 1 158, 448 x 2 83, 224 x 4 71; without 224 x 4 47, 128 x 8 49; 20000 x
+  // 2048 without 256 x 1 43, 64 x 4 32; 200000 x 128 16 x 1 38, 8 x 2 32.
   const int groups = groups_of(H);
   if (groups <= 16) MOE_NORM_WARP(2, 8);
   else if (groups <= 32) MOE_NORM_WARP(2, 16);
