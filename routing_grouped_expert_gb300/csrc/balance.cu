@@ -13,18 +13,19 @@
 //
 // Forward: blocks of consecutive tokens sum p in registers and count choices in shared
 // memory; each (block, sequence) pair that meets has a slot of its own, number block +
-// sequence (pairs that meet lie on a staircase, so their numbers differ).  The last blocks
-// then add the slots in order: a block announces its slots by the launch's own number, and
-// the last ones wait for all of them, the very last for the others' sums.  Blocks start in
-// order, so a block that waits holds up none that it waits for; waits are bounded all the
-// same.  No atomics on floats: results are the same from run to run.
+// sequence (pairs that meet lie on a staircase, so their numbers differ).  More blocks behind
+// those then add the slots in order: a block announces its slots by the launch's own number,
+// and the adding ones wait for all of them, the very last for the others' sums.  Blocks
+// start in order, and a block waits only for blocks before it, which are running or done by
+// then: it holds up none that it waits for, however few blocks fit the SMs beside other
+// work.  Waits are bounded all the same.  No atomics on floats: results are the same from run to run.
 //
-// 40001 x 256 logits: 17.7 us in one sequence, 22.7 in 24 with a mask (42 MB, 6.2 us at the
+// 40001 x 256 logits: 18.5 us in one sequence, 23.7 in 24 with a mask (42 MB, 6.2 us at the
 // rate of a plain copy).  Of a call's time, rows are done after 11 us (median; memory from a
 // cold start), announced by 14, the slots added by 17.4: the last part is a chain of loads
 // through L2, each waiting for the one before.  131072 x 256: 35.5 us (0.57).  One token: 6.3.
 // Two launches, the second one cluster: 24 and 33 us.
-// The gradient: 40001 x 256 in 13.7 us (0.88), onto dlogits, 24 sequences, 22.5 (0.80),
+// The gradient: 40001 x 256 in 13.9 us (0.87), onto dlogits, 24 sequences, 22.5 (0.80),
 // 131072 x 256 in 47.9 (0.83); 8192 x 64 in 3.5, latency.
 #include <math.h>
 
@@ -466,13 +467,13 @@ __global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(B
   __shared__ BalanceShared sh;
   extern __shared__ float sums[];   // [kWarps * 32 / L][E]
   const int block = blockIdx.x, blocks = a.blocks;
-  if (block < blocks) sum_tokens<S>(a, block, sh, sums);   // a batch of no token has one block
-  // the threads' slots, seen by this one past a barrier, are released with the word
-  if (threadIdx.x == 0 && block < blocks) {
-    announce(a.done + block, a.launch | (uint64_t)sh.bad);
+  if (block < blocks) {
+    sum_tokens<S>(a, block, sh, sums);
+    // the threads' slots, seen by this one past a barrier, are released with the word
+    if (threadIdx.x == 0) announce(a.done + block, a.launch | (uint64_t)sh.bad);
+    return;
   }
-  const int rank = block - ((int)gridDim.x - a.adders);
-  if (rank < 0) return;
+  const int rank = block - blocks;
   const bool last = rank == a.adders - 1;
   int bad = 0;   // 1: not finite, 2: outside, 4: late
   if (last && a.seq_offsets != nullptr)
@@ -641,7 +642,7 @@ int chunk_of(int T) {
   return (int)(c < kMinChunk ? kMinChunk : (c + kRound - 1) / kRound * kRound);
 }
 // Warps that share a sequence's 32 experts, each adding up to 20 of their slots, and the
-// blocks that this takes, half of all at most.
+// blocks that this takes, half as many as sum tokens at most.
 int share_of(int blocks, int S) {
   int share = 1;
   while (share < kWarps && 20 * share < blocks / S + 1) share *= 2;
@@ -705,7 +706,7 @@ cudaError_t launch_sum(const BalanceArgs& a, cudaStream_t s) {
   const int smem = kWarps * (32 / S::L) * a.E * 4;
   const cudaError_t e = allow_smem(balance_kernel<S>, smem);
   if (e != cudaSuccess) return e;
-  balance_kernel<S><<<a.blocks > 0 ? a.blocks : 1, kThreads, smem, s>>>(a);
+  balance_kernel<S><<<a.blocks + a.adders, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 cudaError_t launch_balance(BalanceArgs a, cudaStream_t s) {

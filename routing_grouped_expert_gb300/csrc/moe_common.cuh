@@ -478,7 +478,7 @@ struct BalanceArgs {
   bool softmax;
   float factor;                 // alpha E / (S k)
   int chunk, blocks;            // tokens per block, blocks
-  int adders, share;            // blocks that add the slots (the last ones), warps that share some
+  int adders, share;            // blocks behind those that add the slots, warps that share some
   uint64_t launch;              // this launch's number, a multiple of 4
   int* status;                  // workspace: the status word,
   uint64_t* done;               // [blocks + adders]  `launch` from the blocks and adders that are

@@ -104,3 +104,45 @@ def test_two_streams_at_once():
     for (m, *_), w in zip(sets, want):
         for n in w.params:
             assert torch.equal(m.params[n], w.params[n]), n
+
+
+def test_beside_a_layer_that_fills_the_device():
+    """The operators on one stream while the expert layer, which takes every SM for
+    as long as it runs, runs on another: the bits of each alone, no wait that ran out."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    bf = torch.bfloat16
+    E, H, F, k = 32, 2048, 1024, 4
+    x, logits = r(8192, H).to(bf), r(8192, E)
+    W = [(r(E, H, F) / H ** 0.5).to(bf), (r(E, H, F) / H ** 0.5).to(bf), (r(E, F, H) / F ** 0.5).to(bf)]
+    l, idx = r(30000, 256), torch.randint(0, 256, (30000, 8), generator=g, device="cuda").int()
+    offsets = torch.arange(0, 30001, 500, device="cuda", dtype=torch.int32)
+    w, dy = 1 + 0.1 * r(H), r(8192, H).to(bf)
+    ws = [moe.Workspace() for _ in range(3)]
+
+    def operators():
+        loss, counts, tokens = moe.moe_balance_loss(l, idx, 0.01, seq_offsets=offsets, ws=ws[0])
+        dl = moe.moe_balance_loss_backward(loss, counts, tokens, l, 8, 0.01, seq_offsets=offsets)
+        y, h, stats = moe.moe_layer_norm(x, w)
+        return (loss, counts, tokens, dl, y, stats) + \
+            moe.moe_layer_norm_backward(dy, h, stats, w, has_bias=False, ws=ws[1])[:2]
+
+    def layer():
+        return moe.moe_forward(x, logits, *W, k, ws=ws[2])
+
+    want, out = operators(), layer()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got, outs = [], []
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            outs.append(layer())
+        with torch.cuda.stream(b):
+            got.append(operators())
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, out)
+    for some in got:
+        assert all(torch.equal(p, q) for p, q in zip(some, want))
+    for v in ws:
+        assert moe.moe_get_device_status(v) == 0
