@@ -964,7 +964,7 @@ class AdamWState:
         if master:
             self.master = zeros(at, torch.float32)
             for i, p in enumerate(self.params):
-                self.of(self.master, i).copy_(p)
+                self.of(self.master, i).copy_(p.detach())
         self.decay = tuple(decay)
         self._bind()
 

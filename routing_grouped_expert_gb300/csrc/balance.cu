@@ -20,10 +20,10 @@
 // then: it holds up none that it waits for, however few blocks fit the SMs beside other
 // work.  Waits are bounded all the same.  No atomics on floats: results are the same from run to run.
 //
-// 40001 x 256 logits: 18.5 us in one sequence, 23.7 in 24 with a mask (42 MB, 6.2 us at the
+// 40001 x 256 logits: 17.7 us in one sequence, 22.8 in 24 with a mask (42 MB, 6.2 us at the
 // rate of a plain copy).  Of a call's time, rows are done after 11 us (median; memory from a
 // cold start), announced by 14, the slots added by 17.4: the last part is a chain of loads
-// through L2, each waiting for the one before.  131072 x 256: 35.5 us (0.57).  One token: 6.3.
+// through L2, each waiting for the one before.  131072 x 256: 34.6 us (0.59).  One token: 6.4.
 // Two launches, the second one cluster: 24 and 33 us.
 // The gradient: 40001 x 256 in 13.9 us (0.87), onto dlogits, 24 sequences, 22.5 (0.80),
 // 131072 x 256 in 47.9 (0.83); 8192 x 64 in 3.5, latency.
@@ -370,6 +370,26 @@ __device__ __forceinline__ int wait_for(const uint64_t* at, uint64_t launch) {
 __device__ __forceinline__ void announce(uint64_t* at, uint64_t launch) {
   asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(launch) : "memory");
 }
+// A number handed to another block in the words that announce it, beside one half of the
+// launch's number each: nothing else has to be visible with it, and a store that waits for
+// none before it takes 1 us less of the launch's end.  kLate: the wait before it ran out.
+constexpr uint32_t kLate = 0x7fc0dead;   // a NaN that no arithmetic makes
+__device__ __forceinline__ void post(uint64_t* at, uint64_t launch, uint32_t bits) {
+  const uint64_t w0 = (launch & ~0xffffffffull) | bits, w1 = launch << 32 | bits;
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(w0) : "memory");
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at + 1), "l"(w1) : "memory");
+}
+__device__ __forceinline__ uint32_t wait_posted(const uint64_t* at, uint64_t launch) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  do {
+    uint64_t w0, w1;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w0) : "l"(at) : "memory");
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w1) : "l"(at + 1) : "memory");
+    const uint32_t bits = (uint32_t)w0;
+    if (w0 == ((launch & ~0xffffffffull) | bits) && w1 == (launch << 32 | bits)) return bits;
+  } while (ptx::globaltimer_ns() - t0 < kWaitLimitNs);
+  return kLate;
+}
 
 // Adder `rank` of a.adders: its share of the slots' sums, in order, and of the counts, once
 // `wait` has returned.  Returns the share's loss, in the first warp.
@@ -485,28 +505,28 @@ __global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(B
     for (int b = threadIdx.x; b < blocks; b += kThreads) bad |= wait_for(a.done + b, a.launch);
     __syncthreads();
   });
-  uint64_t* added = a.done + blocks;
+  uint64_t* added = a.done + blocks;   // two words each
+  const int late = __syncthreads_or(bad & 4);
   if (!last) {
-    const int late = __syncthreads_or(bad & 4);
-    if (threadIdx.x == 0) {
-      a.shares[rank] = share;
-      announce(added + rank, a.launch | (uint64_t)(late != 0));
-    }
+    if (threadIdx.x == 0) post(added + 2 * rank, a.launch, late ? kLate : __float_as_uint(share));
     return;
   }
   // the last block: the shares in order, and what the blocks have to report
-  for (int r = threadIdx.x; r < a.adders - 1; r += kThreads)
-    if (wait_for(added + r, a.launch) != 0) bad |= 4;
-  bad = __reduce_or_sync(0xffffffffu, (unsigned)bad);
   if (threadIdx.x == 0) sh.bad = 0;
   __syncthreads();
+  bad = __reduce_or_sync(0xffffffffu, (unsigned)bad);
   if (bad != 0 && (threadIdx.x & 31) == 0) atomicOr(&sh.bad, bad);
+  float v = 0.f;
+  if (threadIdx.x < 32)
+    for (int r = threadIdx.x; r < a.adders - 1; r += 32) {
+      const uint32_t bits = wait_posted(added + 2 * r, a.launch);
+      if (bits == kLate) atomicOr(&sh.bad, 4);
+      else v += __uint_as_float(bits);
+    }
   __syncthreads();
   // nobody reads the numbers any more: a captured launch comes again under the same one
-  for (int b = threadIdx.x; b < blocks + a.adders - 1; b += kThreads) a.done[b] = 0;
+  for (int b = threadIdx.x; b < blocks + 2 * a.adders; b += kThreads) a.done[b] = 0;
   if (threadIdx.x < 32) {
-    float v = 0.f;
-    for (int r = threadIdx.x; r < a.adders - 1; r += 32) v += __ldcg(a.shares + r);
     v = warp_sum(v) + share;
     if (threadIdx.x == 0) {
       *a.loss = v;
@@ -683,8 +703,7 @@ size_t balance_layout(int T, int E, int S, BalanceArgs* a, void* ws) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes, 256); return at; };
   const int adders = adders_of(blocks, E, S);
-  const size_t status = take(256), done = take((size_t)(blocks + adders) * 8);
-  const size_t shares = take((size_t)adders * 4);
+  const size_t status = take(256), done = take((size_t)(blocks + 2 * adders) * 8);
   const size_t n = take(slots * 4), p = take(slots * E * 4), c = take(slots * E * 4);
   if (a != nullptr) {
     a->chunk = chunk;
@@ -693,7 +712,6 @@ size_t balance_layout(int T, int E, int S, BalanceArgs* a, void* ws) {
     a->share = share_of(blocks, S);
     a->status = ws_ptr<int>(ws, status);
     a->done = ws_ptr<uint64_t>(ws, done);
-    a->shares = ws_ptr<float>(ws, shares);
     a->part_n = ws_ptr<int>(ws, n);
     a->part_p = ws_ptr<float>(ws, p);
     a->part_c = ws_ptr<int>(ws, c);

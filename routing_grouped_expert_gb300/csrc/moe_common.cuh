@@ -481,9 +481,9 @@ struct BalanceArgs {
   int adders, share;            // blocks behind those that add the slots, warps that share some
   uint64_t launch;              // this launch's number, a multiple of 4
   int* status;                  // workspace: the status word,
-  uint64_t* done;               // [blocks + adders]  `launch` from the blocks and adders that are
-                                // done, and in its lowest bits what they have to report,
-  float* shares;                // [adders]  the adders' shares of the loss,
+  uint64_t* done;               // [blocks]  `launch` from the blocks that are done, and in its
+                                // lowest bits what they have to report; [adders][2]  the adders'
+                                // shares of the loss beside the halves of `launch`,
   int* part_n;                  // [blocks + S]  tokens,
   float* part_p;                // [blocks + S][E]  sums of probabilities,
   int* part_c;                  // [blocks + S][E]  and counts of a block's part of a sequence

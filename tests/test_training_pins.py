@@ -231,6 +231,10 @@ def test_adamw_state_layout(monkeypatch):
     st = moe.AdamWState(b, master=True)
     assert torch.equal(st.of(st.master, 0), b[0].float())
     assert torch.equal(st.of(st.master, 1), b[1].float())
+    # leaves of a graph: the masters are none
+    leaf = torch.randn(8).to(torch.bfloat16).requires_grad_(True)
+    masters = moe.AdamWState([leaf], master=True).master
+    assert not masters.requires_grad and masters.grad_fn is None
     flat = torch.zeros(64)
     with pytest.raises(ValueError, match="share memory"):
         moe.AdamWState([flat[32:], flat[:36]])
