@@ -971,6 +971,8 @@ class AdamWState:
     def _bind(self):
         """What a step compares with and hands over, for all parameters at once."""
         first, count = self.params[0], len(self.params)
+        # whatever becomes of a parameter, the memory that a step writes stays its own
+        self._held = [p.detach() for p in self.params]
         self._shapes = [p.shape for p in self.params]
         self._ptrs = [p.data_ptr() for p in self.params]
         self._devices = [first.get_device()] * count
@@ -980,7 +982,7 @@ class AdamWState:
 
     def __getstate__(self):   # copies and pickles have parameters, and places, of their own
         return {k: v for k, v in self.__dict__.items()
-                if k not in ("_table", "_ptrs", "_devices", "_shapes")}
+                if k not in ("_table", "_ptrs", "_devices", "_shapes", "_held")}
 
     def __setstate__(self, state):
         self.__dict__.update(state)

@@ -106,6 +106,23 @@ def test_balance(case, score):
     check(case, *make(case, score))
 
 
+@pytest.mark.parametrize("E", [2, 9, 20, 33, 50, 77, 100, 128, 131, 333, 512, 516])
+def test_every_way_to_hold_a_row(E):
+    case = (1100, E, min(E, 5), [0, 3, 700, 1090], True)
+    for score in ("softmax", "sigmoid"):
+        check(case, *make(case, score))
+
+
+@pytest.mark.parametrize("S", [600, 2000, 65536])
+def test_many_sequences(S):
+    """Most of them empty: more than a block keeps at hand, and all that are allowed."""
+    T, E, k = 700, 8, 2
+    r = np.random.default_rng(S)
+    offsets = np.sort(r.integers(0, T + 1, S + 1))
+    case = (T, E, k, offsets.tolist(), True)
+    check(case, *make(case, "softmax"))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("shift", [-300.0, -60.0, 60.0, 300.0])
 def test_far_logits(score, shift):

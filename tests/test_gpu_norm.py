@@ -106,6 +106,18 @@ def test_backward(size, types):
     check_backward(d, h, stats, got)
 
 
+@pytest.mark.parametrize("types", TYPES, ids=str)
+@pytest.mark.parametrize("size", [(5000, 33), (3000, 255), (2500, 500), (2000, 1001), (1300, 2047),
+                                  (900, 4099), (500, 7170), (400, 9001), (320, 12002)], ids=str)
+def test_many_rows_of_odd_widths(size, types):
+    """Blocks that take several rows, none of which starts on a 16-byte boundary of its own."""
+    d = make(*size, *types)
+    y, h, stats = moe.moe_layer_norm(d["x"], d["weight"], d["bias"], 1e-5, residual=d["residual"])
+    check_forward(d, y, h, stats, 1e-5)
+    got = moe.moe_layer_norm_backward(d["dy"], h, stats, d["weight"], dh=d["dh"])
+    check_backward(d, h, stats, got, d["dh"])
+
+
 def test_gradient_equals_differences():
     """The GPU's gradients against central differences of the definition."""
     d = make(3, 40, F32, F32)
