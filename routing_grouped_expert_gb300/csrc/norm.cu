@@ -88,10 +88,8 @@ norm_kernel(const T* __restrict__ x, const T* __restrict__ residual, const W* __
     float a[8];
     v[i].get(a);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sum += a[j];
-      mine += kBlock && inside<kVec>(i, j, t);
-    }
+    for (int j = 0; j < 8; ++j) sum += a[j];
+    if (kBlock) mine += __popc(inside<kVec>(i, t));
   }
   const int count = kBlock ? __reduce_add_sync(0xffffffffu, mine) : H;
   const float u = count > 0 ? lanes_sum<kLanes>(sum) / count : 0.f;
@@ -100,11 +98,21 @@ norm_kernel(const T* __restrict__ x, const T* __restrict__ residual, const W* __
   for (int i = 0; i < n; ++i) {
     float a[8];
     v[i].get(a);
+    const uint32_t in = inside<kVec>(i, t);
+    if (in == 0xffu) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float d = inside<kVec>(i, j, t) ? a[j] - u : 0.f;
-      s.x += d;
-      s.y = fmaf(d, d, s.y);
+      for (int j = 0; j < 8; ++j) {
+        const float d = a[j] - u;
+        s.x += d;
+        s.y = fmaf(d, d, s.y);
+      }
+    } else if constexpr (!kVec) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = in >> j & 1u ? a[j] - u : 0.f;
+        s.x += d;
+        s.y = fmaf(d, d, s.y);
+      }
     }
   }
   s.x = lanes_sum<kLanes>(s.x);

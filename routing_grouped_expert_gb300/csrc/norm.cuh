@@ -39,6 +39,13 @@ struct Eight<bf16> {
     v = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  // keeps value j where bit j is set
+  __device__ __forceinline__ void keep(uint32_t bits) {
+    auto word = [&](int i) {
+      return (bits >> (2 * i) & 1u ? 0xffffu : 0u) | (bits >> (2 * i + 1) & 1u ? 0xffff0000u : 0u);
+    };
+    v = make_uint4(v.x & word(0), v.y & word(1), v.z & word(2), v.w & word(3));
+  }
 };
 template <>
 struct Eight<float> {
@@ -67,6 +74,13 @@ struct Eight<float> {
     v[1] = make_float4(f[4], f[5], f[6], f[7]);
   }
   __device__ __forceinline__ void zero() { v[0] = v[1] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void keep(uint32_t bits) {
+    float f[8];
+    get(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = bits >> j & 1u ? f[j] : 0.f;
+    set(f);
+  }
 };
 __device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -98,12 +112,25 @@ template <bool kVec>
 __device__ __forceinline__ bool whole(const Team& t, int c) {
   return kVec ? c < t.H : c >= 0 && c + 8 <= t.H;
 }
+// Which of group i's eight places are in the row, as bits.
+template <bool kVec>
+__device__ __forceinline__ uint32_t inside(int i, const Team& t) {
+  const int c = column<kVec>(t, i);
+  if (whole<kVec>(t, c)) return 0xffu;
+  if (kVec || c >= t.H) return 0u;
+  return (c < 0 ? 0xffu << -c : 0xffu) & (c + 8 > t.H ? 0xffu >> (c + 8 - t.H) : 0xffu);
+}
+// kShared: the row is a copy in shared memory, with room for its first and last groups'
+// missing values.
 template <bool kShared = false, bool kVec, typename T>
 __device__ __forceinline__ void get(Eight<T>& e, const T* row, int i, const Team& t) {
   const int c = column<kVec>(t, i);
-  if (whole<kVec>(t, c)) {
-    if constexpr (kShared) e.load_shared(row + c);
-    else e.load(row + c);
+  if constexpr (kShared) {
+    if (c < t.H) e.load_shared(row + c);
+    else e.zero();
+    if (!kVec && c < t.H && !whole<kVec>(t, c)) e.keep(inside<kVec>(i, t));
+  } else if (whole<kVec>(t, c)) {
+    e.load(row + c);
   } else {
     e.zero();
     if constexpr (!kVec) {
@@ -127,17 +154,52 @@ __device__ __forceinline__ void put(T* row, int i, const Team& t, const Eight<T>
       if (c + j >= 0 && c + j < t.H) row[c + j] = from_f32<T>(f[j]);
   }
 }
-// The columns' own values, whose place in memory has nothing to do with the rows'.
+// Of the words from a 16-byte boundary on (x), those that begin `skip` words later, for any
+// skip below 4: a choice between two places for each of its bits.
+template <int have, int want>
+__device__ __forceinline__ void skip_words(uint32_t (&x)[have], int skip) {
+#pragma unroll
+  for (int i = 0; i < want + 1 && i + 2 < have; ++i) x[i] = skip & 2 ? x[i + 2] : x[i];
+#pragma unroll
+  for (int i = 0; i < want && i + 1 < have; ++i) x[i] = skip & 1 ? x[i + 1] : x[i];
+}
+// The columns' own values, whose place in memory has nothing to do with the rows'.  Where
+// eight of them do not start on a 16-byte boundary they are cut out of the pieces around them:
+// one by one, a warp's take four passes through L1 each.
 template <bool kVec, typename W>
 __device__ __forceinline__ void get_column(Eight<W>& e, const W* w, int i, const Team& t) {
   if constexpr (kVec) {
     get<false, kVec>(e, w, i, t);
   } else {
     const int c = column<kVec>(t, i);
-    float f[8];
+    constexpr int kPiece = 16 / sizeof(W);
+    const int s = c & (kPiece - 1);
+    // the pieces lie within the array, or are those of its end
+    if (c >= 0 && c - s + 8 + kPiece <= t.H) {
+      const uint4* from = reinterpret_cast<const uint4*>(w + (c - s));
+      if constexpr (sizeof(W) == 2) {
+        const uint4 a = __ldg(from), b = __ldg(from + 1);
+        uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        skip_words<8, 5>(x, s >> 1);
+        uint32_t y[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c + j >= 0 && c + j < t.H ? to_f32(w[c + j]) : 0.f;
-    e.set(f);
+        for (int j = 0; j < 4; ++j) y[j] = s & 1 ? __funnelshift_r(x[j], x[j + 1], 16) : x[j];
+        e.v = make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+        const uint4 a = __ldg(from), b = __ldg(from + 1), d = __ldg(from + 2);
+        uint32_t x[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, d.x, d.y, d.z, d.w};
+        skip_words<12, 8>(x, s);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(x[j]);
+        e.set(f);
+      }
+    } else {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = c + j >= 0 && c + j < t.H ? to_f32(w[c + j]) : 0.f;
+      e.set(f);
+    }
   }
 }
 template <bool kVec>
@@ -153,12 +215,6 @@ __device__ __forceinline__ void put_column(float* w, int i, const Team& t, const
       if (c + j >= 0 && c + j < t.H) w[c + j] = f[j];
   }
 }
-template <bool kVec>
-__device__ __forceinline__ bool inside(int i, int j, const Team& t) {
-  const int c = column<kVec>(t, i) + (kVec ? 0 : j);
-  return c >= 0 && c < t.H;
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);

@@ -163,7 +163,8 @@ struct RowRing {
   int H, stages, pitch, tensors;
   long long rows;
 
-  static __host__ __device__ int pitch_of(int H) { return (H * (int)sizeof(T) + 31) / 16 * 16; }
+  // a row and its first and last groups' missing values
+  static __host__ __device__ int pitch_of(int H) { return (H * (int)sizeof(T) + 15 + 8 * (int)sizeof(T) + 15) / 16 * 16; }
   __device__ __forceinline__ T* at(int stage, int tensor) const {
     return reinterpret_cast<T*>(buf + (size_t)(stage * tensors + tensor) * pitch);
   }
