@@ -10,8 +10,8 @@
 //
 // Bound by memory: 8192 x 7168 bf16 with a residual in 71.0 us (470 MB, 0.98 of the rate of a
 // plain copy; DRAM read 235 MB), 12000 x 4096 in 58.5 (0.99), 40001 x 512 in 25.9 (0.93),
-// without a residual 47 (0.73: half the bytes in flight).  Rows of 7170 113 us (0.61): their
-// weights are taken one by one.
+// without a residual 47 (0.73: half the bytes in flight).  Rows of 7170 104 us (0.67): their
+// weights are cut out of the pieces around them, and a row's ends taken one by one.
 #include "norm.cuh"
 
 namespace moe {

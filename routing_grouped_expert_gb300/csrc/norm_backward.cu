@@ -9,7 +9,7 @@
 //
 // Bound by memory: 8192 x 7168 bf16 with dh in 76.5 us (470 MB, 0.90 of the rate of a plain
 // copy), of which the second launch is about 5; 12000 x 4096 64 (0.90), 20000 x 2048 55
-// (0.88), 40001 x 512 35 (0.70: a row per warp, its latency), rows of 7170 116 (0.60: the
+// (0.88), 40001 x 512 35 (0.70: a row per warp, its latency), rows of 7170 91 (0.76: the
 // fetching thread's work and the rows' ends), rows of 16384 144 (0.54: eight groups of a
 // thread do not fit its registers).  Few rows: 1 in 5.4 us, 128 of 7168 in 8.9, mostly the
 // two launches and their first loads.
