@@ -606,7 +606,10 @@ moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
  *                  block's e4m3 values are multiplied by.
  * A block's scale is its largest magnitude over 448 (0 where that is below the
  * normal fp32 range: the block is then zero), and a value is rounded to the
- * nearest e4m3 one; the step itself uses m and v before that rounding.  8-bit
+ * nearest e4m3 one; the step itself uses m and v before that rounding.  A root
+ * that is held as zero (below 2^-10 scale) counts as 2^-11 scale in the next
+ * step, so that an element whose gradient is zero then does not move by what is
+ * left of its first moment over eps.  8-bit
  * arrays hold whole blocks, zero past a tensor's end.  State arrays that are
  * zero are those of step 0.
  *

@@ -213,6 +213,8 @@ __device__ __forceinline__ float to_units(float2 (&f)[4], float most) {
   return some ? scale : 0.f;
 }
 
+constexpr float kLeast = 1.f / 2048.f;   // the smallest e4m3 value is 2^-9
+
 // Eight elements of a thread, as they lie in memory.  P, G: types of the parameters and
 // gradients.  k8: 8-bit moments.
 //
@@ -264,8 +266,11 @@ __device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float r
     m = rm.get(i);
     v = rv.get(i);
     if constexpr (k8) {
+      // A root that is held as zero in a block that is not stands for a quarter of the
+      // smallest value, which is rounded to zero again: where the first moment is still
+      // there and the gradient is zero (an expert without a token), its step stays bounded.
       m = __fmul2_rn(m, both(sm));
-      v = __fmul2_rn(v, both(sv));
+      v = __fmul2_rn(make_float2(fmaxf(v.x, kLeast), fmaxf(v.y, kLeast)), both(sv));
       v = __fmul2_rn(v, v);
     }
   };

@@ -45,6 +45,8 @@ def moments(st, i):
     if st.bits == 32:
         return m, v
     block = (a + np.arange(n)) // BLOCK
+    # a root that is held as zero counts as 2^-11 of its block's unit
+    v = np.maximum(v, 2.0 ** -11)
     return m * to64(st.exp_avg_scale)[block], (v * to64(st.exp_avg_sq_scale)[block]) ** 2
 
 
@@ -242,6 +244,25 @@ def test_a_scale_that_is_not_finite_skips_the_step(bits):
             torch.testing.assert_close(a, b, rtol=4 * U, atol=0)
         else:
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_roots_held_as_zero_do_not_let_a_step_run_away():
+    """Gradients 2^18.3 below their block's largest: the root is rounded to zero, the first
+    moment is not.  When their gradient is exactly zero then, they move by no more than a
+    few rates, not by the moment over eps."""
+    p = [torch.zeros(256, device="cuda")]
+    st = moe.AdamWState(p, bits=8)
+    c = moe.AdamWConfig(lr=0.01, beta1=0.9, beta2=0.97, eps=1e-12, weight_decay=0.0)
+    g = torch.full((256,), 100.0 * 2.0 ** -18.9, device="cuda")
+    g[0] = 100.0
+    moe.moe_adamw_step(st, [g], c, 1)
+    # m keeps 2^-18.9 of its largest as its smallest value only with a larger gradient
+    st.exp_avg.view(torch.uint8)[1:] = 1
+    assert (st.exp_avg_sq.float()[1:] == 0).all() and (st.exp_avg.float()[1:] > 0).all()
+    before, held_before = p[0].clone(), held(st)
+    moe.moe_adamw_step(st, [torch.zeros_like(g)], c, 2)
+    check_step(st, [torch.zeros_like(g)], c, 2, held_before)
+    assert ((p[0] - before).abs()[1:] < 20 * 0.01).all()
 
 
 @pytest.mark.parametrize("scale", [1e-30, 1e-38, 0.0])
