@@ -234,6 +234,7 @@ struct BalanceShared {
   float sums[kWarps][33];
   int cnts[kWarps][33];
 };
+static_assert(sizeof(BalanceShared) <= 12 * 1024, "allow_smem");
 
 // One block of tokens: the sums and counts of each sequence that it meets, into their slots.
 template <typename S>

@@ -1,0 +1,47 @@
+"""Kernels whose dynamic shared memory, with what they hold statically, is just over the 48 KB
+that a kernel has without asking.  A larger call before would have asked for them too, so each
+operator's sizes run in a process of their own."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def run_alone(code):
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_norm_gradients():
+    """Rings of 48,561 to 49,152 bytes."""
+    run_alone("""
+from tests import test_gpu_norm as N
+import routing_grouped_expert_gb300 as moe
+for dtype, dh, widths in ((N.BF, False, (1497, 1512, 1520, 2001, 2016, 2032)),
+                          (N.BF, True, (1329, 1344, 1608, 1616, 2008, 2024)),
+                          (N.F32, False, (1208, 1216, 1505, 1520, 2009, 2032)),
+                          (N.F32, True, (1337, 1352, 2016, 2036))):
+    for H in widths:
+        d = N.make(7, H, dtype, dtype)
+        y, h, stats = moe.moe_layer_norm(d["x"], d["weight"], d["bias"], 1e-5)
+        extra = d["dh"] if dh else None
+        N.check_backward(d, h, stats, moe.moe_layer_norm_backward(d["dy"], h, stats, d["weight"], dh=extra),
+                         extra)
+""")
+
+
+def test_balance_loss():
+    """Sums of 605 to 768 experts: 38,720 to 49,152 bytes beside 10,448."""
+    run_alone("""
+from tests import test_gpu_balance as B
+for E in (605, 608, 640, 700, 767, 768):
+    for score in ("softmax", "sigmoid"):
+        case = (150, E, 6, [0, 70, 140], True)
+        B.check(case, *B.make(case, score))
+""")
