@@ -385,7 +385,7 @@ cudaError_t launch_scan(int32_t* chunk_hist, int C, int E, int32_t* counts, int3
                         int32_t* block_off, int32_t* num_blocks, int32_t* block_expert,
                         int beta, cudaStream_t s, bool pdl) {
   const size_t smem = scan_in_smem(C, E) ? (size_t)C * E * 4 : 0;
-  if (smem > 48 * 1024) {
+  if (smem > 47 * 1024) {   // 48 KB less what the kernel holds statically, it has anyway
     static const cudaError_t attr = cudaFuncSetAttribute(
         scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScanSmemMax);
     if (attr != cudaSuccess) return attr;

@@ -45,3 +45,19 @@ for E in (605, 608, 640, 700, 767, 768):
         case = (150, E, 6, [0, 70, 140], True)
         B.check(case, *B.make(case, score))
 """)
+
+
+def test_permutation():
+    """Tables of counts of chunks x experts, 4 bytes each: 49,152 bytes beside 132."""
+    run_alone("""
+import numpy as np
+import torch
+import routing_grouped_expert_gb300 as moe
+from oracle import moe_oracle as O
+from tests.helpers import to_np
+g = torch.Generator().manual_seed(1)
+for T, E, k in ((3050, 256, 8), (16300, 64, 6), (6100, 128, 8), (1780, 438, 8)):
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    for a, b in zip(moe.moe_permute(idx.cuda(), E), O.permute(idx.numpy(), E)):
+        np.testing.assert_array_equal(to_np(a), b)
+""")
