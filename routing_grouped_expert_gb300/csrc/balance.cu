@@ -722,8 +722,9 @@ size_t balance_layout(int T, int E, int S, BalanceArgs* a, void* ws) {
 
 template <typename S>
 cudaError_t launch_sum(const BalanceArgs& a, cudaStream_t s) {
-  const int smem = kWarps * (32 / S::L) * a.E * 4;
-  const cudaError_t e = allow_smem(balance_kernel<S>, smem);
+  constexpr int of_expert = kWarps * (32 / S::L) * 4;
+  const int smem = of_expert * a.E;
+  const cudaError_t e = allow_smem(balance_kernel<S>, smem, of_expert * S::n * S::L);
   if (e != cudaSuccess) return e;
   balance_kernel<S><<<a.blocks + a.adders, kThreads, smem, s>>>(a);
   return cudaGetLastError();

@@ -237,11 +237,12 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
 
 // Allows a kernel `smem` bytes of dynamic shared memory.  48 KB, less what it holds
 // statically (12 KB at the most in those that ask here), it has anyway: asking takes half a
-// microsecond.
+// microsecond.  `most` is what is asked for, the same for all launches of a kernel: the limit is
+// the kernel's, not a launch's, and two threads may launch it at once.
 template <typename... KArgs>
-inline cudaError_t allow_smem(void (*kern)(KArgs...), int smem) {
+inline cudaError_t allow_smem(void (*kern)(KArgs...), int smem, int most) {
   if (smem <= 36 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
 // ------------------------------------------------------------ launchers

@@ -339,7 +339,7 @@ cudaError_t backward_t(const void* dy, const void* h, const float* stats, const 
     const auto kern = norm_backward_ring_kernel<T, W, f.n, kVec, team, f.per>;                    \
     int stages = ring_bytes(f.per) / stage;                                                       \
     stages = stages < kMaxStages ? stages : kMaxStages;                                           \
-    const cudaError_t e = allow_smem(kern, stages * stage);                                       \
+    const cudaError_t e = allow_smem(kern, stages * stage, ring_bytes(f.per));                    \
     if (e != cudaSuccess) return e;                                                               \
     kern<<<blocks, team_of(H, f.n), stages * stage, s>>>(gt, ht, st, wt, rt, rows, H, stages, xt, part, \
                                                          flags);                                  \

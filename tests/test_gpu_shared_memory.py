@@ -4,8 +4,14 @@ operator's sizes run in a process of their own."""
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
+import torch
+
+import routing_grouped_expert_gb300 as moe
+from tests import test_gpu_balance as B
+from tests import test_gpu_norm as N
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +67,43 @@ for T, E, k in ((3050, 256, 8), (16300, 64, 6), (6100, 128, 8), (1780, 438, 8)):
     for a, b in zip(moe.moe_permute(idx.cuda(), E), O.permute(idx.numpy(), E)):
         np.testing.assert_array_equal(to_np(a), b)
 """)
+
+
+def test_two_threads():
+    """Calls of two sizes of one kernel, by two threads on streams of their own."""
+    def both(calls, times):
+        failed = []
+
+        def loop(call, stream):
+            try:
+                with torch.cuda.stream(stream):
+                    for _ in range(times):
+                        call()
+                stream.synchronize()
+            except Exception as e:   # noqa: BLE001
+                failed.append(e)
+
+        threads = [threading.Thread(target=loop, args=(c, torch.cuda.Stream())) for c in calls]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failed, failed
+
+    def norm(H):
+        d = N.make(64, H, N.BF, N.BF)
+        y, h, stats = moe.moe_layer_norm(d["x"], d["weight"], d["bias"])
+        ws = moe.Workspace()
+        ws.ensure(moe.moe_layer_norm_workspace_size(64, H))
+        return lambda: moe.moe_layer_norm_backward(d["dy"], h, stats, d["weight"], dh=d["dh"], ws=ws)
+
+    def balance(E):
+        l, idx, kw = B.make((64, E, 4, None, False), "softmax")
+        l, idx, ws = l.cuda(), idx.cuda(), moe.Workspace()
+        ws.ensure(moe.moe_balance_workspace_size(64, E))
+        return lambda: moe.moe_balance_loss(l, idx, 0.01, ws=ws, **kw)
+
+    calls = [norm(H) for H in (4096, 2064, 2560, 3600)], [balance(E) for E in (1024, 800)]
+    torch.cuda.synchronize()
+    both(calls[0], 1500)
+    both(calls[1], 1500)
