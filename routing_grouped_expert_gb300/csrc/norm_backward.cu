@@ -46,7 +46,9 @@ __device__ __forceinline__ float2 block_sum2(float2 v, float2* part) {
 // gridDim.x is a multiple of 8 or each block has one row, so that all of a block's rows
 // begin at the same place between 16-byte boundaries.  Works on pairs, with d = h - mean:
 //   dw += (dy rstd) d,  db += dy,  u = w dy,  a = sum u,  c = sum u d
-//   dx = dh - rstd a / H + rstd u - (rstd^3 c / H) d
+//   dx = dh + rstd (u - a / H - (rstd^2 c / H) d)
+// rstd^2 c / H is formed from the right, where it is rstd times a mean of u xhat: rstd^2 by itself
+// may leave fp32 with a small eps, in rows of padding say, in which c is 0.
 // The thread's part of a row, from `get_row(tensor, i, group)`, and dx.
 template <typename T, typename W, int n, bool kVec, int kTeam>
 struct Backward {
@@ -88,15 +90,15 @@ struct Backward {
     return make_float2(sa.x + sa.y, sc.x + sc.y);
   }
   __device__ __forceinline__ void give(T* dx, float2 s, float2 st) const {
-    const float a = -st.y * (s.x / t.H), c = -st.y * st.y * st.y * (s.y / t.H);
+    const float a = -(s.x / t.H), c = -st.y * (st.y * (s.y / t.H));
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float2 x = __ffma2_rn(u[i][j], make_float2(st.y, st.y), make_float2(a, a));
+        float2 x = __fadd2_rn(u[i][j], make_float2(a, a));
         x = __ffma2_rn(d[i][j], make_float2(c, c), x);
-        x = __fadd2_rn(x, r[i].pair(j));
+        x = __ffma2_rn(x, make_float2(st.y, st.y), r[i].pair(j));
         v[2 * j] = x.x;
         v[2 * j + 1] = x.y;
       }
