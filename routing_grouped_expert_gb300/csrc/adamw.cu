@@ -250,13 +250,13 @@ struct Group {
   }
   // Their step; returns whether an element was left as it was.
   template <bool kWhole>
-  __device__ __forceinline__ bool step(int left, float rate, float keep, float root, float gs,
+  __device__ __forceinline__ bool step(int left, float rate, float shrink, float root, float gs,
                                        const Hyper& h);
 };
 
 template <typename P, typename G, bool kMaster, bool k8>
 template <bool kWhole>
-__device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float rate, float keep,
+__device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float rate, float shrink,
                                                                float root, float gs,
                                                                const Hyper& h) {
   float2 m[4], v[4], p[4];
@@ -288,7 +288,10 @@ __device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float r
     const float2 r = root2(v[i]);
     const float2 d = __ffma2_rn(r, both(root), both(h.eps));
     const float2 s = __fmul2_rn(m[i], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
-    p[i] = __ffma2_rn(s, both(rate), __fmul2_rn(rp.get(i), both(keep)));
+    // all that is added to p, and then one rounding: a factor 1 - lr decay would itself be a
+    // multiple of 2^-24, and a decay of 2e-8 a step none
+    const float2 w = rp.get(i);
+    p[i] = __fadd2_rn(w, __ffma2_rn(w, both(shrink), __fmul2_rn(s, both(rate))));
     if constexpr (k8) v[i] = r;
   }
   const bool bad = isnan(nan.x + nan.y);
@@ -372,13 +375,13 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
     inv1 = 1.f / -expm1f(s * h.log_b1);
     root = rsqrtf(-expm1f(s * h.log_b2));
   }
-  const float rate = -lr * inv1, keep = 1.f - lr * t.decay;
+  const float rate = -lr * inv1, shrink = -lr * t.decay;
   const float gs = h.grad_scale != nullptr ? __ldg(h.grad_scale) : 1.f;
   bool bad = false;
   if (whole) {
 #pragma unroll
     for (int u = 0; u < kTurns; ++u)
-      bad |= group[u].template step<true>(8, rate, keep, root, gs, h);
+      bad |= group[u].template step<true>(8, rate, shrink, root, gs, h);
   } else {
 #pragma unroll 1
     for (int u = 0; u < kTurns; ++u) {
@@ -394,7 +397,7 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
       part.m_scale += u * (kTurn / MOE_ADAMW_BLOCK);
       part.v_scale += u * (kTurn / MOE_ADAMW_BLOCK);
       part.template load<false>(left);
-      bad |= part.template step<false>(left, rate, keep, root, gs, h);
+      bad |= part.template step<false>(left, rate, shrink, root, gs, h);
     }
   }
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0)

@@ -1,0 +1,43 @@
+"""What an AdamW step rounds, and where: what many steps would add up."""
+import numpy as np
+import pytest
+import torch
+
+import routing_grouped_expert_gb300 as moe
+from oracle import training as R
+from tests import test_gpu_adamw as A
+
+pytestmark = pytest.mark.gpu
+
+U = A.U
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("kind", [(A.BF, True), (A.F32, False)], ids=str)
+@pytest.mark.parametrize("rate", [2e-8, 5e-8, 1e-7])
+def test_a_small_decay_is_not_lost(rate, kind, bits):
+    """Weights from 1 to 2 that decay by less than their rounding in a step, lr * decay of
+    2e-8 to 1e-7: over elements and steps the decay has to come out in the mean.  Each step is
+    compared with the oracle's from what the GPU held before.  A weight's rounding is off by at most
+    2^-24, evenly spread while the update (17 units of the last place and more) is random: over
+    N = 2^16 elements and 20 steps the mean of the sums deviates by 2^-24 sqrt(20 / 3) / 2^8 =
+    6.0e-10; six of those, and the steps' own error of 32 U times 2e-6 each, of either sign:
+    3.6e-9 + 20 * 3.8e-12.  Twice that is allowed; the decay lost is 20 * 1.5 * 2e-8 = 6e-7."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    n, lr = 1 << 16, 2e-6
+    r = lambda: torch.randn(n, generator=g, device="cuda")  # noqa: E731
+    p = (1 + torch.rand(n, generator=g, device="cuda")).to(kind[0])
+    st = moe.AdamWState([p], bits=bits, master=kind[1])
+    c = moe.AdamWConfig(lr=lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=rate / lr)
+    for t in (1, 2, 3):
+        moe.moe_adamw_step(st, [r()], moe.AdamWConfig(lr=1e-3, beta2=0.95, weight_decay=0.0), t)
+    if kind[1]:     # the masters fill the range, not bf16 values alone
+        st.master.copy_(1 + torch.rand(n, generator=g, device="cuda"))
+    total = np.zeros(n)
+    for t in range(4, 24):
+        (w, m, v), = A.held(st)
+        grad = r()
+        moe.moe_adamw_step(st, [grad], c, t)
+        want = R.adamw(w, A.to64(grad), m, v, t, lr, c.beta1, c.beta2, c.eps, c.weight_decay)[0]
+        total += A.held(st)[0][0] - want
+    assert abs(total.mean()) <= 2 * (3.6e-9 + 20 * 3.8e-12)
