@@ -621,8 +621,10 @@ moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
  *
  * An element whose moments would not be finite (a gradient that is NaN or
  * infinite, or too large to be squared) is left as it was, and
- * MOE_ERR_NONFINITE is set in the device status: a grad_scale that is not
- * finite skips the whole step.
+ * MOE_ERR_NONFINITE is set in the device status.  (8 bits: its moments are held
+ * in the units of its block, and rounded again where these change.)  With a
+ * grad_scale that is not finite the whole step is skipped, and nothing but the
+ * status is written.
  *
  * param_type, grad_type: moe_dtype, of all tensors of the call; masters only
  * beside bf16 parameters.  Tensors and scales are 16-byte aligned, the other

@@ -377,6 +377,12 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
   }
   const float rate = -lr * inv1, shrink = -lr * t.decay;
   const float gs = h.grad_scale != nullptr ? __ldg(h.grad_scale) : 1.f;
+  // no element takes a step: 8-bit moments would be rounded again by their blocks' largest
+  // values, and the scales
+  if (!(fabsf(gs) < INFINITY)) {
+    if ((threadIdx.x & 31) == 0) status_report(status, launch, MOE_ERR_NONFINITE);
+    return;
+  }
   bool bad = false;
   if (whole) {
 #pragma unroll

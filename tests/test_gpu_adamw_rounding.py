@@ -41,3 +41,29 @@ def test_a_small_decay_is_not_lost(rate, kind, bits):
         want = R.adamw(w, A.to64(grad), m, v, t, lr, c.beta1, c.beta2, c.eps, c.weight_decay)[0]
         total += A.held(st)[0][0] - want
     assert abs(total.mean()) <= 2 * (3.6e-9 + 20 * 3.8e-12)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("kind", A.KINDS, ids=str)
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+def test_a_skipped_step_writes_nothing(scale, kind, bits):
+    """With a scale that is not finite nothing changes, nor do 8-bit moments' scales, which a
+    rounding of 448 scale / 448 would move: blocks whose largest value is not 448 (a state from
+    elsewhere), and ones that end within a tensor's last block, among them."""
+    sizes = [5000, 33, 256, 4096]
+    st, grads, g = A.make(sizes, kind[0], A.F32, bits, kind[1])
+    c = moe.AdamWConfig(lr=0.01)
+    moe.moe_adamw_step(st, grads, c, 1)
+    if bits == 8:
+        for s in (st.exp_avg_scale, st.exp_avg_sq_scale):
+            s.mul_(1 + torch.rand(s.shape, generator=g, device="cuda"))
+        st.exp_avg[:256] = (st.exp_avg[:256].float() / 4).to(st.exp_avg.dtype)
+    flats = [t for t in (st.master, st.exp_avg, st.exp_avg_sq, st.exp_avg_scale,
+                         st.exp_avg_sq_scale, *st.params) if t is not None]
+    before = [t.clone() for t in flats]
+    ws = moe.Workspace()
+    for t in range(2, 12):
+        moe.moe_adamw_step(st, grads, c, t, grad_scale=torch.tensor(scale, device="cuda"), ws=ws)
+        assert moe.moe_get_device_status(ws) == 2
+    for a, b in zip(flats, before):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
