@@ -67,3 +67,42 @@ def test_a_skipped_step_writes_nothing(scale, kind, bits):
         assert moe.moe_get_device_status(ws) == 2
     for a, b in zip(flats, before):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_small_roots():
+    """Second moments down to the smallest subnormal, with an eps below their roots: the step
+    stays that of the moments.  Their own rounding, up to 2^-150 in the product with beta2 and
+    8 U of it, moves a root by what it moves v; the rest of the step is 24 U."""
+    n = 1 << 14
+    g = torch.Generator(device="cuda").manual_seed(3)
+    u = torch.rand(n, generator=g, device="cuda", dtype=torch.float64)
+    v = (10.0 ** (-44.5 + 20 * u)).float()
+    m = v.double().sqrt().float() * torch.randn(n, generator=g, device="cuda")
+    p = torch.zeros(n, device="cuda")
+    st = moe.AdamWState([p])
+    st.exp_avg.copy_(m)
+    st.exp_avg_sq.copy_(v)
+    c = moe.AdamWConfig(lr=0.01, beta1=0.9, beta2=0.99, eps=1e-30, weight_decay=0.0)
+    (_, m, v), = A.held(st)
+    moe.moe_adamw_step(st, [torch.zeros(n, device="cuda")], c, 100)
+    m, v, inv = c.beta1 * m, c.beta2 * v, c.lr / (1 - c.beta1 ** 100)
+    error = 8 * U * v + 2.0 ** -150
+    low, high = (inv * np.abs(m) / (np.sqrt(np.maximum(x, 0) / (1 - c.beta2 ** 100)) + c.eps)
+                 for x in (v + error, v - error))
+    got = np.abs(A.to64(p))
+    assert (got >= low * (1 - 24 * U) - 1e-44).all() and (got <= high * (1 + 24 * U) + 1e-44).all()
+
+
+def test_small_roots_in_8_bits():
+    """The same of roots held in 8 bits: a block's largest, of v = 1e-40, decays by the root of
+    beta2.  v is off by 2^-150 a product, four of them: 3e-5 of v."""
+    p = [torch.zeros(256, device="cuda")]
+    st = moe.AdamWState(p, bits=8)
+    codes = torch.linspace(64, 448, 256, device="cuda").to(st.exp_avg_sq.dtype)
+    st.exp_avg_sq.copy_(codes)
+    st.exp_avg_sq_scale.fill_(1e-20 / 448)
+    c = moe.AdamWConfig(lr=0.01, beta1=0.9, beta2=0.99, eps=1e-30, weight_decay=0.0)
+    moe.moe_adamw_step(st, [torch.zeros(256, device="cuda")], c, 100)
+    want = 1e-20 / 448 * 0.99 ** 0.5
+    assert abs(float(st.exp_avg_sq_scale) / want - 1) <= 3e-5
+    assert torch.equal(st.exp_avg_sq.view(torch.uint8), codes.view(torch.uint8))
