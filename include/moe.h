@@ -604,8 +604,8 @@ moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
  *   exp_avg_sq     v in fp32, or its square root in e4m3;
  *   exp_avg_scale, exp_avg_sq_scale   (8 bits) fp32 [one per block]: what the
  *                  block's e4m3 values are multiplied by.
- * A block's scale is its largest magnitude over 448 (0 where that is below the
- * normal fp32 range: the block is then zero), and a value is rounded to the
+ * A block's scale is its largest magnitude times fl(1 / 448) (0 where that is
+ * below the normal fp32 range: the block is then zero), and a value is rounded to the
  * nearest e4m3 one; the step itself uses m and v before that rounding.  A root
  * that is held as zero (below 2^-10 scale) counts as 2^-11 scale in the next
  * step, so that an element whose gradient is zero then does not move by what is

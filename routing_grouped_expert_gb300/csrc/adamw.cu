@@ -5,7 +5,7 @@
 //
 // p is the fp32 master weight where there is one (the parameter is then its rounding),
 // else the parameter itself.  m and v are fp32, or e4m3 in blocks of 256 elements with an
-// fp32 scale each: the block's largest magnitude over 448; v is held as its square root,
+// fp32 scale each: the block's largest magnitude times fl(1 / 448); v is held as its square root,
 // which halves the range its exponents have to span.  The step itself uses m and v before
 // they are rounded.
 //
@@ -204,7 +204,7 @@ __device__ __forceinline__ float block_max(const float2 (&f)[4]) {
     asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(f[i].x), "f"(f[i].y));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
-// f / scale with scale = `most` / 448, most the block's largest magnitude; returns the
+// f / scale with scale = `most` fl(1 / 448), most the block's largest magnitude; returns the
 // scale.  Quotients are correctly rounded (Markstein: with the correctly rounded
 // reciprocal, one correction of the quotient by its remainder).  Blocks whose scale is
 // below the normal range become zero.

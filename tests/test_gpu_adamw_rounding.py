@@ -106,3 +106,50 @@ def test_small_roots_in_8_bits():
     want = 1e-20 / 448 * 0.99 ** 0.5
     assert abs(float(st.exp_avg_sq_scale) / want - 1) <= 3e-5
     assert torch.equal(st.exp_avg_sq.view(torch.uint8), codes.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", A.KINDS, ids=str)
+@pytest.mark.parametrize("size", [1.0, 1e-6, 1e-13, 1e6])
+def test_moments_are_those_of_elementary_operations(size, kind):
+    """m, v, the root, the scale and the quotient in fp32, each operation rounded to nearest and
+    none fused: fp32 moments, 8-bit codes and scales are equal bit for bit.  Gradients of `size`
+    down to 1e-8 of it in a block, some zero; betas and a gradient scale that round."""
+    f = np.float32
+    for bits in (32, 8):
+        st, grads, g = A.make([1 << 17, 4099, 255], kind[0], A.F32, bits, kind[1], seed=11)
+        c = moe.AdamWConfig(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8)
+        scale = torch.tensor(0.37, device="cuda")
+        b1, b2, o1, o2 = f(c.beta1), f(c.beta2), f(1 - c.beta1), f(1 - c.beta2)
+        for t in (1, 2, 3):
+            spread = [10.0 ** (-8 * torch.rand(x.shape, generator=g, device="cuda") ** 4) for x in grads]
+            grads = [size * s * torch.randn(s.shape, generator=g, device="cuda") for s in spread]
+            for x in grads:
+                x[torch.rand(x.shape, generator=g, device="cuda") < 0.05] = 0.0
+            all_of = lambda x: x.float().cpu().numpy()  # noqa: E731
+            m, v = all_of(st.exp_avg), all_of(st.exp_avg_sq)
+            if bits == 8:
+                m = m * np.repeat(all_of(st.exp_avg_scale), A.BLOCK)
+                v = np.maximum(v, f(2.0 ** -11)) * np.repeat(all_of(st.exp_avg_sq_scale), A.BLOCK)
+                v = v * v
+            moe.moe_adamw_step(st, grads, c, t, grad_scale=scale)
+            for i, x in enumerate(grads):
+                a = st.starts[i]
+                x = all_of(x) * f(0.37)
+                pad = -len(x) % A.BLOCK
+                x = np.concatenate([x, np.zeros(pad, f)])
+                at = slice(a, a + len(x))
+                m[at] = m[at] * b1 + x * o1
+                v[at] = v[at] * b2 + (x * o2) * x
+            assert m.dtype == v.dtype == f
+            if bits == 32:
+                assert np.array_equal(m, all_of(st.exp_avg)) and np.array_equal(v, all_of(st.exp_avg_sq))
+                continue
+            for x, flat, scales in ((m, st.exp_avg, st.exp_avg_scale),
+                                    (np.sqrt(v), st.exp_avg_sq, st.exp_avg_sq_scale)):
+                x = x.reshape(-1, A.BLOCK)
+                unit = np.abs(x).max(axis=1) * f(1 / 448)
+                assert np.array_equal(unit, all_of(scales))
+                with np.errstate(divide="ignore", invalid="ignore"):
+                    q = np.where(unit[:, None] > 0, x / unit[:, None], f(0))
+                codes = torch.from_numpy(q.reshape(-1)).to(torch.float8_e4m3fn)
+                assert torch.equal(codes.view(torch.uint8), flat.cpu().view(torch.uint8))
