@@ -568,7 +568,7 @@ moe_status moe_layer_norm_backward(const void* dy, const void* h, const float* s
  * and choices are not looked at.  ws (forward): moe_balance_workspace_size
  * bytes, about 8 E for each sequence and each block of up to T / 304 tokens; the
  * backward takes none.  Limits: 1 <= S <= MOE_MAX_SEQUENCES, alpha
- * finite.
+ * and alpha E / (S k) finite in fp32.
  */
 #define MOE_MAX_SEQUENCES 65536
 size_t moe_balance_workspace_size(int T, int E, int S);
@@ -629,8 +629,9 @@ moe_status moe_balance_loss_backward(const float* dloss, const int32_t* counts,
  * param_type, grad_type: moe_dtype, of all tensors of the call; masters only
  * beside bf16 parameters.  Tensors and scales are 16-byte aligned, the other
  * state arrays 32-byte.  No tensor may appear twice.
- * 0 <= beta < 1, eps a normal fp32 number, weight_decay, decay and
- * lr finite, step >= 1 (with step_at it is not looked at).  ws: 256 bytes.
+ * 0 <= beta < 1, eps a normal fp32 number, lr, weight_decay, decay and
+ * weight_decay * decay finite in fp32, step >= 1 (with step_at it is not looked
+ * at).  ws: 256 bytes.
  */
 #define MOE_ADAMW_BLOCK 256
 typedef struct {

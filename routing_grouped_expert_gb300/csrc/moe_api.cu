@@ -853,14 +853,17 @@ moe_status moe_plan_replicas(const int32_t* counts, int E, int G, int beta, int 
 
 namespace {
 bool is_finite(double v) { return v - v == 0.0; }
+bool is_finite_f32(double v) { return is_finite((float)v); }   // as the kernels take it
 bool ok_norm_sizes(int T, int H) { return T >= 0 && H >= 1 && H <= MOE_MAX_NORM_WIDTH; }
 bool ok_norm_types(int type, int weight_type) {
   return (type == MOE_F32 && weight_type == MOE_F32) ||
          (type == MOE_BF16 && (weight_type == MOE_F32 || weight_type == MOE_BF16));
 }
+double balance_factor(float alpha, int E, int k, int S) { return (double)alpha * E / ((double)S * k); }
 bool ok_balance_sizes(int T, int E, int k, int S, int score, float alpha) {
   return ok_route_sizes(T, E, k) && S >= 1 && S <= MOE_MAX_SEQUENCES &&
-         (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID) && is_finite(alpha);
+         (score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID) &&
+         is_finite_f32(balance_factor(alpha, E, k, S));
 }
 BalanceArgs balance_args(const float* logits, int score, float alpha, const int32_t* seq_offsets,
                          const uint8_t* mask, int T, int E, int k, int S) {
@@ -873,7 +876,7 @@ BalanceArgs balance_args(const float* logits, int score, float alpha, const int3
   a.k = k;
   a.S = S;
   a.softmax = score == MOE_SCORE_SOFTMAX;
-  a.factor = (float)((double)alpha * E / ((double)S * k));
+  a.factor = (float)balance_factor(alpha, E, k, S);
   return a;
 }
 }  // namespace
@@ -969,8 +972,8 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, const void* const* gr
     return MOE_ERR_INVALID_ARG;
   const moe_adamw_config& c = *config;
   const auto beta_ok = [](double b) { return b >= 0.0 && b < 1.0; };
-  if (!is_finite(c.lr) || !beta_ok(c.beta1) || !beta_ok(c.beta2) || !is_finite(c.eps) ||
-      !(c.eps >= 1.17549435e-38) || !is_finite(c.weight_decay) || (c.state_bits != 32 && c.state_bits != 8) ||
+  if (!is_finite_f32(c.lr) || !beta_ok(c.beta1) || !beta_ok(c.beta2) || !is_finite_f32(c.eps) ||
+      !(c.eps >= 1.17549435e-38) || !is_finite_f32(c.weight_decay) || (c.state_bits != 32 && c.state_bits != 8) ||
       (step_at == nullptr && step < 1))
     return MOE_ERR_INVALID_ARG;
   const auto aligned32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };
@@ -982,7 +985,8 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, const void* const* gr
   for (int i = 0; i < count; ++i) {
     const moe_adamw_tensor& t = tensors[i];
     if (t.n < 0 || t.start < 0 || t.start % MOE_ADAMW_BLOCK != 0 ||
-        t.start / MOE_ADAMW_BLOCK > 0xffffffffLL || t.n >= (1LL << 40) || !is_finite(t.decay) ||
+        t.start / MOE_ADAMW_BLOCK > 0xffffffffLL || t.n >= (1LL << 40) || !is_finite_f32(t.decay) ||
+        !is_finite_f32(c.weight_decay * t.decay) ||
         (t.n > 0 && (!ok_ptr(t.param) || !ok_ptr(grads[i]))))
       return MOE_ERR_INVALID_ARG;
     any |= t.n > 0;
