@@ -124,6 +124,15 @@ def _check(code: int, what: str):
         raise MoeError(code, what)
 
 
+def _refused(code: int, what: str, **tensors):
+    """_check of a call that failed, naming a tensor that is not 16-byte aligned."""
+    if code == 1:
+        for name, t in tensors.items():
+            if t is not None and t.data_ptr() % 16:
+                raise MoeError(code, f"{what}: {name} is not 16-byte aligned")
+    _check(code, what)
+
+
 def _p(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -784,9 +793,12 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias=None, eps: float 
         _beside(stats, torch.float32, (T, 2), dev, "stats")
     elif want_stats:
         stats = torch.empty((T, 2), dtype=torch.float32, device=x.device)
-    _check(load_library().moe_layer_norm(_p(x), _p(residual), _p(weight), _p(bias), eps, T, H, dt,
+    code = load_library().moe_layer_norm(_p(x), _p(residual), _p(weight), _p(bias), eps, T, H, dt,
                                          wt, _p(y), None if residual is None else _p(h), _p(stats),
-                                         _stream()), "moe_layer_norm")
+                                         _stream())
+    if code != MOE_OK:
+        _refused(code, "moe_layer_norm", x=x, residual=residual, weight=weight, bias=bias, y=y,
+                 h=h, stats=stats)
     return y, x if residual is None else h, stats
 
 
@@ -818,9 +830,12 @@ def moe_layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, stats: torch.Tens
     dw = torch.empty_like(weight)
     db = torch.empty_like(weight) if has_bias else None
     buf = _ws(ws, moe_layer_norm_workspace_size(T, H)).buf
-    _check(load_library().moe_layer_norm_backward(
+    code = load_library().moe_layer_norm_backward(
         _p(dy), _p(h), _p(stats), _p(weight), _p(dh), T, H, dt, wt, _p(dx), _p(dw), _p(db),
-        _p(buf), buf.numel(), _stream()), "moe_layer_norm_backward")
+        _p(buf), buf.numel(), _stream())
+    if code != MOE_OK:
+        _refused(code, "moe_layer_norm_backward", dy=dy, h=h, stats=stats, weight=weight, dh=dh,
+                 dx=dx)
     return dx, dw, db
 
 
@@ -859,9 +874,12 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, alpha: float,
     counts = torch.empty((S, E), dtype=torch.int32, device=device)
     tokens = torch.empty((S,), dtype=torch.int32, device=device)
     buf = _ws(ws, moe_balance_workspace_size(T, E, S)).buf
-    _check(load_library().moe_balance_loss(
+    code = load_library().moe_balance_loss(
         _p(logits), _p(topk_idx), ROUTE_SCORES[score], alpha, _p(seq_offsets), _p(mask), T, E, k, S,
-        _p(loss), _p(counts), _p(tokens), _p(buf), buf.numel(), _stream()), "moe_balance_loss")
+        _p(loss), _p(counts), _p(tokens), _p(buf), buf.numel(), _stream())
+    if code != MOE_OK:
+        _refused(code, "moe_balance_loss", logits=logits, topk_idx=topk_idx,
+                 seq_offsets=seq_offsets, mask=mask)
     return loss, counts, tokens
 
 
@@ -882,10 +900,12 @@ def moe_balance_loss_backward(dloss, counts: torch.Tensor, tokens: torch.Tensor,
     else:
         _beside(onto, torch.float32, (T, E), dev, "onto")
         dlogits = onto
-    _check(load_library().moe_balance_loss_backward(
+    code = load_library().moe_balance_loss_backward(
         _p(dloss), _p(counts), _p(tokens), _p(logits), ROUTE_SCORES[score], alpha,
-        _p(seq_offsets), _p(mask), T, E, k, S, int(onto is not None), _p(dlogits), _stream()),
-        "moe_balance_loss_backward")
+        _p(seq_offsets), _p(mask), T, E, k, S, int(onto is not None), _p(dlogits), _stream())
+    if code != MOE_OK:
+        _refused(code, "moe_balance_loss_backward", counts=counts, tokens=tokens, logits=logits,
+                 seq_offsets=seq_offsets, mask=mask, onto=onto)
     return dlogits
 
 
@@ -997,7 +1017,7 @@ class AdamWState:
 def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None, grad_scale=None,
                    ws: Workspace | None = None) -> None:
     """One AdamW step on the state's parameters, in place, by gradients of their
-    shapes (all bf16 or all fp32).  step: its number (1 for the first), or an
+    shapes (all bf16 or all fp32; 16-byte aligned).  step: its number (1 for the first), or an
     int64 tensor of one element that holds it on the device; lr, grad_scale:
     device scalars, in the place of config.lr and 1."""
     grads, n = list(grads), len(state.params)
@@ -1035,11 +1055,13 @@ def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None,
     c = _AdamWConfigStruct(config.lr, config.beta1, config.beta2, config.eps, config.weight_decay,
                            state.bits)
     buf = _ws(ws, 256).buf
-    _check(load_library().moe_adamw_step(
+    code = load_library().moe_adamw_step(
         state._table, table.buffer_info()[0], n, state.param_type, gt,
         ctypes.byref(c), step, _p(step_at), _p(lr), _p(grad_scale), _p(state.master),
         _p(state.exp_avg), _p(state.exp_avg_sq), _p(state.exp_avg_scale),
-        _p(state.exp_avg_sq_scale), _p(buf), buf.numel(), _stream()), "moe_adamw_step")
+        _p(state.exp_avg_sq_scale), _p(buf), buf.numel(), _stream())
+    if code != MOE_OK:
+        _refused(code, "moe_adamw_step", **{f"grads[{i}]": g for i, g in enumerate(grads) if g.numel()})
 
 
 def moe_plan_workspace_size(E: int, G: int) -> int:

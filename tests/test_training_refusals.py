@@ -1,9 +1,11 @@
 """What the training operators refuse on the host: factors that are finite in 64 bits and not in
-the fp32 that the kernels work with."""
+the fp32 that the kernels work with; tensors that are not 16-byte aligned, by name."""
 import ctypes
 
 import pytest
+import torch
 
+import routing_grouped_expert_gb300 as moe
 from routing_grouped_expert_gb300 import binding
 
 P = ctypes.c_void_p(4096)   # never read
@@ -29,3 +31,30 @@ def test_balance_refuses_factors_that_leave_fp32():
                                 None) == INVALID
     assert lib.moe_balance_loss_backward(None, P, P, P, 0, -3e38, None, None, 4, 8, 2, 1, 0, P,
                                          None) == INVALID
+
+
+@pytest.mark.gpu
+def test_misaligned_tensors_are_named():
+    """Views cut out of a buffer at odd places."""
+    cut = lambda n, dtype, at=1: torch.zeros(n + at, dtype=dtype, device="cuda")[at:]  # noqa: E731
+    whole = lambda *n: torch.zeros(n, device="cuda")  # noqa: E731
+
+    def names(name, call, *args, **kw):
+        with pytest.raises(moe.MoeError, match=name + " is not 16-byte aligned"):
+            call(*args, **kw)
+
+    st = moe.AdamWState([whole(5), whole(0), whole(100)])
+    names(r"grads\[2\]", moe.moe_adamw_step, st, [whole(5), whole(0), cut(100, torch.float32)],
+          moe.AdamWConfig(), 1)
+    x = whole(4, 16)
+    names("weight", moe.moe_layer_norm, x, cut(16, torch.float32))
+    names("x", moe.moe_layer_norm, cut(64, torch.float32).view(4, 16), whole(16))
+    names("dh", moe.moe_layer_norm_backward, x, x, whole(4, 2), whole(16),
+          dh=cut(64, torch.float32).view(4, 16))
+    idx = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    offsets = cut(2, torch.int32)
+    names("mask", moe.moe_balance_loss, x, idx, 0.1, mask=cut(4, torch.bool))
+    names("seq_offsets", moe.moe_balance_loss, x, idx, 0.1, seq_offsets=offsets)
+    _, counts, tokens = moe.moe_balance_loss(x, idx, 0.1)
+    names("mask", moe.moe_balance_loss_backward, None, counts, tokens, x, 2, 0.1,
+          mask=cut(4, torch.bool))
