@@ -1049,8 +1049,8 @@ def moe_adamw_step(state: AdamWState, grads, config: AdamWConfig, step, lr=None,
             raise ValueError("step: expected an int, or one int64 value on the device")
         step_at, step = step, 1
     for name, t in (("lr", lr), ("grad_scale", grad_scale)):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != 1 or
-                              t.get_device() != dev):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or
+                              t.numel() != 1 or t.get_device() != dev):
             raise ValueError(f"{name}: expected one float32 value on the device")
     c = _AdamWConfigStruct(config.lr, config.beta1, config.beta2, config.eps, config.weight_decay,
                            state.bits)

@@ -58,3 +58,11 @@ def test_misaligned_tensors_are_named():
     _, counts, tokens = moe.moe_balance_loss(x, idx, 0.1)
     names("mask", moe.moe_balance_loss_backward, None, counts, tokens, x, 2, 0.1,
           mask=cut(4, torch.bool))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["lr", "grad_scale"])
+def test_numbers_in_the_place_of_device_scalars(name):
+    st = moe.AdamWState([torch.zeros(5, device="cuda")])
+    with pytest.raises(ValueError, match=name):
+        moe.moe_adamw_step(st, [torch.zeros(5, device="cuda")], moe.AdamWConfig(), 1, **{name: 0.1})
