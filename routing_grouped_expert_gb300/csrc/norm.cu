@@ -44,9 +44,9 @@ __device__ __forceinline__ float2 join_moments(int H, float count, float u, floa
 // thread.  A row stays in registers as it lies in memory.
 template <typename T, typename W, int n, bool kVec, bool kResidual, int L, int kTeam, int kPer>
 __global__ void __launch_bounds__(kTeam, kPer)
-norm_kernel(const T* __restrict__ x, const T* __restrict__ residual, const W* __restrict__ weight,
-            const W* __restrict__ bias, float eps, int rows, int H, T* __restrict__ y,
-            T* __restrict__ h, float2* __restrict__ stats) {
+norm_kernel(const T* x, const T* residual, const W* __restrict__ weight,
+            const W* __restrict__ bias, float eps, int rows, int H, T* y, T* h,
+            float2* __restrict__ stats) {
   constexpr bool kBlock = L == 0;
   constexpr int kLanes = kBlock ? 32 : L;
   __shared__ Moments sh;

@@ -10,14 +10,16 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// Eight values as they lie in memory: one 16-byte access of bf16, two of fp32.
+// Eight values as they lie in memory: one 16-byte access of bf16, two of fp32.  load_column:
+// of memory that no kernel here writes; rows may be those that the same kernel writes (h in the
+// place of x, dx in that of dy).
 template <typename T>
 struct Eight;
 template <>
 struct Eight<bf16> {
   uint4 v;
-  __device__ __forceinline__ void load(const bf16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void load_shared(const bf16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_column(const bf16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ float2 pair(int i) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -51,12 +53,12 @@ template <>
 struct Eight<float> {
   float4 v[2];
   __device__ __forceinline__ void load(const float* p) {
-    v[0] = __ldg(reinterpret_cast<const float4*>(p));
-    v[1] = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void load_shared(const float* p) {
     v[0] = reinterpret_cast<const float4*>(p)[0];
     v[1] = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void load_column(const float* p) {
+    v[0] = __ldg(reinterpret_cast<const float4*>(p));
+    v[1] = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = v[0];
@@ -126,7 +128,7 @@ template <bool kShared = false, bool kVec, typename T>
 __device__ __forceinline__ void get(Eight<T>& e, const T* row, int i, const Team& t) {
   const int c = column<kVec>(t, i);
   if constexpr (kShared) {
-    if (c < t.H) e.load_shared(row + c);
+    if (c < t.H) e.load(row + c);
     else e.zero();
     if (!kVec && c < t.H && !whole<kVec>(t, c)) e.keep(inside<kVec>(i, t));
   } else if (whole<kVec>(t, c)) {
@@ -168,10 +170,11 @@ __device__ __forceinline__ void skip_words(uint32_t (&x)[have], int skip) {
 // one by one, a warp's take four passes through L1 each.
 template <bool kVec, typename W>
 __device__ __forceinline__ void get_column(Eight<W>& e, const W* w, int i, const Team& t) {
+  const int c = column<kVec>(t, i);
   if constexpr (kVec) {
-    get<false, kVec>(e, w, i, t);
+    if (c < t.H) e.load_column(w + c);
+    else e.zero();
   } else {
-    const int c = column<kVec>(t, i);
     constexpr int kPiece = 16 / sizeof(W);
     const int s = c & (kPiece - 1);
     // the pieces lie within the array, or are those of its end

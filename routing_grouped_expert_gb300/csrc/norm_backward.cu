@@ -130,9 +130,8 @@ struct Backward {
 // Rows too wide for a ring of two: read where they lie.
 template <typename T, typename W, int n, bool kVec, int kTeam>
 __global__ void __launch_bounds__(kTeam, 1)
-norm_backward_kernel(const T* __restrict__ dy, const T* __restrict__ h,
-                     const float2* __restrict__ stats, const W* __restrict__ weight,
-                     const T* __restrict__ dh, int rows, int H, T* __restrict__ dx,
+norm_backward_kernel(const T* dy, const T* h, const float2* __restrict__ stats,
+                     const W* __restrict__ weight, const T* dh, int rows, int H, T* dx,
                      float* __restrict__ part, int* __restrict__ flags) {
   pdl_trigger();
   __shared__ float2 sums[2][32];
@@ -198,10 +197,9 @@ struct RowRing {
 // Rows fetched ahead by bulk copies.  flags [gridDim.x]: whether a copy did not come.
 template <typename T, typename W, int n, bool kVec, int kTeam, int kPer>
 __global__ void __launch_bounds__(kTeam, kPer)
-norm_backward_ring_kernel(const T* __restrict__ dy, const T* __restrict__ h,
-                          const float2* __restrict__ stats, const W* __restrict__ weight,
-                          const T* __restrict__ dh, int rows, int H, int stages,
-                          T* __restrict__ dx, float* __restrict__ part, int* __restrict__ flags) {
+norm_backward_ring_kernel(const T* dy, const T* h, const float2* __restrict__ stats,
+                          const W* __restrict__ weight, const T* dh, int rows, int H, int stages,
+                          T* dx, float* __restrict__ part, int* __restrict__ flags) {
   pdl_trigger();   // the next kernel waits for this one's end all the same
   extern __shared__ __align__(16) char smem[];
   __shared__ uint64_t full[kMaxStages];
