@@ -747,6 +747,17 @@ moe_status moe_diag_wait_timeout(void* ws, size_t ws_bytes, long long limit_ns,
 moe_status moe_diag_count_wait_timeout(void* ws, size_t ws_bytes, long long limit_ns,
                                        void* stream);
 
+/*
+ * Diagnostic (no counterpart on the pages): for the calling thread's calls of
+ * moe_balance_loss and moe_layer_norm_backward from here on, bounded waits run
+ * out after `limit_ns` (1 ms .. 2 s; 0: their usual second), and a part that
+ * others wait for -- the first block's sums, or its first row -- comes late by
+ * as many nanoseconds as the device int64 at `hold_at` holds (2 s at most; null:
+ * by none).  The word is read when the call runs, so a captured call can be late
+ * once.  With both 0 calls are as usual again.
+ */
+moe_status moe_diag_hold(const int64_t* hold_at, long long limit_ns);
+
 /* Static, NUL-terminated description of a status code. */
 const char* moe_status_string(moe_status s);
 

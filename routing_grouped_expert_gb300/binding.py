@@ -54,6 +54,7 @@ SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_diag_wait_timeout": (_I, [_VP, _SZ, ctypes.c_longlong, _VP]),
     "moe_diag_count_wait_timeout": (_I, [_VP, _SZ, ctypes.c_longlong, _VP]),
+    "moe_diag_hold": (_I, [_VP, ctypes.c_longlong]),
     "moe_workspace_size_train": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_forward_train": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _SZ, _VP]),
     "moe_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP,
@@ -236,6 +237,12 @@ def moe_diag_count_wait_timeout(ws: Workspace, limit_ns: int) -> None:
     """Make the bounded token-block counter wait run out (see include/moe.h)."""
     _check(load_library().moe_diag_count_wait_timeout(ws.ptr, ws.nbytes, limit_ns, _stream()),
            "moe_diag_count_wait_timeout")
+
+
+def moe_diag_hold(hold_at: torch.Tensor | None = None, limit_ns: int = 0) -> None:
+    """Shorten bounded waits of this thread's calls, and hold up a part that is waited for (see
+    include/moe.h)."""
+    _check(load_library().moe_diag_hold(_p(hold_at), limit_ns), "moe_diag_hold")
 
 
 def moe_route_topk(logits: torch.Tensor, k: int, topk_idx=None, topk_w=None,

@@ -36,7 +36,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // Over the L lanes of a row, for R rows at once.
 template <int L, int R>
@@ -359,13 +358,14 @@ __device__ __forceinline__ void sum_tokens(const BalanceArgs& a, int block, Bala
 
 // Wait for what other blocks write: until *at is `launch` but for its two lowest bits, which
 // are returned; 4: the wait ran out.
-__device__ __forceinline__ int wait_for(const uint64_t* at, uint64_t launch) {
+__device__ __forceinline__ int wait_for(const uint64_t* at, uint64_t launch,
+                                        uint64_t limit) {
   uint64_t v;
   const uint64_t t0 = ptx::globaltimer_ns();
   do {
     asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
     if ((v & ~3ull) == launch) return (int)(v & 3u);
-  } while (ptx::globaltimer_ns() - t0 < kWaitLimitNs);
+  } while (ptx::globaltimer_ns() - t0 < limit);
   return 4;
 }
 __device__ __forceinline__ void announce(uint64_t* at, uint64_t launch) {
@@ -380,7 +380,8 @@ __device__ __forceinline__ void post(uint64_t* at, uint64_t launch, uint32_t bit
   asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(w0) : "memory");
   asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at + 1), "l"(w1) : "memory");
 }
-__device__ __forceinline__ uint32_t wait_posted(const uint64_t* at, uint64_t launch) {
+__device__ __forceinline__ uint32_t wait_posted(const uint64_t* at, uint64_t launch,
+                                                uint64_t limit) {
   const uint64_t t0 = ptx::globaltimer_ns();
   do {
     uint64_t w0, w1;
@@ -388,7 +389,7 @@ __device__ __forceinline__ uint32_t wait_posted(const uint64_t* at, uint64_t lau
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w1) : "l"(at + 1) : "memory");
     const uint32_t bits = (uint32_t)w0;
     if (w0 == ((launch & ~0xffffffffull) | bits) && w1 == (launch << 32 | bits)) return bits;
-  } while (ptx::globaltimer_ns() - t0 < kWaitLimitNs);
+  } while (ptx::globaltimer_ns() - t0 < limit);
   return kLate;
 }
 
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(B
   extern __shared__ float sums[];   // [kWarps * 32 / L][E]
   const int block = blockIdx.x, blocks = a.blocks;
   if (block < blocks) {
+    if (block == 0 && threadIdx.x == 0) ptx::hold_up(a.hold.at);
     sum_tokens<S>(a, block, sh, sums);
     // the threads' slots, seen by this one past a barrier, are released with the word
     if (threadIdx.x == 0) announce(a.done + block, a.launch | (uint64_t)sh.bad);
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(B
       if (o < 0 || o > a.T || (s > 0 && o < __ldg(a.seq_offsets + s - 1))) bad |= 2;
     }
   const float share = add_slots(a, rank, sh, [&]() {
-    for (int b = threadIdx.x; b < blocks; b += kThreads) bad |= wait_for(a.done + b, a.launch);
+    for (int b = threadIdx.x; b < blocks; b += kThreads) bad |= wait_for(a.done + b, a.launch, a.hold.limit);
     __syncthreads();
   });
   uint64_t* added = a.done + blocks;   // two words each
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(B
   float v = 0.f;
   if (threadIdx.x < 32)
     for (int r = threadIdx.x; r < a.adders - 1; r += 32) {
-      const uint32_t bits = wait_posted(added + 2 * r, a.launch);
+      const uint32_t bits = wait_posted(added + 2 * r, a.launch, a.hold.limit);
       if (bits == kLate) atomicOr(&sh.bad, 4);
       else v += __uint_as_float(bits);
     }
@@ -731,6 +733,7 @@ cudaError_t launch_sum(const BalanceArgs& a, cudaStream_t s) {
 }
 cudaError_t launch_balance(BalanceArgs a, cudaStream_t s) {
   a.launch = unique_number() << 2;
+  a.hold = diag_hold();
 #define CASE(S) return launch_sum<MOE_UNWRAP S>(a, s)
   MOE_BALANCE_SHAPE(a.E, CASE);
 #undef CASE

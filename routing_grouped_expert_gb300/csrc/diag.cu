@@ -26,7 +26,22 @@ __global__ void count_wait_timeout_kernel(int* status, const int* cnt,
     moe::set_status(status, MOE_ERR_TIMEOUT, moe::kWaitDetailDrain + 2);
 }
 
+thread_local moe::Hold g_hold{1000000000ull, nullptr};
+
 }  // namespace
+
+namespace moe {
+Hold diag_hold() { return g_hold; }
+}  // namespace moe
+
+extern "C" moe_status moe_diag_hold(const int64_t* hold_at, long long limit_ns) {
+  if ((reinterpret_cast<uintptr_t>(hold_at) & 7u) != 0 ||
+      (limit_ns != 0 && (limit_ns < 1000000LL || limit_ns > 2000000000LL)))
+    return MOE_ERR_INVALID_ARG;
+  g_hold = moe::Hold{limit_ns != 0 ? (uint64_t)limit_ns : 1000000000ull,
+                     reinterpret_cast<const long long*>(hold_at)};
+  return MOE_OK;
+}
 
 extern "C" moe_status moe_diag_count_wait_timeout(void* ws, size_t ws_bytes, long long limit_ns,
                                                   void* stream) {

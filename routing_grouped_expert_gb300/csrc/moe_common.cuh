@@ -458,6 +458,14 @@ cudaError_t launch_adapter_backward(const AdapterSizes& z, const __nv_bfloat16* 
                                     __nv_bfloat16* dx, __nv_bfloat16* dA, __nv_bfloat16* dB,
                                     void* ws, cudaStream_t s);
 
+// What moe_diag_hold asks for: when the waits of the calling thread's launches run out, and how
+// long a part that others wait for is held up (device; null: not).
+struct Hold {
+  uint64_t limit;
+  const long long* at;
+};
+Hold diag_hold();
+
 // Layer norm (norm.cu).  type, weight_type: moe_dtype.
 constexpr int kNormHeader = 16384;   // bytes ahead of the shares in the backward's workspace:
                                     // the status word, then a flag for each block
@@ -493,6 +501,7 @@ struct BalanceArgs {
   float* loss;                  // outputs
   int32_t* counts;              // [S, E]
   int32_t* tokens;              // [S]
+  Hold hold;
 };
 // Workspace bytes; fills in the workspace pointers and the launch shape of `a`.
 size_t balance_layout(int T, int E, int S, BalanceArgs* a, void* ws);

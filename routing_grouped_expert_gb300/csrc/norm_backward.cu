@@ -155,7 +155,6 @@ norm_backward_kernel(const T* dy, const T* h, const float2* __restrict__ stats,
 // come by bulk copies of whole 16-byte pieces: where rows do not start on one, a copy takes
 // the pieces that its row touches, and the last few values of a tensor that does not end on
 // one are copied one by one.
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr int kMaxStages = 8;
 template <typename T>
 struct RowRing {
@@ -199,7 +198,7 @@ template <typename T, typename W, int n, bool kVec, int kTeam, int kPer>
 __global__ void __launch_bounds__(kTeam, kPer)
 norm_backward_ring_kernel(const T* dy, const T* h, const float2* __restrict__ stats,
                           const W* __restrict__ weight, const T* dh, int rows, int H, int stages,
-                          T* dx, float* __restrict__ part, int* __restrict__ flags) {
+                          T* dx, float* __restrict__ part, int* __restrict__ flags, Hold hold) {
   pdl_trigger();   // the next kernel waits for this one's end all the same
   extern __shared__ __align__(16) char smem[];
   __shared__ uint64_t full[kMaxStages];
@@ -216,6 +215,7 @@ norm_backward_ring_kernel(const T* dy, const T* h, const float2* __restrict__ st
   __syncthreads();
   long long ahead = blockIdx.x;   // the next row to be fetched
   const int cut = kVec ? 0 : cut_of<T>(blockIdx.x, H);   // of all of the block's rows
+  if (me == 0 && blockIdx.x == 0) ptx::hold_up(hold.at);
   if (me == 0)
     for (int s = 0; s < stages && ahead < rows; ++s, ahead += gridDim.x)
       ring.fetch(s, ahead, cut, from);
@@ -225,10 +225,12 @@ norm_backward_ring_kernel(const T* dy, const T* h, const float2* __restrict__ st
   float2 next = __ldg(stats + blockIdx.x);
   int turn = 0, stage = 0;
   uint32_t phase = 0;
-  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+  long long at = blockIdx.x;   // the row that is worked on
+  for (; at < rows; at += gridDim.x) {
+    const long long row = at;
     const float2 st = next;
     if (row + gridDim.x < rows) next = __ldg(stats + row + gridDim.x);
-    if (!ptx::mbar_wait(&full[stage], phase, nullptr, kWaitLimitNs)) dead[turn] = 1;
+    if (!ptx::mbar_wait(&full[stage], phase, nullptr, hold.limit)) dead[turn] = 1;
     float2 s = b.template take<true>(ring.row(stage, 0, cut), ring.row(stage, 1, cut),
                                      dh != nullptr ? ring.row(stage, 2, cut) : nullptr, st);
     s = block_sum2<kTeam>(s, sums[turn]);   // the other half is read no more: one barrier ago
@@ -248,9 +250,16 @@ norm_backward_ring_kernel(const T* dy, const T* h, const float2* __restrict__ st
   if (me == 0) {
     const bool late = dead[0] | dead[1];
     flags[blockIdx.x] = late;
-    // what is still on its way has to arrive before the block's memory is another's
+    // what is still on its way has to arrive before the block's memory is another's: the rows
+    // from the one that was waited for to the last that was asked for, a place further each
     if (late)
-      for (int s = 0; s < stages; ++s) ptx::mbar_wait(&full[s], phase ^ (s < stage), nullptr, kWaitLimitNs);
+      for (; at < ahead; at += gridDim.x) {
+        ptx::mbar_wait(&full[stage], phase, nullptr, hold.limit);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
   }
   b.end(part + (size_t)blockIdx.x * 2 * H);
 }
@@ -342,7 +351,7 @@ cudaError_t backward_t(const void* dy, const void* h, const float* stats, const 
     const cudaError_t e = allow_smem(kern, stages * stage, ring_bytes(f.per));                    \
     if (e != cudaSuccess) return e;                                                               \
     kern<<<blocks, team_of(H, f.n), stages * stage, s>>>(gt, ht, st, wt, rt, rows, H, stages, xt, part, \
-                                                         flags);                                  \
+                                                         flags, diag_hold());                                  \
   } while (0)
   if (rows > 0) {
     switch (shape_of(H)) {

@@ -21,6 +21,16 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// Comes back as many nanoseconds later as the word at `at` holds, two seconds at most; at once
+// without one.
+__device__ __forceinline__ void hold_up(const long long* at) {
+  if (at == nullptr) return;
+  const long long ns = *reinterpret_cast<const volatile long long*>(at);
+  const uint64_t t0 = globaltimer_ns();
+  while ((long long)(globaltimer_ns() - t0) < (ns < 2000000000ll ? ns : 2000000000ll)) {
+  }
+}
+
 // ------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
