@@ -368,8 +368,23 @@ __device__ __forceinline__ int wait_for(const uint64_t* at, uint64_t launch,
   } while (ptx::globaltimer_ns() - t0 < limit);
   return 4;
 }
-__device__ __forceinline__ void announce(uint64_t* at, uint64_t launch) {
-  asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(launch) : "memory");
+// The words of a launch are cleared before it ends, since a captured one comes again under its
+// number: by the last block, which has seen them all.  Where it gave up it exchanges them for
+// `spent`, and a block that then finds that in its word clears it itself.
+__device__ __forceinline__ uint64_t spent(uint64_t launch) { return launch ^ 4u; }   // no launch's
+__device__ __forceinline__ void clear(uint64_t* at) {
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(0ull) : "memory");
+}
+__device__ __forceinline__ uint64_t exchange(uint64_t* at, uint64_t v) {
+  uint64_t old;
+  asm volatile("atom.exch.relaxed.gpu.global.b64 %0, [%1], %2;" : "=l"(old) : "l"(at), "l"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ void announce(uint64_t* at, uint64_t launch, int bits) {
+  uint64_t old;
+  asm volatile("atom.exch.release.gpu.global.b64 %0, [%1], %2;"
+               : "=l"(old) : "l"(at), "l"(launch | (uint64_t)bits) : "memory");
+  if (old == spent(launch)) clear(at);
 }
 // A number handed to another block in the words that announce it, beside one half of the
 // launch's number each: nothing else has to be visible with it, and a store that waits for
@@ -378,7 +393,10 @@ constexpr uint32_t kLate = 0x7fc0dead;   // a NaN that no arithmetic makes
 __device__ __forceinline__ void post(uint64_t* at, uint64_t launch, uint32_t bits) {
   const uint64_t w0 = (launch & ~0xffffffffull) | bits, w1 = launch << 32 | bits;
   asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at), "l"(w0) : "memory");
-  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(at + 1), "l"(w1) : "memory");
+  if (exchange(at + 1, w1) == spent(launch)) {
+    clear(at);
+    clear(at + 1);
+  }
 }
 __device__ __forceinline__ uint32_t wait_posted(const uint64_t* at, uint64_t launch,
                                                 uint64_t limit) {
@@ -493,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(B
     if (block == 0 && threadIdx.x == 0) ptx::hold_up(a.hold.at);
     sum_tokens<S>(a, block, sh, sums);
     // the threads' slots, seen by this one past a barrier, are released with the word
-    if (threadIdx.x == 0) announce(a.done + block, a.launch | (uint64_t)sh.bad);
+    if (threadIdx.x == 0) announce(a.done + block, a.launch, sh.bad);
     return;
   }
   const int rank = block - blocks;
@@ -527,8 +545,17 @@ __global__ void __launch_bounds__(kThreads, S::n <= 16 ? 2 : 1) balance_kernel(B
       else v += __uint_as_float(bits);
     }
   __syncthreads();
-  // nobody reads the numbers any more: a captured launch comes again under the same one
-  for (int b = threadIdx.x; b < blocks + 2 * a.adders; b += kThreads) a.done[b] = 0;
+  if (sh.bad & 4) {   // some are still to come
+    for (int b = threadIdx.x; b < blocks; b += kThreads)
+      if ((exchange(a.done + b, spent(a.launch)) & ~3ull) == a.launch) clear(a.done + b);
+    for (int r = threadIdx.x; r < a.adders - 1; r += kThreads)
+      if (exchange(added + 2 * r + 1, spent(a.launch)) >> 32 == (a.launch & 0xffffffffull)) {
+        clear(added + 2 * r);
+        clear(added + 2 * r + 1);
+      }
+  } else {
+    for (int b = threadIdx.x; b < blocks + 2 * a.adders; b += kThreads) a.done[b] = 0;
+  }
   if (threadIdx.x < 32) {
     v = warp_sum(v) + share;
     if (threadIdx.x == 0) {

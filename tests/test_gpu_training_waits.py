@@ -77,3 +77,27 @@ def test_limits_are_checked_and_put_back():
     ws = moe.Workspace()
     moe.moe_balance_loss(l, idx, 0.01, ws=ws, **kw)
     assert moe.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T", [40, 3000, 60000])
+def test_replay_after_a_late_one(hold, T):
+    """A replay in which a block came late, after the others had given up, and then one with
+    other inputs in which it comes last, but in time: that one is right, its status clean."""
+    case = (T, 40, 4, [0, T // 3, T], True)
+    (l, idx, kw), (l2, idx2, kw2) = balance(case), balance(case, seed=5)
+    ws = moe.Workspace()
+    call = lambda: moe.moe_balance_loss(l, idx, 0.01, ws=ws, **kw)  # noqa: E731
+    want = moe.moe_balance_loss(l2, idx2, 0.01, **kw2)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    hold.fill_(5 * LIMIT)
+    graph.replay()
+    assert moe.moe_get_device_status(ws) == TIMEOUT
+    for a, b in ((l, l2), (idx, idx2), (kw["mask"], kw2["mask"])):
+        a.copy_(b)
+    hold.fill_(LIMIT // 4)
+    graph.replay()
+    assert moe.moe_get_device_status(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
