@@ -258,14 +258,14 @@ struct Group {
   }
   // Their step; returns whether an element was left as it was.
   template <bool kWhole>
-  __device__ __forceinline__ bool step(int left, float rate, float shrink, float root, float gs,
-                                       const Hyper& h);
+  __device__ __forceinline__ bool step(int left, float rate, float keep, float more, float root,
+                                       float gs, const Hyper& h);
 };
 
 template <typename P, typename G, bool kMaster, bool k8>
 template <bool kWhole>
-__device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float rate, float shrink,
-                                                               float root, float gs,
+__device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float rate, float keep,
+                                                               float more, float root, float gs,
                                                                const Hyper& h) {
   float2 m[4], v[4], p[4];
   float2 nan = both(0.f);   // turns NaN with the first moment that is not finite
@@ -300,10 +300,8 @@ __device__ __forceinline__ bool Group<P, G, kMaster, k8>::step(int left, float r
   auto next = [&](int i, const float2& r) {
     const float2 d = __ffma2_rn(r, both(root), both(h.eps));
     const float2 s = __fmul2_rn(m[i], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
-    // all that is added to p, and then one rounding: a factor 1 - lr decay would itself be a
-    // multiple of 2^-24, and a decay of 2e-8 a step none
     const float2 w = rp.get(i);
-    p[i] = __fadd2_rn(w, __ffma2_rn(w, both(shrink), __fmul2_rn(s, both(rate))));
+    p[i] = __ffma2_rn(w, both(keep), __ffma2_rn(w, both(more), __fmul2_rn(s, both(rate))));
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -397,6 +395,9 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
     root = rsqrtf(-expm1f(s * h.log_b2));
   }
   const float rate = -lr * inv1, shrink = -lr * t.decay;
+  // 1 - lr decay as a sum, so that p is rounded once: by itself it would be a multiple of 2^-24,
+  // and a decay of 2e-8 a step none.  Both parts above zero leave an infinite weight as it is.
+  const float keep = __fadd_rd(__fadd_rd(1.f, shrink), -0x1p-24f), more = (1.f - keep) + shrink;
   const float gs = h.grad_scale != nullptr ? __ldg(h.grad_scale) : 1.f;
   // no element takes a step: 8-bit moments would be rounded again by their blocks' largest
   // values, and the scales
@@ -408,7 +409,7 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
   if (whole) {
 #pragma unroll
     for (int u = 0; u < kTurns; ++u)
-      bad |= group[u].template step<true>(8, rate, shrink, root, gs, h);
+      bad |= group[u].template step<true>(8, rate, keep, more, root, gs, h);
   } else {
 #pragma unroll 1
     for (int u = 0; u < kTurns; ++u) {
@@ -424,7 +425,7 @@ adamw_kernel(const __grid_constant__ Table<N> table, State st, Hyper h, int* sta
       part.m_scale += u * (kTurn / MOE_ADAMW_BLOCK);
       part.v_scale += u * (kTurn / MOE_ADAMW_BLOCK);
       part.template load<false>(left);
-      bad |= part.template step<false>(left, rate, shrink, root, gs, h);
+      bad |= part.template step<false>(left, rate, keep, more, root, gs, h);
     }
   }
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0)

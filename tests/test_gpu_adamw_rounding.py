@@ -153,3 +153,30 @@ def test_moments_are_those_of_elementary_operations(size, kind):
                     q = np.where(unit[:, None] > 0, x / unit[:, None], f(0))
                 codes = torch.from_numpy(q.reshape(-1)).to(torch.float8_e4m3fn)
                 assert torch.equal(codes.view(torch.uint8), flat.cpu().view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", A.KINDS, ids=str)
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("decay", [0.0, 0.1])
+def test_infinite_weights_stay_infinite(decay, bits, kind):
+    """A weight held at -inf, as a mask is, is no less by a step; its neighbours step as ever, and
+    the status is clean."""
+    sizes = [700, 300]
+    sets = [A.make(sizes, kind[0], A.F32, bits, kind[1]) for _ in range(2)]
+    c = moe.AdamWConfig(lr=0.01, weight_decay=decay)
+    at = [(0, 3, float("inf")), (0, 699, -float("inf")), (1, 100, -float("inf"))]
+    (st, grads, _), (ref, same, _) = sets
+    for i, j, v in at:
+        st.params[i][j] = v
+        if kind[1]:
+            st.of(st.master, i)[j] = v
+    ws = moe.Workspace()
+    for t in (1, 2, 3):
+        moe.moe_adamw_step(st, grads, c, t, ws=ws)
+        assert moe.moe_get_device_status(ws) == 0
+        moe.moe_adamw_step(ref, same, c, t)
+    for i, j, v in at:
+        assert float(st.params[i][j]) == v
+        ref.params[i][j] = v
+    assert all(torch.equal(a, b) for a, b in zip(st.params, ref.params))
+    assert torch.equal(st.exp_avg.view(torch.uint8), ref.exp_avg.view(torch.uint8))
