@@ -242,6 +242,8 @@ def moe_diag_count_wait_timeout(ws: Workspace, limit_ns: int) -> None:
 def moe_diag_hold(hold_at: torch.Tensor | None = None, limit_ns: int = 0) -> None:
     """Shorten bounded waits of this thread's calls, and hold up a part that is waited for (see
     include/moe.h)."""
+    if hold_at is not None:
+        _need(hold_at, torch.int64, (1,), "hold_at")
     _check(load_library().moe_diag_hold(_p(hold_at), limit_ns), "moe_diag_hold")
 
 

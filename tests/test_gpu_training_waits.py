@@ -71,6 +71,9 @@ def test_limits_are_checked_and_put_back():
         moe.moe_diag_hold(None, 10)
     with pytest.raises(moe.MoeError):
         moe.moe_diag_hold(None, 3_000_000_000)
+    for word in (torch.zeros(1, dtype=torch.int64), torch.zeros(1, dtype=torch.int32, device="cuda")):
+        with pytest.raises((TypeError, ValueError)):     # on the host, of another type
+            moe.moe_diag_hold(word, LIMIT)
     moe.moe_diag_hold(torch.full((1,), 5 * LIMIT, device="cuda"), LIMIT)
     moe.moe_diag_hold()
     l, idx, kw = balance()
