@@ -9,10 +9,10 @@
 // which halves the range its exponents have to span.  The step itself uses m and v before
 // they are rounded.
 //
-// Every array is read and written once, which bounds it: 704 M bf16 parameters in 2.77 ms
-// with fp32 moments and masters (19.7 GB, 1.05 of the rate of a plain copy) and in 1.15 ms
-// with 8-bit moments (7.1 GB, 0.91; the schedulers issue in two thirds of their cycles).
-// 150 ragged tensors of 15.3 M parameters: 68 us (0.93) and, gradients in fp32, 62 us.
+// Every array is read and written once, which bounds it: 704 M bf16 parameters in 2.76 ms
+// with fp32 moments and masters (19.7 GB, 1.05 of the rate of a plain copy) and in 1.10 ms
+// with 8-bit moments (7.1 GB, 0.95; the schedulers issue in three quarters of their cycles).
+// 150 ragged tensors of 15.3 M parameters: 68 us (0.93) and, gradients in fp32, 52 us (0.82).
 //
 // Blocks of 2048 elements in launch order: what is in flight then lies close together in
 // each array.  A block that went on to further chunks, with its loads ahead in registers or
@@ -33,7 +33,7 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 // Groups of eight elements per thread, all on their way at once, and blocks per SM.  8-bit
-// moments, ms: 128 threads of one group 1.27, of two 1.13 (8 blocks) 1.16 (6) 1.25 (5), of
+// moments, ms, before small roots had a path of their own (two groups now 1.10): 128 threads of one group 1.27, of two 1.13 (8 blocks) 1.16 (6) 1.25 (5), of
 // three 1.20; 256 threads of one 1.33; 64 of two 1.15.  fp32 moments: 2.76 to 2.77 in all.
 constexpr int kThreads = 128;
 constexpr int kTurns = 2;

@@ -20,10 +20,10 @@
 // then: it holds up none that it waits for, however few blocks fit the SMs beside other
 // work.  Waits are bounded all the same.  No atomics on floats: results are the same from run to run.
 //
-// 40001 x 256 logits: 17.7 us in one sequence, 22.8 in 24 with a mask (42 MB, 6.2 us at the
+// 40001 x 256 logits: 17.0 us in one sequence, 22.5 in 24 with a mask (42 MB, 6.2 us at the
 // rate of a plain copy).  Of a call's time, rows are done after 11 us (median; memory from a
 // cold start), announced by 14, the slots added by 17.4: the last part is a chain of loads
-// through L2, each waiting for the one before.  131072 x 256: 34.6 us (0.59).  One token: 6.4.
+// through L2, each waiting for the one before.  131072 x 256: 34.2 us (0.60).  One token: 6.8.
 // Two launches, the second one cluster: 24 and 33 us.
 // The gradient: 40001 x 256 in 13.9 us (0.87), onto dlogits, 24 sequences, 22.5 (0.80),
 // 131072 x 256 in 47.9 (0.83); 8192 x 64 in 3.5, latency.

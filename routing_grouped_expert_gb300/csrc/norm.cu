@@ -8,10 +8,12 @@
 // the variance is taken around the mean (a second pass over the registers), not as a
 // difference of two large sums.  Sums are fp32 in a fixed order.
 //
-// Bound by memory: 8192 x 7168 bf16 with a residual in 71.0 us (470 MB, 0.98 of the rate of a
-// plain copy; DRAM read 235 MB), 12000 x 4096 in 58.5 (0.99), 40001 x 512 in 25.9 (0.93),
-// without a residual 47 (0.73: half the bytes in flight).  Rows of 7170 104 us (0.67): their
-// weights are cut out of the pieces around them, and a row's ends taken one by one.
+// Bound by memory: 8192 x 7168 bf16 with a residual in 70.8 us (470 MB, 0.98 of the rate of a
+// plain copy; DRAM read 235 MB), 12000 x 4096 in 58.8 (0.98), 40001 x 512 in 26.2 (0.92),
+// without a residual 46 (0.75: half the bytes in flight).  fp32: 8192 x 4096 81.7 us (0.97),
+// 4096 x 7168 76.0 (0.91), without a residual 44.5 (0.78), 2000 x 16384 107 (0.72: its groups do
+// not fit the registers).  Rows of 7170 102 us (0.68): their weights are cut out of the pieces
+// around them, and a row's ends taken one by one.
 #include "norm.cuh"
 
 namespace moe {

@@ -7,11 +7,12 @@
 // One pass over dy, h and dh: each block adds the dw and db of its rows in registers, and a
 // second launch adds the blocks' shares.  Sums are fp32 in a fixed order.
 //
-// Bound by memory: 8192 x 7168 bf16 with dh in 76.5 us (470 MB, 0.90 of the rate of a plain
-// copy), of which the second launch is about 5; 12000 x 4096 64 (0.90), 20000 x 2048 55
-// (0.88), 40001 x 512 35 (0.70: a row per warp, its latency), rows of 7170 91 (0.76: the
-// fetching thread's work and the rows' ends), rows of 16384 144 (0.54: eight groups of a
-// thread do not fit its registers).  Few rows: 1 in 5.4 us, 128 of 7168 in 8.9, mostly the
+// Bound by memory: 8192 x 7168 bf16 with dh in 77.1 us (470 MB, 0.90 of the rate of a plain
+// copy), of which the second launch is about 5; 12000 x 4096 64.5 (0.90), 20000 x 2048 55
+// (0.88), 40001 x 512 35 (0.70: a row per warp, its latency), 200000 x 128 76 (0.40: the same),
+// rows of 7170 101 (0.69: the fetching thread's work and the rows' ends), 4000 x 16384 144 to 147
+// (0.54: eight groups of a thread do not fit its registers).  fp32: 4096 x 7168 74.7 us (0.93),
+// without dh 61.3 (0.84), 8192 x 4096 89 (0.89), 2000 x 16384 157 (0.49).  Few rows: 1 in 5.4 us, 128 of 7168 in 8.9, mostly the
 // two launches and their first loads.
 #include "norm.cuh"
 
@@ -49,7 +50,7 @@ __device__ __forceinline__ float2 block_sum2(float2 v, float2* part) {
 //   dx = dh + rstd (u - a / H - (rstd^2 c / H) d)
 // rstd^2 c / H is formed from the right, where it is rstd times a mean of u xhat: rstd^2 by itself
 // may leave fp32 with a small eps, in rows of padding say, in which c is 0.
-// The thread's part of a row, from `get_row(tensor, i, group)`, and dx.
+// The thread's part of a row, and of dx.
 template <typename T, typename W, int n, bool kVec, int kTeam>
 struct Backward {
   Team t;
